@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes as C
 import os
 import threading
+from typing import Any, NamedTuple
 
 __all__ = [
     "RFP2Error", "build", "lib", "library_path", "status_str",
@@ -28,6 +29,8 @@ __all__ = [
     "rfp2_pack_weights", "rfp2_pack_weights_weighted", "hfp4_pack_weights", "rfp2_validate_weights",
     "rfp2_debug_half_partials", "rfp2_debug_wait_timeout", "rfp2_row_bytes", "hfp4_row_bytes",
     "rfp2_set_weight_prefetch", "rfp2_weight_prefetch",
+    "KVCache", "rfp2_rope_frequencies", "rfp2_rope", "rfp2_kv_alloc", "rfp2_kv_write", "rfp2_kv_read",
+    "rfp2_attn_decode", "rfp2_attn_decode_workspace", "rfp2_attn_decode_workspace_bytes",
 ]
 
 MAX_BATCH = 8
@@ -53,6 +56,7 @@ def build(force: bool = False) -> str:
 
 
 _P, _I64, _I32, _SZ = C.c_void_p, C.c_int64, C.c_int, C.c_size_t
+_F32, _F64 = C.c_float, C.c_double
 
 _SIGNATURES = {
     "rfp2_status_str": (C.c_char_p, [_I32]),
@@ -84,6 +88,15 @@ _SIGNATURES = {
     "rfp2_debug_wait_timeout": (_I32, [_P, _P]),
     "rfp2_set_weight_prefetch": (_I32, [_I32]),
     "rfp2_weight_prefetch": (_I32, []),
+    "rfp2_rope_frequencies": (_I32, [_I64, _F64, _I32, _F64, _F64, _F64, _F64, _P, _P]),
+    "rfp2_rope": (_I32, [_P, _I32, _I64, _I64, _I64, _I64, _I64, _P, _P, _I64, _F32, _I32, _P, _I64,
+                         _I64, _P]),
+    "rfp2_kv_write": (_I32, [_P, _P, _I32] + [_I64] * 5 + [_P, _P, _P, _I64, _F32, _I32]
+                      + [_P] * 4 + [_I64] * 4 + [_P, _P]),
+    "rfp2_kv_read": (_I32, [_P] * 4 + [_I64] * 4 + [_P, _I64, _I32, _P, _P, _P, _P]),
+    "rfp2_attn_decode_workspace_bytes": (_SZ, [_I64] * 5),
+    "rfp2_attn_decode": (_I32, [_P, _I32] + [_I64] * 7 + [_P] * 4 + [_I64] * 3
+                         + [_P, _I64, _I64, _P, _F32, _I64, _F32, _P, _P, _P, _SZ, _P, _P]),
 }
 
 
@@ -437,3 +450,207 @@ def rfp2_debug_wait_timeout(dev_status):
     _need(dev_status, torch.int32, "dev_status")
     _check(lib().rfp2_debug_wait_timeout(_ptr(dev_status), _stream()), "rfp2_debug_wait_timeout")
     return dev_status
+
+
+# -- attention between the products -----------------------------------------------------
+
+_ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3}
+_ROPE_INTERLEAVED, _ROPE_INVERSE = 1, 2
+_dtype_codes = None
+
+
+class KVCache(NamedTuple):
+    """A paged key-value cache in Q8 blocks: codes int8 [pages, heads, page_size, D] and scales
+    fp32 [pages, heads, page_size, D/32], for keys and for values.  Calls take any such four."""
+    k_codes: Any
+    k_scales: Any
+    v_codes: Any
+    v_scales: Any
+
+
+def _dtype_code(t, name):
+    """The library's code of an activation tensor's type (fp32, bf16 or f16)."""
+    global _dtype_codes
+    if _dtype_codes is None:
+        torch = _torch()
+        _dtype_codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    try:
+        return _dtype_codes[t.dtype]
+    except KeyError:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}") from None
+
+
+def _rows(t, dims, name):
+    """A CUDA tensor of `dims` dimensions whose last one is contiguous: its shape and strides."""
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {len(shape)}")
+    if stride[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return shape, stride
+
+
+def _cache_sizes(cache):
+    torch = _torch()
+    kc, ks, vc, vs = cache
+    for t, dtype, name in ((kc, torch.int8, "k_codes"), (vc, torch.int8, "v_codes"),
+                           (ks, torch.float32, "k_scales"), (vs, torch.float32, "v_scales")):
+        _need(t, dtype, name)
+    shape = kc.shape
+    if len(shape) != 4:
+        raise ValueError("k_codes must be [pages, heads, page_size, D]")
+    scales = (shape[0], shape[1], shape[2], shape[3] // 32)
+    if vc.shape != shape or ks.shape != scales or vs.shape != scales:
+        raise ValueError("the cache's codes must be [pages, heads, page_size, D], its scales "
+                         "[pages, heads, page_size, D/32]")
+    return shape
+
+
+def rfp2_rope_frequencies(R, base=10000.0, scaling="plain", stretch=1.0, trained=4096.0, fast=32.0,
+                          slow=1.0, device="cuda"):
+    """Rotary frequencies for R rotated values: (inv_freq fp32 [R/2] on `device`, factor).
+    scaling: "plain", "linear" (all divided by stretch), "base" (a larger base) or "ramp" (by the
+    pair's turns over the `trained` length; factor = 0.1 ln(stretch) + 1)."""
+    torch = _torch()
+    f = torch.empty(max(R // 2, 0), dtype=torch.float32)
+    factor = C.c_float()
+    _check(lib().rfp2_rope_frequencies(R, base, _ROPE_SCALINGS[scaling], stretch, trained, fast, slow,
+                                       f.data_ptr(), C.addressof(factor)), "rfp2_rope_frequencies")
+    return f.to(device), factor.value
+
+
+def rfp2_rope(x, positions, inv_freq, out=None, interleaved=False, inverse=False, factor=1.0):
+    """Rotary positions: x [T, H, D] (any token and head strides) with the first 2*len(inv_freq)
+    values of each head rotated by positions int32 [T]; out=x rotates in place.  inverse=True
+    negates the angles (the gradient)."""
+    torch = _torch()
+    (T, H, D), xs = _rows(x, 3, "x")
+    code = _dtype_code(x, "x")
+    _need(positions, torch.int32, "positions")
+    _need(inv_freq, torch.float32, "inv_freq")
+    if positions.numel() != T:
+        raise ValueError("positions needs one value per token")
+    if out is None:
+        out = _empty((T, H, D), x.dtype, x)
+    shape, os_ = _rows(out, 3, "out")
+    if shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out must have x's shape and type")
+    _check(lib().rfp2_rope(x.data_ptr(), code, T, H, D, xs[0], xs[1], positions.data_ptr(),
+                           inv_freq.data_ptr(), 2 * inv_freq.numel(), factor,
+                           (_ROPE_INTERLEAVED if interleaved else 0) | (_ROPE_INVERSE if inverse else 0),
+                           out.data_ptr(), os_[0], os_[1], _stream()), "rfp2_rope")
+    return out
+
+
+def rfp2_kv_alloc(pages, heads, page_size, D, device="cuda"):
+    """A zeroed KVCache of `pages` pages."""
+    torch = _torch()
+    return KVCache(*(torch.zeros((pages, heads, page_size, n), dtype=dtype, device=device)
+                     for n, dtype in ((D, torch.int8), (D // 32, torch.float32)) * 2))
+
+
+def rfp2_kv_write(cache, k, v, slots, positions=None, inv_freq=None, interleaved=False, factor=1.0,
+                  dev_status=None):
+    """Quantise k, v [T, heads, D] into the cache at slots int64 [T] (page * page_size + offset;
+    -1 leaves a token out).  With positions and inv_freq, k is rotated on the way in."""
+    torch = _torch()
+    pages, heads, page_size, D = _cache_sizes(cache)
+    shape, ks = _rows(k, 3, "k")
+    vshape, vs = _rows(v, 3, "v")
+    code = _dtype_code(k, "k")
+    T = shape[0]
+    if shape[1] != heads or shape[2] != D or vshape != shape or v.dtype != k.dtype:
+        raise ValueError("k and v must be [T, heads, D] of one type, as the cache has them")
+    _need(slots, torch.int64, "slots")
+    if slots.numel() != T:
+        raise ValueError("slots needs one value per token")
+    R = 0
+    if positions is not None:
+        _need(positions, torch.int32, "positions")
+        if positions.numel() != T:
+            raise ValueError("positions needs one value per token")
+        positions = positions.data_ptr()
+    if inv_freq is not None:
+        _need(inv_freq, torch.float32, "inv_freq")
+        R = 2 * inv_freq.numel()
+        inv_freq = inv_freq.data_ptr()
+    _check(lib().rfp2_kv_write(k.data_ptr(), v.data_ptr(), code, T, ks[0], ks[1], vs[0], vs[1],
+                               slots.data_ptr(), positions, inv_freq, R, factor,
+                               _ROPE_INTERLEAVED if interleaved else 0,
+                               cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(),
+                               cache[3].data_ptr(), pages, heads, page_size, D, _ptr(dev_status),
+                               _stream()), "rfp2_kv_write")
+
+
+def rfp2_kv_read(cache, slots, dtype=None, k=None, v=None, dev_status=None):
+    """The values at slots int64 [T]: (k, v), each [T, heads, D] of `dtype` (fp32 unless given;
+    or the type of the k and v passed to be filled).  A slot of -1 reads as zeros."""
+    torch = _torch()
+    pages, heads, page_size, D = _cache_sizes(cache)
+    _need(slots, torch.int64, "slots")
+    T = slots.numel()
+    like = next((t for t in (k, v) if t is not None), None)
+    dtype = dtype or (like.dtype if like is not None else torch.float32)
+    k = _empty((T, heads, D), dtype, slots) if k is None else _need(k, dtype, "k")
+    v = _empty((T, heads, D), dtype, slots) if v is None else _need(v, dtype, "v")
+    if k.shape != (T, heads, D) or v.shape != (T, heads, D):
+        raise ValueError("k and v must be [T, heads, D]")
+    _check(lib().rfp2_kv_read(cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(),
+                              cache[3].data_ptr(), pages, heads, page_size, D, slots.data_ptr(), T,
+                              _dtype_code(k, "k"), k.data_ptr(), v.data_ptr(), _ptr(dev_status),
+                              _stream()), "rfp2_kv_read")
+    return k, v
+
+
+def rfp2_attn_decode_workspace_bytes(B: int, nq: int, Hq: int, heads: int, D: int) -> int:
+    return int(lib().rfp2_attn_decode_workspace_bytes(B, nq, Hq, heads, D))
+
+
+def rfp2_attn_decode_workspace(q, heads):
+    """A zeroed workspace for rfp2_attn_decode of q [B, nq, Hq, D] over `heads` key heads; calls in
+    one stream may share it."""
+    torch = _torch()
+    B, nq, Hq, D = q.shape
+    return torch.zeros(rfp2_attn_decode_workspace_bytes(B, nq, Hq, heads, D), dtype=torch.uint8,
+                       device=q.device)
+
+
+def rfp2_attn_decode(q, cache, table, lens, scale=None, window=0, softcap=0.0, out=None, lse=None,
+                     workspace=None, dev_status=None):
+    """Attention of each sequence's newest tokens over the paged cache: q [B, nq, Hq, D], table int32
+    [B, width] of pages, lens int32 [B] of keys held (the nq newest among them).  Returns out
+    [B, nq, Hq, D] of q's type and lse fp32 [B, nq, Hq].  scale: D**-0.5 unless given; window: only the
+    last `window` keys (0: all); softcap: scores become softcap * tanh(s / softcap) (0: as they are).
+    workspace: from rfp2_attn_decode_workspace (zero before its first use)."""
+    torch = _torch()
+    pages, heads, page_size, D = _cache_sizes(cache)
+    (B, nq, Hq, Dq), qs = _rows(q, 4, "q")
+    code = _dtype_code(q, "q")
+    _need(lens, torch.int32, "lens")
+    (Bt, width), ts = _rows(table, 2, "table")
+    if table.dtype != torch.int32:
+        raise TypeError(f"table must be {torch.int32}, got {table.dtype}")
+    if Dq != D or Bt != B or lens.numel() != B:
+        raise ValueError("q must be [B, nq, Hq, D] with the cache's D, table [B, width], lens [B]")
+    if out is None:
+        out = _empty((B, nq, Hq, D), q.dtype, q)
+    elif _need(out, q.dtype, "out").shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is None:
+        lse = _empty((B, nq, Hq), torch.float32, q)
+    elif _need(lse, torch.float32, "lse").shape != q.shape[:3]:
+        raise ValueError("lse must be [B, nq, Hq]")
+    if workspace is None:
+        workspace = rfp2_attn_decode_workspace(q, heads)
+    else:
+        _need(workspace, torch.uint8, "workspace")
+    _check(lib().rfp2_attn_decode(q.data_ptr(), code, B, nq, Hq, D, qs[0], qs[1], qs[2],
+                                  cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(),
+                                  cache[3].data_ptr(), pages, heads, page_size, table.data_ptr(), width,
+                                  ts[0] if B > 1 else max(ts[0], width), lens.data_ptr(),
+                                  D ** -0.5 if scale is None else scale, window, softcap,
+                                  out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+                                  workspace.numel(), _ptr(dev_status), _stream()), "rfp2_attn_decode")
+    return out, lse

@@ -364,6 +364,132 @@ rfp2_status rfp2_debug_half_partials(const uint8_t *W, int64_t M, int64_t K, con
  * the context stays usable.  Errors: EINVAL, EALIGN, ECUDA. */
 rfp2_status rfp2_debug_wait_timeout(int32_t *dev_status, rfp2_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention between the products of a decoder layer: rotary positions, a paged
+ * key-value cache held in Q8 blocks, and the attention of the newest tokens
+ * over it.  Values of activations may be fp32 (what the GEMVs return), bf16 or
+ * f16; all arithmetic is fp32, rounded once at the end.
+ */
+typedef enum { RFP2_F32 = 0, RFP2_BF16 = 1, RFP2_F16 = 2 } rfp2_dtype;
+
+/* Layout of rotated pairs, and direction. */
+#define RFP2_ROPE_INTERLEAVED 1 /* pairs (2i, 2i+1); without it (i, i + R/2) */
+#define RFP2_ROPE_INVERSE 2     /* angles negated: the gradient of the rotation */
+
+/* How rfp2_rope_frequencies stretches a context. */
+typedef enum {
+    RFP2_ROPE_PLAIN = 0,   /* base^(-2i/R) */
+    RFP2_ROPE_LINEAR = 1,  /* every frequency divided by `stretch` */
+    RFP2_ROPE_BASE = 2,    /* base raised to base * stretch^(R/(R-2)) */
+    RFP2_ROPE_RAMP = 3     /* by turns over the trained length (YaRN, Peng et al.
+                              2023): kept from `fast` turns up, divided by
+                              `stretch` below `slow` turns, linear in the turns'
+                              share of [slow, fast] between */
+} rfp2_rope_scaling;
+
+/* Rotary frequencies, host memory: inv_freq[i], i < R/2, computed in double
+ * and rounded once.  *factor (optional) gets the scale that goes with them:
+ * 1, or 0.1 ln(stretch) + 1 for RFP2_ROPE_RAMP.  `trained`, `fast` and `slow`
+ * are read by RFP2_ROPE_RAMP alone (usual: 32 and 1).
+ * Errors: EINVAL (null, unknown scaling, base, stretch or trained not
+ * positive and finite, fast <= slow), ESHAPE (R odd, < 2 or > 65536, or R < 4
+ * with RFP2_ROPE_BASE).
+ */
+rfp2_status rfp2_rope_frequencies(int64_t R, double base, int scaling, double stretch,
+                                  double trained, double fast, double slow, float *inv_freq,
+                                  float *factor);
+
+/* Rotary positions.  The first R of each head's D values are rotated in pairs
+ * (a, b) by theta = position * inv_freq[i]: (a cos - b sin, b cos + a sin) *
+ * factor; the others are copied.  theta is the exact product of the integer
+ * position and the fp32 frequency, so long contexts keep their angles.
+ *   x    `dtype` [T, H, D] device: D contiguous, tokens x_token_stride and
+ *        heads x_head_stride elements apart (any strides).
+ *   out  the same type, its own strides; out == x with the same strides
+ *        rotates in place, any other overlap is not allowed.
+ *   positions int32 [T], any value; inv_freq fp32 [R/2], finite; both device.
+ *   flags RFP2_ROPE_*.
+ * Errors: EINVAL (null, negative size, bad dtype or flags), ESHAPE (R or D
+ * odd, R < 0, R > D or R > 4096, D or H > 65536, T > 2^31 - 1), EALIGN (a
+ * pointer not aligned to its type), ECUDA.
+ */
+rfp2_status rfp2_rope(const void *x, int dtype, int64_t T, int64_t H, int64_t D,
+                      int64_t x_token_stride, int64_t x_head_stride, const int32_t *positions,
+                      const float *inv_freq, int64_t R, float factor, int flags, void *out,
+                      int64_t out_token_stride, int64_t out_head_stride, rfp2_stream_t stream);
+
+/* The paged key-value cache: four arrays, for keys and for values each
+ *   codes  int8 [pages, heads, page_size, D]
+ *   scales fp32 [pages, heads, page_size, D/32]
+ * contiguous, codes and scales 16-byte aligned; D % 32 == 0, 32 <= D <= 256;
+ * any page_size >= 1.  A value is code * scale: Q8_1-style blocks of 32
+ * neighbouring values of one token's head, quantized as rfp2_quantize_act does
+ * (scale = max|a| / 127, code = round-half-away(a / scale)).  A block that
+ * holds an infinity or a NaN reads back as NaN.  A token's place is its slot:
+ * page * page_size + offset.
+ *
+ * rfp2_kv_write: k, v `dtype` [T, heads, D] device (D contiguous, any token
+ *   and head strides) into the slots int64 [T] device.  A slot of -1 leaves
+ *   its token out; any other slot outside the cache is not written and stores
+ *   RFP2_EBADID to *dev_status.  Two tokens of one call must not share a slot.
+ *   With positions int32 [T] and inv_freq fp32 [R/2] (both or neither), k is
+ *   rotated on the way in as rfp2_rope would, in fp32 and without a rounding
+ *   before the quantization; flags: RFP2_ROPE_INTERLEAVED.
+ * rfp2_kv_read: the values at the slots into k, v `dtype` [T, heads, D]
+ *   contiguous (either may be NULL).  A slot of -1 reads as zeros, any other
+ *   slot outside the cache as NaN with RFP2_EBADID in *dev_status.
+ * Errors: EINVAL, ESHAPE (D, page_size, T > 2^31 - 1, pages * heads *
+ * page_size >= 2^40), EALIGN, ECUDA.
+ */
+rfp2_status rfp2_kv_write(const void *k, const void *v, int dtype, int64_t T,
+                          int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                          int64_t v_head_stride, const int64_t *slots, const int32_t *positions,
+                          const float *inv_freq, int64_t R, float factor, int flags,
+                          int8_t *k_codes, float *k_scales, int8_t *v_codes, float *v_scales,
+                          int64_t pages, int64_t heads, int64_t page_size, int64_t D,
+                          int32_t *dev_status, rfp2_stream_t stream);
+rfp2_status rfp2_kv_read(const int8_t *k_codes, const float *k_scales, const int8_t *v_codes,
+                         const float *v_scales, int64_t pages, int64_t heads, int64_t page_size,
+                         int64_t D, const int64_t *slots, int64_t T, int dtype, void *k, void *v,
+                         int32_t *dev_status, rfp2_stream_t stream);
+
+/* Attention of each sequence's newest tokens over the paged cache.
+ * Sequence b holds lens[b] keys, its newest nq tokens' own among them; key j
+ * is at place j % page_size of page table[b, j / page_size].  Query i of nq
+ * sees the keys j < lens[b] - nq + 1 + i, and with window > 0 only the last
+ * `window` of those.  Query head h reads key head h / (Hq / heads):
+ *   s = scale * q . k,  with softcap > 0: s = softcap * tanh(s / softcap)
+ *   out = sum_j softmax(s)_j v_j,  lse = log sum_j exp(s_j) (natural).
+ * A query that sees no key gets out = 0 and lse = -infinity.
+ *   q    `dtype` [B, nq, Hq, D] device: D contiguous, any other strides.
+ *   out  `dtype` [B, nq, Hq, D] contiguous; lse fp32 [B, nq, Hq] or NULL.
+ *   table int32 [B, table_width] device (rows table_stride apart), lens int32
+ *        [B] device.  Only the entries that hold visible keys are read; one
+ *        outside [0, pages) makes its sequence's rows NaN (rows that see none
+ *        of that page's keys may stay finite) and stores RFP2_EBADID, as does
+ *        a length outside [0, table_width * page_size].
+ *   workspace  device, 256-byte aligned, of
+ *        rfp2_attn_decode_workspace_bytes(B, nq, Hq, heads, D) bytes, ZERO
+ *        before its first use; every call leaves it fit for the next one of
+ *        any sizes.  Calls that overlap on the GPU must not share it.
+ * The length is split over the GPU and joined in a fixed order: the same call
+ * gives the same bits.
+ * Errors: EINVAL, ESHAPE (Hq % heads, D, page_size, B or nq < 1, nq * Hq >
+ * 65536, table_width * page_size > 2^30, table_stride < table_width, pages *
+ * heads * page_size >= 2^32), EALIGN, EWORKSPACE, ECUDA.
+ */
+size_t rfp2_attn_decode_workspace_bytes(int64_t B, int64_t nq, int64_t Hq, int64_t heads,
+                                        int64_t D);
+rfp2_status rfp2_attn_decode(const void *q, int dtype, int64_t B, int64_t nq, int64_t Hq,
+                             int64_t D, int64_t q_batch_stride, int64_t q_token_stride,
+                             int64_t q_head_stride, const int8_t *k_codes, const float *k_scales,
+                             const int8_t *v_codes, const float *v_scales, int64_t pages,
+                             int64_t heads, int64_t page_size, const int32_t *table,
+                             int64_t table_width, int64_t table_stride, const int32_t *lens,
+                             float scale, int64_t window, float softcap, void *out, float *lse,
+                             void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                             rfp2_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
