@@ -271,9 +271,8 @@ def test_pages_and_lengths_outside_the_cache(g):
     out, lse = g.rfp2_attn_decode(q, cache, table, lens, dev_status=st)
     assert int(st) == 7
     assert bool(out[1:].isnan().all()) and bool(lse[1:].isnan().all())
-    ok = Case(4, 1, 4, 2, 64, 16, [50, 50, 50, 50], seed=2)
-    good, good_lse = _run(g, ok)
-    assert torch.equal(out[0], good[0]) and torch.equal(lse[0], good_lse[0])
+    c.q, c.k, c.v = c.q[:1], c.k[:1], c.v[:1]
+    c.check(out[:1], lse[:1], lens=c.lens[:1])
 
 
 def test_the_sum_of_two_halves(g):
