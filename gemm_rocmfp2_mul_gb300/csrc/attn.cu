@@ -8,8 +8,8 @@ using namespace rfp2;
 
 namespace {
 
-// Two partial results a CTA (the units that a stretch begins and ends in), of
-// 16 columns' references, sums and values.
+// Partial results: two a CTA and one a warp, of 16 columns' references, sums
+// and values.
 size_t partial_bytes(int64_t D) { return (size_t)(32 + 16 * D) * 4; }
 
 }  // namespace
@@ -17,7 +17,8 @@ size_t partial_bytes(int64_t D) { return (size_t)(32 + 16 * D) * 4; }
 extern "C" size_t rfp2_attn_decode_workspace_bytes(int64_t B, int64_t nq, int64_t Hq,
                                                    int64_t heads, int64_t D) {
     if (B < 1 || nq < 1 || Hq < 1 || heads < 1 || Hq % heads != 0 || D < 32 || D > 256) return 0;
-    return kAttnCounterBytes + 4 * (size_t)sm_count(current_device()) * partial_bytes(D);
+    return kAttnCounterBytes +
+           2 * (size_t)sm_count(current_device()) * (2 + kAttnWarps) * partial_bytes(D);
 }
 
 extern "C" rfp2_status rfp2_attn_decode(const void *q, int dtype, int64_t B, int64_t nq,
@@ -70,6 +71,7 @@ extern "C" rfp2_status rfp2_attn_decode(const void *q, int dtype, int64_t B, int
     a.page_shift = -1;
     for (int s = 0; s < 31; ++s)
         if (page_size == (1ll << s)) a.page_shift = s;
+    a.whole_pages = page_size % kAttnTile == 0;
     a.dtype = dtype;
     const int64_t words = 16 / size;
     a.q_words = aligned(q, 16) && a.qb % words == 0 && a.qt % words == 0 && a.qh % words == 0;

@@ -5,13 +5,15 @@
 //   out = sum_j p_j dV[j, b] vq[j] / sum_j p_j,  p_j = exp(s_j - max s),  lse = max s + ln sum_j p_j
 //
 // Bound by memory: each key of a head is 2 (D + D/8) bytes, read once for all
-// its query heads and tokens ("columns").  Work is cut in tiles of 16 keys; the
-// tiles of all (sequence, key head, column tile) units lie on one line that the
-// CTAs share out evenly whatever the lengths are, and tile x of a CTA goes to
-// warp x % 8.  Each warp streams its tiles through its own ring in shared
-// memory (cp.async) and keeps its own softmax state; the warps join at the end
-// of a unit's stretch, and a unit that several CTAs share is joined by the last
-// of them to finish, always in the order of the keys.
+// its query heads and tokens ("columns").  Work is cut in tiles of 16 keys.  The
+// tiles of all (sequence, key head, column tile) units lie on one line, with a
+// gap before each unit that stands for its fixed cost, and the warps of the
+// grid share the line out evenly whatever the lengths are.  A warp streams its
+// stretch through its own ring in shared memory (cp.async), keeps its own
+// softmax state and meets no barrier on the way; units that lie within its
+// stretch it writes itself.  What it holds of units that reach beyond is joined
+// at the end: within the CTA through shared memory, between CTAs through the
+// workspace by the last of them to arrive, always in the order of the keys.
 //
 // Products run on f16 matrix instructions (16 keys x 8 columns x 16 values):
 // codes are exact in f16, q goes in scaled by a power of two (one f16 piece is
@@ -30,8 +32,10 @@ namespace rfp2 {
 
 constexpr int kAttnWarps = 8;
 constexpr int kAttnThreads = kAttnWarps * 32;
-constexpr int kAttnTile = 16;         // keys
-constexpr int kAttnMaxBatch = 1024;   // sequences of one launch
+constexpr int kAttnTile = 16;        // keys
+constexpr int kAttnGap = 2;          // a unit's fixed cost, in tiles
+constexpr int kAttnMinStretch = 2;   // of a warp, in tiles
+constexpr int kAttnMaxBatch = 512;   // sequences of one launch
 constexpr int kAttnCounterBytes = 4096;
 
 struct AttnArgs {
@@ -43,6 +47,7 @@ struct AttnArgs {
     int64_t pages, table_stride, capacity;
     int B, nq, Hq, heads, group, columns, column_tiles;
     int page_size, page_shift;  // shift: log2 of page_size, or -1
+    int whole_pages;            // page_size % 16 == 0: a tile lies in one page
     int dtype, q_words;         // q_words: q can be read as 16-byte words
     float scale, softcap;
     int64_t window;
@@ -53,61 +58,60 @@ struct AttnArgs {
     int32_t *status;
 };
 
-// One piece of the row layout: strides (bytes) of a tile's rows in shared
-// memory, padded so that the fragment reads meet no bank twice.  K is read 8
-// bytes a lane, four keys a half-warp: 32-byte steps between keys need an odd
-// number of them a row.  V is read 4 bytes a lane, keys two apart: an odd number
-// of 16-byte steps.
+// A tile in shared memory.  K is read 8 bytes a lane, four keys a half-warp, so
+// the 32-byte steps between keys are made odd (or, for 256 values, a key's
+// blocks are permuted by its two low bits).  V is read 4 bytes a lane, keys two
+// apart, so a row gets an odd number of 16-byte steps.  Neither read meets a
+// bank twice.
 template <int NB>
 struct AttnLayout {
     static constexpr int D = 32 * NB;
-    static constexpr int k_stride = NB % 2 ? D : D + 32;
+    static constexpr bool k_permuted = NB == 8;
+    static constexpr int k_stride = NB % 2 || k_permuted ? D : D + 32;
     static constexpr int v_stride = D + 16;
     static constexpr int k_bytes = kAttnTile * k_stride, v_bytes = kAttnTile * v_stride;
     static constexpr int scale_bytes = kAttnTile * NB * 4;
     static constexpr int stage_bytes = k_bytes + v_bytes + 2 * scale_bytes;
 };
 
-// Shared memory: rings, then the join buffer, the warps' references and sums,
-// and the sequences' tile prefix.
-template <int NB, int NT>
-struct AttnShared {
-    static constexpr int chunk = NB >= 2 ? 64 : 32;  // values joined at a time
-    static constexpr int row = chunk + 4;            // floats, padded against bank conflicts
-    static constexpr int join_bytes = kAttnWarps * 8 * NT * row * 4;
-    static constexpr int state_bytes = 2 * kAttnWarps * 8 * NT * 4;
-    static constexpr int other = join_bytes + state_bytes + 64;
-    static constexpr int stages_for(int budget) {
-        const int s = (budget - other - (kAttnMaxBatch + 1) * 12) /
-                      (kAttnWarps * AttnLayout<NB>::stage_bytes);
-        return s > 8 ? 8 : s;
-    }
+// What the warps leave of a unit that reaches beyond their stretch.
+struct AttnPiece {
+    int present, starts;  // starts: holds the unit's first tile
+    int b, hk, ct;
+    int64_t unit0;        // the unit's place on the line
 };
 
 template <int NB, int NT>
 constexpr int attn_ctas_per_sm() { return NB * NT <= 2 ? 2 : 1; }
+// The warps' sums of the scan, the pieces and their columns' states, and the
+// line's prefix.
+template <int NT>
+constexpr int attn_small_bytes(int B) {
+    return 64 + 2 * kAttnWarps * ((int)sizeof(AttnPiece) + 4 * 8 * NT * 4) + (B + 1) * 8;
+}
 template <int NB, int NT>
 constexpr int attn_stages() {
-    return AttnShared<NB, NT>::stages_for((attn_ctas_per_sm<NB, NT>() == 2 ? 113 : 227) * 1024);
+    const int budget = (attn_ctas_per_sm<NB, NT>() == 2 ? 113 : 227) * 1024;
+    const int s = (budget - attn_small_bytes<NT>(kAttnMaxBatch)) / (kAttnWarps * AttnLayout<NB>::stage_bytes);
+    return s > 8 ? 8 : s;
 }
 template <int NB, int NT>
 int attn_smem(int B) {
-    return kAttnWarps * attn_stages<NB, NT>() * AttnLayout<NB>::stage_bytes +
-           AttnShared<NB, NT>::other + (B + 1) * 8 + B * 4;
+    return kAttnWarps * attn_stages<NB, NT>() * AttnLayout<NB>::stage_bytes + attn_small_bytes<NT>(B);
 }
+// Floats of one partial result: references, sums, values of the columns.
+template <int NB, int NT>
+constexpr int attn_slot() { return 8 * NT * (2 + 32 * NB); }
 
-RFP2_DEV void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-                 : "memory");
+RFP2_DEV void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 template <int N>
-RFP2_DEV void cp_async_small(uint32_t dst, const void *src, uint32_t bytes) {
+RFP2_DEV void cp_async_small(uint32_t dst, const void *src) {
     if constexpr (N == 16)
-        cp_async16(dst, src, bytes);
+        cp_async16(dst, src);
     else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N),
-                     "r"(bytes)
-                     : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
 }
 RFP2_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -154,35 +158,78 @@ RFP2_DEV float log2_fast(float x) {
     return y;
 }
 
-// A place on the line of tiles: unit (b, hk, ct) and tile t of its `tiles`.
+// A key's NB scales, in the widest words that divide its row.
+template <int NB>
+RFP2_DEV void load_scales(const float *p, float (&d)[NB]) {
+    if constexpr (NB % 4 == 0) {
+#pragma unroll
+        for (int n = 0; n < NB; n += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(p + n);
+            d[n] = v.x, d[n + 1] = v.y, d[n + 2] = v.z, d[n + 3] = v.w;
+        }
+    } else if constexpr (NB % 2 == 0) {
+#pragma unroll
+        for (int n = 0; n < NB; n += 2) {
+            const float2 v = *reinterpret_cast<const float2 *>(p + n);
+            d[n] = v.x, d[n + 1] = v.y;
+        }
+    } else {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) d[n] = p[n];
+    }
+}
+
+// A place on the line: unit (b, hk, ct) of `tiles` tiles that begins (with its
+// gap) at `unit0`.
 struct AttnPlace {
-    int b, hk, ct, t, tiles;
+    int b, hk, ct, tiles;
+    int64_t unit0;
+};
+
+RFP2_DEV int64_t quotient(int64_t a, int64_t b) {  // a, b >= 0; 64-bit division is slow
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// The line's share of each warp: `each` places, one more for the first `extra`.
+struct AttnShare {
+    int64_t each, extra;
+    RFP2_DEV int64_t begin(int64_t worker) const { return worker * each + min(worker, extra); }
+    RFP2_DEV int64_t worker_of(int64_t x) const {
+        const int64_t more = extra * (each + 1);
+        return x < more ? quotient(x, each + 1) : extra + quotient(x - more, each);
+    }
 };
 
 template <int NB, int NT, int PIECES>
 __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
     attn_kernel(const AttnArgs a) {
     using L = AttnLayout<NB>;
-    using S = AttnShared<NB, NT>;
-    constexpr int D = L::D, STAGES = attn_stages<NB, NT>(), COLS = 8 * NT;
+    constexpr int D = L::D, STAGES = attn_stages<NB, NT>(), COLS = 8 * NT, SLOT = attn_slot<NB, NT>();
+    static_assert(SLOT * 4 <= STAGES * L::stage_bytes, "a warp's partial result fits its ring");
+    static_assert(STAGES >= 2, "");
     constexpr float kShift = 8.0f, kMost = 15.0f;  // p dV aims at 2^8 and stays below 2^15
     constexpr float kNone = -3.4e38f;              // the reference before any key
     // p is up to 2^15 / dV: 2^125 where the values are tiny (dV is taken as 2^-110 at least here)
     constexpr float kSumScale = 2.3283064365386963e-10f, kSumShift = 32.0f;  // 2^-32
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *rings = smem;
-    float *join = reinterpret_cast<float *>(rings + kAttnWarps * STAGES * L::stage_bytes);
-    float *state_r = join + S::join_bytes / 4, *state_l = state_r + kAttnWarps * COLS;
-    int64_t *small = reinterpret_cast<int64_t *>(state_l + kAttnWarps * COLS);  // 8 words of 8 bytes
-    int64_t *prefix = small + 8;                                                // [B + 1]
-    int32_t *slen = reinterpret_cast<int32_t *>(prefix + a.B + 1);              // [B]
+    int64_t *small = reinterpret_cast<int64_t *>(rings + kAttnWarps * STAGES * L::stage_bytes);  // 8
+    AttnPiece *pieces = reinterpret_cast<AttnPiece *>(small + 8);  // [warps][head, tail]
+    float *piece_r = reinterpret_cast<float *>(pieces + 2 * kAttnWarps);  // [pieces][COLS]
+    float *piece_l = piece_r + 2 * kAttnWarps * COLS;
+    float *group_r = piece_l + 2 * kAttnWarps * COLS, *group_l = group_r + 2 * kAttnWarps * COLS;
+    int64_t *prefix = reinterpret_cast<int64_t *>(group_l + 2 * kAttnWarps * COLS);  // [B + 1]
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
     pdl_wait();
     pdl_launch_dependents();
 
-    // ---- the line of tiles: how many each sequence has, and their prefix ----
+    // ---- the line: each sequence's length on it for one unit, and their prefix ----
+    const auto length_of = [&](int b) {  // -1: not a length
+        const int len = a.lens[b];
+        return len < 0 || len > a.capacity ? -1 : len;
+    };
     const auto tile_low = [&](int len) {
         if (a.window == 0) return 0;
         const int64_t low = (int64_t)len - a.nq + 1 - a.window;
@@ -192,18 +239,14 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
         int64_t run = 0;
         for (int b0 = 0; b0 < a.B; b0 += kAttnThreads) {
             const int b = b0 + tid;
-            int tiles = 0;
+            int cost = 0;
             if (b < a.B) {
-                int len = a.lens[b];
-                if (len < 0 || len > a.capacity) {
-                    if (blockIdx.x == 0) record_status(a.status, RFP2_EBADID);
-                    len = -1;
-                }
-                slen[b] = len;
-                // a sequence without keys still has its rows written
-                tiles = max(1, (len + kAttnTile - 1) / kAttnTile - tile_low(len));
+                const int len = length_of(b);
+                if (len < 0 && blockIdx.x == 0) record_status(a.status, RFP2_EBADID);
+                // a sequence without keys has one tile too: its rows are written
+                cost = kAttnGap + max(1, (len + kAttnTile - 1) / kAttnTile - tile_low(len));
             }
-            int64_t incl = tiles;
+            int64_t incl = cost;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const int64_t up = __shfl_up_sync(0xffffffffu, incl, off);
@@ -211,145 +254,253 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
             }
             if (b0) __syncthreads();
             if (lane == 31) small[warp] = incl;
+            if (b0 == 0 && tid < 2 * kAttnWarps) pieces[tid].present = 0;
             __syncthreads();
-            int64_t before = 0, total = 0;
+            int64_t before = 0, all = 0;
 #pragma unroll
             for (int w = 0; w < kAttnWarps; ++w) {
                 before += w < warp ? small[w] : 0;
-                total += small[w];
+                all += small[w];
             }
-            if (b < a.B) prefix[b] = run + before + incl - tiles;
-            run += total;
+            if (b < a.B) prefix[b] = run + before + incl - cost;
+            run += all;
         }
         if (tid == 0) prefix[a.B] = run;
         __syncthreads();
     }
     const int units_of = a.heads * a.column_tiles;
     const int64_t total = prefix[a.B] * units_of;
-    // at least one tile a warp: a short stretch is not worth a join
-    const int64_t parts = min((int64_t)gridDim.x, (total + kAttnWarps - 1) / kAttnWarps);
+    // some tiles for each warp: shorter stretches are not worth their joins
+    const int64_t parts = min((int64_t)gridDim.x,
+                              (total + kAttnMinStretch * kAttnWarps - 1) / (kAttnMinStretch * kAttnWarps));
     if ((int64_t)blockIdx.x >= parts) return;
-    const int64_t x0 = blockIdx.x * total / parts, x1 = (blockIdx.x + 1) * total / parts;
+    AttnShare share;
+    share.each = quotient(total, parts * kAttnWarps);
+    share.extra = total - share.each * parts * kAttnWarps;
+    const int64_t worker = (int64_t)blockIdx.x * kAttnWarps + warp;
+    const int64_t y0 = share.begin(worker), y1 = share.begin(worker + 1);
 
     AttnPlace first;
     {
-        int lo = 0, hi = a.B;  // the last b with prefix[b] * units_of <= x0
+        int lo = 0, hi = a.B;  // the last b with prefix[b] * units_of <= y0
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (prefix[mid] * units_of <= x0) lo = mid; else hi = mid;
+            if (prefix[mid] * units_of <= y0) lo = mid; else hi = mid;
         }
+        const int cost = (int)(prefix[lo + 1] - prefix[lo]);
+        const int64_t off = y0 - prefix[lo] * units_of;
+        const int unit = (int)quotient(off, cost);
         first.b = lo;
-        first.tiles = (int)(prefix[lo + 1] - prefix[lo]);
-        const int64_t off = x0 - prefix[lo] * units_of;
-        const int unit = (int)(off / first.tiles);
-        first.t = (int)(off - (int64_t)unit * first.tiles);
+        first.tiles = cost - kAttnGap;
+        first.unit0 = prefix[lo] * units_of + (int64_t)unit * cost;
         first.hk = unit / a.column_tiles;
         first.ct = unit - first.hk * a.column_tiles;
     }
     const auto next_unit = [&](AttnPlace &p) {
+        p.unit0 += p.tiles + kAttnGap;
         if (++p.ct == a.column_tiles) {
             p.ct = 0;
             if (++p.hk == a.heads) {
                 p.hk = 0;
                 ++p.b;
-                p.tiles = p.b < a.B ? (int)(prefix[p.b + 1] - prefix[p.b]) : 1;
+                p.tiles = p.b < a.B ? (int)(prefix[p.b + 1] - prefix[p.b]) - kAttnGap : 1;
             }
         }
+    };
+    // this warp's tiles [from, to) of a unit
+    const auto tiles_from = [&](const AttnPlace &p) {
+        return (int)max((int64_t)0, y0 - p.unit0 - kAttnGap);
+    };
+    const auto tiles_to = [&](const AttnPlace &p) {
+        return (int)max((int64_t)0, min((int64_t)p.tiles, y1 - p.unit0 - kAttnGap));
     };
 
-    // ---- the loads: this warp's tiles x0 + warp, + 8, ... ----
+    // ---- the loads, STAGES - 1 tiles ahead ----
     const uint32_t ring = smem_addr(rings) + warp * STAGES * L::stage_bytes;
     AttnPlace lp = first;
-    int64_t lx = x0 + warp;  // tile of the next load
-    lp.t += warp;
-    const auto settle = [&]() {
-        while (lx < x1 && lp.t >= lp.tiles) {
-            lp.t -= lp.tiles;
+    int lt = 0, lt_end = 0, l_len = 0, l_low = 0;  // tile of the next load; of its unit
+    bool loading = true;
+    // Pages of the tiles to come.  Where a tile lies in one page, lane i holds that of tile page_at + i
+    // and the 32 after those are on their way; else those of the next tile's keys.
+    int32_t page = -1, page_after = -1;
+    int page_at = 0;
+    const auto page_of_key = [&](int j) {
+        return j < l_len ? a.table[lp.b * a.table_stride +
+                                   (a.page_shift >= 0 ? j >> a.page_shift : j / a.page_size)]
+                         : -1;
+    };
+    const auto page_of_tile = [&](int t) { return t < lt_end ? page_of_key((l_low + t) * kAttnTile) : -1; };
+    const auto fetch_pages = [&]() {  // of a new unit
+        if (a.whole_pages) {
+            page_at = lt;
+            page = page_of_tile(lt + lane);
+            page_after = page_of_tile(lt + 32 + lane);
+        } else {
+            page = page_of_key((l_low + lt) * kAttnTile + (lane & (kAttnTile - 1)));
+        }
+    };
+    // enters units until one has tiles in this stretch
+    const auto enter = [&]() {
+        while (true) {
+            if (lp.unit0 + kAttnGap >= y1) {
+                loading = false;
+                return;
+            }
+            lt = tiles_from(lp);
+            lt_end = tiles_to(lp);
+            if (lt < lt_end) break;
             next_unit(lp);
         }
+        l_len = length_of(lp.b);
+        l_low = tile_low(l_len);
+        fetch_pages();
     };
-    int32_t next_page = 0;  // of key `lane` of the next tile, fetched ahead of its use
-    int next_key = -1;
-    const auto fetch_page = [&]() {
-        next_key = -1;
-        if (lx < x1 && lane < kAttnTile) {
-            const int len = slen[lp.b];
-            const int j = (tile_low(len) + lp.t) * kAttnTile + lane;
-            if (j < len) {
-                next_key = j;
-                next_page = a.table[lp.b * a.table_stride +
-                                    (a.page_shift >= 0 ? j >> a.page_shift : j / a.page_size)];
-            }
+    enter();
+    // a unit's rows of q on their way while the unit before is worked on
+    const auto prefetch_q = [&](const AttnPlace &p) {
+        constexpr int LINES = D * (PIECES == 2 ? 4 : 2) / 64;  // at least one address of each 128-byte line
+        const int c0 = p.ct * COLS, live = min(COLS, a.columns - c0);
+        for (int k = lane; k < live * LINES; k += 32) {
+            const int c = c0 + k / LINES, i = c / a.group, h = p.hk * a.group + c - i * a.group;
+            const int64_t at = p.b * a.qb + i * a.qt + h * a.qh;
+            const char *src = static_cast<const char *>(a.q) + at * (PIECES == 2 ? 4 : 2) + (k % LINES) * 64;
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(src));
         }
     };
-    settle();
-    fetch_page();
     const auto load_tile = [&](int stage) {
-        if (lx < x1) {
+        if (loading) {
             const uint32_t k_at = ring + stage * L::stage_bytes, v_at = k_at + L::k_bytes,
                            s_at = v_at + L::v_bytes;
-            // row of the cache arrays, or -1 (no such key), -2 (no such page)
-            constexpr uint32_t kNoKey = 0xFFFFFFFFu, kNoPage = 0xFFFFFFFEu;
-            uint32_t row = kNoKey;
-            if (next_key >= 0) {
-                if (next_page < 0 || next_page >= a.pages) {
-                    row = kNoPage;
-                    record_status(a.status, RFP2_EBADID);
-                } else {
-                    const uint32_t off = a.page_shift >= 0 ? next_key & (a.page_size - 1)
-                                                           : next_key % a.page_size;
-                    row = ((uint32_t)next_page * a.heads + lp.hk) * a.page_size + off;
-                }
-            }
             constexpr int CH = D / 16;
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const int id = lane + 32 * i, r = id / CH, c = id - r * CH;
-                const uint32_t src = __shfl_sync(0xffffffffu, row, r);
-                const bool ok = src < kNoPage;
-                const int64_t at = ok ? (int64_t)src * D + 16 * c : 0;
-                cp_async16(k_at + r * L::k_stride + 16 * c, a.k_codes + at, ok ? 16 : 0);
-                cp_async16(v_at + r * L::v_stride + 16 * c, a.v_codes + at, ok ? 16 : 0);
-            }
-            // scales: 2 x 16 rows of NB floats, in the widest words that divide a row
+            // scales: rows of NB floats, in the widest words that divide a row
             constexpr int W = NB % 4 == 0 ? 4 : NB % 2 == 0 ? 2 : 1, PER = NB / W;
+            const int key0 = (l_low + lt) * kAttnTile;
+            const auto k_place = [&](int r, int c) {  // of 16-byte word c of key r
+                return r * L::k_stride + 16 * (L::k_permuted ? c ^ ((r & 3) << 1) : c);
+            };
+            if (a.whole_pages) {
+                if (lt - page_at == 32) {
+                    page = page_after;
+                    page_at = lt;
+                    page_after = page_of_tile(lt + 32 + lane);
+                }
+                const int32_t next_page = __shfl_sync(0xffffffffu, page, lt - page_at);
+                // sixteen rows that follow one another; those past the sequence's end are masked later
+                if (key0 >= l_len) {
+                    // an empty sequence: nothing to read, and its place is masked
+                } else if (next_page < 0 || next_page >= a.pages) {
+                    record_status(a.status, RFP2_EBADID);
+                    float *p = reinterpret_cast<float *>(rings + (s_at - smem_addr(rings)));
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int id = lane + 32 * i, r2 = id / PER, c = id - r2 * PER;
-                const uint32_t src = __shfl_sync(0xffffffffu, row, r2 & 15);
-                const bool ok = src < kNoPage;
-                const int64_t at = ok ? (int64_t)src * NB + W * c : 0;
-                const uint32_t dst = s_at + (r2 * NB + W * c) * 4;
-                if (src == kNoPage && r2 < 16) {
-                    // a key whose page does not exist: its scores are NaN
-                    float *p = reinterpret_cast<float *>(rings + (dst - smem_addr(rings)));
-#pragma unroll
-                    for (int e = 0; e < W; ++e) p[e] = CUDART_NAN_F;
+                    for (int i = 0; i < (kAttnTile * NB + 31) / 32; ++i)
+                        if (lane + 32 * i < kAttnTile * NB) p[lane + 32 * i] = CUDART_NAN_F;
                 } else {
-                    cp_async_small<4 * W>(dst, (r2 < 16 ? a.k_scales : a.v_scales) + at, ok ? 4 * W : 0);
+                    const uint32_t off = a.page_shift >= 0 ? key0 & (a.page_size - 1) : key0 % a.page_size;
+                    const uint32_t row = ((uint32_t)next_page * a.heads + lp.hk) * a.page_size + off;
+                    const int8_t *kp = a.k_codes + (int64_t)row * D + 16 * lane;
+                    const int8_t *vp = a.v_codes + (int64_t)row * D + 16 * lane;
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) {
+                        const int id = lane + 32 * i, r = id / CH, c = id - r * CH;
+                        cp_async16(k_at + k_place(r, c), kp + 512 * i);
+                        cp_async16(v_at + r * L::v_stride + 16 * c, vp + 512 * i);
+                    }
+                    const float *ks = a.k_scales + (int64_t)row * NB, *vs = a.v_scales + (int64_t)row * NB;
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        const int id = lane + 32 * i, half = id >= 16 * PER, at = W * (id - half * 16 * PER);
+                        cp_async_small<4 * W>(s_at + 4 * W * id, (half ? vs : ks) + at);
+                    }
+                }
+            } else {
+                // row of the cache arrays of key `lane`, or -1 (no such key), -2 (no such page)
+                constexpr uint32_t kNoKey = 0xFFFFFFFFu, kNoPage = 0xFFFFFFFEu;
+                uint32_t row = kNoKey;
+                const int j = key0 + lane;
+                if (lane < kAttnTile && j < l_len) {
+                    if (page < 0 || page >= a.pages) {
+                        row = kNoPage;
+                        record_status(a.status, RFP2_EBADID);
+                    } else {
+                        const uint32_t off = a.page_shift >= 0 ? j & (a.page_size - 1) : j % a.page_size;
+                        row = ((uint32_t)page * a.heads + lp.hk) * a.page_size + off;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    const int id = lane + 32 * i, r = id / CH, c = id - r * CH;
+                    const uint32_t src = __shfl_sync(0xffffffffu, row, r);
+                    if (src < kNoPage) {
+                        const int64_t at = (int64_t)src * D + 16 * c;
+                        cp_async16(k_at + k_place(r, c), a.k_codes + at);
+                        cp_async16(v_at + r * L::v_stride + 16 * c, a.v_codes + at);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const int id = lane + 32 * i, r2 = id / PER, c = id - r2 * PER;
+                    const uint32_t src = __shfl_sync(0xffffffffu, row, r2 & 15);
+                    const uint32_t dst = s_at + (r2 * NB + W * c) * 4;
+                    if (src == kNoPage) {
+                        // a key whose page does not exist: its scores are NaN
+                        float *p = reinterpret_cast<float *>(rings + (dst - smem_addr(rings)));
+#pragma unroll
+                        for (int e = 0; e < W; ++e) p[e] = CUDART_NAN_F;
+                    } else if (src != kNoKey) {
+                        cp_async_small<4 * W>(dst, (r2 < 16 ? a.k_scales : a.v_scales) + (int64_t)src * NB + W * c);
+                    }
                 }
             }
-            lx += kAttnWarps;
-            lp.t += kAttnWarps;
-            settle();
-            fetch_page();
+            if (++lt == lt_end) {
+                next_unit(lp);
+                enter();
+                if (loading) prefetch_q(lp);
+            } else if (!a.whole_pages) {
+                fetch_pages();
+            }
         }
         cp_async_commit();
     };
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) load_tile(s);
 
-    // ---- stretches of units ----
+    // ---- outputs: four values d .. d + 3 of column c of a unit, and its lse ----
+    const auto row_of = [&](int b, int hk, int cg) {
+        const int i = cg / a.group;
+        return ((int64_t)b * a.nq + i) * a.Hq + hk * a.group + cg - i * a.group;
+    };
+    const auto store_four = [&](int64_t row, int d, const float (&y)[4]) {
+        const int64_t at = row * D + d;
+        if (PIECES == 2) {
+            *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
+        } else {
+            uint2 u;
+            if (a.dtype == RFP2_BF16) {
+                __nv_bfloat16 v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = from_f32<__nv_bfloat16>(y[e]);
+                memcpy(&u, v, 8);
+            } else {
+                __half v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = from_f32<__half>(y[e]);
+                memcpy(&u, v, 8);
+            }
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) = u;
+        }
+    };
+    const auto lse_of = [&](float m, float l) {
+        return l == 0.0f ? -CUDART_INF_F : (m + kSumShift) * 0.6931471805599453f + logf(l);
+    };
+
+    // ---- the units of this stretch ----
     int stage = 0;
-    AttnPlace p = first;
-    int64_t x = x0;
-    while (x < x1) {
-        const int64_t end_x = min(x1, x + (p.tiles - p.t));  // of this stretch
-        const int len = slen[p.b], low = tile_low(len);
+    bool filled = false;
+    for (AttnPlace p = first; p.unit0 + kAttnGap < y1; next_unit(p)) {
+        const int from = tiles_from(p), to = tiles_to(p);
+        if (from >= to) continue;
+        const int len = length_of(p.b), low = tile_low(len);
 
         // columns: this lane's two of each tile in the score layout
         int col_end[NT][2];
-        int min_end = 0x7fffffff, max_end = 0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -357,22 +508,18 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
                 const int c = min(p.ct * COLS + nt * 8 + 2 * t4 + e, a.columns - 1);
                 col_end[nt][e] = len - a.nq + 1 + c / a.group;
             }
-        {
-            const int c0 = p.ct * COLS, c1 = min(c0 + COLS, a.columns) - 1;
-            min_end = len - a.nq + 1 + c0 / a.group;
-            max_end = len - a.nq + 1 + c1 / a.group;
-        }
-        const int64_t max_begin = a.window ? (int64_t)max_end - a.window : 0;
+        const int c_last = min(p.ct * COLS + COLS, a.columns) - 1;
+        const int min_end = len - a.nq + 1 + p.ct * COLS / a.group;
+        const int64_t max_begin = a.window ? len - a.nq + 1 + c_last / a.group - a.window : 0;
 
-        // q of column g: values 32 b + 8 t4 .. + 7, scaled by a power of two
+        // q of column g: values 32 n + 8 t4 .. + 7, scaled by a power of two
         uint32_t qf[NT][NB][2][PIECES][2];
-        float col_scale[NT][2], block_scale[NT][2];
-        bool far = false;
+        float col_scale[NT][2];
+        int up_most = 0, up_least = 0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int c = p.ct * COLS + nt * 8 + g;
             float v[NB][8];
-            float top = 0.0f;
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -380,35 +527,43 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
             if (c < a.columns) {
                 const int i = c / a.group, h = p.hk * a.group + c - i * a.group;
                 const int64_t at = p.b * a.qb + i * a.qt + h * a.qh + 8 * t4;
+                if (PIECES == 2) {
+                    const float *src = static_cast<const float *>(a.q) + at;
+                    if (a.q_words) {
 #pragma unroll
-                for (int n = 0; n < NB; ++n) {
-                    if (PIECES == 2) {
-                        const float *src = static_cast<const float *>(a.q) + at + 32 * n;
-                        if (a.q_words) {
-                            load_values<float, 8>(src, v[n]);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) v[n][e] = src[e];
-                        }
-                    } else if (a.dtype == RFP2_BF16) {
-                        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) + at + 32 * n;
-                        if (a.q_words) {
-                            load_values<__nv_bfloat16, 8>(src, v[n]);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) v[n][e] = to_f32(src[e]);
-                        }
+                        for (int n = 0; n < NB; ++n) load_values<float, 8>(src + 32 * n, v[n]);
                     } else {
-                        const __half *src = static_cast<const __half *>(a.q) + at + 32 * n;
+#pragma unroll
+                        for (int n = 0; n < NB; ++n)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) v[n][e] = src[32 * n + e];
+                    }
+                } else {
+                    const uint16_t *src = static_cast<const uint16_t *>(a.q) + at;
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) {
+                        uint16_t u[8];
                         if (a.q_words) {
-                            load_values<__half, 8>(src, v[n]);
+                            const uint4 w = *reinterpret_cast<const uint4 *>(src + 32 * n);
+                            memcpy(u, &w, 16);
                         } else {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) v[n][e] = to_f32(src[e]);
+                            for (int e = 0; e < 8; ++e) u[e] = src[32 * n + e];
                         }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            v[n][e] = a.dtype == RFP2_BF16 ? __uint_as_float((uint32_t)u[e] << 16)
+                                                           : __half2float(__ushort_as_half(u[e]));
                     }
                 }
             }
+            if (!filled) {
+                // the first tiles, behind the first unit's q: what comes later queues behind them
+#pragma unroll 1
+                for (int s = 0; s < STAGES - 1; ++s) load_tile(s);
+                filled = true;
+            }
+            float top = 0.0f;
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -417,8 +572,9 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             // 2^up brings the largest value to [2^14, 2^15); a zero row stays as it is
             const int up = top > 0.0f ? min(141 - (int)(__float_as_uint(top) >> 23), 126) : 0;
+            up_most = max(up_most, up);
+            up_least = min(up_least, up);
             const float by = __uint_as_float((uint32_t)(127 + up) << 23);
-            const float back = __uint_as_float((uint32_t)(127 - up) << 23);
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -433,23 +589,26 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
                             qf[nt][n][s][1][h] = pack_f16(u - f.x, w - f.y);
                         }
                     }
-            far |= up > 40 || up < -40;
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                block_scale[nt][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * t4 + e));
+                col_scale[nt][e] = __uint_as_float(
+                    (uint32_t)(127 - __shfl_sync(0xffffffffu, up, 4 * (2 * t4 + e))) << 23);
         }
-        // q's power of two goes back in at the end, or, where it is so far from 1 that it has to meet
-        // scales as far on the other side, into every block's sum
-        far = __any_sync(0xffffffffu, far);
+        // q far from 1 is for keys as far on the other side: their scales are brought 2^60 nearer, so
+        // that no sum on the way leaves fp32's range
+        const bool tiny = __any_sync(0xffffffffu, up_most > 60);
+        const bool far = tiny || __any_sync(0xffffffffu, up_least < -60);
+        const float near_by = tiny ? 8.673617379884035e-19f : 1.152921504606847e18f;  // 2^-60, 2^60
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                col_scale[nt][e] = (far ? 1.0f : block_scale[nt][e]) * a.scale *
-                                   (a.softcap > 0.0f ? 1.0f : 1.4426950408889634f);
+            for (int e = 0; e < 2; ++e) {
+                if (far) col_scale[nt][e] *= tiny ? 1.152921504606847e18f : 8.673617379884035e-19f;
+                col_scale[nt][e] *= a.scale * (a.softcap > 0.0f ? 1.0f : 1.4426950408889634f);
+            }
 
         float o[NT][NB][2][4];          // [column tile][block][pair of values][accumulator]
-        float ref[NT][2], sum[NT][2];   // r - 8, and this lane's share of the sum of p
+        float ref[NT][2], sum[NT][2];   // r - 8, and this lane's share of the sum of p, times 2^-32
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -462,31 +621,53 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
             sum[nt][0] = sum[nt][1] = 0.0f;
         }
 
-        // tiles of this stretch that are this warp's: (tile - x0) % 8 == warp
-        int skip = (int)((warp - (x - x0)) & (kAttnWarps - 1));
-        for (int64_t xt = x + skip; xt < end_x; xt += kAttnWarps) {
+        for (int t = from; t < to; ++t) {
             cp_async_wait<STAGES - 2>();
             __syncwarp();
             load_tile(stage == 0 ? STAGES - 1 : stage - 1);
-            const uint8_t *tile = rings + (warp * STAGES + stage) * L::stage_bytes;
-            stage = stage + 1 == STAGES ? 0 : stage + 1;
-            const uint8_t *kt = tile, *vt = tile + L::k_bytes;
+            const uint8_t *kt = rings + (warp * STAGES + stage) * L::stage_bytes, *vt = kt + L::k_bytes;
             const float *ks = reinterpret_cast<const float *>(vt + L::v_bytes), *vs = ks + kAttnTile * NB;
-            const int key0 = (low + p.t + (int)(xt - x)) * kAttnTile;
+            stage = stage + 1 == STAGES ? 0 : stage + 1;
+            const int key0 = (low + t) * kAttnTile;
+
+            // scales of keys g and g + 8
+            float dk[2][NB], dv[2][NB];
+            uint32_t top_d[2] = {0u, 0u};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                load_scales<NB>(ks + (g + 8 * k) * NB, dk[k]);
+                load_scales<NB>(vs + (g + 8 * k) * NB, dv[k]);
+#pragma unroll
+                for (int n = 0; n < NB; ++n) top_d[k] = max(top_d[k], __float_as_uint(dv[k][n]));
+            }
+            // an infinite, NaN or negative scale is no measure of range
+            if (__any_sync(0xffffffffu, max(top_d[0], top_d[1]) >= 0x7F800000u)) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    top_d[k] = 0u;
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) {
+                        const uint32_t u = __float_as_uint(dv[k][n]) & 0x7FFFFFFFu;
+                        top_d[k] = max(top_d[k], u < 0x7F800000u ? u : 0u);
+                    }
+                }
+            }
+            const float lg[2] = {fmaxf(log2_fast(__uint_as_float(top_d[0])), -110.0f),
+                                 fmaxf(log2_fast(__uint_as_float(top_d[1])), -110.0f)};
+            if (far)
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    dk[0][n] *= near_by;
+                    dk[1][n] *= near_by;
+                }
 
             // scores of keys g and g + 8
             float sc[NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sc[nt][e] = 0.0f;
-            float top_d[2] = {0.0f, 0.0f};
-            float dv[2][NB];
-#pragma unroll
             for (int n = 0; n < NB; ++n) {
-                const uint2 lo = *reinterpret_cast<const uint2 *>(kt + g * L::k_stride + 32 * n + 8 * t4);
-                const uint2 hi = *reinterpret_cast<const uint2 *>(kt + (g + 8) * L::k_stride + 32 * n + 8 * t4);
-                const float d0 = ks[g * NB + n], d1 = ks[(g + 8) * NB + n];
+                const int at = 32 * (L::k_permuted ? n ^ (g & 3) : n) + 8 * t4;
+                const uint2 lo = *reinterpret_cast<const uint2 *>(kt + g * L::k_stride + at);
+                const uint2 hi = *reinterpret_cast<const uint2 *>(kt + (g + 8) * L::k_stride + at);
                 float c[NT][4];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -505,42 +686,39 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
                         for (int piece = PIECES - 1; piece >= 0; --piece)
                             mma_f16(c[nt], f, qf[nt][n][s][piece][0], qf[nt][n][s][piece][1]);
                 }
-                if (far)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) c[nt][e] *= block_scale[nt][e & 1];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    sc[nt][0] += d0 * c[nt][0];
-                    sc[nt][1] += d0 * c[nt][1];
-                    sc[nt][2] += d1 * c[nt][2];
-                    sc[nt][3] += d1 * c[nt][3];
-                }
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    dv[k][n] = vs[(g + 8 * k) * NB + n];
-                    // an infinite or NaN scale is no measure of range
-                    top_d[k] = fmaxf(top_d[k], dv[k][n] <= 3.4e38f ? dv[k][n] : 0.0f);
-                }
+                    for (int e = 0; e < 4; ++e)
+                        sc[nt][e] = n ? sc[nt][e] + dk[e >> 1][n] * c[nt][e] : dk[e >> 1][n] * c[nt][e];
             }
-            const float lg[2] = {fmaxf(log2_fast(top_d[0]), -110.0f), fmaxf(log2_fast(top_d[1]), -110.0f)};
 
             const bool whole = key0 + kAttnTile <= min_end && key0 >= max_begin;
             bool more = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float s = sc[nt][e] * col_scale[nt][e & 1];
-                    if (a.softcap > 0.0f) s = a.softcap * tanhf(s / a.softcap) * 1.4426950408889634f;
-                    if (!whole) {
+                for (int e = 0; e < 4; ++e) sc[nt][e] *= col_scale[nt][e & 1];
+            if (a.softcap > 0.0f)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sc[nt][e] = a.softcap * tanhf(sc[nt][e] / a.softcap) * 1.4426950408889634f;
+            if (!whole) {
+                // out of sight: no weight, whatever the value's scale is there
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
                         const int j = key0 + g + 8 * (e >> 1), end = col_end[nt][e & 1];
-                        if (j >= end || (a.window && j < end - a.window)) s = -CUDART_INF_F;
+                        if (j >= end || (a.window && j < end - a.window)) sc[nt][e] = -CUDART_INF_F;
                     }
-                    sc[nt][e] = s;
-                    more |= s - ref[nt][e & 1] + lg[e >> 1] > kMost;
-                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) more |= sc[nt][e] - ref[nt][e & 1] + lg[e >> 1] > kMost;
             if (__any_sync(0xffffffffu, more)) {
                 // a larger reference for the columns that need one
 #pragma unroll
@@ -582,7 +760,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         float u = pr[nt][2 * k] * dv[k][n], w = pr[nt][2 * k + 1] * dv[k][n];
-                        if (!whole) {  // whatever the scale of a key out of sight is
+                        if (!whole) {
                             if (sc[nt][2 * k] == -CUDART_INF_F) u = 0.0f;
                             if (sc[nt][2 * k + 1] == -CUDART_INF_F) w = 0.0f;
                         }
@@ -624,158 +802,221 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
             }
         }
 
-        // ---- the warps join ----
+        // ---- the end of the unit, or of the stretch ----
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float l = sum[nt][e];
-                l += __shfl_xor_sync(0xffffffffu, l, 4);
-                l += __shfl_xor_sync(0xffffffffu, l, 8);
-                l += __shfl_xor_sync(0xffffffffu, l, 16);
-                if (g == 0) {
-                    state_r[warp * COLS + nt * 8 + 2 * t4 + e] = ref[nt][e];
-                    state_l[warp * COLS + nt * 8 + 2 * t4 + e] = l;
-                }
+                sum[nt][e] += __shfl_xor_sync(0xffffffffu, sum[nt][e], 4);
+                sum[nt][e] += __shfl_xor_sync(0xffffffffu, sum[nt][e], 8);
+                sum[nt][e] += __shfl_xor_sync(0xffffffffu, sum[nt][e], 16);
             }
-        __syncthreads();
-        const auto top_of = [&](int c) {
-            float m = kNone;
+        if (from == 0 && to == p.tiles) {
 #pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) m = fmaxf(m, state_r[w * COLS + c]);
-            return m;
-        };
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+                for (int e = 0; e < 2; ++e) {
+                    const int cg = p.ct * COLS + nt * 8 + 2 * t4 + e;
+                    if (cg >= a.columns) continue;
+                    const int64_t row = row_of(p.b, p.hk, cg);
+                    const float l = sum[nt][e], inv = l == 0.0f ? 0.0f : kSumScale / l;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float by = exp2_fast(ref[nt][e] - top_of(nt * 8 + 2 * t4 + e));
-#pragma unroll
-                for (int n = 0; n < NB; ++n)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        o[nt][n][h][e] *= by;
-                        o[nt][n][h][e + 2] *= by;
+                    for (int n = 0; n < NB; ++n) {
+                        float y[4] = {o[nt][n][0][e] * inv, o[nt][n][0][e + 2] * inv, o[nt][n][1][e] * inv,
+                                      o[nt][n][1][e + 2] * inv};
+                        if (len < 0) y[0] = y[1] = y[2] = y[3] = CUDART_NAN_F;
+                        store_four(row, 32 * n + 4 * g, y);
                     }
-            }
-
-        const bool split = p.t != 0 || end_x - x != p.tiles;
-        constexpr int SLOT = 2 * COLS + COLS * D;  // floats: references, sums, values
-        const int64_t unit0 = x - p.t;             // first tile of the unit on the line
-        float *slot = a.partials + (2 * (int64_t)blockIdx.x + (x != x0)) * SLOT;
-        const auto store_row = [&](int c, int d, const float (&y)[4]) {
-            const int cg = p.ct * COLS + c, i = cg / a.group;
-            const int64_t at = (((int64_t)p.b * a.nq + i) * a.Hq + p.hk * a.group + cg - i * a.group) * D + d;
-            if (PIECES == 2) {
-                *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
-            } else if (a.dtype == RFP2_BF16) {
-                __nv_bfloat16 v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = from_f32<__nv_bfloat16>(y[e]);
-                uint2 u;
-                memcpy(&u, v, 8);
-                *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + at) = u;
+                    if (a.lse && g == 0) a.lse[row] = len < 0 ? CUDART_NAN_F : lse_of(ref[nt][e], l);
+                }
+        } else {
+            // a head (the unit ends here) goes to the workspace: the ring is in use.  A tail is the
+            // stretch's last: it goes to the ring, which its loads have left.
+            const bool tail = to != p.tiles;
+            float *slot;
+            if (tail) {
+                cp_async_wait<0>();
+                __syncwarp();
+                slot = reinterpret_cast<float *>(rings + warp * STAGES * L::stage_bytes);
             } else {
-                __half v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = from_f32<__half>(y[e]);
-                uint2 u;
-                memcpy(&u, v, 8);
-                *reinterpret_cast<uint2 *>(static_cast<__half *>(a.out) + at) = u;
+                slot = a.partials + (2 * (int64_t)gridDim.x + worker) * SLOT;
             }
-        };
-        const auto store_lse = [&](int c, float m, float l) {
-            const int cg = p.ct * COLS + c, i = cg / a.group;
-            a.lse[((int64_t)p.b * a.nq + i) * a.Hq + p.hk * a.group + cg - i * a.group] =
-                len < 0 ? CUDART_NAN_F : l == 0.0f ? -CUDART_INF_F : (m + kSumShift) * 0.6931471805599453f + logf(l);
-        };
-        const int live = min(COLS, a.columns - p.ct * COLS);
-        constexpr int CHUNK = S::chunk;
 #pragma unroll
-        for (int d0 = 0; d0 < D; d0 += CHUNK) {
-            if (d0) __syncthreads();
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int n = d0 / 32; n < NB && n < (d0 + CHUNK) / 32; ++n)
+                for (int e = 0; e < 2; ++e) {
+                    const int c = nt * 8 + 2 * t4 + e;
+                    if (g == 0) {
+                        piece_r[(2 * warp + tail) * COLS + c] = ref[nt][e];
+                        piece_l[(2 * warp + tail) * COLS + c] = sum[nt][e];
+                    }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        *reinterpret_cast<float4 *>(join + (warp * COLS + nt * 8 + 2 * t4 + e) * S::row +
-                                                    32 * n - d0 + 4 * g) =
+                    for (int n = 0; n < NB; ++n)
+                        *reinterpret_cast<float4 *>(slot + c * D + 32 * n + 4 * g) =
                             make_float4(o[nt][n][0][e], o[nt][n][0][e + 2], o[nt][n][1][e], o[nt][n][1][e + 2]);
-            __syncthreads();
-            const int words = min(CHUNK, D - d0) / 4;
-            for (int i = tid; i < live * words; i += kAttnThreads) {
-                const int c = i / words, d = 4 * (i - c * words);
-                float y[4] = {0.0f, 0.0f, 0.0f, 0.0f}, l = 0.0f;
-                const float m = top_of(c);
-#pragma unroll
-                for (int w = 0; w < kAttnWarps; ++w) {
-                    const float4 v = *reinterpret_cast<const float4 *>(join + (w * COLS + c) * S::row + d);
-                    y[0] += v.x;
-                    y[1] += v.y;
-                    y[2] += v.z;
-                    y[3] += v.w;
-                    l += state_l[w * COLS + c] * exp2_fast(state_r[w * COLS + c] - m);
                 }
-                if (split) {
-                    *reinterpret_cast<float4 *>(slot + 2 * COLS + c * D + d0 + d) = make_float4(y[0], y[1], y[2], y[3]);
-                    if (d0 + d == 0) {
-                        slot[c] = m;
-                        slot[COLS + c] = l;
-                    }
-                } else {
-                    const float inv = kSumScale / l;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] = len < 0 ? CUDART_NAN_F : l == 0.0f ? 0.0f : y[e] * inv;
-                    store_row(c, d0 + d, y);
-                    if (a.lse && d0 + d == 0) store_lse(c, m, l);
-                }
+            if (lane == 0) {
+                AttnPiece &x = pieces[2 * warp + tail];
+                x.starts = from == 0;
+                x.b = p.b;
+                x.hk = p.hk;
+                x.ct = p.ct;
+                x.unit0 = p.unit0;
+                x.present = 1;
             }
         }
-        if (split) {
-            // CTAs of this unit: those that hold its first and its last tile, and between
-            const int64_t c0 = ((unit0 + 1) * parts - 1) / total;
-            const int64_t c1 = ((unit0 + p.tiles) * parts - 1) / total;
-            __threadfence();
-            __syncthreads();
-            int *flag = reinterpret_cast<int *>(small);
-            if (tid == 0) *flag = atomicAdd(a.counters + c0, 1) == (int)(c1 - c0);
-            __syncthreads();
-            if (*flag) {
-                __threadfence();
-                if (tid == 0) a.counters[c0] = 0;
-                const int words = D / 4;
-                const int64_t slot0 = 2 * c0 + (unit0 != c0 * total / parts);
-                for (int i = tid; i < live * words; i += kAttnThreads) {
-                    const int c = i / words, d = 4 * (i - c * words);
-                    float m = kNone, l = 0.0f, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    for (int64_t k = c0; k <= c1; ++k)
-                        m = fmaxf(m, __ldcg(a.partials + (k == c0 ? slot0 : 2 * k) * SLOT + c));
-                    for (int64_t k = c0; k <= c1; ++k) {
-                        const float *from = a.partials + (k == c0 ? slot0 : 2 * k) * SLOT;
-                        const float by = exp2_fast(__ldcg(from + c) - m);
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(from + 2 * COLS + c * D + d));
-                        l += __ldcg(from + COLS + c) * by;
-                        y[0] += v.x * by;
-                        y[1] += v.y * by;
-                        y[2] += v.z * by;
-                        y[3] += v.w * by;
-                    }
-                    const float inv = kSumScale / l;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] = l == 0.0f ? 0.0f : y[e] * inv;
-                    store_row(c, d, y);
-                    if (a.lse && d == 0) store_lse(c, m, l);
-                }
-            }
-        }
-        __syncthreads();  // the join buffer and the states are free again
-        p.t = 0;
-        next_unit(p);
-        x = end_x;
     }
     cp_async_wait<0>();
+    __syncthreads();
+
+    // ---- the CTA's pieces: those of one unit follow one another, a head is its last ----
+    constexpr int WORDS = COLS * D / 4;
+    const uint32_t present = __ballot_sync(0xffffffffu, lane < 2 * kAttnWarps && pieces[lane & (2 * kAttnWarps - 1)].present);
+    if (present == 0) return;
+    uint32_t ends = present & 0x55555555u;         // heads, and a last tail
+    ends |= present & (0x80000000u >> __clz(present));
+    const int groups = __popc(ends);
+    const auto members_of = [&](int j, int &last) {  // pieces of group j, as bits
+        uint32_t rest = ends, below = 0;
+        for (int k = 0; k < j; ++k) {
+            below = 2u * (rest & -rest) - 1u;
+            rest &= rest - 1;
+        }
+        last = __ffs(rest) - 1;
+        return present & ((2u << last) - 1u) & ~below;
+    };
+    if (tid < groups * COLS) {
+        // each piece's weight beside its group's reference, and the group's sum
+        const int j = tid / COLS, c = tid - j * COLS;
+        int last;
+        const uint32_t members = members_of(j, last);
+        float m = kNone, l = 0.0f;
+        for (uint32_t u = members; u; u &= u - 1) m = fmaxf(m, piece_r[(__ffs(u) - 1) * COLS + c]);
+        for (uint32_t u = members; u; u &= u - 1) {
+            const int at = (__ffs(u) - 1) * COLS + c;
+            const float by = exp2_fast(piece_r[at] - m);
+            l += piece_l[at] * by;
+            piece_r[at] = by;
+        }
+        group_r[tid] = m;
+        group_l[tid] = l;
+    }
+    __syncthreads();
+    bool split = false;
+    for (int k = tid; k < groups * WORDS; k += kAttnThreads) {
+        const int j = k / WORDS, c = (k - j * WORDS) / (D / 4), d = 4 * (k % (D / 4));
+        int last;
+        const uint32_t members = members_of(j, last);
+        const AttnPiece &u = pieces[__ffs(members) - 1];
+        if (c >= a.columns - u.ct * COLS) continue;
+        float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (uint32_t rest = members; rest; rest &= rest - 1) {
+            const int i = __ffs(rest) - 1;
+            const float *from = (i & 1) ? reinterpret_cast<const float *>(rings + (i >> 1) * STAGES * L::stage_bytes)
+                                        : a.partials + (2 * (int64_t)gridDim.x + blockIdx.x * kAttnWarps + (i >> 1)) * SLOT;
+            const float by = piece_r[i * COLS + c];
+            const float4 v = *reinterpret_cast<const float4 *>(from + c * D + d);
+            y[0] += v.x * by;
+            y[1] += v.y * by;
+            y[2] += v.z * by;
+            y[3] += v.w * by;
+        }
+        const float m = group_r[j * COLS + c], l = group_l[j * COLS + c];
+        if (u.starts && (last & 1) == 0) {
+            const float inv = l == 0.0f ? 0.0f : kSumScale / l;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] *= inv;
+            const int64_t row = row_of(u.b, u.hk, u.ct * COLS + c);
+            store_four(row, d, y);
+            if (a.lse && d == 0) a.lse[row] = lse_of(m, l);
+        } else {
+            // a unit of several CTAs
+            float *mine = a.partials + (2 * (int64_t)blockIdx.x + u.starts) * SLOT;
+            *reinterpret_cast<float4 *>(mine + 2 * COLS + c * D + d) = make_float4(y[0], y[1], y[2], y[3]);
+            if (d == 0) {
+                mine[c] = m;
+                mine[COLS + c] = l;
+            }
+            split = true;
+        }
+    }
+    if (!__syncthreads_or(split)) return;
+
+    // ---- units of several CTAs: the first group, if it did not start here, and the last, if it does
+    // not end here.  The last CTA of each to arrive joins it. ----
+    int *arrived = reinterpret_cast<int *>(small);
+    const auto span_of = [&](const AttnPiece &u, int64_t &c0, int64_t &c1) {
+        const int64_t t0 = u.unit0 + kAttnGap, tiles = prefix[u.b + 1] - prefix[u.b] - kAttnGap;
+        c0 = share.worker_of(t0) / kAttnWarps;
+        c1 = share.worker_of(t0 + tiles - 1) / kAttnWarps;
+    };
+    const int last_piece = 31 - __clz(present), first_piece = __ffs(present) - 1;
+    int last_first;
+    const int last_group = __ffs(members_of(groups - 1, last_first)) - 1;  // its first piece
+    const bool split0 = !pieces[first_piece].starts;
+    const bool split1 = (last_piece & 1) && !(split0 && groups == 1);
+    __threadfence();
+    __syncthreads();
+    if (lane == 0 && warp < 2) {
+        int joins = 0;
+        if (warp == 0 ? split0 : split1) {
+            int64_t c0, c1;
+            span_of(pieces[warp == 0 ? first_piece : last_group], c0, c1);
+            joins = atomicAdd(a.counters + c0, 1) == (int)(c1 - c0);
+            if (joins) a.counters[c0] = 0;
+        }
+        arrived[warp] = joins;
+    }
+    __syncthreads();
+    for (int which = 0; which < 2; ++which) {
+        if (!arrived[which]) continue;
+        __threadfence();
+        const AttnPiece u = pieces[which == 0 ? first_piece : last_group];
+        int64_t c0, c1;
+        span_of(u, c0, c1);
+        const int n = (int)(c1 - c0 + 1), live = min(COLS, a.columns - u.ct * COLS);
+        const auto from_of = [&](int i) { return a.partials + (2 * (c0 + i) + (i == 0)) * SLOT; };
+        // weights of the CTAs' parts; a warp takes columns in turn
+        float *weight = reinterpret_cast<float *>(rings);  // [n][COLS]; the pieces there are done with
+        for (int c = warp; c < live; c += kAttnWarps) {
+            float m = kNone, l = 0.0f;
+            for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldcg(from_of(i) + c));
+#pragma unroll
+            for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+            for (int i = lane; i < n; i += 32) {
+                const float by = exp2_fast(__ldcg(from_of(i) + c) - m);
+                l += __ldcg(from_of(i) + COLS + c) * by;
+                weight[i * COLS + c] = by;
+            }
+#pragma unroll
+            for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+            if (lane == 0) {
+                group_r[c] = m;
+                group_l[c] = l;
+            }
+        }
+        __syncthreads();
+        for (int k = tid; k < live * (D / 4); k += kAttnThreads) {
+            const int c = k / (D / 4), d = 4 * (k - c * (D / 4));
+            float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+            for (int i = 0; i < n; ++i) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(from_of(i) + 2 * COLS + c * D + d));
+                const float by = weight[i * COLS + c];
+                y[0] += v.x * by;
+                y[1] += v.y * by;
+                y[2] += v.z * by;
+                y[3] += v.w * by;
+            }
+            const float l = group_l[c], inv = l == 0.0f ? 0.0f : kSumScale / l;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] *= inv;
+            const int64_t row = row_of(u.b, u.hk, u.ct * COLS + c);
+            store_four(row, d, y);
+            if (a.lse && d == 0) a.lse[row] = lse_of(group_r[c], l);
+        }
+        __syncthreads();
+    }
 }
 
 // Launches one group of sequences; a.B <= kAttnMaxBatch.
