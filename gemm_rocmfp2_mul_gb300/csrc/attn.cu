@@ -8,8 +8,8 @@ using namespace rfp2;
 
 namespace {
 
-// Partial results: two a CTA and one a warp, of 16 columns' references, sums
-// and values.
+// Partial results: two a CTA and one for each of up to 16 warps, of 16 columns'
+// references, sums and values.
 size_t partial_bytes(int64_t D) { return (size_t)(32 + 16 * D) * 4; }
 
 }  // namespace
@@ -18,7 +18,7 @@ extern "C" size_t rfp2_attn_decode_workspace_bytes(int64_t B, int64_t nq, int64_
                                                    int64_t heads, int64_t D) {
     if (B < 1 || nq < 1 || Hq < 1 || heads < 1 || Hq % heads != 0 || D < 32 || D > 256) return 0;
     return kAttnCounterBytes +
-           2 * (size_t)sm_count(current_device()) * (2 + kAttnWarps) * partial_bytes(D);
+           2 * (size_t)sm_count(current_device()) * (2 + 16) * partial_bytes(D);
 }
 
 extern "C" rfp2_status rfp2_attn_decode(const void *q, int dtype, int64_t B, int64_t nq,

@@ -30,11 +30,9 @@
 
 namespace rfp2 {
 
-constexpr int kAttnWarps = 8;
-constexpr int kAttnThreads = kAttnWarps * 32;
 constexpr int kAttnTile = 16;        // keys
 constexpr int kAttnGap = 2;          // a unit's fixed cost, in tiles
-constexpr int kAttnMinStretch = 2;   // of a warp, in tiles
+constexpr int kAttnMinStretch = 1;   // of a warp, in tiles
 constexpr int kAttnMaxBatch = 512;   // sequences of one launch
 constexpr int kAttnCounterBytes = 4096;
 
@@ -82,22 +80,26 @@ struct AttnPiece {
 };
 
 template <int NB, int NT>
+constexpr int attn_warps() { return NB * NT > 2 && NB * NT <= 4 ? 12 : 8; }
+template <int NB, int NT>
 constexpr int attn_ctas_per_sm() { return NB * NT <= 2 ? 2 : 1; }
 // The warps' sums of the scan, the pieces and their columns' states, and the
 // line's prefix.
-template <int NT>
+template <int NB, int NT>
 constexpr int attn_small_bytes(int B) {
-    return 64 + 2 * kAttnWarps * ((int)sizeof(AttnPiece) + 4 * 8 * NT * 4) + (B + 1) * 8;
+    return 128 + 2 * attn_warps<NB, NT>() * ((int)sizeof(AttnPiece) + 4 * 8 * NT * 4) + (B + 1) * 8;
 }
 template <int NB, int NT>
 constexpr int attn_stages() {
     const int budget = (attn_ctas_per_sm<NB, NT>() == 2 ? 113 : 227) * 1024;
-    const int s = (budget - attn_small_bytes<NT>(kAttnMaxBatch)) / (kAttnWarps * AttnLayout<NB>::stage_bytes);
+    const int s = (budget - attn_small_bytes<NB, NT>(kAttnMaxBatch)) /
+                  (attn_warps<NB, NT>() * AttnLayout<NB>::stage_bytes);
     return s > 8 ? 8 : s;
 }
 template <int NB, int NT>
 int attn_smem(int B) {
-    return kAttnWarps * attn_stages<NB, NT>() * AttnLayout<NB>::stage_bytes + attn_small_bytes<NT>(B);
+    return attn_warps<NB, NT>() * attn_stages<NB, NT>() * AttnLayout<NB>::stage_bytes +
+           attn_small_bytes<NB, NT>(B);
 }
 // Floats of one partial result: references, sums, values of the columns.
 template <int NB, int NT>
@@ -149,12 +151,12 @@ RFP2_DEV float2 unpack_f16(uint32_t h) {
 }
 RFP2_DEV float exp2_fast(float x) {
     float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 RFP2_DEV float log2_fast(float x) {
     float y;
-    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
@@ -201,24 +203,25 @@ struct AttnShare {
 };
 
 template <int NB, int NT, int PIECES>
-__global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
+__global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB, NT>())
     attn_kernel(const AttnArgs a) {
     using L = AttnLayout<NB>;
+    constexpr int WARPS = attn_warps<NB, NT>(), THREADS = 32 * WARPS;
     constexpr int D = L::D, STAGES = attn_stages<NB, NT>(), COLS = 8 * NT, SLOT = attn_slot<NB, NT>();
     static_assert(SLOT * 4 <= STAGES * L::stage_bytes, "a warp's partial result fits its ring");
-    static_assert(STAGES >= 2, "");
+    static_assert(STAGES >= 2 && WARPS <= 16, "");
     constexpr float kShift = 8.0f, kMost = 15.0f;  // p dV aims at 2^8 and stays below 2^15
     constexpr float kNone = -3.4e38f;              // the reference before any key
     // p is up to 2^15 / dV: 2^125 where the values are tiny (dV is taken as 2^-110 at least here)
     constexpr float kSumScale = 2.3283064365386963e-10f, kSumShift = 32.0f;  // 2^-32
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *rings = smem;
-    int64_t *small = reinterpret_cast<int64_t *>(rings + kAttnWarps * STAGES * L::stage_bytes);  // 8
-    AttnPiece *pieces = reinterpret_cast<AttnPiece *>(small + 8);  // [warps][head, tail]
-    float *piece_r = reinterpret_cast<float *>(pieces + 2 * kAttnWarps);  // [pieces][COLS]
-    float *piece_l = piece_r + 2 * kAttnWarps * COLS;
-    float *group_r = piece_l + 2 * kAttnWarps * COLS, *group_l = group_r + 2 * kAttnWarps * COLS;
-    int64_t *prefix = reinterpret_cast<int64_t *>(group_l + 2 * kAttnWarps * COLS);  // [B + 1]
+    int64_t *small = reinterpret_cast<int64_t *>(rings + WARPS * STAGES * L::stage_bytes);  // 16
+    AttnPiece *pieces = reinterpret_cast<AttnPiece *>(small + 16);  // [warps][head, tail]
+    float *piece_r = reinterpret_cast<float *>(pieces + 2 * WARPS);  // [pieces][COLS]
+    float *piece_l = piece_r + 2 * WARPS * COLS;
+    float *group_r = piece_l + 2 * WARPS * COLS, *group_l = group_r + 2 * WARPS * COLS;
+    int64_t *prefix = reinterpret_cast<int64_t *>(group_l + 2 * WARPS * COLS);  // [B + 1]
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
@@ -237,7 +240,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
     };
     {
         int64_t run = 0;
-        for (int b0 = 0; b0 < a.B; b0 += kAttnThreads) {
+        for (int b0 = 0; b0 < a.B; b0 += THREADS) {
             const int b = b0 + tid;
             int cost = 0;
             if (b < a.B) {
@@ -254,11 +257,11 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
             }
             if (b0) __syncthreads();
             if (lane == 31) small[warp] = incl;
-            if (b0 == 0 && tid < 2 * kAttnWarps) pieces[tid].present = 0;
+            if (b0 == 0 && tid < 2 * WARPS) pieces[tid].present = 0;
             __syncthreads();
             int64_t before = 0, all = 0;
 #pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) {
+            for (int w = 0; w < WARPS; ++w) {
                 before += w < warp ? small[w] : 0;
                 all += small[w];
             }
@@ -272,12 +275,12 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
     const int64_t total = prefix[a.B] * units_of;
     // some tiles for each warp: shorter stretches are not worth their joins
     const int64_t parts = min((int64_t)gridDim.x,
-                              (total + kAttnMinStretch * kAttnWarps - 1) / (kAttnMinStretch * kAttnWarps));
+                              (total + kAttnMinStretch * WARPS - 1) / (kAttnMinStretch * WARPS));
     if ((int64_t)blockIdx.x >= parts) return;
     AttnShare share;
-    share.each = quotient(total, parts * kAttnWarps);
-    share.extra = total - share.each * parts * kAttnWarps;
-    const int64_t worker = (int64_t)blockIdx.x * kAttnWarps + warp;
+    share.each = quotient(total, parts * WARPS);
+    share.extra = total - share.each * parts * WARPS;
+    const int64_t worker = (int64_t)blockIdx.x * WARPS + warp;
     const int64_t y0 = share.begin(worker), y1 = share.begin(worker + 1);
 
     AttnPlace first;
@@ -641,7 +644,8 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
                 for (int n = 0; n < NB; ++n) top_d[k] = max(top_d[k], __float_as_uint(dv[k][n]));
             }
             // an infinite, NaN or negative scale is no measure of range
-            if (__any_sync(0xffffffffu, max(top_d[0], top_d[1]) >= 0x7F800000u)) {
+            const bool odd = __any_sync(0xffffffffu, max(top_d[0], top_d[1]) >= 0x7F800000u);
+            if (odd) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     top_d[k] = 0u;
@@ -751,26 +755,36 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
                     sum[nt][e & 1] += pr[nt][e] * kSumScale;
                 }
 
+            // p dV in the layout that the products take it in
+            uint32_t pb[NB][NT][PIECES][2];
+            const auto weigh = [&](bool odd) {
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float u = pr[nt][2 * k] * dv[k][n], w = pr[nt][2 * k + 1] * dv[k][n];
+                            if (odd) {  // a key out of sight has no weight, whatever its scale is
+                                if (sc[nt][2 * k] == -CUDART_INF_F) u = 0.0f;
+                                if (sc[nt][2 * k + 1] == -CUDART_INF_F) w = 0.0f;
+                            }
+                            const uint32_t hi = pack_f16(u, w);
+                            pb[n][nt][0][k] = transpose8x8(hi);
+                            if constexpr (PIECES == 2) {
+                                const float2 f = unpack_f16(hi);
+                                pb[n][nt][1][k] = transpose8x8(pack_f16(u - f.x, w - f.y));
+                            }
+                        }
+            };
+            if (odd)
+                weigh(true);
+            else
+                weigh(false);
+
             // values: out^T += V^T (p dV), keys 2 t4, + 1, + 8, + 9
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
-                uint32_t pb[NT][PIECES][2];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float u = pr[nt][2 * k] * dv[k][n], w = pr[nt][2 * k + 1] * dv[k][n];
-                        if (!whole) {
-                            if (sc[nt][2 * k] == -CUDART_INF_F) u = 0.0f;
-                            if (sc[nt][2 * k + 1] == -CUDART_INF_F) w = 0.0f;
-                        }
-                        const uint32_t hi = pack_f16(u, w);
-                        pb[nt][0][k] = transpose8x8(hi);
-                        if constexpr (PIECES == 2) {
-                            const float2 f = unpack_f16(hi);
-                            pb[nt][1][k] = transpose8x8(pack_f16(u - f.x, w - f.y));
-                        }
-                    }
                 const uint8_t *vp = vt + 2 * t4 * L::v_stride + 32 * n + 4 * g;
                 uint32_t w[4];
 #pragma unroll
@@ -790,12 +804,12 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
                         if constexpr (PIECES == 2) {
                             // the matrix unit cuts sums off; a long chain of them is kept in fp32 adds
                             float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            mma_f16(c, f, pb[nt][1][0], pb[nt][1][1]);
-                            mma_f16(c, f, pb[nt][0][0], pb[nt][0][1]);
+                            mma_f16(c, f, pb[n][nt][1][0], pb[n][nt][1][1]);
+                            mma_f16(c, f, pb[n][nt][0][0], pb[n][nt][0][1]);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) o[nt][n][h][e] += c[e];
                         } else {
-                            mma_f16(o[nt][n][h], f, pb[nt][0][0], pb[nt][0][1]);
+                            mma_f16(o[nt][n][h], f, pb[n][nt][0][0], pb[n][nt][0][1]);
                         }
                     }
                 }
@@ -871,7 +885,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
 
     // ---- the CTA's pieces: those of one unit follow one another, a head is its last ----
     constexpr int WORDS = COLS * D / 4;
-    const uint32_t present = __ballot_sync(0xffffffffu, lane < 2 * kAttnWarps && pieces[lane & (2 * kAttnWarps - 1)].present);
+    const uint32_t present = __ballot_sync(0xffffffffu, lane < 2 * WARPS && pieces[min(lane, 2 * WARPS - 1)].present);
     if (present == 0) return;
     uint32_t ends = present & 0x55555555u;         // heads, and a last tail
     ends |= present & (0x80000000u >> __clz(present));
@@ -903,7 +917,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
     }
     __syncthreads();
     bool split = false;
-    for (int k = tid; k < groups * WORDS; k += kAttnThreads) {
+    for (int k = tid; k < groups * WORDS; k += THREADS) {
         const int j = k / WORDS, c = (k - j * WORDS) / (D / 4), d = 4 * (k % (D / 4));
         int last;
         const uint32_t members = members_of(j, last);
@@ -913,7 +927,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
         for (uint32_t rest = members; rest; rest &= rest - 1) {
             const int i = __ffs(rest) - 1;
             const float *from = (i & 1) ? reinterpret_cast<const float *>(rings + (i >> 1) * STAGES * L::stage_bytes)
-                                        : a.partials + (2 * (int64_t)gridDim.x + blockIdx.x * kAttnWarps + (i >> 1)) * SLOT;
+                                        : a.partials + (2 * (int64_t)gridDim.x + blockIdx.x * WARPS + (i >> 1)) * SLOT;
             const float by = piece_r[i * COLS + c];
             const float4 v = *reinterpret_cast<const float4 *>(from + c * D + d);
             y[0] += v.x * by;
@@ -947,8 +961,8 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
     int *arrived = reinterpret_cast<int *>(small);
     const auto span_of = [&](const AttnPiece &u, int64_t &c0, int64_t &c1) {
         const int64_t t0 = u.unit0 + kAttnGap, tiles = prefix[u.b + 1] - prefix[u.b] - kAttnGap;
-        c0 = share.worker_of(t0) / kAttnWarps;
-        c1 = share.worker_of(t0 + tiles - 1) / kAttnWarps;
+        c0 = share.worker_of(t0) / WARPS;
+        c1 = share.worker_of(t0 + tiles - 1) / WARPS;
     };
     const int last_piece = 31 - __clz(present), first_piece = __ffs(present) - 1;
     int last_first;
@@ -978,7 +992,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
         const auto from_of = [&](int i) { return a.partials + (2 * (c0 + i) + (i == 0)) * SLOT; };
         // weights of the CTAs' parts; a warp takes columns in turn
         float *weight = reinterpret_cast<float *>(rings);  // [n][COLS]; the pieces there are done with
-        for (int c = warp; c < live; c += kAttnWarps) {
+        for (int c = warp; c < live; c += WARPS) {
             float m = kNone, l = 0.0f;
             for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldcg(from_of(i) + c));
 #pragma unroll
@@ -996,7 +1010,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm<NB, NT>())
             }
         }
         __syncthreads();
-        for (int k = tid; k < live * (D / 4); k += kAttnThreads) {
+        for (int k = tid; k < live * (D / 4); k += THREADS) {
             const int c = k / (D / 4), d = 4 * (k - c * (D / 4));
             float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 8
@@ -1031,7 +1045,7 @@ cudaError_t attn_launch(const AttnArgs &a, int sms, cudaStream_t stream) {
         if (device < 64) ready[device].store(1, std::memory_order_relaxed);
     }
     return launch(attn_kernel<NB, NT, PIECES>, dim3((unsigned)(sms * attn_ctas_per_sm<NB, NT>())),
-                  dim3(kAttnThreads), attn_smem<NB, NT>(a.B), stream, true, a);
+                  dim3(32 * attn_warps<NB, NT>()), attn_smem<NB, NT>(a.B), stream, true, a);
 }
 
 // Column tiles of 8 or, from 9 columns up, 16 (where the registers hold them).
