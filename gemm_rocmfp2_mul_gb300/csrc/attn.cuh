@@ -87,7 +87,7 @@ constexpr int attn_ctas_per_sm() { return NB * NT <= 2 ? 2 : 1; }
 // line's prefix.
 template <int NB, int NT>
 constexpr int attn_small_bytes(int B) {
-    return 128 + 2 * attn_warps<NB, NT>() * ((int)sizeof(AttnPiece) + 4 * 8 * NT * 4) + (B + 1) * 8;
+    return 128 + 2 * attn_warps<NB, NT>() * ((int)sizeof(AttnPiece) + 2 * 8 * NT * 4) + (B + 1) * 8;
 }
 template <int NB, int NT>
 constexpr int attn_stages() {
@@ -220,8 +220,7 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
     AttnPiece *pieces = reinterpret_cast<AttnPiece *>(small + 16);  // [warps][head, tail]
     float *piece_r = reinterpret_cast<float *>(pieces + 2 * WARPS);  // [pieces][COLS]
     float *piece_l = piece_r + 2 * WARPS * COLS;
-    float *group_r = piece_l + 2 * WARPS * COLS, *group_l = group_r + 2 * WARPS * COLS;
-    int64_t *prefix = reinterpret_cast<int64_t *>(group_l + 2 * WARPS * COLS);  // [B + 1]
+    int64_t *prefix = reinterpret_cast<int64_t *>(piece_l + 2 * WARPS * COLS);  // [B + 1]
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
@@ -492,6 +491,16 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
     };
     const auto lse_of = [&](float m, float l) {
         return l == 0.0f ? -CUDART_INF_F : (m + kSumShift) * 0.6931471805599453f + logf(l);
+    };
+
+    // four values d .. d + 3 of column c of a unit that is joined: references and sums m and l
+    const auto finish = [&](const AttnPiece &u, int c, int d, float (&y)[4], float m, float l) {
+        const float inv = l == 0.0f ? 0.0f : kSumScale / l;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] *= inv;
+        const int64_t row = row_of(u.b, u.hk, u.ct * COLS + c);
+        store_four(row, d, y);
+        if (a.lse && d == 0) a.lse[row] = lse_of(m, l);
     };
 
     // ---- the units of this stretch ----
@@ -890,59 +899,57 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
     uint32_t ends = present & 0x55555555u;         // heads, and a last tail
     ends |= present & (0x80000000u >> __clz(present));
     const int groups = __popc(ends);
-    const auto members_of = [&](int j, int &last) {  // pieces of group j, as bits
+    const auto members_of = [&](int j) {  // pieces of group j, as bits
         uint32_t rest = ends, below = 0;
         for (int k = 0; k < j; ++k) {
             below = 2u * (rest & -rest) - 1u;
             rest &= rest - 1;
         }
-        last = __ffs(rest) - 1;
-        return present & ((2u << last) - 1u) & ~below;
+        return present & (2u * (rest & -rest) - 1u) & ~below;
     };
-    if (tid < groups * COLS) {
-        // each piece's weight beside its group's reference, and the group's sum
-        const int j = tid / COLS, c = tid - j * COLS;
-        int last;
-        const uint32_t members = members_of(j, last);
-        float m = kNone, l = 0.0f;
-        for (uint32_t u = members; u; u &= u - 1) m = fmaxf(m, piece_r[(__ffs(u) - 1) * COLS + c]);
-        for (uint32_t u = members; u; u &= u - 1) {
-            const int at = (__ffs(u) - 1) * COLS + c;
-            const float by = exp2_fast(piece_r[at] - m);
-            l += piece_l[at] * by;
-            piece_r[at] = by;
-        }
-        group_r[tid] = m;
-        group_l[tid] = l;
-    }
-    __syncthreads();
-    bool split = false;
+    const AttnPiece *head_unit = pieces + __ffs(present) - 1;                 // of the first group
+    const AttnPiece *tail_unit = pieces + __ffs(members_of(groups - 1)) - 1;  // of the last
+    const bool split0 = !head_unit->starts;
+    const bool split1 = (31 - __clz(present)) % 2 == 1 && !(split0 && groups == 1);
     for (int k = tid; k < groups * WORDS; k += THREADS) {
         const int j = k / WORDS, c = (k - j * WORDS) / (D / 4), d = 4 * (k % (D / 4));
-        int last;
-        const uint32_t members = members_of(j, last);
+        const uint32_t members = members_of(j), tails = members & ~0x55555555u, head = members & 0x55555555u;
         const AttnPiece &u = pieces[__ffs(members) - 1];
         if (c >= a.columns - u.ct * COLS) continue;
-        float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (uint32_t rest = members; rest; rest &= rest - 1) {
-            const int i = __ffs(rest) - 1;
-            const float *from = (i & 1) ? reinterpret_cast<const float *>(rings + (i >> 1) * STAGES * L::stage_bytes)
-                                        : a.partials + (2 * (int64_t)gridDim.x + blockIdx.x * WARPS + (i >> 1)) * SLOT;
-            const float by = piece_r[i * COLS + c];
-            const float4 v = *reinterpret_cast<const float4 *>(from + c * D + d);
+        float y[4] = {0.0f, 0.0f, 0.0f, 0.0f}, l = 0.0f, m = kNone, r[WARPS];
+        float4 hv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const int hw = head ? __ffs(head) - 1 : 0;
+        if (head) {
+            hv = *reinterpret_cast<const float4 *>(
+                a.partials + (2 * (int64_t)gridDim.x + blockIdx.x * WARPS + (hw >> 1)) * SLOT + c * D + d);
+            m = piece_r[hw * COLS + c];
+        }
+        const float hr = m;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            r[w] = tails >> (2 * w + 1) & 1u ? piece_r[(2 * w + 1) * COLS + c] : kNone;
+            m = fmaxf(m, r[w]);
+        }
+        const auto add = [&](const float4 &v, float by) {
             y[0] += v.x * by;
             y[1] += v.y * by;
             y[2] += v.z * by;
             y[3] += v.w * by;
-        }
-        const float m = group_r[j * COLS + c], l = group_l[j * COLS + c];
-        if (u.starts && (last & 1) == 0) {
-            const float inv = l == 0.0f ? 0.0f : kSumScale / l;
+        };
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] *= inv;
-            const int64_t row = row_of(u.b, u.hk, u.ct * COLS + c);
-            store_four(row, d, y);
-            if (a.lse && d == 0) a.lse[row] = lse_of(m, l);
+        for (int w = 0; w < WARPS; ++w)
+            if (tails >> (2 * w + 1) & 1u) {
+                const float by = exp2_fast(r[w] - m);
+                l += piece_l[(2 * w + 1) * COLS + c] * by;
+                add(*reinterpret_cast<const float4 *>(rings + w * STAGES * L::stage_bytes + (c * D + d) * 4), by);
+            }
+        if (head) {
+            const float by = exp2_fast(hr - m);
+            l += piece_l[hw * COLS + c] * by;
+            add(hv, by);
+        }
+        if (u.starts && head) {
+            finish(u, c, d, y, m, l);
         } else {
             // a unit of several CTAs
             float *mine = a.partials + (2 * (int64_t)blockIdx.x + u.starts) * SLOT;
@@ -951,83 +958,93 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
                 mine[c] = m;
                 mine[COLS + c] = l;
             }
-            split = true;
         }
     }
-    if (!__syncthreads_or(split)) return;
+    if (!split0 && !split1) return;
 
     // ---- units of several CTAs: the first group, if it did not start here, and the last, if it does
     // not end here.  The last CTA of each to arrive joins it. ----
-    int *arrived = reinterpret_cast<int *>(small);
-    const auto span_of = [&](const AttnPiece &u, int64_t &c0, int64_t &c1) {
-        const int64_t t0 = u.unit0 + kAttnGap, tiles = prefix[u.b + 1] - prefix[u.b] - kAttnGap;
-        c0 = share.worker_of(t0) / WARPS;
-        c1 = share.worker_of(t0 + tiles - 1) / WARPS;
-    };
-    const int last_piece = 31 - __clz(present), first_piece = __ffs(present) - 1;
-    int last_first;
-    const int last_group = __ffs(members_of(groups - 1, last_first)) - 1;  // its first piece
-    const bool split0 = !pieces[first_piece].starts;
-    const bool split1 = (last_piece & 1) && !(split0 && groups == 1);
+    int *arrived = reinterpret_cast<int *>(small);  // [2][2]: joins, CTAs
+    int64_t *from_cta = small + 2;                  // [2]
     __threadfence();
     __syncthreads();
     if (lane == 0 && warp < 2) {
-        int joins = 0;
+        int joins = 0, n = 0;
         if (warp == 0 ? split0 : split1) {
-            int64_t c0, c1;
-            span_of(pieces[warp == 0 ? first_piece : last_group], c0, c1);
-            joins = atomicAdd(a.counters + c0, 1) == (int)(c1 - c0);
+            const AttnPiece *u = warp == 0 ? head_unit : tail_unit;
+            const int64_t t0 = u->unit0 + kAttnGap, tiles = prefix[u->b + 1] - prefix[u->b] - kAttnGap;
+            const int64_t c0 = share.worker_of(t0) / WARPS, c1 = share.worker_of(t0 + tiles - 1) / WARPS;
+            n = (int)(c1 - c0) + 1;
+            joins = atomicAdd(a.counters + c0, 1) == n - 1;
             if (joins) a.counters[c0] = 0;
+            from_cta[warp] = c0;
         }
-        arrived[warp] = joins;
+        arrived[2 * warp] = joins;
+        arrived[2 * warp + 1] = n;
     }
     __syncthreads();
+#pragma unroll 1
     for (int which = 0; which < 2; ++which) {
-        if (!arrived[which]) continue;
+        if (!arrived[2 * which]) continue;
         __threadfence();
-        const AttnPiece u = pieces[which == 0 ? first_piece : last_group];
-        int64_t c0, c1;
-        span_of(u, c0, c1);
-        const int n = (int)(c1 - c0 + 1), live = min(COLS, a.columns - u.ct * COLS);
-        const auto from_of = [&](int i) { return a.partials + (2 * (c0 + i) + (i == 0)) * SLOT; };
-        // weights of the CTAs' parts; a warp takes columns in turn
-        float *weight = reinterpret_cast<float *>(rings);  // [n][COLS]; the pieces there are done with
-        for (int c = warp; c < live; c += WARPS) {
-            float m = kNone, l = 0.0f;
-            for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldcg(from_of(i) + c));
+        const AttnPiece &u = which == 0 ? *head_unit : *tail_unit;
+        const int n = arrived[2 * which + 1], live = min(COLS, a.columns - u.ct * COLS);
+        // the CTAs' parts: of the first its second slot, of the others their first
+        const float *parts0 = a.partials + (2 * from_cta[which] + 1) * SLOT;
+        const auto part_of = [&](int i) { return parts0 + (i ? (2 * i - 1) * (int64_t)SLOT : 0); };
+        constexpr int AHEAD = 8;  // parts on their way while the weights are found
+        for (int k0 = 0; k0 < live * (D / 4); k0 += THREADS) {
+            const int k = k0 + tid, c = k / (D / 4), d = 4 * (k - c * (D / 4));
+            const bool mine = c < live;
+            float4 v[AHEAD];
 #pragma unroll
-            for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-            for (int i = lane; i < n; i += 32) {
-                const float by = exp2_fast(__ldcg(from_of(i) + c) - m);
-                l += __ldcg(from_of(i) + COLS + c) * by;
-                weight[i * COLS + c] = by;
-            }
+            for (int i = 0; i < AHEAD; ++i)
+                if (mine && i < n) v[i] = __ldcg(reinterpret_cast<const float4 *>(part_of(i) + 2 * COLS + c * D + d));
+            if (k0 == 0) {
+                // weights of the parts, and the columns' references and sums; a warp takes columns in turn
+                float *weight = reinterpret_cast<float *>(rings);  // [n][COLS]; the pieces there are done with
+                for (int cc = warp; cc < live; cc += WARPS) {
+                    float r = lane < n ? __ldcg(part_of(lane) + cc) : kNone;
+                    float s = lane < n ? __ldcg(part_of(lane) + COLS + cc) : 0.0f;
+                    float m = r;
+                    for (int i = lane + 32; i < n; i += 32) m = fmaxf(m, __ldcg(part_of(i) + cc));
 #pragma unroll
-            for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-            if (lane == 0) {
-                group_r[c] = m;
-                group_l[c] = l;
+                    for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+                    float l = 0.0f;
+                    for (int i = lane; i < n; i += 32) {
+                        if (i != lane) {
+                            r = __ldcg(part_of(i) + cc);
+                            s = __ldcg(part_of(i) + COLS + cc);
+                        }
+                        const float by = exp2_fast(r - m);
+                        l += s * by;
+                        weight[i * COLS + cc] = by;
+                    }
+#pragma unroll
+                    for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+                    if (lane == 0) {
+                        piece_r[cc] = m;
+                        piece_l[cc] = l;
+                    }
+                }
+                __syncthreads();
             }
-        }
-        __syncthreads();
-        for (int k = tid; k < live * (D / 4); k += THREADS) {
-            const int c = k / (D / 4), d = 4 * (k - c * (D / 4));
+            if (!mine) continue;
+            const float *weight = reinterpret_cast<const float *>(rings) + c;
             float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 8
-            for (int i = 0; i < n; ++i) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(from_of(i) + 2 * COLS + c * D + d));
-                const float by = weight[i * COLS + c];
-                y[0] += v.x * by;
-                y[1] += v.y * by;
-                y[2] += v.z * by;
-                y[3] += v.w * by;
-            }
-            const float l = group_l[c], inv = l == 0.0f ? 0.0f : kSumScale / l;
+            const auto add = [&](const float4 &x, float by) {
+                y[0] += x.x * by;
+                y[1] += x.y * by;
+                y[2] += x.z * by;
+                y[3] += x.w * by;
+            };
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] *= inv;
-            const int64_t row = row_of(u.b, u.hk, u.ct * COLS + c);
-            store_four(row, d, y);
-            if (a.lse && d == 0) a.lse[row] = lse_of(group_r[c], l);
+            for (int i = 0; i < AHEAD; ++i)
+                if (i < n) add(v[i], weight[i * COLS]);
+#pragma unroll 8
+            for (int i = AHEAD; i < n; ++i)
+                add(__ldcg(reinterpret_cast<const float4 *>(part_of(i) + 2 * COLS + c * D + d)), weight[i * COLS]);
+            finish(u, c, d, y, piece_r[c], piece_l[c]);
         }
         __syncthreads();
     }
