@@ -65,13 +65,25 @@ RFP2_DEV void store_values(T *p, const float (&v)[N]) {
 // Rotary angles.  theta = position * f in turns is position * (f / 2 pi) mod
 // 1.  With f / 2 pi mod 1 as a 64-bit binary fraction, the product with an
 // integer position wraps at whole turns by itself: no range reduction, and no
-// loss of angle however long the context is (one fp64 multiply per frequency;
-// error below 2^-54 turns per position for f <= 1).
+// loss of angle however long the context is.  The fraction is the exact
+// product of f's 24 bits with 128 bits of 1 / 2 pi, in integers: fp64 is slow
+// here.
 RFP2_DEV uint64_t turn_fraction(float f) {
-    double t = static_cast<double>(f) * 0.15915494309189533577;  // 1 / (2 pi)
-    t -= floor(t);
-    // t rounds to 1 for a tiny negative f; the fraction wraps to 0 there
-    return t < 1.0 ? __double2ull_rz(t * 18446744073709551616.0) : 0ull;
+    constexpr uint64_t hi = 0x28BE60DB9391054Aull, lo = 0x7F09D5F47D4D3770ull;  // 2^128 / 2 pi
+    const uint32_t bits = __float_as_uint(f), e = bits >> 23 & 255u;
+    const uint64_t m = e ? (bits & 0x7FFFFFu) | 0x800000u : (bits & 0x7FFFFFu) << 1;
+    // m * (hi, lo) in words w2 w1 w0, to be divided by 2^(150 - e)
+    const uint64_t w0 = m * lo, c0 = __umul64hi(m, lo), p1 = m * hi, w1 = p1 + c0;
+    const uint64_t w2 = __umul64hi(m, hi) + (w1 < p1);
+    const int s = 150 - (int)e;
+    uint64_t r;
+    if (s >= 64)
+        r = s >= 128 ? 0ull : w2 >> (s - 64);
+    else if (s > 0)
+        r = w1 >> s | w2 << (64 - s);
+    else
+        r = s == 0 ? w1 : s > -64 ? w1 << -s | w0 >> (64 + s) : 0ull;
+    return bits >> 31 ? 0ull - r : r;
 }
 
 // (cos, sin) of position turns of `fraction`: the top 32 bits as a signed
@@ -84,6 +96,18 @@ RFP2_DEV float2 rotary_cos_sin(int position, uint64_t fraction) {
     sincospif(half_turns, &s, &c);
     return make_float2(c, s);
 }
+
+// n / d for 0 <= n < 2^31 by a multiplication: with 2^(s-1) < d <= 2^s and
+// mul = floor(2^32 (2^s - d) / d) + 1, n / d = (mulhi(n, mul) + n) >> s.
+struct FastDiv {
+    uint32_t d, mul, shift;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t divisor) : d(divisor), shift(0) {
+        while ((1ull << shift) < d) ++shift;
+        mul = (uint32_t)(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
+    }
+    RFP2_DEV uint32_t operator()(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
 
 // Host: bytes of one value, 0 for an unknown type.
 inline int dtype_bytes(int dtype) {

@@ -4,9 +4,9 @@
 // Its gradient is the same kernel with the angles negated.
 //
 // Bound by memory: 2 * size bytes a value against four multiplies and a share
-// of a cos/sin pair.  A CTA takes a few tokens and a run of their heads: its
-// threads first compute each (token, pair)'s cos and sin once into shared
-// memory, then walk the heads' rows.
+// of a cos/sin pair.  A CTA takes a few tokens and a run of their heads.  Each
+// thread first sends off its rows' loads, then the CTA computes the cos and
+// sin of its (token, pair)s once into shared memory while they travel.
 #include <algorithm>
 
 #include "activation.cuh"
@@ -15,7 +15,8 @@ namespace rfp2 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxPairs = 2048;  // (token, pair) entries of a CTA's cos/sin table
+constexpr int kAhead = 4;        // steps of a thread whose loads travel together
+constexpr int kMaxPairs = 2048;  // (token, pair) entries of a CTA's table
 
 struct RopeArgs {
     const void *x;
@@ -26,90 +27,147 @@ struct RopeArgs {
     int H, D, pairs;
     int tokens, heads;  // of a CTA
     float factor;
-    int inverse, copy;  // copy: the values past R move to `out`
+    int inverse;
+    int turned, steps;  // steps of a row: those that turn, and those that copy what lies past R
+    FastDiv by_pairs, by_steps, by_heads;
 };
 
-// V pairs a step: 2V values, as two runs of V.  V = 1 takes any alignment.
+// 2V values of a row: V pairs, as two runs of V values.  Runs are 16 bytes, or
+// (V = 1) single values of any alignment.
+template <typename T, int V>
+struct alignas(V * sizeof(T)) Runs {
+    T u[V], w[V];
+    RFP2_DEV void load(const T *p, const T *q) { copy(u, p), copy(w, q); }
+    RFP2_DEV void store(T *p, T *q) const { copy(p, u), copy(q, w); }
+    static RFP2_DEV void copy(T *to, const T *from) {
+        if constexpr (V * sizeof(T) == 16) {
+            *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(from);
+        } else {
+            *to = *from;
+        }
+    }
+};
+
+// The place of pair p in the table of V's layout: 16-byte words of four pairs,
+// those of a thread's first four before those of its second, so that
+// neighbouring threads read neighbouring words.
+template <int V>
+RFP2_DEV int table_place(int p, int pairs) {
+    return V == 8 ? ((p >> 2 & 1) * (pairs >> 3) + (p >> 3)) * 4 + (p & 3) : p;
+}
+
 template <typename T, int V, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
-    extern __shared__ float2 table[];  // [tokens][pairs]
+__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a) {
+    extern __shared__ __align__(16) float table[];  // [tokens][cos, sin][pairs]
     pdl_wait();
     pdl_launch_dependents();
     const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
     const int h0 = blockIdx.y * a.heads;
     const int nt = (int)min((int64_t)a.tokens, a.T - t0), nh = min(a.heads, a.H - h0);
+    const int n = nt * a.heads * a.steps;
+
+    // step i: token t, head h, values at `at` and `at2` of its row; h may lie past the last head
+    const auto place = [&](int i, int &t, int &h, int &s, int &at, int &at2) {
+        const int row = a.by_steps(i);
+        s = i - row * a.steps;
+        t = a.by_heads(row);
+        h = row - t * a.heads;
+        if (s < a.turned && !INTERLEAVED) {
+            at = V * s;
+            at2 = at + a.pairs;
+        } else {
+            at = 2 * V * s;
+            at2 = at + V;
+        }
+        return i < n && h < nh;
+    };
+    const auto load = [&](int i, Runs<T, V> &x) {
+        int t, h, s, at, at2;
+        if (!place(i, t, h, s, at, at2)) return;
+        const T *p = static_cast<const T *>(a.x) + (t0 + t) * a.xt + (h0 + h) * a.xh;
+        x.load(p + at, p + at2);
+    };
+    const auto turn = [&](int i, Runs<T, V> &x) {
+        int t, h, s, at, at2;
+        if (!place(i, t, h, s, at, at2)) return;
+        if (s < a.turned) {
+            const float *cs = table + 2 * t * a.pairs;
+            float c[V], sn[V];
+            if constexpr (V == 1) {
+                c[0] = cs[s];
+                sn[0] = cs[a.pairs + s];
+            } else {
+#pragma unroll
+                for (int w = 0; w < V / 4; ++w) {
+                    const float *q = cs + (w * (a.pairs >> 3) + s) * 4;
+                    const float4 u = *reinterpret_cast<const float4 *>(q);
+                    const float4 v = *reinterpret_cast<const float4 *>(q + a.pairs);
+                    c[4 * w] = u.x, c[4 * w + 1] = u.y, c[4 * w + 2] = u.z, c[4 * w + 3] = u.w;
+                    sn[4 * w] = v.x, sn[4 * w + 1] = v.y, sn[4 * w + 2] = v.z, sn[4 * w + 3] = v.w;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                // pair e: values 2e and 2e + 1 of the run of 2V, or e of each run
+                T &p = INTERLEAVED ? (2 * e < V ? x.u[2 * e % V] : x.w[2 * e % V]) : x.u[e];
+                T &q = INTERLEAVED ? (2 * e + 1 < V ? x.u[(2 * e + 1) % V] : x.w[(2 * e + 1) % V]) : x.w[e];
+                const float u = to_f32(p), w = to_f32(q);
+                p = from_f32<T>(u * c[e] - w * sn[e]);
+                q = from_f32<T>(w * c[e] + u * sn[e]);
+            }
+        }
+        T *o = static_cast<T *>(a.out) + (t0 + t) * a.ot + (h0 + h) * a.oh;
+        x.store(o + at, o + at2);
+    };
+
+    Runs<T, V> x[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) load(threadIdx.x + k * kThreads, x[k]);
     for (int i = threadIdx.x; i < nt * a.pairs; i += kThreads) {
-        const int t = i / a.pairs, p = i - t * a.pairs;
-        float2 cs = rotary_cos_sin(a.positions[t0 + t], turn_fraction(a.inv_freq[p]));
-        cs.x *= a.factor;
-        cs.y *= a.inverse ? -a.factor : a.factor;
-        table[i] = cs;
+        const int t = a.by_pairs(i), p = i - t * a.pairs;
+        const float2 cs = rotary_cos_sin(a.positions[t0 + t], turn_fraction(a.inv_freq[p]));
+        float *at = table + 2 * t * a.pairs + table_place<V>(p, a.pairs);
+        at[0] = cs.x * a.factor;
+        at[a.pairs] = cs.y * (a.inverse ? -a.factor : a.factor);
     }
     __syncthreads();
-    const int turned = a.pairs / V;  // steps that turn; V divides pairs
-    const int steps = turned + (a.copy ? (a.D / 2 - a.pairs) / V : 0);
-    const int n = nt * nh * steps;
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        const int row = i / steps, s = i - row * steps;
-        const int t = row / nh, h = row - t * nh;
-        const T *x = static_cast<const T *>(a.x) + (t0 + t) * a.xt + (h0 + h) * a.xh;
-        T *o = static_cast<T *>(a.out) + (t0 + t) * a.ot + (h0 + h) * a.oh;
-        float u[V], w[V];
-        if (s < turned) {
-            const float2 *cs = table + t * a.pairs + s * V;
-            if (INTERLEAVED) {
-                load_values<T, V>(x + 2 * V * s, u);
-                load_values<T, V>(x + 2 * V * s + V, w);
-                float y[2 * V];
+    for (int i = threadIdx.x; i < n; i += kAhead * kThreads) {
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    y[e] = u[e];
-                    y[V + e] = w[e];
-                }
+        for (int k = 0; k < kAhead; ++k) turn(i + k * kThreads, x[k]);
+        if (i + kAhead * kThreads < n)
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float p = y[2 * e], q = y[2 * e + 1];
-                    y[2 * e] = p * cs[e].x - q * cs[e].y;
-                    y[2 * e + 1] = q * cs[e].x + p * cs[e].y;
-                }
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    u[e] = y[e];
-                    w[e] = y[V + e];
-                }
-                store_values<T, V>(o + 2 * V * s, u);
-                store_values<T, V>(o + 2 * V * s + V, w);
-            } else {
-                load_values<T, V>(x + V * s, u);
-                load_values<T, V>(x + a.pairs + V * s, w);
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float p = u[e], q = w[e];
-                    u[e] = p * cs[e].x - q * cs[e].y;
-                    w[e] = q * cs[e].x + p * cs[e].y;
-                }
-                store_values<T, V>(o + V * s, u);
-                store_values<T, V>(o + a.pairs + V * s, w);
-            }
-        } else {
-            const int at = 2 * a.pairs + 2 * V * (s - turned);
-            load_values<T, V>(x + at, u);
-            load_values<T, V>(x + at + V, w);
-            store_values<T, V>(o + at, u);
-            store_values<T, V>(o + at + V, w);
-        }
+            for (int k = 0; k < kAhead; ++k) load(i + (kAhead + k) * kThreads, x[k]);
     }
 }
 
 template <typename T>
-cudaError_t launch_rope(RopeArgs &a, bool interleaved, cudaStream_t stream) {
-    constexpr int V = 16 / sizeof(T);
-    const auto even = [](int64_t v) { return v % V == 0; };
+cudaError_t launch_rope(RopeArgs &a, bool interleaved, bool copy, cudaStream_t stream) {
+    constexpr int W = 16 / sizeof(T);
+    const auto even = [](int64_t v) { return v % W == 0; };
     const bool wide = aligned(a.x, 16) && aligned(a.out, 16) && even(a.xt) && even(a.xh) &&
                       even(a.ot) && even(a.oh) && even(a.pairs) && even(a.D / 2 - a.pairs);
+    const int V = wide ? W : 1;
+    a.turned = a.pairs / V;
+    a.steps = a.turned + (copy ? (a.D / 2 - a.pairs) / V : 0);
+    // up to 8 steps a thread: tokens share a CTA where a token's heads are fewer, and heads are divided
+    // where they are more.  But a few CTAs for every SM before that, so that none waits for another.
+    constexpr int kSteps = 8 * kThreads;
+    const int64_t ctas = 6 * (int64_t)sm_count(current_device());
+    a.heads = std::max(1, std::min(a.H, kSteps / std::max(1, a.steps)));
+    while (a.heads > 1 && a.heads * a.steps > kThreads && a.T * ((a.H + a.heads - 1) / a.heads) < ctas)
+        a.heads = (a.heads + 1) / 2;
+    a.tokens = 1;
+    if (a.heads == a.H) {
+        const int64_t most = std::min<int64_t>(kSteps / (a.heads * std::max(1, a.steps)), a.T / ctas);
+        a.tokens = (int)std::max<int64_t>(1, std::min<int64_t>(most, kMaxPairs / std::max(1, a.pairs)));
+    }
+    a.by_pairs = FastDiv(std::max(1, a.pairs));
+    a.by_steps = FastDiv(std::max(1, a.steps));
+    a.by_heads = FastDiv(a.heads);
+    if (a.steps == 0) return cudaSuccess;  // nothing turns, in place
     const dim3 grid((unsigned)((a.T + a.tokens - 1) / a.tokens), (a.H + a.heads - 1) / a.heads);
-    const size_t smem = (size_t)a.tokens * a.pairs * sizeof(float2);
-    void (*k)(RopeArgs) = wide ? (interleaved ? rope_kernel<T, V, true> : rope_kernel<T, V, false>)
+    const size_t smem = (size_t)a.tokens * a.pairs * 8;
+    void (*k)(RopeArgs) = wide ? (interleaved ? rope_kernel<T, W, true> : rope_kernel<T, W, false>)
                                : (interleaved ? rope_kernel<T, 1, true> : rope_kernel<T, 1, false>);
     return launch(k, grid, dim3(kThreads), smem, stream, true, a);
 }
@@ -175,12 +233,9 @@ extern "C" rfp2_status rfp2_rope(const void *x, int dtype, int64_t T, int64_t H,
     a.pairs = (int)(R / 2);
     a.factor = factor;
     a.inverse = (flags & RFP2_ROPE_INVERSE) != 0;
-    a.copy = R < D && x != out;
-    a.tokens = 1;
-    a.heads = 8;
-    const bool interleaved = (flags & RFP2_ROPE_INTERLEAVED) != 0;
+    const bool copy = x != out, interleaved = (flags & RFP2_ROPE_INTERLEAVED) != 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return from_cuda(dtype == RFP2_F32    ? launch_rope<float>(a, interleaved, s)
-                     : dtype == RFP2_BF16 ? launch_rope<__nv_bfloat16>(a, interleaved, s)
-                                          : launch_rope<__half>(a, interleaved, s));
+    return from_cuda(dtype == RFP2_F32    ? launch_rope<float>(a, interleaved, copy, s)
+                     : dtype == RFP2_BF16 ? launch_rope<__nv_bfloat16>(a, interleaved, copy, s)
+                                          : launch_rope<__half>(a, interleaved, copy, s));
 }
