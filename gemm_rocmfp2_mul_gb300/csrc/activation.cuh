@@ -97,6 +97,14 @@ RFP2_DEV float2 rotary_cos_sin(int position, uint64_t fraction) {
     return make_float2(c, s);
 }
 
+// The place of pair p in a table of `pairs` cosines or sines that is read four
+// to a 16-byte word.  V = 8: a thread reads eight; its first words come before
+// all second words, so that neighbouring threads read neighbouring words.
+template <int V>
+RFP2_DEV int table_place(int p, int pairs) {
+    return V == 8 ? ((p >> 2 & 1) * (pairs >> 3) + (p >> 3)) * 4 + (p & 3) : p;
+}
+
 // n / d for 0 <= n < 2^31 by a multiplication: with 2^(s-1) < d <= 2^s and
 // mul = floor(2^32 (2^s - d) / d) + 1, n / d = (mulhi(n, mul) + n) >> s.
 struct FastDiv {

@@ -15,7 +15,40 @@ namespace rfp2 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;  // steps of a thread whose loads travel together
+constexpr int kMaxTable = 4096;  // (token, pair) entries of a CTA's table
+
+// A token's steps (a head's eight or, reading fp32, four values of key and of
+// value) are dealt to neighbouring threads; a CTA holds `rows` tokens at a
+// time, or a stretch of a token that has more steps than the CTA threads.  So a
+// thread keeps its head and its place in the row, and goes from token to token.
+struct Deal {
+    int steps, rows, tokens;  // steps of a token; tokens at a time; tokens of a CTA
+    FastDiv by_steps, by_chunks;
+    RFP2_DEV bool mine(int chunks, int &row, int &h, int &c, int &step) const {
+        row = rows > 1 ? by_steps(threadIdx.x) : 0;
+        step = threadIdx.x - row * steps + blockIdx.y * kThreads;
+        h = by_chunks(step);
+        c = step - h * chunks;
+        return row < rows && step < steps;
+    }
+};
+
+// `ahead`: tokens of a thread whose loads travel together.  Few tokens are
+// spread over the SMs.
+Deal deal(int64_t T, int64_t heads, int64_t chunks, int ahead, int64_t most) {
+    Deal w;
+    w.steps = (int)(heads * chunks);
+    w.rows = std::max(1, kThreads / w.steps);
+    const int64_t by_sms = T / (4 * (int64_t)sm_count(current_device()));
+    w.tokens = (int)std::max<int64_t>(1, std::min({(int64_t)w.rows * ahead, by_sms, most}));
+    w.rows = std::min(w.rows, w.tokens);
+    w.by_steps = FastDiv((uint32_t)w.steps);
+    w.by_chunks = FastDiv((uint32_t)chunks);
+    return w;
+}
+dim3 grid_of(const Deal &w, int64_t T) {
+    return dim3((unsigned)((T + w.tokens - 1) / w.tokens), (unsigned)((w.steps + kThreads - 1) / kThreads));
+}
 
 struct WriteArgs {
     const void *k, *v;
@@ -26,8 +59,9 @@ struct WriteArgs {
     int8_t *k_codes, *v_codes;
     float *k_scales, *v_scales;
     int64_t pages, page_size;
-    int heads, D, pairs, tokens, interleaved;
-    FastDiv by_pairs, by_token, by_chunks;  // a token's pairs, steps (of keys or values), a row's steps
+    int heads, D, pairs, interleaved;
+    Deal deal;
+    FastDiv by_pairs;
     float factor;
     int32_t *status;
 };
@@ -59,26 +93,57 @@ struct alignas(8 * sizeof(T)) Eight {
     }
 };
 
-// Codes of eight values by their block's scale d, as two words.  z = a / d to
-// within 2^-14 by an approximate reciprocal; where z is not within 2^-12 of a
-// half-integer it rounds as the IEEE quotient does, else, and for scales so
-// small that the reciprocal or z may leave fp32's range, the division decides.
+RFP2_DEV float max_abs(float a, float b, float c) {  // of |a|, |b|, |c|; a NaN stays
+    float y;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// Codes of a block whose scale is zero, not finite, or so small that a
+// reciprocal or a product of it leaves fp32's range.
+__device__ __noinline__ uint2 codes_of_odd(const float (&x)[8], float d) {
+    uint2 w = make_uint2(0u, 0u);
+    if (!(d > 0.0f && d <= 3.402823466e38f)) return w;
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e) {
+        const int q = (int)fminf(fmaxf(roundf(__fdiv_rn(x[e], d)), -127.0f), 127.0f);
+        (e < 4 ? w.x : w.y) |= (uint32_t)(q & 255) << (8 * (e & 3));
+    }
+    return w;
+}
+
+// round-half-away(fl(x / d)) for eight values and 2^-100 <= d < inf, as bytes of
+// two words, without a division.
+//
+// 1/d to 2^-22 and a little more either way brackets x / d and its rounded
+// quotient: where both products round to the same integer (adding 1.5 * 2^23
+// rounds, and leaves the integer in the low bits), that is the result.  Else a
+// half-integer H = n + 1/2 lies between, as often happens for 16-bit types, and
+// fl(|x| / d) >= H exactly when |x| / d >= H - u/2, u being fp32's spacing just
+// below H (at equality |x| would need 25 bits).  R = |x| - H d is a small
+// multiple of d's last place, so the fused product gives it exactly, and
+// (u/2) d is d times a power of two: 2^(k-24) for H in (2^k, 2^(k+1)), 2^-26 for
+// H = 1/2, in both cases the power of two below H's predecessor times 2^-24.
 RFP2_DEV uint2 codes_of(const float (&x)[8], float d) {
-    constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer
+    constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
     float by;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(by) : "f"(d));
-    uint32_t q[8];
-    float off = 0.0f;
+    const float more = by * (1.0f + 0x1p-20f), less = by * (1.0f - 0x1p-20f);
+    uint32_t q[8], differ = 0u;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float z = x[e] * by, r = z + kMagic;
-        off = fmaxf(off, fabsf(z - (r - kMagic)));
-        q[e] = __float_as_uint(r);
+        q[e] = __float_as_uint(fmaf(x[e], less, kMagic));
+        differ |= q[e] ^ __float_as_uint(fmaf(x[e], more, kMagic));
     }
-    if (off > 0.5f - 0x1p-12f || d < 0x1p-100f) {
+    if (differ) {
+        const float scaled = d * 0x1p-24f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            q[e] = (uint32_t)(int)fminf(fmaxf(roundf(__fdiv_rn(x[e], d)), -127.0f), 127.0f);
+        for (int e = 0; e < 8; ++e) {
+            const float far = fmaf(x[e], more, kMagic), H = fabsf(__uint_as_float(q[e]) - kMagic) + 0.5f;
+            const float below = __uint_as_float((__float_as_uint(H) - 1u) & 0x7F800000u);
+            const bool up = fmaf(-H, d, fabsf(x[e])) > -below * scaled;
+            q[e] = up ? __float_as_uint(far) : q[e];
+        }
     }
     uint2 w;
     w.x = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
@@ -86,98 +151,45 @@ RFP2_DEV uint2 codes_of(const float (&x)[8], float d) {
     return w;
 }
 
+// Eight values of a block, in four neighbouring lanes, to the cache.
+RFP2_DEV void write_block(const float (&x)[8], int64_t row, int c, int D, int8_t *codes, float *scales) {
+    float top = max_abs(max_abs(x[0], x[1], x[2]), max_abs(x[3], x[4], x[5]), max_abs(x[6], x[7], x[7]));
+    const uint32_t lanes = 0xFu << (threadIdx.x & 28);
+    top = max_abs(top, __shfl_xor_sync(lanes, top, 1), top);
+    top = max_abs(top, __shfl_xor_sync(lanes, top, 2), top);
+    const float d = __fdiv_rn(top, 127.0f);
+    const uint2 w = d >= 0x1p-100f && d <= 3.402823466e38f ? codes_of(x, d) : codes_of_odd(x, d);
+    *reinterpret_cast<uint2 *>(codes + row * D + 8 * c) = w;
+    if ((c & 3) == 0) scales[row * (D / 32) + (c >> 2)] = d;
+}
+
 template <typename T, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 3) kv_write_kernel(const WriteArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) kv_write_kernel(const WriteArgs a) {
+    constexpr int AHEAD = 4 / sizeof(T);
     extern __shared__ __align__(16) uint8_t smem[];
-    int64_t *row0 = reinterpret_cast<int64_t *>(smem);                // [tokens]
-    float2 *table = reinterpret_cast<float2 *>(smem + 8 * a.tokens);  // [tokens][pairs]
+    float *table = reinterpret_cast<float *>(smem);                                       // [tokens][cos, sin][pairs]
+    int64_t *row0 = reinterpret_cast<int64_t *>(smem + 8 * a.deal.tokens * a.pairs);      // [tokens]
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
-    const int nt = (int)min((int64_t)a.tokens, a.T - t0);
-    const int chunks = a.D / 8, per_token = a.heads * chunks;
-    const int n = 2 * nt * per_token;  // a multiple of 8, so blocks' four lanes go together
-
-    // step i: keys or values of token t, values 8c .. 8c + 7 of head h
-    const auto place = [&](int i, int &t, int &is_v, int &h, int &c) {
-        const int token2 = a.by_token(i), rest = i - token2 * per_token;
-        t = token2 >> 1;
-        is_v = token2 & 1;
-        h = a.by_chunks(rest);
-        c = rest - h * chunks;
-    };
-    const auto row_of = [&](int t, int is_v, int h) {
-        return is_v ? static_cast<const T *>(a.v) + (t0 + t) * a.vt + h * a.vh
-                    : static_cast<const T *>(a.k) + (t0 + t) * a.kt + h * a.kh;
-    };
-    const auto load = [&](int i, Eight<T, WIDE> &x) {
-        if (i >= n) return;
-        int t, is_v, h, c;
-        place(i, t, is_v, h, c);
-        x.load(row_of(t, is_v, h) + 8 * c);
-    };
-    const auto write = [&](int i, const Eight<T, WIDE> &raw) {
-        if (i >= n) return;
-        int t, is_v, h, c;
-        place(i, t, is_v, h, c);
-        float x[8];
+    const int64_t t0 = (int64_t)blockIdx.x * a.deal.tokens;
+    const int nt = (int)min((int64_t)a.deal.tokens, a.T - t0);
+    int row, h, c, step;
+    const bool mine = a.deal.mine(a.D / 8, row, h, c, step);
+    const T *k = static_cast<const T *>(a.k) + t0 * a.kt + h * a.kh + 8 * c;
+    const T *v = static_cast<const T *>(a.v) + t0 * a.vt + h * a.vh + 8 * c;
+    Eight<T, WIDE> x[AHEAD], y[AHEAD];
+    const auto load = [&](int t) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = to_f32(raw.v[e]);
-        if (!is_v && 8 * c < 2 * a.pairs) {
-            const float2 *cs = table + t * a.pairs;
-            const T *row = row_of(t, 0, h);
-            if (a.interleaved) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int p = 4 * c + e;
-                    if (p < a.pairs) {
-                        const float u = x[2 * e], w = x[2 * e + 1];
-                        x[2 * e] = u * cs[p].x - w * cs[p].y;
-                        x[2 * e + 1] = w * cs[p].x + u * cs[p].y;
-                    }
-                }
-            } else if (a.pairs % 8 == 0) {
-                // the eight lie in one half; their partners, in the other, have just been read nearby
-                const bool low = 8 * c < a.pairs;
-                Eight<T, WIDE> y;
-                y.load(row + 8 * c + (low ? a.pairs : -a.pairs));
-                const float2 *p = cs + 8 * c - (low ? 0 : a.pairs);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float w = to_f32(y.v[e]);
-                    x[e] = x[e] * p[e].x + (low ? -w : w) * p[e].y;
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int j = 8 * c + e;
-                    if (j < a.pairs)
-                        x[e] = x[e] * cs[j].x - to_f32(row[j + a.pairs]) * cs[j].y;
-                    else if (j < 2 * a.pairs)
-                        x[e] = x[e] * cs[j - a.pairs].x + to_f32(row[j - a.pairs]) * cs[j - a.pairs].y;
-                }
+        for (int i = 0; i < AHEAD; ++i)
+            if (mine && t + i * a.deal.rows < nt) {
+                x[i].load(k + (t + i * a.deal.rows) * a.kt);
+                y[i].load(v + (t + i * a.deal.rows) * a.vt);
             }
-        }
-        // the maximum of |a| as bits: a NaN is above everything and stays
-        uint32_t top = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
-        const uint32_t lanes = 0xFu << (threadIdx.x & 28);
-        top = max(top, __shfl_xor_sync(lanes, top, 1));
-        top = max(top, __shfl_xor_sync(lanes, top, 2));
-        const int64_t base = row0[t];
-        if (base < 0) return;
-        const float d = __fdiv_rn(__uint_as_float(top), 127.0f);
-        // a block that is zero, or not finite, has codes 0
-        const uint2 w = top < 0x7F800000u && d != 0.0f ? codes_of(x, d) : make_uint2(0u, 0u);
-        const int64_t row = base + (int64_t)h * a.page_size;
-        *reinterpret_cast<uint2 *>((is_v ? a.v_codes : a.k_codes) + row * a.D + 8 * c) = w;
-        if ((c & 3) == 0) (is_v ? a.v_scales : a.k_scales)[row * (a.D / 32) + (c >> 2)] = d;
     };
-
-    Eight<T, WIDE> x[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) load(threadIdx.x + k * kThreads, x[k]);
+    load(row);
+    // four cosines a word; where eight neighbouring pairs go to a thread, in the order that it reads
+    const bool words = a.interleaved ? a.pairs % 4 == 0 : a.pairs % 8 == 0;
+    const bool halves = words && !a.interleaved;
     for (int i = threadIdx.x; i < nt; i += kThreads) {
         row0[i] = slot_row(a.slots[t0 + i], a.pages, a.page_size, a.heads);
         if (row0[i] == -2) record_status(a.status, RFP2_EBADID);
@@ -185,15 +197,73 @@ __global__ void __launch_bounds__(kThreads, 3) kv_write_kernel(const WriteArgs a
     for (int i = threadIdx.x; i < nt * a.pairs; i += kThreads) {
         const int t = a.by_pairs(i), p = i - t * a.pairs;
         const float2 cs = rotary_cos_sin(a.positions[t0 + t], turn_fraction(a.inv_freq[p]));
-        table[i] = make_float2(cs.x * a.factor, cs.y * a.factor);
+        float *at = table + 2 * t * a.pairs + (halves ? table_place<8>(p, a.pairs) : p);
+        at[0] = cs.x * a.factor;
+        at[a.pairs] = cs.y * a.factor;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kAhead * kThreads) {
+    if (!mine) return;
+
+    // the eight keys of this thread's place in token t's row, turned
+    const auto turn = [&](int t, float (&u)[8]) {
+        const float *cs = table + 2 * t * a.pairs;
+        if (halves) {
+            // the eight lie in one half; their partners, in the other, have just been read nearby
+            const bool low = 8 * c < a.pairs;
+            const int p = c - (low ? 0 : a.pairs >> 3);
+            Eight<T, WIDE> z;
+            z.load(k + t * a.kt + (low ? a.pairs : -a.pairs));
+            const float sign = low ? -1.0f : 1.0f;
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) write(i + k * kThreads, x[k]);
-        if (i + kAhead * kThreads < n)
+            for (int w = 0; w < 2; ++w) {
+                const float *q = cs + (w * (a.pairs >> 3) + p) * 4;
+                const float4 co = *reinterpret_cast<const float4 *>(q);
+                const float4 si = *reinterpret_cast<const float4 *>(q + a.pairs);
+                const float cc[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) load(i + (kAhead + k) * kThreads, x[k]);
+                for (int e = 0; e < 4; ++e)
+                    u[4 * w + e] = u[4 * w + e] * cc[e] + sign * ss[e] * to_f32(z.v[4 * w + e]);
+            }
+        } else if (words) {
+            const float4 co = *reinterpret_cast<const float4 *>(cs + 4 * c);
+            const float4 si = *reinterpret_cast<const float4 *>(cs + a.pairs + 4 * c);
+            const float cc[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float p = u[2 * e], q = u[2 * e + 1];
+                u[2 * e] = p * cc[e] - q * ss[e];
+                u[2 * e + 1] = q * cc[e] + p * ss[e];
+            }
+        } else {
+            // pairs that lie anyhow: each value with its partner, from memory
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int j = 8 * c + e;
+                if (j >= 2 * a.pairs) continue;
+                const bool first = a.interleaved ? j % 2 == 0 : j < a.pairs;
+                const int p = a.interleaved ? j / 2 : first ? j : j - a.pairs;
+                const int away = a.interleaved ? (first ? 1 : -1) : (first ? a.pairs : -a.pairs);
+                const float other = to_f32(k[t * a.kt + e + away]);
+                u[e] = u[e] * cs[p] + (first ? -cs[a.pairs + p] : cs[a.pairs + p]) * other;
+            }
+        }
+    };
+    for (int t = row; t < nt; t += AHEAD * a.deal.rows) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int at = t + i * a.deal.rows;
+            if (at >= nt || row0[at] < 0) continue;
+            const int64_t to = row0[at] + (int64_t)h * a.page_size;
+            float u[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[e] = to_f32(x[i].v[e]);
+            if (8 * c < 2 * a.pairs) turn(at, u);
+            write_block(u, to, c, a.D, a.k_codes, a.k_scales);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[e] = to_f32(y[i].v[e]);
+            write_block(u, to, c, a.D, a.v_codes, a.v_scales);
+        }
+        load(t + AHEAD * a.deal.rows);
     }
 }
 
@@ -203,79 +273,76 @@ struct ReadArgs {
     const int64_t *slots;
     int64_t T, pages, page_size;
     void *k, *v;
-    int heads, D, tokens;
-    FastDiv by_token, by_chunks;
+    int heads, D;
+    Deal deal;
     int32_t *status;
 };
 
-// A step is a 16-byte word of outputs.
+// E codes to a 16-byte word of outputs.
+template <typename T, int E>
+RFP2_DEV void read_word(const uint32_t (&w)[E / 4], float d, T *out) {
+    float x[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        // the code's byte above 2^23 + 128, exact, less as much
+        const uint32_t u = __byte_perm(w[e >> 2] ^ 0x80808080u, 0x4B000000u, 0x7440 + (e & 3));
+        x[e] = (__uint_as_float(u) - 8388736.0f) * d;
+    }
+    store_values<T, E>(out, x);
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) kv_read_kernel(const ReadArgs a) {
-    constexpr int E = 16 / sizeof(T);
+__global__ void __launch_bounds__(kThreads, 6) kv_read_kernel(const ReadArgs a) {
+    constexpr int E = 16 / sizeof(T), AHEAD = 2;
     extern __shared__ int64_t row0[];  // [tokens]
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
-    const int nt = (int)min((int64_t)a.tokens, a.T - t0);
+    const int64_t t0 = (int64_t)blockIdx.x * a.deal.tokens;
+    const int nt = (int)min((int64_t)a.deal.tokens, a.T - t0);
     for (int i = threadIdx.x; i < nt; i += kThreads) {
         row0[i] = slot_row(a.slots[t0 + i], a.pages, a.page_size, a.heads);
         if (row0[i] == -2) record_status(a.status, RFP2_EBADID);
     }
+    int row, h, c, step;
+    const bool mine = a.deal.mine(a.D / E, row, h, c, step);
     __syncthreads();
-    const int chunks = a.D / E, per_token = a.heads * chunks;
-    const int n = 2 * nt * per_token;
-    for (int i0 = threadIdx.x; i0 < n; i0 += kAhead * kThreads) {
-        uint32_t w[kAhead][E / 4];
-        float d[kAhead];
-        T *out[kAhead];
+    if (!mine) return;
+    T *k = static_cast<T *>(a.k), *v = static_cast<T *>(a.v);
+    for (int t = row; t < nt; t += AHEAD * a.deal.rows) {
+        uint32_t kw[AHEAD][E / 4], vw[AHEAD][E / 4];
+        float kd[AHEAD], vd[AHEAD];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int i = i0 + k * kThreads;
-            out[k] = nullptr;
-            if (i >= n) continue;
-            const int token2 = a.by_token(i), rest = i - token2 * per_token, t = token2 >> 1;
-            T *to = static_cast<T *>(token2 & 1 ? a.v : a.k);
-            if (!to) continue;
-            out[k] = to + ((t0 + t) * per_token + rest) * E;
-            const int h = a.by_chunks(rest), c = rest - h * chunks;
-            const int64_t base = row0[t];
+        for (int i = 0; i < AHEAD; ++i) {
+            const int at = t + i * a.deal.rows;
+            const int64_t base = at < nt ? row0[at] : -1;
 #pragma unroll
-            for (int e = 0; e < E / 4; ++e) w[k][e] = 0u;
-            d[k] = base == -1 ? 0.0f : CUDART_NAN_F;
+            for (int e = 0; e < E / 4; ++e) kw[i][e] = vw[i][e] = 0u;
+            kd[i] = vd[i] = base == -1 ? 0.0f : CUDART_NAN_F;
             if (base >= 0) {
-                const int64_t row = base + (int64_t)h * a.page_size;
-                const int8_t *from = (token2 & 1 ? a.v_codes : a.k_codes) + row * a.D + E * c;
+                const int64_t from = base + (int64_t)h * a.page_size;
+                const uint32_t *ks = reinterpret_cast<const uint32_t *>(a.k_codes + from * a.D + E * c);
+                const uint32_t *vs = reinterpret_cast<const uint32_t *>(a.v_codes + from * a.D + E * c);
                 if constexpr (E == 8) {
-                    const uint2 u = *reinterpret_cast<const uint2 *>(from);
-                    w[k][0] = u.x;
-                    w[k][1] = u.y;
+                    const uint2 p = *reinterpret_cast<const uint2 *>(ks), q = *reinterpret_cast<const uint2 *>(vs);
+                    kw[i][0] = p.x, kw[i][1] = p.y;
+                    vw[i][0] = q.x, vw[i][1] = q.y;
                 } else {
-                    w[k][0] = *reinterpret_cast<const uint32_t *>(from);
+                    kw[i][0] = *ks;
+                    vw[i][0] = *vs;
                 }
-                d[k] = (token2 & 1 ? a.v_scales : a.k_scales)[row * (a.D / 32) + c / (32 / E)];
+                kd[i] = a.k_scales[from * (a.D / 32) + c / (32 / E)];
+                vd[i] = a.v_scales[from * (a.D / 32) + c / (32 / E)];
             }
         }
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            if (!out[k]) continue;
-            float x[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                // the code's byte above 2^23 + 128, exact, less as much
-                const uint32_t u = __byte_perm(w[k][e >> 2] ^ 0x80808080u, 0x4B000000u, 0x7440 + (e & 3));
-                x[e] = (__uint_as_float(u) - 8388736.0f) * d[k];
-            }
-            store_values<T, E>(out[k], x);
+        for (int i = 0; i < AHEAD; ++i) {
+            const int at = t + i * a.deal.rows;
+            if (at >= nt) continue;
+            const int64_t to = ((t0 + at) * a.deal.steps + step) * E;
+            if (k) read_word<T, E>(kw[i], kd[i], k + to);
+            if (v) read_word<T, E>(vw[i], vd[i], v + to);
         }
     }
-}
-
-// Tokens of a CTA: enough for kAhead steps a thread, but a few CTAs for every
-// SM before that, and no more table than `most`.
-int tokens_a_cta(int64_t T, int64_t steps_a_token, int64_t most) {
-    const int64_t by_work = std::max<int64_t>(1, kAhead * kThreads / steps_a_token);
-    const int64_t by_sms = std::max<int64_t>(1, T / (6 * (int64_t)sm_count(current_device())));
-    return (int)std::max<int64_t>(1, std::min({by_work, by_sms, most}));
 }
 
 rfp2_status check_cache(const void *k_codes, const void *k_scales, const void *v_codes,
@@ -343,19 +410,16 @@ extern "C" rfp2_status rfp2_kv_write(const void *k, const void *v, int dtype, in
     a.heads = (int)heads;
     a.D = (int)D;
     a.pairs = positions ? (int)(R / 2) : 0;
-    const int64_t chunks = D / 8;
-    a.tokens = tokens_a_cta(T, 2 * heads * chunks, 4096 / std::max(1, a.pairs));
     a.by_pairs = FastDiv(std::max(1, a.pairs));
-    a.by_token = FastDiv((uint32_t)(heads * chunks));
-    a.by_chunks = FastDiv((uint32_t)chunks);
+    a.deal = deal(T, heads, D / 8, 4 / size, kMaxTable / std::max(1, a.pairs));
     a.interleaved = (flags & RFP2_ROPE_INTERLEAVED) != 0;
     a.factor = factor;
     a.status = dev_status;
     const int64_t V = 16 / size;
     const bool wide = aligned(k, 16) && aligned(v, 16) && a.kt % V == 0 && a.kh % V == 0 &&
                       a.vt % V == 0 && a.vh % V == 0;
-    const dim3 grid((unsigned)((T + a.tokens - 1) / a.tokens));
-    const size_t smem = (size_t)a.tokens * (8 + 8 * (size_t)a.pairs);
+    const dim3 grid = grid_of(a.deal, T);
+    const size_t smem = (size_t)a.deal.tokens * (8 + 8 * (size_t)a.pairs);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return from_cuda(dtype == RFP2_F32    ? launch_write<float>(a, wide, grid, smem, s)
                      : dtype == RFP2_BF16 ? launch_write<__nv_bfloat16>(a, wide, grid, smem, s)
@@ -388,14 +452,11 @@ extern "C" rfp2_status rfp2_kv_read(const int8_t *k_codes, const float *k_scales
     a.v = v;
     a.heads = (int)heads;
     a.D = (int)D;
-    const int64_t chunks = D / (16 / dtype_bytes(dtype));
-    a.tokens = tokens_a_cta(T, 2 * heads * chunks, 1024);
-    a.by_token = FastDiv((uint32_t)(heads * chunks));
-    a.by_chunks = FastDiv((uint32_t)chunks);
     a.status = dev_status;
-    const dim3 grid((unsigned)((T + a.tokens - 1) / a.tokens));
+    a.deal = deal(T, heads, D * dtype_bytes(dtype) / 16, 2, 1024);
+    const dim3 grid = grid_of(a.deal, T);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const size_t smem = 8 * (size_t)a.tokens;
+    const size_t smem = 8 * (size_t)a.deal.tokens;
     return from_cuda(
         dtype == RFP2_F32    ? launch(kv_read_kernel<float>, grid, dim3(kThreads), smem, s, true, a)
         : dtype == RFP2_BF16 ? launch(kv_read_kernel<__nv_bfloat16>, grid, dim3(kThreads), smem, s, true, a)

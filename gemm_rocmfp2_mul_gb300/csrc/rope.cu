@@ -48,14 +48,6 @@ struct alignas(V * sizeof(T)) Runs {
     }
 };
 
-// The place of pair p in the table of V's layout: 16-byte words of four pairs,
-// those of a thread's first four before those of its second, so that
-// neighbouring threads read neighbouring words.
-template <int V>
-RFP2_DEV int table_place(int p, int pairs) {
-    return V == 8 ? ((p >> 2 & 1) * (pairs >> 3) + (p >> 3)) * 4 + (p & 3) : p;
-}
-
 template <typename T, int V, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a) {
     extern __shared__ __align__(16) float table[];  // [tokens][cos, sin][pairs]
