@@ -117,6 +117,26 @@ struct FastDiv {
     RFP2_DEV uint32_t operator()(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
 };
 
+// The cosines and sines of tokens [0, n) of a CTA into shared memory: table
+// [n][cos, sin][pairs], times factor and sine_factor; pair p at table_place<V>.
+// A thread stays with its pairs, so their fractions are found once.
+template <int V, int THREADS>
+RFP2_DEV void rotary_table(float *table, const int32_t *positions, const float *inv_freq, int n,
+                           int pairs, const FastDiv &by_pairs, float factor, float sine_factor) {
+    const int row = pairs < THREADS ? (int)by_pairs(threadIdx.x) : 0;
+    const int rows = pairs < THREADS ? (int)by_pairs(THREADS) : 1;
+    if (row >= rows) return;
+    for (int p = threadIdx.x - row * pairs; p < pairs; p += THREADS) {
+        const uint64_t fraction = turn_fraction(inv_freq[p]);
+        float *at = table + table_place<V>(p, pairs);
+        for (int t = row; t < n; t += rows) {
+            const float2 cs = rotary_cos_sin(positions[t], fraction);
+            at[2 * t * pairs] = cs.x * factor;
+            at[(2 * t + 1) * pairs] = cs.y * sine_factor;
+        }
+    }
+}
+
 // Host: bytes of one value, 0 for an unknown type.
 inline int dtype_bytes(int dtype) {
     return dtype == RFP2_F32 ? 4 : dtype == RFP2_BF16 || dtype == RFP2_F16 ? 2 : 0;

@@ -66,14 +66,14 @@ struct WriteArgs {
     int32_t *status;
 };
 
-// Row of the cache arrays (of D codes, D / 32 scales) at which a slot's head 0
-// lies; the next head is page_size rows on.  -1: left out, -2: no such slot.
-RFP2_DEV int64_t slot_row(int64_t slot, int64_t pages, int64_t page_size, int heads) {
+// Place in the codes (a 32nd of that in the scales) of a slot's head 0; the next
+// head is page_size * D on.  -1: left out, -2: no such slot.
+RFP2_DEV int64_t slot_place(int64_t slot, int64_t pages, int64_t page_size, int heads, int D) {
     if (slot == -1) return -1;
     if (slot < 0 || slot >= pages * page_size) return -2;
     const int64_t page = (slot | page_size) >> 32 ? slot / page_size
                                                   : (int64_t)((uint32_t)slot / (uint32_t)page_size);
-    return page * heads * page_size + (slot - page * page_size);
+    return (page * heads * page_size + (slot - page * page_size)) * D;
 }
 
 // Eight values as they lie in memory.  WIDE: rows of 16-byte words; else any
@@ -99,20 +99,15 @@ RFP2_DEV float max_abs(float a, float b, float c) {  // of |a|, |b|, |c|; a NaN 
     return y;
 }
 
-// Codes of a block whose scale is zero, not finite, or so small that a
-// reciprocal or a product of it leaves fp32's range.
-__device__ __noinline__ uint2 codes_of_odd(const float (&x)[8], float d) {
-    uint2 w = make_uint2(0u, 0u);
-    if (!(d > 0.0f && d <= 3.402823466e38f)) return w;
-#pragma unroll 1
-    for (int e = 0; e < 8; ++e) {
-        const int q = (int)fminf(fmaxf(roundf(__fdiv_rn(x[e], d)), -127.0f), 127.0f);
-        (e < 4 ? w.x : w.y) |= (uint32_t)(q & 255) << (8 * (e & 3));
-    }
-    return w;
+// round-half-away(fl(x / d)) by the division, as a byte; 0 where the block is
+// zero or not finite.  For scales so small that a reciprocal or a product of
+// them leaves fp32's range.
+__device__ __noinline__ uint32_t code_of_odd(float x, float d) {
+    if (!(d > 0.0f && d <= 3.402823466e38f)) return 0u;
+    return (uint32_t)(int)fminf(fmaxf(roundf(__fdiv_rn(x, d)), -127.0f), 127.0f) & 255u;
 }
 
-// round-half-away(fl(x / d)) for eight values and 2^-100 <= d < inf, as bytes of
+// round-half-away(fl(x / d)) for eight values and 2^-90 <= d < inf, as bytes of
 // two words, without a division.
 //
 // 1/d to 2^-22 and a little more either way brackets x / d and its rounded
@@ -139,7 +134,9 @@ RFP2_DEV uint2 codes_of(const float (&x)[8], float d) {
         const float scaled = d * 0x1p-24f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float far = fmaf(x[e], more, kMagic), H = fabsf(__uint_as_float(q[e]) - kMagic) + 0.5f;
+            const float far = fmaf(x[e], more, kMagic);
+            if (q[e] == __float_as_uint(far)) continue;
+            const float H = fabsf(__uint_as_float(q[e]) - kMagic) + 0.5f;
             const float below = __uint_as_float((__float_as_uint(H) - 1u) & 0x7F800000u);
             const bool up = fmaf(-H, d, fabsf(x[e])) > -below * scaled;
             q[e] = up ? __float_as_uint(far) : q[e];
@@ -151,16 +148,31 @@ RFP2_DEV uint2 codes_of(const float (&x)[8], float d) {
     return w;
 }
 
-// Eight values of a block, in four neighbouring lanes, to the cache.
-RFP2_DEV void write_block(const float (&x)[8], int64_t row, int c, int D, int8_t *codes, float *scales) {
+// Eight values of a block, in four neighbouring lanes, to the cache's codes;
+// the block's scale at the place that goes with them.
+RFP2_DEV void write_block(const float (&x)[8], int8_t *codes, float *scale, bool first) {
     float top = max_abs(max_abs(x[0], x[1], x[2]), max_abs(x[3], x[4], x[5]), max_abs(x[6], x[7], x[7]));
     const uint32_t lanes = 0xFu << (threadIdx.x & 28);
     top = max_abs(top, __shfl_xor_sync(lanes, top, 1), top);
     top = max_abs(top, __shfl_xor_sync(lanes, top, 2), top);
-    const float d = __fdiv_rn(top, 127.0f);
-    const uint2 w = d >= 0x1p-100f && d <= 3.402823466e38f ? codes_of(x, d) : codes_of_odd(x, d);
-    *reinterpret_cast<uint2 *>(codes + row * D + 8 * c) = w;
-    if ((c & 3) == 0) scales[row * (D / 32) + (c >> 2)] = d;
+    // top / 127 rounded to nearest: the rounded product with 1/127, corrected by its exact remainder
+    // (Markstein 1990; checked for every significand).  Away from the ends of fp32's range.
+    constexpr float kOver127 = 1.0f / 127.0f;
+    const float near_d = top * kOver127;
+    float d = fmaf(fmaf(-near_d, 127.0f, top), kOver127, near_d);
+    uint2 w = make_uint2(0u, 0u);
+    if (d >= 0x1p-90f && d <= 3.402823466e38f) {
+        w = codes_of(x, d);
+    } else {
+        d = __fdiv_rn(top, 127.0f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            w.x |= code_of_odd(x[e], d) << (8 * e);
+            w.y |= code_of_odd(x[4 + e], d) << (8 * e);
+        }
+    }
+    *reinterpret_cast<uint2 *>(codes) = w;
+    if (first) *scale = d;
 }
 
 template <typename T, bool WIDE>
@@ -168,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv_write_kernel(const WriteArgs a
     constexpr int AHEAD = 4 / sizeof(T);
     extern __shared__ __align__(16) uint8_t smem[];
     float *table = reinterpret_cast<float *>(smem);                                       // [tokens][cos, sin][pairs]
-    int64_t *row0 = reinterpret_cast<int64_t *>(smem + 8 * a.deal.tokens * a.pairs);      // [tokens]
+    int64_t *place = reinterpret_cast<int64_t *>(smem + 8 * a.deal.tokens * a.pairs);      // [tokens]
     pdl_wait();
     pdl_launch_dependents();
     const int64_t t0 = (int64_t)blockIdx.x * a.deal.tokens;
@@ -191,15 +203,14 @@ __global__ void __launch_bounds__(kThreads, 4) kv_write_kernel(const WriteArgs a
     const bool words = a.interleaved ? a.pairs % 4 == 0 : a.pairs % 8 == 0;
     const bool halves = words && !a.interleaved;
     for (int i = threadIdx.x; i < nt; i += kThreads) {
-        row0[i] = slot_row(a.slots[t0 + i], a.pages, a.page_size, a.heads);
-        if (row0[i] == -2) record_status(a.status, RFP2_EBADID);
+        place[i] = slot_place(a.slots[t0 + i], a.pages, a.page_size, a.heads, a.D);
+        if (place[i] == -2) record_status(a.status, RFP2_EBADID);
     }
-    for (int i = threadIdx.x; i < nt * a.pairs; i += kThreads) {
-        const int t = a.by_pairs(i), p = i - t * a.pairs;
-        const float2 cs = rotary_cos_sin(a.positions[t0 + t], turn_fraction(a.inv_freq[p]));
-        float *at = table + 2 * t * a.pairs + (halves ? table_place<8>(p, a.pairs) : p);
-        at[0] = cs.x * a.factor;
-        at[a.pairs] = cs.y * a.factor;
+    if (a.pairs) {
+        if (halves)
+            rotary_table<8, kThreads>(table, a.positions + t0, a.inv_freq, nt, a.pairs, a.by_pairs, a.factor, a.factor);
+        else
+            rotary_table<1, kThreads>(table, a.positions + t0, a.inv_freq, nt, a.pairs, a.by_pairs, a.factor, a.factor);
     }
     __syncthreads();
     if (!mine) return;
@@ -248,20 +259,21 @@ __global__ void __launch_bounds__(kThreads, 4) kv_write_kernel(const WriteArgs a
             }
         }
     };
+    const int64_t own = (int64_t)h * a.page_size * a.D + 8 * c;
     for (int t = row; t < nt; t += AHEAD * a.deal.rows) {
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             const int at = t + i * a.deal.rows;
-            if (at >= nt || row0[at] < 0) continue;
-            const int64_t to = row0[at] + (int64_t)h * a.page_size;
+            if (at >= nt || place[at] < 0) continue;
+            const int64_t to = place[at] + own;
             float u[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) u[e] = to_f32(x[i].v[e]);
             if (8 * c < 2 * a.pairs) turn(at, u);
-            write_block(u, to, c, a.D, a.k_codes, a.k_scales);
+            write_block(u, a.k_codes + to, a.k_scales + (to >> 5), (c & 3) == 0);
 #pragma unroll
             for (int e = 0; e < 8; ++e) u[e] = to_f32(y[i].v[e]);
-            write_block(u, to, c, a.D, a.v_codes, a.v_scales);
+            write_block(u, a.v_codes + to, a.v_scales + (to >> 5), (c & 3) == 0);
         }
         load(t + AHEAD * a.deal.rows);
     }
@@ -294,34 +306,35 @@ RFP2_DEV void read_word(const uint32_t (&w)[E / 4], float d, T *out) {
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 6) kv_read_kernel(const ReadArgs a) {
     constexpr int E = 16 / sizeof(T), AHEAD = 2;
-    extern __shared__ int64_t row0[];  // [tokens]
+    extern __shared__ int64_t place[];  // [tokens]
     pdl_wait();
     pdl_launch_dependents();
     const int64_t t0 = (int64_t)blockIdx.x * a.deal.tokens;
     const int nt = (int)min((int64_t)a.deal.tokens, a.T - t0);
     for (int i = threadIdx.x; i < nt; i += kThreads) {
-        row0[i] = slot_row(a.slots[t0 + i], a.pages, a.page_size, a.heads);
-        if (row0[i] == -2) record_status(a.status, RFP2_EBADID);
+        place[i] = slot_place(a.slots[t0 + i], a.pages, a.page_size, a.heads, a.D);
+        if (place[i] == -2) record_status(a.status, RFP2_EBADID);
     }
     int row, h, c, step;
     const bool mine = a.deal.mine(a.D / E, row, h, c, step);
     __syncthreads();
     if (!mine) return;
     T *k = static_cast<T *>(a.k), *v = static_cast<T *>(a.v);
+    const int64_t own = (int64_t)h * a.page_size * a.D + E * c;
     for (int t = row; t < nt; t += AHEAD * a.deal.rows) {
         uint32_t kw[AHEAD][E / 4], vw[AHEAD][E / 4];
         float kd[AHEAD], vd[AHEAD];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             const int at = t + i * a.deal.rows;
-            const int64_t base = at < nt ? row0[at] : -1;
+            const int64_t base = at < nt ? place[at] : -1;
 #pragma unroll
             for (int e = 0; e < E / 4; ++e) kw[i][e] = vw[i][e] = 0u;
             kd[i] = vd[i] = base == -1 ? 0.0f : CUDART_NAN_F;
             if (base >= 0) {
-                const int64_t from = base + (int64_t)h * a.page_size;
-                const uint32_t *ks = reinterpret_cast<const uint32_t *>(a.k_codes + from * a.D + E * c);
-                const uint32_t *vs = reinterpret_cast<const uint32_t *>(a.v_codes + from * a.D + E * c);
+                const int64_t from = base + own;
+                const uint32_t *ks = reinterpret_cast<const uint32_t *>(a.k_codes + from);
+                const uint32_t *vs = reinterpret_cast<const uint32_t *>(a.v_codes + from);
                 if constexpr (E == 8) {
                     const uint2 p = *reinterpret_cast<const uint2 *>(ks), q = *reinterpret_cast<const uint2 *>(vs);
                     kw[i][0] = p.x, kw[i][1] = p.y;
@@ -330,8 +343,8 @@ __global__ void __launch_bounds__(kThreads, 6) kv_read_kernel(const ReadArgs a) 
                     kw[i][0] = *ks;
                     vw[i][0] = *vs;
                 }
-                kd[i] = a.k_scales[from * (a.D / 32) + c / (32 / E)];
-                vd[i] = a.v_scales[from * (a.D / 32) + c / (32 / E)];
+                kd[i] = a.k_scales[from >> 5];
+                vd[i] = a.v_scales[from >> 5];
             }
         }
 #pragma unroll
@@ -411,7 +424,7 @@ extern "C" rfp2_status rfp2_kv_write(const void *k, const void *v, int dtype, in
     a.D = (int)D;
     a.pairs = positions ? (int)(R / 2) : 0;
     a.by_pairs = FastDiv(std::max(1, a.pairs));
-    a.deal = deal(T, heads, D / 8, 4 / size, kMaxTable / std::max(1, a.pairs));
+    a.deal = deal(T, heads, D / 8, 16 / size, kMaxTable / std::max(1, a.pairs));
     a.interleaved = (flags & RFP2_ROPE_INTERLEAVED) != 0;
     a.factor = factor;
     a.status = dev_status;

@@ -115,13 +115,8 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a) {
     Runs<T, V> x[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) load(threadIdx.x + k * kThreads, x[k]);
-    for (int i = threadIdx.x; i < nt * a.pairs; i += kThreads) {
-        const int t = a.by_pairs(i), p = i - t * a.pairs;
-        const float2 cs = rotary_cos_sin(a.positions[t0 + t], turn_fraction(a.inv_freq[p]));
-        float *at = table + 2 * t * a.pairs + table_place<V>(p, a.pairs);
-        at[0] = cs.x * a.factor;
-        at[a.pairs] = cs.y * (a.inverse ? -a.factor : a.factor);
-    }
+    rotary_table<V, kThreads>(table, a.positions + t0, a.inv_freq, nt, a.pairs, a.by_pairs, a.factor,
+                              a.inverse ? -a.factor : a.factor);
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += kAhead * kThreads) {
 #pragma unroll
