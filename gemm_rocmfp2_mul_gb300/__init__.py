@@ -7,13 +7,15 @@ torch when the caller does not pass them, passes raw device pointers and the
 current torch stream to the library, and raises :class:`RFP2Error` on a
 non-zero status.  All arithmetic runs in the library's CUDA kernels; there is
 no CPU or PyTorch fallback: if the library is not built or cannot be loaded,
-every call raises.
+every call raises.  Most calls go through ctypes; those of the attention
+operators, small and many, through a compiled binding.
 
 Build the library with :func:`build` (nvcc, sm_103a).
 """
 from __future__ import annotations
 
 import ctypes as C
+import importlib.util
 import os
 import threading
 from typing import Any, NamedTuple
@@ -453,10 +455,13 @@ def rfp2_debug_wait_timeout(dev_status):
 
 
 # -- attention between the products -----------------------------------------------------
+#
+# A decode step makes these calls for every layer, each a few microseconds on the GPU; their
+# arguments are checked and read by _rfp2_binding (csrc/binding.cpp), in less time than that.
 
 _ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3}
 _ROPE_INTERLEAVED, _ROPE_INVERSE = 1, 2
-_dtype_codes = None
+_native = None
 
 
 class KVCache(NamedTuple):
@@ -468,44 +473,20 @@ class KVCache(NamedTuple):
     v_scales: Any
 
 
-def _dtype_code(t, name):
-    """The library's code of an activation tensor's type (fp32, bf16 or f16)."""
-    global _dtype_codes
-    if _dtype_codes is None:
-        torch = _torch()
-        _dtype_codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-    try:
-        return _dtype_codes[t.dtype]
-    except KeyError:
-        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}") from None
-
-
-def _rows(t, dims, name):
-    """A CUDA tensor of `dims` dimensions whose last one is contiguous: its shape and strides."""
-    if not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    shape, stride = t.shape, t.stride()
-    if len(shape) != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, got {len(shape)}")
-    if stride[-1] != 1 and shape[-1] > 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
-    return shape, stride
-
-
-def _cache_sizes(cache):
-    torch = _torch()
-    kc, ks, vc, vs = cache
-    for t, dtype, name in ((kc, torch.int8, "k_codes"), (vc, torch.int8, "v_codes"),
-                           (ks, torch.float32, "k_scales"), (vs, torch.float32, "v_scales")):
-        _need(t, dtype, name)
-    shape = kc.shape
-    if len(shape) != 4:
-        raise ValueError("k_codes must be [pages, heads, page_size, D]")
-    scales = (shape[0], shape[1], shape[2], shape[3] // 32)
-    if vc.shape != shape or ks.shape != scales or vs.shape != scales:
-        raise ValueError("the cache's codes must be [pages, heads, page_size, D], its scales "
-                         "[pages, heads, page_size, D/32]")
-    return shape
+def _binding():
+    """The loaded binding module (raises if it is not built)."""
+    global _native
+    if _native is None:
+        _torch()
+        lib()
+        from . import buildlib as _b
+        if not os.path.exists(_b.BINDING):
+            raise RuntimeError(f"the binding is not built ({_b.BINDING}); run gemm_rocmfp2_mul_gb300.build()")
+        spec = importlib.util.spec_from_file_location("_rfp2_binding", _b.BINDING)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _native = module
+    return _native
 
 
 def rfp2_rope_frequencies(R, base=10000.0, scaling="plain", stretch=1.0, trained=4096.0, fast=32.0,
@@ -525,22 +506,13 @@ def rfp2_rope(x, positions, inv_freq, out=None, interleaved=False, inverse=False
     """Rotary positions: x [T, H, D] (any token and head strides) with the first 2*len(inv_freq)
     values of each head rotated by positions int32 [T]; out=x rotates in place.  inverse=True
     negates the angles (the gradient)."""
-    torch = _torch()
-    (T, H, D), xs = _rows(x, 3, "x")
-    code = _dtype_code(x, "x")
-    _need(positions, torch.int32, "positions")
-    _need(inv_freq, torch.float32, "inv_freq")
-    if positions.numel() != T:
-        raise ValueError("positions needs one value per token")
     if out is None:
-        out = _empty((T, H, D), x.dtype, x)
-    shape, os_ = _rows(out, 3, "out")
-    if shape != x.shape or out.dtype != x.dtype:
-        raise ValueError("out must have x's shape and type")
-    _check(lib().rfp2_rope(x.data_ptr(), code, T, H, D, xs[0], xs[1], positions.data_ptr(),
-                           inv_freq.data_ptr(), 2 * inv_freq.numel(), factor,
-                           (_ROPE_INTERLEAVED if interleaved else 0) | (_ROPE_INVERSE if inverse else 0),
-                           out.data_ptr(), os_[0], os_[1], _stream()), "rfp2_rope")
+        out = _empty(x.shape, x.dtype, x)
+    rc = (_native or _binding()).rope(
+        x, positions, inv_freq, out,
+        (_ROPE_INTERLEAVED if interleaved else 0) | (_ROPE_INVERSE if inverse else 0), factor)
+    if rc:
+        raise RFP2Error(rc, "rfp2_rope")
     return out
 
 
@@ -555,52 +527,25 @@ def rfp2_kv_write(cache, k, v, slots, positions=None, inv_freq=None, interleaved
                   dev_status=None):
     """Quantise k, v [T, heads, D] into the cache at slots int64 [T] (page * page_size + offset;
     -1 leaves a token out).  With positions and inv_freq, k is rotated on the way in."""
-    torch = _torch()
-    pages, heads, page_size, D = _cache_sizes(cache)
-    shape, ks = _rows(k, 3, "k")
-    vshape, vs = _rows(v, 3, "v")
-    code = _dtype_code(k, "k")
-    T = shape[0]
-    if shape[1] != heads or shape[2] != D or vshape != shape or v.dtype != k.dtype:
-        raise ValueError("k and v must be [T, heads, D] of one type, as the cache has them")
-    _need(slots, torch.int64, "slots")
-    if slots.numel() != T:
-        raise ValueError("slots needs one value per token")
-    R = 0
-    if positions is not None:
-        _need(positions, torch.int32, "positions")
-        if positions.numel() != T:
-            raise ValueError("positions needs one value per token")
-        positions = positions.data_ptr()
-    if inv_freq is not None:
-        _need(inv_freq, torch.float32, "inv_freq")
-        R = 2 * inv_freq.numel()
-        inv_freq = inv_freq.data_ptr()
-    _check(lib().rfp2_kv_write(k.data_ptr(), v.data_ptr(), code, T, ks[0], ks[1], vs[0], vs[1],
-                               slots.data_ptr(), positions, inv_freq, R, factor,
-                               _ROPE_INTERLEAVED if interleaved else 0,
-                               cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(),
-                               cache[3].data_ptr(), pages, heads, page_size, D, _ptr(dev_status),
-                               _stream()), "rfp2_kv_write")
+    rc = (_native or _binding()).kv_write(cache, k, v, slots, positions, inv_freq,
+                                          _ROPE_INTERLEAVED if interleaved else 0, factor, dev_status)
+    if rc:
+        raise RFP2Error(rc, "rfp2_kv_write")
 
 
 def rfp2_kv_read(cache, slots, dtype=None, k=None, v=None, dev_status=None):
     """The values at slots int64 [T]: (k, v), each [T, heads, D] of `dtype` (fp32 unless given;
     or the type of the k and v passed to be filled).  A slot of -1 reads as zeros."""
-    torch = _torch()
-    pages, heads, page_size, D = _cache_sizes(cache)
-    _need(slots, torch.int64, "slots")
-    T = slots.numel()
-    like = next((t for t in (k, v) if t is not None), None)
-    dtype = dtype or (like.dtype if like is not None else torch.float32)
-    k = _empty((T, heads, D), dtype, slots) if k is None else _need(k, dtype, "k")
-    v = _empty((T, heads, D), dtype, slots) if v is None else _need(v, dtype, "v")
-    if k.shape != (T, heads, D) or v.shape != (T, heads, D):
-        raise ValueError("k and v must be [T, heads, D]")
-    _check(lib().rfp2_kv_read(cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(),
-                              cache[3].data_ptr(), pages, heads, page_size, D, slots.data_ptr(), T,
-                              _dtype_code(k, "k"), k.data_ptr(), v.data_ptr(), _ptr(dev_status),
-                              _stream()), "rfp2_kv_read")
+    if k is None or v is None:
+        torch = _torch()
+        like = k if k is not None else v
+        dtype = dtype or (like.dtype if like is not None else torch.float32)
+        shape = (slots.numel(), cache[0].shape[1], cache[0].shape[3])
+        k = _empty(shape, dtype, slots) if k is None else k
+        v = _empty(shape, dtype, slots) if v is None else v
+    rc = (_native or _binding()).kv_read(cache, slots, k, v, dev_status)
+    if rc:
+        raise RFP2Error(rc, "rfp2_kv_read")
     return k, v
 
 
@@ -624,33 +569,14 @@ def rfp2_attn_decode(q, cache, table, lens, scale=None, window=0, softcap=0.0, o
     [B, nq, Hq, D] of q's type and lse fp32 [B, nq, Hq].  scale: D**-0.5 unless given; window: only the
     last `window` keys (0: all); softcap: scores become softcap * tanh(s / softcap) (0: as they are).
     workspace: from rfp2_attn_decode_workspace (zero before its first use)."""
-    torch = _torch()
-    pages, heads, page_size, D = _cache_sizes(cache)
-    (B, nq, Hq, Dq), qs = _rows(q, 4, "q")
-    code = _dtype_code(q, "q")
-    _need(lens, torch.int32, "lens")
-    (Bt, width), ts = _rows(table, 2, "table")
-    if table.dtype != torch.int32:
-        raise TypeError(f"table must be {torch.int32}, got {table.dtype}")
-    if Dq != D or Bt != B or lens.numel() != B:
-        raise ValueError("q must be [B, nq, Hq, D] with the cache's D, table [B, width], lens [B]")
-    if out is None:
-        out = _empty((B, nq, Hq, D), q.dtype, q)
-    elif _need(out, q.dtype, "out").shape != q.shape:
-        raise ValueError("out must have q's shape")
-    if lse is None:
-        lse = _empty((B, nq, Hq), torch.float32, q)
-    elif _need(lse, torch.float32, "lse").shape != q.shape[:3]:
-        raise ValueError("lse must be [B, nq, Hq]")
-    if workspace is None:
-        workspace = rfp2_attn_decode_workspace(q, heads)
-    else:
-        _need(workspace, torch.uint8, "workspace")
-    _check(lib().rfp2_attn_decode(q.data_ptr(), code, B, nq, Hq, D, qs[0], qs[1], qs[2],
-                                  cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(),
-                                  cache[3].data_ptr(), pages, heads, page_size, table.data_ptr(), width,
-                                  ts[0] if B > 1 else max(ts[0], width), lens.data_ptr(),
-                                  D ** -0.5 if scale is None else scale, window, softcap,
-                                  out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-                                  workspace.numel(), _ptr(dev_status), _stream()), "rfp2_attn_decode")
+    if out is None or lse is None or workspace is None:
+        if q.dim() != 4:
+            raise ValueError(f"q must have 4 dimensions, got {q.dim()}")
+        out = _empty(q.shape, q.dtype, q) if out is None else out
+        lse = _empty(q.shape[:3], _torch().float32, q) if lse is None else lse
+        workspace = rfp2_attn_decode_workspace(q, cache[0].shape[1]) if workspace is None else workspace
+    rc = (_native or _binding()).attn_decode(q, cache, table, lens, scale, window, softcap, out, lse, workspace,
+                                             dev_status)
+    if rc:
+        raise RFP2Error(rc, "rfp2_attn_decode")
     return out, lse
