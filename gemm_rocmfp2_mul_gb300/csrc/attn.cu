@@ -81,12 +81,15 @@ extern "C" rfp2_status rfp2_attn_decode(const void *q, int dtype, int64_t B, int
     a.counters = static_cast<int *>(workspace);
     a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kAttnCounterBytes);
     a.status = dev_status;
+    constexpr int64_t kLine = (1ll << 31) - 1;
+    const int64_t line = (a.capacity / kAttnTile + 1 + kAttnGap) * a.heads * a.column_tiles;
+    if (line > kLine) return RFP2_ESHAPE;
     static const AttnFn kinds[] = {attn_d32,  attn_d64,  attn_d96,  attn_d128,
                                    attn_d160, attn_d192, attn_d224, attn_d256};
     const int sms = std::min(sm_count(current_device()), kAttnCounterBytes / 8);
-    // a launch keeps its sequences' lengths in shared memory
-    for (int64_t b0 = 0; b0 < B; b0 += kAttnMaxBatch) {
-        a.B = (int)std::min<int64_t>(B - b0, kAttnMaxBatch);
+    // a launch keeps its sequences' places on the line, 32-bit numbers, in shared memory
+    for (int64_t b0 = 0; b0 < B; b0 += a.B) {
+        a.B = (int)std::min<int64_t>({B - b0, kAttnMaxBatch, kLine / line});
         a.q = static_cast<const uint8_t *>(q) + b0 * q_batch_stride * size;
         a.table = table + b0 * table_stride;
         a.lens = lens + b0;

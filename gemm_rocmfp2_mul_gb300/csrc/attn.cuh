@@ -33,7 +33,7 @@ namespace rfp2 {
 constexpr int kAttnTile = 16;        // keys
 constexpr int kAttnGap = 2;          // a unit's fixed cost, in tiles
 constexpr int kAttnMinStretch = 1;   // of a warp, in tiles
-constexpr int kAttnMaxBatch = 512;   // sequences of one launch
+constexpr int kAttnMaxBatch = 1024;  // sequences of one launch
 constexpr int kAttnCounterBytes = 4096;
 
 struct AttnArgs {
@@ -76,7 +76,7 @@ struct AttnLayout {
 struct AttnPiece {
     int present, starts;  // starts: holds the unit's first tile
     int b, hk, ct;
-    int64_t unit0;        // the unit's place on the line
+    int unit0;            // the unit's place on the line
 };
 
 template <int NB, int NT>
@@ -87,7 +87,7 @@ constexpr int attn_ctas_per_sm() { return NB * NT <= 2 ? 2 : 1; }
 // line's prefix.
 template <int NB, int NT>
 constexpr int attn_small_bytes(int B) {
-    return 128 + 2 * attn_warps<NB, NT>() * ((int)sizeof(AttnPiece) + 2 * 8 * NT * 4) + (B + 1) * 8;
+    return 128 + 2 * attn_warps<NB, NT>() * ((int)sizeof(AttnPiece) + 2 * 8 * NT * 4) + (B + 1) * 4;
 }
 template <int NB, int NT>
 constexpr int attn_stages() {
@@ -184,21 +184,16 @@ RFP2_DEV void load_scales(const float *p, float (&d)[NB]) {
 // A place on the line: unit (b, hk, ct) of `tiles` tiles that begins (with its
 // gap) at `unit0`.
 struct AttnPlace {
-    int b, hk, ct, tiles;
-    int64_t unit0;
+    int b, hk, ct, tiles, unit0;
 };
-
-RFP2_DEV int64_t quotient(int64_t a, int64_t b) {  // a, b >= 0; 64-bit division is slow
-    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
-}
 
 // The line's share of each warp: `each` places, one more for the first `extra`.
 struct AttnShare {
-    int64_t each, extra;
-    RFP2_DEV int64_t begin(int64_t worker) const { return worker * each + min(worker, extra); }
-    RFP2_DEV int64_t worker_of(int64_t x) const {
-        const int64_t more = extra * (each + 1);
-        return x < more ? quotient(x, each + 1) : extra + quotient(x - more, each);
+    uint32_t each, extra;
+    RFP2_DEV int begin(uint32_t worker) const { return (int)(worker * each + min(worker, extra)); }
+    RFP2_DEV uint32_t worker_of(uint32_t x) const {
+        const uint32_t more = extra * (each + 1);
+        return x < more ? x / (each + 1) : extra + (x - more) / each;
     }
 };
 
@@ -216,11 +211,11 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
     constexpr float kSumScale = 2.3283064365386963e-10f, kSumShift = 32.0f;  // 2^-32
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *rings = smem;
-    int64_t *small = reinterpret_cast<int64_t *>(rings + WARPS * STAGES * L::stage_bytes);  // 16
-    AttnPiece *pieces = reinterpret_cast<AttnPiece *>(small + 16);  // [warps][head, tail]
-    float *piece_r = reinterpret_cast<float *>(pieces + 2 * WARPS);  // [pieces][COLS]
+    int *small = reinterpret_cast<int *>(rings + WARPS * STAGES * L::stage_bytes);  // 32
+    AttnPiece *pieces = reinterpret_cast<AttnPiece *>(small + 32);                  // [warps][head, tail]
+    float *piece_r = reinterpret_cast<float *>(pieces + 2 * WARPS);                 // [pieces][COLS]
     float *piece_l = piece_r + 2 * WARPS * COLS;
-    int64_t *prefix = reinterpret_cast<int64_t *>(piece_l + 2 * WARPS * COLS);  // [B + 1]
+    int *prefix = reinterpret_cast<int *>(piece_l + 2 * WARPS * COLS);  // [B + 1]
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
@@ -237,50 +232,58 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
         const int64_t low = (int64_t)len - a.nq + 1 - a.window;
         return low > 0 ? (int)(low / kAttnTile) : 0;
     };
-    {
-        int64_t run = 0;
+    const auto cost_of = [&](int b) {
+        const int len = length_of(b);
+        if (len < 0 && blockIdx.x == 0) record_status(a.status, RFP2_EBADID);
+        // a sequence without keys has one tile too: its rows are written
+        return kAttnGap + max(1, (len + kAttnTile - 1) / kAttnTile - tile_low(len));
+    };
+    if (lane < 2) pieces[2 * warp + lane].present = 0;
+    if (a.B <= 32) {
+        // every warp by itself
+        int incl = lane < a.B ? cost_of(lane) : 0;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += up;
+        }
+        if (lane < a.B) prefix[lane + 1] = incl;
+        if (lane == 0) prefix[0] = 0;
+        __syncwarp();
+    } else {
+        int run = 0;
         for (int b0 = 0; b0 < a.B; b0 += THREADS) {
             const int b = b0 + tid;
-            int cost = 0;
-            if (b < a.B) {
-                const int len = length_of(b);
-                if (len < 0 && blockIdx.x == 0) record_status(a.status, RFP2_EBADID);
-                // a sequence without keys has one tile too: its rows are written
-                cost = kAttnGap + max(1, (len + kAttnTile - 1) / kAttnTile - tile_low(len));
-            }
-            int64_t incl = cost;
+            int incl = b < a.B ? cost_of(b) : 0;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
-                const int64_t up = __shfl_up_sync(0xffffffffu, incl, off);
+                const int up = __shfl_up_sync(0xffffffffu, incl, off);
                 if (lane >= off) incl += up;
             }
             if (b0) __syncthreads();
             if (lane == 31) small[warp] = incl;
-            if (b0 == 0 && tid < 2 * WARPS) pieces[tid].present = 0;
             __syncthreads();
-            int64_t before = 0, all = 0;
-#pragma unroll
+            int before = 0, all = 0;
             for (int w = 0; w < WARPS; ++w) {
                 before += w < warp ? small[w] : 0;
                 all += small[w];
             }
-            if (b < a.B) prefix[b] = run + before + incl - cost;
+            if (b < a.B) prefix[b + 1] = run + before + incl;
             run += all;
         }
-        if (tid == 0) prefix[a.B] = run;
+        if (tid == 0) prefix[0] = 0;
         __syncthreads();
     }
     const int units_of = a.heads * a.column_tiles;
-    const int64_t total = prefix[a.B] * units_of;
+    const int total = prefix[a.B] * units_of;
     // some tiles for each warp: shorter stretches are not worth their joins
-    const int64_t parts = min((int64_t)gridDim.x,
-                              (total + kAttnMinStretch * WARPS - 1) / (kAttnMinStretch * WARPS));
-    if ((int64_t)blockIdx.x >= parts) return;
+    const int parts = min((int)gridDim.x, (total - 1) / (kAttnMinStretch * WARPS) + 1);
+    if ((int)blockIdx.x >= parts) return;
     AttnShare share;
-    share.each = quotient(total, parts * WARPS);
+    share.each = (uint32_t)total / (uint32_t)(parts * WARPS);
     share.extra = total - share.each * parts * WARPS;
-    const int64_t worker = (int64_t)blockIdx.x * WARPS + warp;
-    const int64_t y0 = share.begin(worker), y1 = share.begin(worker + 1);
+    const int worker = blockIdx.x * WARPS + warp;
+    const int y0 = share.begin(worker), y1 = share.begin(worker + 1);
 
     AttnPlace first;
     {
@@ -289,13 +292,12 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
             const int mid = (lo + hi) >> 1;
             if (prefix[mid] * units_of <= y0) lo = mid; else hi = mid;
         }
-        const int cost = (int)(prefix[lo + 1] - prefix[lo]);
-        const int64_t off = y0 - prefix[lo] * units_of;
-        const int unit = (int)quotient(off, cost);
+        const int cost = prefix[lo + 1] - prefix[lo];
+        const int unit = (uint32_t)(y0 - prefix[lo] * units_of) / (uint32_t)cost;
         first.b = lo;
         first.tiles = cost - kAttnGap;
-        first.unit0 = prefix[lo] * units_of + (int64_t)unit * cost;
-        first.hk = unit / a.column_tiles;
+        first.unit0 = prefix[lo] * units_of + unit * cost;
+        first.hk = a.column_tiles == 1 ? unit : unit / a.column_tiles;
         first.ct = unit - first.hk * a.column_tiles;
     }
     const auto next_unit = [&](AttnPlace &p) {
@@ -305,16 +307,16 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
             if (++p.hk == a.heads) {
                 p.hk = 0;
                 ++p.b;
-                p.tiles = p.b < a.B ? (int)(prefix[p.b + 1] - prefix[p.b]) - kAttnGap : 1;
+                p.tiles = p.b < a.B ? prefix[p.b + 1] - prefix[p.b] - kAttnGap : 1;
             }
         }
     };
     // this warp's tiles [from, to) of a unit
     const auto tiles_from = [&](const AttnPlace &p) {
-        return (int)max((int64_t)0, y0 - p.unit0 - kAttnGap);
+        return max(0, y0 - p.unit0 - kAttnGap);
     };
     const auto tiles_to = [&](const AttnPlace &p) {
-        return (int)max((int64_t)0, min((int64_t)p.tiles, y1 - p.unit0 - kAttnGap));
+        return max(0, min(p.tiles, y1 - p.unit0 - kAttnGap));
     };
 
     // ---- the loads, STAGES - 1 tiles ahead ----
@@ -862,7 +864,7 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
                 __syncwarp();
                 slot = reinterpret_cast<float *>(rings + warp * STAGES * L::stage_bytes);
             } else {
-                slot = a.partials + (2 * (int64_t)gridDim.x + worker) * SLOT;
+                slot = a.partials + (2 * gridDim.x + worker) * (int64_t)SLOT;
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -921,7 +923,7 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
         const int hw = head ? __ffs(head) - 1 : 0;
         if (head) {
             hv = *reinterpret_cast<const float4 *>(
-                a.partials + (2 * (int64_t)gridDim.x + blockIdx.x * WARPS + (hw >> 1)) * SLOT + c * D + d);
+                a.partials + (2 * gridDim.x + blockIdx.x * WARPS + (hw >> 1)) * (int64_t)SLOT + c * D + d);
             m = piece_r[hw * COLS + c];
         }
         const float hr = m;
@@ -964,19 +966,21 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
 
     // ---- units of several CTAs: the first group, if it did not start here, and the last, if it does
     // not end here.  The last CTA of each to arrive joins it. ----
-    int *arrived = reinterpret_cast<int *>(small);  // [2][2]: joins, CTAs
-    int64_t *from_cta = small + 2;                  // [2]
-    __threadfence();
+    int *arrived = small, *from_cta = small + 4;  // [2][2]: joins, CTAs; [2]
     __syncthreads();
     if (lane == 0 && warp < 2) {
         int joins = 0, n = 0;
         if (warp == 0 ? split0 : split1) {
             const AttnPiece *u = warp == 0 ? head_unit : tail_unit;
-            const int64_t t0 = u->unit0 + kAttnGap, tiles = prefix[u->b + 1] - prefix[u->b] - kAttnGap;
-            const int64_t c0 = share.worker_of(t0) / WARPS, c1 = share.worker_of(t0 + tiles - 1) / WARPS;
-            n = (int)(c1 - c0) + 1;
+            const int t0 = u->unit0 + kAttnGap, tiles = prefix[u->b + 1] - prefix[u->b] - kAttnGap;
+            const int c0 = share.worker_of(t0) / WARPS, c1 = share.worker_of(t0 + tiles - 1) / WARPS;
+            n = c1 - c0 + 1;
+            __threadfence();  // the CTA's parts, before it is counted
             joins = atomicAdd(a.counters + c0, 1) == n - 1;
-            if (joins) a.counters[c0] = 0;
+            if (joins) {
+                __threadfence();  // the other CTAs' parts, after they are
+                a.counters[c0] = 0;
+            }
             from_cta[warp] = c0;
         }
         arrived[2 * warp] = joins;
@@ -986,13 +990,12 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
         if (!arrived[2 * which]) continue;
-        __threadfence();
         const AttnPiece &u = which == 0 ? *head_unit : *tail_unit;
         const int n = arrived[2 * which + 1], live = min(COLS, a.columns - u.ct * COLS);
         // the CTAs' parts: of the first its second slot, of the others their first
-        const float *parts0 = a.partials + (2 * from_cta[which] + 1) * SLOT;
+        const float *parts0 = a.partials + (2 * from_cta[which] + 1) * (int64_t)SLOT;
         const auto part_of = [&](int i) { return parts0 + (i ? (2 * i - 1) * (int64_t)SLOT : 0); };
-        constexpr int AHEAD = 8;  // parts on their way while the weights are found
+        constexpr int AHEAD = 16;  // parts on their way while the weights are found
         for (int k0 = 0; k0 < live * (D / 4); k0 += THREADS) {
             const int k = k0 + tid, c = k / (D / 4), d = 4 * (k - c * (D / 4));
             const bool mine = c < live;

@@ -475,7 +475,8 @@ rfp2_status rfp2_kv_read(const int8_t *k_codes, const float *k_scales, const int
  * The length is split over the GPU and joined in a fixed order: the same call
  * gives the same bits.
  * Errors: EINVAL, ESHAPE (Hq % heads, D, page_size, B or nq < 1, nq * Hq >
- * 65536, table_width * page_size > 2^30, table_stride < table_width, pages *
+ * 65536, table_width * page_size > 2^30, or > 2^35 / (heads *
+ * ceil(nq * Hq / heads / 8)); table_stride < table_width, pages *
  * heads * page_size >= 2^32), EALIGN, EWORKSPACE, ECUDA.
  */
 size_t rfp2_attn_decode_workspace_bytes(int64_t B, int64_t nq, int64_t Hq, int64_t heads,
