@@ -324,24 +324,17 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
     AttnPlace lp = first;
     int lt = 0, lt_end = 0, l_len = 0, l_low = 0;  // tile of the next load; of its unit
     bool loading = true;
-    // Pages of the tiles to come.  Where a tile lies in one page, lane i holds that of tile page_at + i
-    // and the 32 after those are on their way; else those of the next tile's keys.
+    // Pages of the tiles to come, those of the `block` tiles from page_at on, and the ones after them on
+    // their way.  Where a tile lies in one page, lane i holds that of tile page_at + i; else that of the
+    // i-th key from tile page_at on.
+    const int block = a.whole_pages ? 32 : 2, key_step = a.whole_pages ? kAttnTile : 1;
     int32_t page = -1, page_after = -1;
     int page_at = 0;
-    const auto page_of_key = [&](int j) {
+    const auto pages_from = [&](int t) {
+        const int j = (l_low + t) * kAttnTile + lane * key_step;
         return j < l_len ? a.table[lp.b * a.table_stride +
                                    (a.page_shift >= 0 ? j >> a.page_shift : j / a.page_size)]
                          : -1;
-    };
-    const auto page_of_tile = [&](int t) { return t < lt_end ? page_of_key((l_low + t) * kAttnTile) : -1; };
-    const auto fetch_pages = [&]() {  // of a new unit
-        if (a.whole_pages) {
-            page_at = lt;
-            page = page_of_tile(lt + lane);
-            page_after = page_of_tile(lt + 32 + lane);
-        } else {
-            page = page_of_key((l_low + lt) * kAttnTile + (lane & (kAttnTile - 1)));
-        }
     };
     // enters units until one has tiles in this stretch
     const auto enter = [&]() {
@@ -357,7 +350,9 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
         }
         l_len = length_of(lp.b);
         l_low = tile_low(l_len);
-        fetch_pages();
+        page_at = lt;
+        page = pages_from(lt);
+        page_after = lt + block < lt_end ? pages_from(lt + block) : -1;
     };
     enter();
     // a unit's rows of q on their way while the unit before is worked on
@@ -382,12 +377,12 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
             const auto k_place = [&](int r, int c) {  // of 16-byte word c of key r
                 return r * L::k_stride + 16 * (L::k_permuted ? c ^ ((r & 3) << 1) : c);
             };
+            if (lt - page_at == block) {
+                page = page_after;
+                page_at = lt;
+                page_after = lt + block < lt_end ? pages_from(lt + block) : -1;
+            }
             if (a.whole_pages) {
-                if (lt - page_at == 32) {
-                    page = page_after;
-                    page_at = lt;
-                    page_after = page_of_tile(lt + 32 + lane);
-                }
                 const int32_t next_page = __shfl_sync(0xffffffffu, page, lt - page_at);
                 // sixteen rows that follow one another; those past the sequence's end are masked later
                 if (key0 >= l_len) {
@@ -420,14 +415,15 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
                 // row of the cache arrays of key `lane`, or -1 (no such key), -2 (no such page)
                 constexpr uint32_t kNoKey = 0xFFFFFFFFu, kNoPage = 0xFFFFFFFEu;
                 uint32_t row = kNoKey;
-                const int j = key0 + lane;
-                if (lane < kAttnTile && j < l_len) {
-                    if (page < 0 || page >= a.pages) {
+                const int j = key0 + (lane & (kAttnTile - 1));
+                const int32_t own_page = __shfl_sync(0xffffffffu, page, (lt - page_at) * kAttnTile + (lane & (kAttnTile - 1)));
+                if (j < l_len) {
+                    if (own_page < 0 || own_page >= a.pages) {
                         row = kNoPage;
                         record_status(a.status, RFP2_EBADID);
                     } else {
                         const uint32_t off = a.page_shift >= 0 ? j & (a.page_size - 1) : j % a.page_size;
-                        row = ((uint32_t)page * a.heads + lp.hk) * a.page_size + off;
+                        row = ((uint32_t)own_page * a.heads + lp.hk) * a.page_size + off;
                     }
                 }
 #pragma unroll
@@ -459,8 +455,6 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
                 next_unit(lp);
                 enter();
                 if (loading) prefetch_q(lp);
-            } else if (!a.whole_pages) {
-                fetch_pages();
             }
         }
         cp_async_commit();
