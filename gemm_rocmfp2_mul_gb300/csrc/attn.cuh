@@ -56,20 +56,23 @@ struct AttnArgs {
     int32_t *status;
 };
 
-// A tile in shared memory.  K is read 8 bytes a lane, four keys a half-warp, so
-// the 32-byte steps between keys are made odd (or, for 256 values, a key's
-// blocks are permuted by its two low bits).  V is read 4 bytes a lane, keys two
-// apart, so a row gets an odd number of 16-byte steps.  Neither read meets a
-// bank twice.
+// A tile in shared memory.  K is read 8 bytes a lane, four keys a half-warp, V 4
+// bytes a lane, keys two apart.  Rows of a multiple of 128 bytes have their
+// 32-byte blocks permuted by the two bits in which those keys differ; others are
+// padded, so that K's rows are an odd number of 32-byte steps apart and V's an
+// odd number of 16-byte steps.  Neither read meets a bank twice.
 template <int NB>
 struct AttnLayout {
     static constexpr int D = 32 * NB;
-    static constexpr bool k_permuted = NB == 8;
-    static constexpr int k_stride = NB % 2 || k_permuted ? D : D + 32;
-    static constexpr int v_stride = D + 16;
+    static constexpr bool permuted = NB % 4 == 0;
+    static constexpr int k_stride = permuted || NB % 2 ? D : D + 32;
+    static constexpr int v_stride = permuted ? D : D + 16;
     static constexpr int k_bytes = kAttnTile * k_stride, v_bytes = kAttnTile * v_stride;
     static constexpr int scale_bytes = kAttnTile * NB * 4;
     static constexpr int stage_bytes = k_bytes + v_bytes + 2 * scale_bytes;
+    // block n of key r lies where block n ^ k_order(r), n ^ v_order(r) would
+    static RFP2_DEV int k_order(int r) { return permuted ? r & 3 : 0; }
+    static RFP2_DEV int v_order(int r) { return permuted ? r >> 1 & 3 : 0; }
 };
 
 // What the warps leave of a unit that reaches beyond their stretch.
@@ -79,27 +82,37 @@ struct AttnPiece {
     int unit0;            // the unit's place on the line
 };
 
-template <int NB, int NT>
-constexpr int attn_warps() { return NB * NT > 2 && NB * NT <= 4 ? 12 : 8; }
+// PIECES of the f16 operands: 1 for 16-bit activations; 2 for fp32, taken by two
+// products; kPaired for fp32 of up to four columns, the second pieces being
+// columns 4 .. 7 of the same products.
+constexpr int kPaired = 3;
+
+// Warps: the tile's work is a long chain, so as many as the registers hold.  By
+// head size x columns (what a warp accumulates): 128 values x 8 at 128 registers,
+// 16 warps (12 where two pieces of q take 168); beyond that 8.  Small ones run
+// two CTAs of 8.
+template <int NB, int NT, int PIECES>
+constexpr int attn_warps() { return NB * NT <= 2 || NB * NT > 4 ? 8 : PIECES == 2 ? 12 : 16; }
 template <int NB, int NT>
 constexpr int attn_ctas_per_sm() { return NB * NT <= 2 ? 2 : 1; }
+
 // The warps' sums of the scan, the pieces and their columns' states, and the
 // line's prefix.
-template <int NB, int NT>
+template <int WARPS, int NT>
 constexpr int attn_small_bytes(int B) {
-    return 128 + 2 * attn_warps<NB, NT>() * ((int)sizeof(AttnPiece) + 2 * 8 * NT * 4) + (B + 1) * 4;
+    return 128 + 2 * WARPS * ((int)sizeof(AttnPiece) + 2 * 8 * NT * 4) + (B + 1) * 4;
 }
-template <int NB, int NT>
+template <int NB, int NT, int PIECES>
 constexpr int attn_stages() {
+    constexpr int W = attn_warps<NB, NT, PIECES>();
     const int budget = (attn_ctas_per_sm<NB, NT>() == 2 ? 113 : 227) * 1024;
-    const int s = (budget - attn_small_bytes<NB, NT>(kAttnMaxBatch)) /
-                  (attn_warps<NB, NT>() * AttnLayout<NB>::stage_bytes);
+    const int s = (budget - attn_small_bytes<W, NT>(kAttnMaxBatch)) / (W * AttnLayout<NB>::stage_bytes);
     return s > 8 ? 8 : s;
 }
-template <int NB, int NT>
+template <int NB, int NT, int PIECES>
 int attn_smem(int B) {
-    return attn_warps<NB, NT>() * attn_stages<NB, NT>() * AttnLayout<NB>::stage_bytes +
-           attn_small_bytes<NB, NT>(B);
+    constexpr int W = attn_warps<NB, NT, PIECES>();
+    return W * attn_stages<NB, NT, PIECES>() * AttnLayout<NB>::stage_bytes + attn_small_bytes<W, NT>(B);
 }
 // Floats of one partial result: references, sums, values of the columns.
 template <int NB, int NT>
@@ -144,10 +157,14 @@ RFP2_DEV uint32_t pack_f16(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
     return d;
 }
-RFP2_DEV float2 unpack_f16(uint32_t h) {
-    __half2 v;
-    memcpy(&v, &h, 4);
-    return __half22float2(v);
+// What is left of (lo, hi) beside the two f16 of h, as two f16.
+RFP2_DEV uint32_t rest_f16(uint32_t h, float lo, float hi) {
+    float u, v;
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n"
+        " sub.rn.f32.f16 %0, a, %3;\n sub.rn.f32.f16 %1, b, %4;\n}\n"
+        : "=f"(u), "=f"(v)
+        : "r"(h), "f"(lo), "f"(hi));
+    return pack_f16(-u, -v);
 }
 RFP2_DEV float exp2_fast(float x) {
     float y;
@@ -198,11 +215,14 @@ struct AttnShare {
 };
 
 template <int NB, int NT, int PIECES>
-__global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB, NT>())
+__global__ void __launch_bounds__(32 * attn_warps<NB, NT, PIECES>(), attn_ctas_per_sm<NB, NT>())
     attn_kernel(const AttnArgs a) {
     using L = AttnLayout<NB>;
-    constexpr int WARPS = attn_warps<NB, NT>(), THREADS = 32 * WARPS;
-    constexpr int D = L::D, STAGES = attn_stages<NB, NT>(), COLS = 8 * NT, SLOT = attn_slot<NB, NT>();
+    constexpr int WARPS = attn_warps<NB, NT, PIECES>(), THREADS = 32 * WARPS;
+    constexpr bool WIDE = PIECES != 1, PAIR = PIECES == kPaired;  // fp32 activations; their pieces as columns
+    constexpr int PARTS = PIECES == 2 ? 2 : 1, PER = PAIR ? 4 : 8;  // fragments of an operand; columns of a tile
+    static_assert(!PAIR || NT == 1, "");
+    constexpr int D = L::D, STAGES = attn_stages<NB, NT, PIECES>(), COLS = 8 * NT, SLOT = attn_slot<NB, NT>();
     static_assert(SLOT * 4 <= STAGES * L::stage_bytes, "a warp's partial result fits its ring");
     static_assert(STAGES >= 2 && WARPS <= 16, "");
     constexpr float kShift = 8.0f, kMost = 15.0f;  // p dV aims at 2^8 and stays below 2^15
@@ -219,6 +239,9 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
+    // this lane's columns of tile nt in the score layout, and whether it is the one that writes them
+    const auto column_of = [&](int nt, int e) { return nt * 8 + ((2 * t4 + e) & (PER - 1)); };
+    const bool writes = !PAIR || t4 < 2;
     pdl_wait();
     pdl_launch_dependents();
 
@@ -357,12 +380,12 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
     enter();
     // a unit's rows of q on their way while the unit before is worked on
     const auto prefetch_q = [&](const AttnPlace &p) {
-        constexpr int LINES = D * (PIECES == 2 ? 4 : 2) / 64;  // at least one address of each 128-byte line
+        constexpr int LINES = D * (WIDE ? 4 : 2) / 64;  // at least one address of each 128-byte line
         const int c0 = p.ct * COLS, live = min(COLS, a.columns - c0);
         for (int k = lane; k < live * LINES; k += 32) {
             const int c = c0 + k / LINES, i = c / a.group, h = p.hk * a.group + c - i * a.group;
             const int64_t at = p.b * a.qb + i * a.qt + h * a.qh;
-            const char *src = static_cast<const char *>(a.q) + at * (PIECES == 2 ? 4 : 2) + (k % LINES) * 64;
+            const char *src = static_cast<const char *>(a.q) + at * (WIDE ? 4 : 2) + (k % LINES) * 64;
             asm volatile("prefetch.global.L1 [%0];" ::"l"(src));
         }
     };
@@ -374,9 +397,9 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
             // scales: rows of NB floats, in the widest words that divide a row
             constexpr int W = NB % 4 == 0 ? 4 : NB % 2 == 0 ? 2 : 1, PER = NB / W;
             const int key0 = (l_low + lt) * kAttnTile;
-            const auto k_place = [&](int r, int c) {  // of 16-byte word c of key r
-                return r * L::k_stride + 16 * (L::k_permuted ? c ^ ((r & 3) << 1) : c);
-            };
+            // of 16-byte word c of key r
+            const auto k_place = [&](int r, int c) { return r * L::k_stride + 16 * (c ^ L::k_order(r) << 1); };
+            const auto v_place = [&](int r, int c) { return r * L::v_stride + 16 * (c ^ L::v_order(r) << 1); };
             if (lt - page_at == block) {
                 page = page_after;
                 page_at = lt;
@@ -402,7 +425,7 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
                     for (int i = 0; i < NB; ++i) {
                         const int id = lane + 32 * i, r = id / CH, c = id - r * CH;
                         cp_async16(k_at + k_place(r, c), kp + 512 * i);
-                        cp_async16(v_at + r * L::v_stride + 16 * c, vp + 512 * i);
+                        cp_async16(v_at + v_place(r, c), vp + 512 * i);
                     }
                     const float *ks = a.k_scales + (int64_t)row * NB, *vs = a.v_scales + (int64_t)row * NB;
 #pragma unroll
@@ -433,7 +456,7 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
                     if (src < kNoPage) {
                         const int64_t at = (int64_t)src * D + 16 * c;
                         cp_async16(k_at + k_place(r, c), a.k_codes + at);
-                        cp_async16(v_at + r * L::v_stride + 16 * c, a.v_codes + at);
+                        cp_async16(v_at + v_place(r, c), a.v_codes + at);
                     }
                 }
 #pragma unroll
@@ -467,7 +490,7 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
     };
     const auto store_four = [&](int64_t row, int d, const float (&y)[4]) {
         const int64_t at = row * D + d;
-        if (PIECES == 2) {
+        if (WIDE) {
             *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
         } else {
             uint2 u;
@@ -513,7 +536,7 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int c = min(p.ct * COLS + nt * 8 + 2 * t4 + e, a.columns - 1);
+                const int c = min(p.ct * COLS + column_of(nt, e), a.columns - 1);
                 col_end[nt][e] = len - a.nq + 1 + c / a.group;
             }
         const int c_last = min(p.ct * COLS + COLS, a.columns) - 1;
@@ -521,12 +544,12 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
         const int64_t max_begin = a.window ? len - a.nq + 1 + c_last / a.group - a.window : 0;
 
         // q of column g: values 32 n + 8 t4 .. + 7, scaled by a power of two
-        uint32_t qf[NT][NB][2][PIECES][2];
+        uint32_t qf[NT][NB][2][PARTS][2];
         float col_scale[NT][2];
         int up_most = 0, up_least = 0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int c = p.ct * COLS + nt * 8 + g;
+            const int c = p.ct * COLS + nt * 8 + (g & (PER - 1));
             float v[NB][8];
 #pragma unroll
             for (int n = 0; n < NB; ++n)
@@ -535,7 +558,7 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
             if (c < a.columns) {
                 const int i = c / a.group, h = p.hk * a.group + c - i * a.group;
                 const int64_t at = p.b * a.qb + i * a.qt + h * a.qh + 8 * t4;
-                if (PIECES == 2) {
+                if (WIDE) {
                     const float *src = static_cast<const float *>(a.q) + at;
                     if (a.q_words) {
 #pragma unroll
@@ -592,15 +615,18 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
                         const float u = v[n][4 * s + 2 * h] * by, w = v[n][4 * s + 2 * h + 1] * by;
                         const uint32_t hi = pack_f16(u, w);
                         qf[nt][n][s][0][h] = hi;
-                        if constexpr (PIECES == 2) {
-                            const float2 f = unpack_f16(hi);
-                            qf[nt][n][s][1][h] = pack_f16(u - f.x, w - f.y);
+                        if constexpr (WIDE) {
+                            const uint32_t lo = rest_f16(hi, u, w);
+                            if constexpr (PAIR)
+                                qf[nt][n][s][0][h] = g < 4 ? hi : lo;
+                            else
+                                qf[nt][n][s][1][h] = lo;
                         }
                     }
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 col_scale[nt][e] = __uint_as_float(
-                    (uint32_t)(127 - __shfl_sync(0xffffffffu, up, 4 * (2 * t4 + e))) << 23);
+                    (uint32_t)(127 - __shfl_sync(0xffffffffu, up, 4 * column_of(0, e))) << 23);
         }
         // q far from 1 is for keys as far on the other side: their scales are brought 2^60 nearer, so
         // that no sum on the way leaves fp32's range
@@ -674,7 +700,7 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
             float sc[NT][4];
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
-                const int at = 32 * (L::k_permuted ? n ^ (g & 3) : n) + 8 * t4;
+                const int at = 32 * (n ^ L::k_order(g)) + 8 * t4;
                 const uint2 lo = *reinterpret_cast<const uint2 *>(kt + g * L::k_stride + at);
                 const uint2 hi = *reinterpret_cast<const uint2 *>(kt + (g + 8) * L::k_stride + at);
                 float c[NT][4];
@@ -692,7 +718,7 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int piece = PIECES - 1; piece >= 0; --piece)
+                        for (int piece = PARTS - 1; piece >= 0; --piece)
                             mma_f16(c[nt], f, qf[nt][n][s][piece][0], qf[nt][n][s][piece][1]);
                 }
 #pragma unroll
@@ -701,6 +727,10 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
                     for (int e = 0; e < 4; ++e)
                         sc[nt][e] = n ? sc[nt][e] + dk[e >> 1][n] * c[nt][e] : dk[e >> 1][n] * c[nt][e];
             }
+
+            if constexpr (PAIR)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[0][e] += __shfl_xor_sync(0xffffffffu, sc[0][e], 2);
 
             const bool whole = key0 + kAttnTile <= min_end && key0 >= max_begin;
             bool more = false;
@@ -761,7 +791,7 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
                 }
 
             // p dV in the layout that the products take it in
-            uint32_t pb[NB][NT][PIECES][2];
+            uint32_t pb[NB][NT][PARTS][2];
             const auto weigh = [&](bool odd) {
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
@@ -775,11 +805,11 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
                                 if (sc[nt][2 * k + 1] == -CUDART_INF_F) w = 0.0f;
                             }
                             const uint32_t hi = pack_f16(u, w);
-                            pb[n][nt][0][k] = transpose8x8(hi);
-                            if constexpr (PIECES == 2) {
-                                const float2 f = unpack_f16(hi);
-                                pb[n][nt][1][k] = transpose8x8(pack_f16(u - f.x, w - f.y));
-                            }
+                            if constexpr (PAIR)
+                                pb[n][nt][0][k] = transpose8x8(t4 < 2 ? hi : rest_f16(hi, u, w));
+                            else
+                                pb[n][nt][0][k] = transpose8x8(hi);
+                            if constexpr (PARTS == 2) pb[n][nt][1][k] = transpose8x8(rest_f16(hi, u, w));
                         }
             };
             if (odd)
@@ -790,7 +820,7 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
             // values: out^T += V^T (p dV), keys 2 t4, + 1, + 8, + 9
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
-                const uint8_t *vp = vt + 2 * t4 * L::v_stride + 32 * n + 4 * g;
+                const uint8_t *vp = vt + 2 * t4 * L::v_stride + 32 * (n ^ L::v_order(2 * t4)) + 4 * g;
                 uint32_t w[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -806,10 +836,10 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
                                            less_1152(__byte_perm(v, 0x64646464u, 0x4342))};
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        if constexpr (PIECES == 2) {
+                        if constexpr (WIDE) {
                             // the matrix unit cuts sums off; a long chain of them is kept in fp32 adds
                             float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            mma_f16(c, f, pb[n][nt][1][0], pb[n][nt][1][1]);
+                            if constexpr (PARTS == 2) mma_f16(c, f, pb[n][nt][1][0], pb[n][nt][1][1]);
                             mma_f16(c, f, pb[n][nt][0][0], pb[n][nt][0][1]);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) o[nt][n][h][e] += c[e];
@@ -830,13 +860,20 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
                 sum[nt][e] += __shfl_xor_sync(0xffffffffu, sum[nt][e], 8);
                 sum[nt][e] += __shfl_xor_sync(0xffffffffu, sum[nt][e], 16);
             }
+        if constexpr (PAIR)
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[0][n][h][e] += __shfl_xor_sync(0xffffffffu, o[0][n][h][e], 2);
         if (from == 0 && to == p.tiles) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int cg = p.ct * COLS + nt * 8 + 2 * t4 + e;
-                    if (cg >= a.columns) continue;
+                    const int cg = p.ct * COLS + column_of(nt, e);
+                    if (!writes || cg >= a.columns) continue;
                     const int64_t row = row_of(p.b, p.hk, cg);
                     const float l = sum[nt][e], inv = l == 0.0f ? 0.0f : kSumScale / l;
 #pragma unroll
@@ -864,7 +901,8 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT>(), attn_ctas_per_sm<NB
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int c = nt * 8 + 2 * t4 + e;
+                    const int c = column_of(nt, e);
+                    if (!writes) continue;
                     if (g == 0) {
                         piece_r[(2 * warp + tail) * COLS + c] = ref[nt][e];
                         piece_l[(2 * warp + tail) * COLS + c] = sum[nt][e];
@@ -1054,12 +1092,12 @@ cudaError_t attn_launch(const AttnArgs &a, int sms, cudaStream_t stream) {
     const int device = current_device();
     if (device >= 64 || !ready[device].load(std::memory_order_relaxed)) {
         const cudaError_t e =
-            set_smem_limit(attn_kernel<NB, NT, PIECES>, attn_smem<NB, NT>(kAttnMaxBatch));
+            set_smem_limit(attn_kernel<NB, NT, PIECES>, attn_smem<NB, NT, PIECES>(kAttnMaxBatch));
         if (e != cudaSuccess) return e;
         if (device < 64) ready[device].store(1, std::memory_order_relaxed);
     }
     return launch(attn_kernel<NB, NT, PIECES>, dim3((unsigned)(sms * attn_ctas_per_sm<NB, NT>())),
-                  dim3(32 * attn_warps<NB, NT>()), attn_smem<NB, NT>(a.B), stream, true, a);
+                  dim3(32 * attn_warps<NB, NT, PIECES>()), attn_smem<NB, NT, PIECES>(a.B), stream, true, a);
 }
 
 // Column tiles of 8 or, from 9 columns up, 16 (where the registers hold them).
@@ -1072,8 +1110,8 @@ cudaError_t attn_by_columns(const AttnArgs &a, int sms, cudaStream_t stream) {
         if (a.columns > 8)
             return a.dtype == RFP2_F32 ? attn_launch<NB, 2, 2>(a, sms, stream)
                                        : attn_launch<NB, 2, 1>(a, sms, stream);
-    return a.dtype == RFP2_F32 ? attn_launch<NB, 1, 2>(a, sms, stream)
-                               : attn_launch<NB, 1, 1>(a, sms, stream);
+    if (a.dtype != RFP2_F32) return attn_launch<NB, 1, 1>(a, sms, stream);
+    return a.columns <= 4 ? attn_launch<NB, 1, kPaired>(a, sms, stream) : attn_launch<NB, 1, 2>(a, sms, stream);
 }
 
 // By blocks of 32 values a head; each is instantiated in one translation unit.
