@@ -33,6 +33,7 @@ namespace rfp2 {
 constexpr int kAttnTile = 16;        // keys
 constexpr int kAttnGap = 2;          // a unit's fixed cost, in tiles
 constexpr int kAttnMinStretch = 1;   // of a warp, in tiles
+constexpr int kAttnInFlight = 112 * 1024;  // bytes of the cache on their way to an SM, at most
 constexpr int kAttnMaxBatch = 1024;  // sequences of one launch
 constexpr int kAttnCounterBytes = 4096;
 
@@ -92,7 +93,7 @@ constexpr int kPaired = 3;
 // 16 warps (12 where two pieces of q take 168); beyond that 8.  Small ones run
 // two CTAs of 8.
 template <int NB, int NT, int PIECES>
-constexpr int attn_warps() { return NB * NT <= 2 || NB * NT > 4 ? 8 : PIECES == 2 ? 12 : 16; }
+constexpr int attn_warps() { return NB * NT <= 2 || NB * NT > 4 ? 8 : 12; }
 template <int NB, int NT>
 constexpr int attn_ctas_per_sm() { return NB * NT <= 2 ? 2 : 1; }
 
@@ -107,7 +108,9 @@ constexpr int attn_stages() {
     constexpr int W = attn_warps<NB, NT, PIECES>();
     const int budget = (attn_ctas_per_sm<NB, NT>() == 2 ? 113 : 227) * 1024;
     const int s = (budget - attn_small_bytes<W, NT>(kAttnMaxBatch)) / (W * AttnLayout<NB>::stage_bytes);
-    return s > 8 ? 8 : s;
+    // the tiles on their way to an SM; the last stage is the one that is worked on
+    const int wanted = 1 + kAttnInFlight / (W * attn_ctas_per_sm<NB, NT>() * kAttnTile * NB * 72);
+    return s < 2 || wanted < 2 ? 2 : s < wanted ? s : wanted;
 }
 template <int NB, int NT, int PIECES>
 int attn_smem(int B) {
