@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv_write_kernel(const WriteArgs a
             const int p = c - (low ? 0 : a.pairs >> 3);
             Eight<T, WIDE> z;
             z.load(k + t * a.kt + (low ? a.pairs : -a.pairs));
-            const float sign = low ? -1.0f : 1.0f;
+            const uint32_t sign = low ? 0x80000000u : 0u;
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
                 const float *q = cs + (w * (a.pairs >> 3) + p) * 4;
@@ -233,7 +233,8 @@ __global__ void __launch_bounds__(kThreads, 4) kv_write_kernel(const WriteArgs a
                 const float cc[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    u[4 * w + e] = u[4 * w + e] * cc[e] + sign * ss[e] * to_f32(z.v[4 * w + e]);
+                    u[4 * w + e] = u[4 * w + e] * cc[e] +
+                                   __uint_as_float(__float_as_uint(ss[e]) ^ sign) * to_f32(z.v[4 * w + e]);
             }
         } else if (words) {
             const float4 co = *reinterpret_cast<const float4 *>(cs + 4 * c);

@@ -15,7 +15,7 @@ namespace rfp2 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;        // steps of a thread whose loads travel together
+constexpr int kAhead = 2;        // steps of a thread whose loads travel together
 constexpr int kMaxPairs = 2048;  // (token, pair) entries of a CTA's table
 
 struct RopeArgs {
@@ -49,7 +49,7 @@ struct alignas(V * sizeof(T)) Runs {
 };
 
 template <typename T, int V, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeArgs a) {
     extern __shared__ __align__(16) float table[];  // [tokens][cos, sin][pairs]
     pdl_wait();
     pdl_launch_dependents();
