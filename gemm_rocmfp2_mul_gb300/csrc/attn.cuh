@@ -33,6 +33,7 @@ namespace rfp2 {
 constexpr int kAttnTile = 16;        // keys
 constexpr int kAttnGap = 2;          // a unit's fixed cost, in tiles
 constexpr int kAttnMinStretch = 1;   // of a warp, in tiles
+constexpr int kAttnWholeUnit = 4;    // tiles a warp up to which a unit stays in one CTA
 constexpr int kAttnInFlight = 112 * 1024;  // bytes of the cache on their way to an SM, at most
 constexpr int kAttnMaxBatch = 1024;  // sequences of one launch
 constexpr int kAttnCounterBytes = 4096;
@@ -265,9 +266,14 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT, PIECES>(), attn_ctas_p
         return kAttnGap + max(1, (len + kAttnTile - 1) / kAttnTile - tile_low(len));
     };
     if (lane < 2) pieces[2 * warp + lane].present = 0;
+    const int units_of = a.heads * a.column_tiles;
+    bool whole_units = false;  // a CTA for every unit
     if (a.B <= 32) {
         // every warp by itself
-        int incl = lane < a.B ? cost_of(lane) : 0;
+        const int cost = lane < a.B ? cost_of(lane) : 0;
+        whole_units = a.B * units_of <= (int)gridDim.x &&
+                      __reduce_max_sync(0xffffffffu, cost) <= kAttnWholeUnit * WARPS;
+        int incl = cost;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int up = __shfl_up_sync(0xffffffffu, incl, off);
@@ -300,31 +306,44 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT, PIECES>(), attn_ctas_p
         if (tid == 0) prefix[0] = 0;
         __syncthreads();
     }
-    const int units_of = a.heads * a.column_tiles;
     const int total = prefix[a.B] * units_of;
-    // some tiles for each warp: shorter stretches are not worth their joins
-    const int parts = min((int)gridDim.x, (total - 1) / (kAttnMinStretch * WARPS) + 1);
+    // Some tiles for each warp: shorter stretches are not worth their joins.  And where there are fewer
+    // units than CTAs, each of a few tiles a warp, a unit stays in one CTA: those tiles cost less than a
+    // join across CTAs.
+    const int parts = whole_units ? a.B * units_of
+                                  : min((int)gridDim.x, (total - 1) / (kAttnMinStretch * WARPS) + 1);
     if ((int)blockIdx.x >= parts) return;
-    AttnShare share;
-    share.each = (uint32_t)total / (uint32_t)(parts * WARPS);
-    share.extra = total - share.each * parts * WARPS;
     const int worker = blockIdx.x * WARPS + warp;
-    const int y0 = share.begin(worker), y1 = share.begin(worker + 1);
-
+    AttnShare share;
     AttnPlace first;
-    {
+    int y0, y1;
+    const auto place_unit = [&](int b, int unit) {
+        const int cost = prefix[b + 1] - prefix[b];
+        first.b = b;
+        first.tiles = cost - kAttnGap;
+        first.unit0 = prefix[b] * units_of + unit * cost;
+        first.hk = a.column_tiles == 1 ? unit : unit / a.column_tiles;
+        first.ct = unit - first.hk * a.column_tiles;
+        return cost;
+    };
+    if (whole_units) {
+        const int b = blockIdx.x / units_of, cost = place_unit(b, blockIdx.x - b * units_of);
+        // from the first tile on: the gap costs nothing here
+        share.each = (uint32_t)(cost - kAttnGap) / WARPS;
+        share.extra = cost - kAttnGap - share.each * WARPS;
+        y0 = first.unit0 + kAttnGap + share.begin(warp);
+        y1 = first.unit0 + kAttnGap + share.begin(warp + 1);
+    } else {
+        share.each = (uint32_t)total / (uint32_t)(parts * WARPS);
+        share.extra = total - share.each * parts * WARPS;
+        y0 = share.begin(worker);
+        y1 = share.begin(worker + 1);
         int lo = 0, hi = a.B;  // the last b with prefix[b] * units_of <= y0
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (prefix[mid] * units_of <= y0) lo = mid; else hi = mid;
         }
-        const int cost = prefix[lo + 1] - prefix[lo];
-        const int unit = (uint32_t)(y0 - prefix[lo] * units_of) / (uint32_t)cost;
-        first.b = lo;
-        first.tiles = cost - kAttnGap;
-        first.unit0 = prefix[lo] * units_of + unit * cost;
-        first.hk = a.column_tiles == 1 ? unit : unit / a.column_tiles;
-        first.ct = unit - first.hk * a.column_tiles;
+        place_unit(lo, (uint32_t)(y0 - prefix[lo] * units_of) / (uint32_t)(prefix[lo + 1] - prefix[lo]));
     }
     const auto next_unit = [&](AttnPlace &p) {
         p.unit0 += p.tiles + kAttnGap;
