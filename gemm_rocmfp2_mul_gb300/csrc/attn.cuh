@@ -118,7 +118,8 @@ int attn_smem(int B) {
     constexpr int W = attn_warps<NB, NT, PIECES>();
     return W * attn_stages<NB, NT, PIECES>() * AttnLayout<NB>::stage_bytes + attn_small_bytes<W, NT>(B);
 }
-// Floats of one partial result: references, sums, values of the columns.
+// Floats of one partial result: the columns' references and sums, and their
+// values.
 template <int NB, int NT>
 constexpr int attn_slot() { return 8 * NT * (2 + 32 * NB); }
 
@@ -174,6 +175,13 @@ RFP2_DEV float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// cap_out tanh(x / 2 log2 e) = cap_out (1 - 2 / (2^x + 1)): off by 2e-7 cap_out,
+// far below the rounding of 16-bit outputs.
+RFP2_DEV float tanh_16(float x, float cap_out) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(exp2_fast(x) + 1.0f));
+    return fmaf(-2.0f * cap_out, r, cap_out);
 }
 RFP2_DEV float log2_fast(float x) {
     float y;
@@ -246,6 +254,9 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT, PIECES>(), attn_ctas_p
     // this lane's columns of tile nt in the score layout, and whether it is the one that writes them
     const auto column_of = [&](int nt, int e) { return nt * 8 + ((2 * t4 + e) & (PER - 1)); };
     const bool writes = !PAIR || t4 < 2;
+    // 16-byte word w of column c of a piece lies where word w ^ slot_order(c) would: so its writers, eight
+    // lanes in four columns, meet no bank twice
+    const auto slot_order = [](int c) { return c & 6; };
     pdl_wait();
     pdl_launch_dependents();
 
@@ -545,6 +556,8 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT, PIECES>(), attn_ctas_p
     };
 
     // ---- the units of this stretch ----
+    const float cap_out = a.softcap * 1.4426950408889634f;
+    const float cap_in = 2.8853900817779268f / a.softcap;  // 2 log2 e / softcap
     int stage = 0;
     bool filled = false;
     for (AttnPlace p = first; p.unit0 + kAttnGap < y1; next_unit(p)) {
@@ -765,7 +778,8 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT, PIECES>(), attn_ctas_p
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        sc[nt][e] = a.softcap * tanhf(sc[nt][e] / a.softcap) * 1.4426950408889634f;
+                        sc[nt][e] = WIDE ? a.softcap * tanhf(sc[nt][e] / a.softcap) * 1.4426950408889634f
+                                         : tanh_16(sc[nt][e] * cap_in, cap_out);
             if (!whole) {
                 // out of sight: no weight, whatever the value's scale is there
 #pragma unroll
@@ -931,7 +945,7 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT, PIECES>(), attn_ctas_p
                     }
 #pragma unroll
                     for (int n = 0; n < NB; ++n)
-                        *reinterpret_cast<float4 *>(slot + c * D + 32 * n + 4 * g) =
+                        *reinterpret_cast<float4 *>(slot + c * D + 4 * ((8 * n + g) ^ slot_order(c))) =
                             make_float4(o[nt][n][0][e], o[nt][n][0][e + 2], o[nt][n][1][e], o[nt][n][1][e + 2]);
                 }
             if (lane == 0) {
@@ -972,12 +986,13 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT, PIECES>(), attn_ctas_p
         const uint32_t members = members_of(j), tails = members & ~0x55555555u, head = members & 0x55555555u;
         const AttnPiece &u = pieces[__ffs(members) - 1];
         if (c >= a.columns - u.ct * COLS) continue;
+        const int at = d ^ 4 * slot_order(c);
         float y[4] = {0.0f, 0.0f, 0.0f, 0.0f}, l = 0.0f, m = kNone, r[WARPS];
         float4 hv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         const int hw = head ? __ffs(head) - 1 : 0;
         if (head) {
             hv = *reinterpret_cast<const float4 *>(
-                a.partials + (2 * gridDim.x + blockIdx.x * WARPS + (hw >> 1)) * (int64_t)SLOT + c * D + d);
+                a.partials + (2 * gridDim.x + blockIdx.x * WARPS + (hw >> 1)) * (int64_t)SLOT + c * D + at);
             m = piece_r[hw * COLS + c];
         }
         const float hr = m;
@@ -997,7 +1012,7 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT, PIECES>(), attn_ctas_p
             if (tails >> (2 * w + 1) & 1u) {
                 const float by = exp2_fast(r[w] - m);
                 l += piece_l[(2 * w + 1) * COLS + c] * by;
-                add(*reinterpret_cast<const float4 *>(rings + w * STAGES * L::stage_bytes + (c * D + d) * 4), by);
+                add(*reinterpret_cast<const float4 *>(rings + w * STAGES * L::stage_bytes + (c * D + at) * 4), by);
             }
         if (head) {
             const float by = exp2_fast(hr - m);
@@ -1009,11 +1024,10 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT, PIECES>(), attn_ctas_p
         } else {
             // a unit of several CTAs
             float *mine = a.partials + (2 * (int64_t)blockIdx.x + u.starts) * SLOT;
-            *reinterpret_cast<float4 *>(mine + 2 * COLS + c * D + d) = make_float4(y[0], y[1], y[2], y[3]);
-            if (d == 0) {
-                mine[c] = m;
-                mine[COLS + c] = l;
-            }
+            const float inv = l == 0.0f ? 0.0f : kSumScale / l;
+            *reinterpret_cast<float4 *>(mine + 2 * COLS + c * D + d) =
+                make_float4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+            if (d == 0) *reinterpret_cast<float2 *>(mine + 2 * c) = make_float2(m, l);
         }
     }
     if (!split0 && !split1) return;
@@ -1046,64 +1060,53 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT, PIECES>(), attn_ctas_p
         if (!arrived[2 * which]) continue;
         const AttnPiece &u = which == 0 ? *head_unit : *tail_unit;
         const int n = arrived[2 * which + 1], live = min(COLS, a.columns - u.ct * COLS);
-        // the CTAs' parts: of the first its second slot, of the others their first
+        // the CTAs' parts, each with its own sum divided out, which weighs it.  Of the first CTA its second
+        // slot, of the others their first
         const float *parts0 = a.partials + (2 * from_cta[which] + 1) * (int64_t)SLOT;
         const auto part_of = [&](int i) { return parts0 + (i ? (2 * i - 1) * (int64_t)SLOT : 0); };
-        constexpr int AHEAD = 16;  // parts on their way while the weights are found
-        for (int k0 = 0; k0 < live * (D / 4); k0 += THREADS) {
-            const int k = k0 + tid, c = k / (D / 4), d = 4 * (k - c * (D / 4));
-            const bool mine = c < live;
-            float4 v[AHEAD];
+        for (int k = tid; k < live * (D / 4); k += THREADS) {
+            const int c = k / (D / 4), d = 4 * (k - c * (D / 4));
+            float m = kNone, l = 0.0f, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            constexpr int AHEAD = 16;  // parts whose loads travel together
+#pragma unroll 1
+            for (int i0 = 0; i0 < n; i0 += AHEAD) {
+                float4 v[AHEAD];
+                float2 r[AHEAD];
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i)
-                if (mine && i < n) v[i] = __ldcg(reinterpret_cast<const float4 *>(part_of(i) + 2 * COLS + c * D + d));
-            if (k0 == 0) {
-                // weights of the parts, and the columns' references and sums; a warp takes columns in turn
-                float *weight = reinterpret_cast<float *>(rings);  // [n][COLS]; the pieces there are done with
-                for (int cc = warp; cc < live; cc += WARPS) {
-                    float r = lane < n ? __ldcg(part_of(lane) + cc) : kNone;
-                    float s = lane < n ? __ldcg(part_of(lane) + COLS + cc) : 0.0f;
-                    float m = r;
-                    for (int i = lane + 32; i < n; i += 32) m = fmaxf(m, __ldcg(part_of(i) + cc));
-#pragma unroll
-                    for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-                    float l = 0.0f;
-                    for (int i = lane; i < n; i += 32) {
-                        if (i != lane) {
-                            r = __ldcg(part_of(i) + cc);
-                            s = __ldcg(part_of(i) + COLS + cc);
-                        }
-                        const float by = exp2_fast(r - m);
-                        l += s * by;
-                        weight[i * COLS + cc] = by;
-                    }
-#pragma unroll
-                    for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-                    if (lane == 0) {
-                        piece_r[cc] = m;
-                        piece_l[cc] = l;
+                for (int i = 0; i < AHEAD; ++i) {
+                    r[i] = make_float2(kNone, 0.0f);
+                    v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (i0 + i < n) {
+                        const float *from = part_of(i0 + i);
+                        r[i] = __ldcg(reinterpret_cast<const float2 *>(from) + c);
+                        v[i] = __ldcg(reinterpret_cast<const float4 *>(from + 2 * COLS + c * D + d));
                     }
                 }
-                __syncthreads();
-            }
-            if (!mine) continue;
-            const float *weight = reinterpret_cast<const float *>(rings) + c;
-            float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            const auto add = [&](const float4 &x, float by) {
-                y[0] += x.x * by;
-                y[1] += x.y * by;
-                y[2] += x.z * by;
-                y[3] += x.w * by;
-            };
+                float top = m;
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i)
-                if (i < n) add(v[i], weight[i * COLS]);
-#pragma unroll 8
-            for (int i = AHEAD; i < n; ++i)
-                add(__ldcg(reinterpret_cast<const float4 *>(part_of(i) + 2 * COLS + c * D + d)), weight[i * COLS]);
-            finish(u, c, d, y, piece_r[c], piece_l[c]);
+                for (int i = 0; i < AHEAD; ++i) top = fmaxf(top, r[i].x);
+                const float keep = exp2_fast(m - top);
+                m = top;
+                l *= keep;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] *= keep;
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    const float by = r[i].y * exp2_fast(r[i].x - m);
+                    l += by;
+                    y[0] += v[i].x * by;
+                    y[1] += v[i].y * by;
+                    y[2] += v[i].z * by;
+                    y[3] += v[i].w * by;
+                }
+            }
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] *= inv;
+            const int64_t row = row_of(u.b, u.hk, u.ct * COLS + c);
+            store_four(row, d, y);
+            if (a.lse && d == 0) a.lse[row] = lse_of(m, l);
         }
-        __syncthreads();
     }
 }
 
