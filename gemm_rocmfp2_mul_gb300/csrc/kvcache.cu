@@ -15,6 +15,7 @@ namespace rfp2 {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWriteTokens = 28, kReadTokens = 18;  // of a CTA, at most
 constexpr int kMaxTable = 4096;  // (token, pair) entries of a CTA's table
 
 // A token's steps (a head's eight or, reading fp32, four values of key and of
@@ -33,14 +34,18 @@ struct Deal {
     }
 };
 
-// `ahead`: tokens of a thread whose loads travel together.  Few tokens are
-// spread over the SMs.
-Deal deal(int64_t T, int64_t heads, int64_t chunks, int ahead, int64_t most) {
+// The tokens are dealt so that the CTAs fill the SMs, `resident` on each, a whole
+// number of times: at most `most` tokens a CTA, and few tokens spread one by one.
+Deal deal(int64_t T, int64_t heads, int64_t chunks, int resident, int64_t most) {
     Deal w;
     w.steps = (int)(heads * chunks);
     w.rows = std::max(1, kThreads / w.steps);
-    const int64_t by_sms = T / (4 * (int64_t)sm_count(current_device()));
-    w.tokens = (int)std::max<int64_t>(1, std::min({(int64_t)w.rows * ahead, by_sms, most}));
+    const int64_t stretches = (w.steps + kThreads - 1) / kThreads;
+    const int64_t at_once = std::max<int64_t>(1, resident * (int64_t)sm_count(current_device()) / stretches);
+    const int64_t waves = (T + at_once * most - 1) / (at_once * most);
+    int64_t tokens = (T + at_once * waves - 1) / (at_once * waves);
+    if (tokens > w.rows) tokens = (tokens + w.rows - 1) / w.rows * w.rows;
+    w.tokens = (int)std::max<int64_t>(1, tokens);
     w.rows = std::min(w.rows, w.tokens);
     w.by_steps = FastDiv((uint32_t)w.steps);
     w.by_chunks = FastDiv((uint32_t)chunks);
@@ -306,7 +311,7 @@ RFP2_DEV void read_word(const uint32_t (&w)[E / 4], float d, T *out) {
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 6) kv_read_kernel(const ReadArgs a) {
-    constexpr int E = 16 / sizeof(T), AHEAD = 2;
+    constexpr int E = 16 / sizeof(T), AHEAD = 1;
     extern __shared__ int64_t place[];  // [tokens]
     pdl_wait();
     pdl_launch_dependents();
@@ -322,40 +327,53 @@ __global__ void __launch_bounds__(kThreads, 6) kv_read_kernel(const ReadArgs a) 
     if (!mine) return;
     T *k = static_cast<T *>(a.k), *v = static_cast<T *>(a.v);
     const int64_t own = (int64_t)h * a.page_size * a.D + E * c;
-    for (int t = row; t < nt; t += AHEAD * a.deal.rows) {
-        uint32_t kw[AHEAD][E / 4], vw[AHEAD][E / 4];
+    struct Batch {
+        uint32_t k[AHEAD][E / 4], v[AHEAD][E / 4];
         float kd[AHEAD], vd[AHEAD];
+    };
+    const auto load = [&](int t, Batch &b) {
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             const int at = t + i * a.deal.rows;
             const int64_t base = at < nt ? place[at] : -1;
 #pragma unroll
-            for (int e = 0; e < E / 4; ++e) kw[i][e] = vw[i][e] = 0u;
-            kd[i] = vd[i] = base == -1 ? 0.0f : CUDART_NAN_F;
+            for (int e = 0; e < E / 4; ++e) b.k[i][e] = b.v[i][e] = 0u;
+            b.kd[i] = b.vd[i] = base == -1 ? 0.0f : CUDART_NAN_F;
             if (base >= 0) {
                 const int64_t from = base + own;
                 const uint32_t *ks = reinterpret_cast<const uint32_t *>(a.k_codes + from);
                 const uint32_t *vs = reinterpret_cast<const uint32_t *>(a.v_codes + from);
                 if constexpr (E == 8) {
                     const uint2 p = *reinterpret_cast<const uint2 *>(ks), q = *reinterpret_cast<const uint2 *>(vs);
-                    kw[i][0] = p.x, kw[i][1] = p.y;
-                    vw[i][0] = q.x, vw[i][1] = q.y;
+                    b.k[i][0] = p.x, b.k[i][1] = p.y;
+                    b.v[i][0] = q.x, b.v[i][1] = q.y;
                 } else {
-                    kw[i][0] = *ks;
-                    vw[i][0] = *vs;
+                    b.k[i][0] = *ks;
+                    b.v[i][0] = *vs;
                 }
-                kd[i] = a.k_scales[from >> 5];
-                vd[i] = a.v_scales[from >> 5];
+                b.kd[i] = a.k_scales[from >> 5];
+                b.vd[i] = a.v_scales[from >> 5];
             }
         }
+    };
+    const auto store = [&](int t, const Batch &b) {
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             const int at = t + i * a.deal.rows;
             if (at >= nt) continue;
             const int64_t to = ((t0 + at) * a.deal.steps + step) * E;
-            if (k) read_word<T, E>(kw[i], kd[i], k + to);
-            if (v) read_word<T, E>(vw[i], vd[i], v + to);
+            if (k) read_word<T, E>(b.k[i], b.kd[i], k + to);
+            if (v) read_word<T, E>(b.v[i], b.vd[i], v + to);
         }
+    };
+    Batch here, next;
+    const int stride = AHEAD * a.deal.rows;
+    load(row, here);
+    for (int t = row; t < nt; t += 2 * stride) {
+        load(t + stride, next);
+        store(t, here);
+        load(t + 2 * stride, here);
+        store(t + stride, next);
     }
 }
 
@@ -425,7 +443,7 @@ extern "C" rfp2_status rfp2_kv_write(const void *k, const void *v, int dtype, in
     a.D = (int)D;
     a.pairs = positions ? (int)(R / 2) : 0;
     a.by_pairs = FastDiv(std::max(1, a.pairs));
-    a.deal = deal(T, heads, D / 8, 16 / size, kMaxTable / std::max(1, a.pairs));
+    a.deal = deal(T, heads, D / 8, 4, std::min(kWriteTokens, kMaxTable / std::max(1, a.pairs)));
     a.interleaved = (flags & RFP2_ROPE_INTERLEAVED) != 0;
     a.factor = factor;
     a.status = dev_status;
@@ -467,7 +485,7 @@ extern "C" rfp2_status rfp2_kv_read(const int8_t *k_codes, const float *k_scales
     a.heads = (int)heads;
     a.D = (int)D;
     a.status = dev_status;
-    a.deal = deal(T, heads, D * dtype_bytes(dtype) / 16, 2, 1024);
+    a.deal = deal(T, heads, D * dtype_bytes(dtype) / 16, 6, kReadTokens);
     const dim3 grid = grid_of(a.deal, T);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const size_t smem = 8 * (size_t)a.deal.tokens;
