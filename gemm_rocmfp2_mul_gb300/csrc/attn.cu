@@ -65,7 +65,7 @@ extern "C" rfp2_status rfp2_attn_decode(const void *q, int dtype, int64_t B, int
     a.heads = (int)heads;
     a.group = (int)(Hq / heads);
     a.columns = (int)(nq * a.group);
-    const int most = D <= 128 && a.columns > 8 ? 16 : 8;
+    const int most = attn_most_columns((int)D, dtype, a.columns);
     a.column_tiles = (a.columns + most - 1) / most;
     a.page_size = (int)page_size;
     a.page_shift = -1;

@@ -31,7 +31,7 @@
 namespace rfp2 {
 
 constexpr int kAttnTile = 16;        // keys
-constexpr int kAttnGap = 2;          // a unit's fixed cost, in tiles
+constexpr int kAttnGap = 4;          // a unit's fixed cost, in tiles
 constexpr int kAttnMinStretch = 1;   // of a warp, in tiles
 constexpr int kAttnWholeUnit = 4;    // tiles a warp up to which a unit stays in one CTA
 constexpr int kAttnInFlight = 112 * 1024;  // bytes of the cache on their way to an SM, at most
@@ -90,13 +90,17 @@ struct AttnPiece {
 constexpr int kPaired = 3;
 
 // Warps: the tile's work is a long chain, so as many as the registers hold.  By
-// head size x columns (what a warp accumulates): 128 values x 8 at 128 registers,
-// 16 warps (12 where two pieces of q take 168); beyond that 8.  Small ones run
-// two CTAs of 8.
+// head size x columns (what a warp accumulates): 12 up to 128 values x 16 at 168
+// registers, where q's fragments of 16 columns wait in shared memory; beyond that
+// 8.  Small ones run two CTAs of 8.
 template <int NB, int NT, int PIECES>
-constexpr int attn_warps() { return NB * NT <= 2 || NB * NT > 4 ? 8 : 12; }
+constexpr int attn_warps() { return NB * NT <= 2 || NB > 4 ? 8 : 12; }
 template <int NB, int NT>
 constexpr int attn_ctas_per_sm() { return NB * NT <= 2 ? 2 : 1; }
+// Bytes of a warp's q fragments in shared memory: each lane's own, for two column
+// tiles.
+template <int NB, int NT, int PIECES>
+constexpr int attn_q_bytes() { return NT == 2 ? NB * 2 * (PIECES == 2 ? 2 : 1) * NT * 256 : 0; }
 
 // The warps' sums of the scan, the pieces and their columns' states, and the
 // line's prefix.
@@ -108,15 +112,17 @@ template <int NB, int NT, int PIECES>
 constexpr int attn_stages() {
     constexpr int W = attn_warps<NB, NT, PIECES>();
     const int budget = (attn_ctas_per_sm<NB, NT>() == 2 ? 113 : 227) * 1024;
-    const int s = (budget - attn_small_bytes<W, NT>(kAttnMaxBatch)) / (W * AttnLayout<NB>::stage_bytes);
+    const int s = (budget - attn_small_bytes<W, NT>(kAttnMaxBatch) - W * attn_q_bytes<NB, NT, PIECES>()) /
+                  (W * AttnLayout<NB>::stage_bytes);
     // the tiles on their way to an SM; the last stage is the one that is worked on
     const int wanted = 1 + kAttnInFlight / (W * attn_ctas_per_sm<NB, NT>() * kAttnTile * NB * 72);
     return s < 2 || wanted < 2 ? 2 : s < wanted ? s : wanted;
 }
 template <int NB, int NT, int PIECES>
-int attn_smem(int B) {
+constexpr int attn_smem(int B) {
     constexpr int W = attn_warps<NB, NT, PIECES>();
-    return W * attn_stages<NB, NT, PIECES>() * AttnLayout<NB>::stage_bytes + attn_small_bytes<W, NT>(B);
+    return W * (attn_stages<NB, NT, PIECES>() * AttnLayout<NB>::stage_bytes + attn_q_bytes<NB, NT, PIECES>()) +
+           attn_small_bytes<W, NT>(B);
 }
 // Floats of one partial result: the columns' references and sums, and their
 // values.
@@ -237,13 +243,17 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT, PIECES>(), attn_ctas_p
     constexpr int D = L::D, STAGES = attn_stages<NB, NT, PIECES>(), COLS = 8 * NT, SLOT = attn_slot<NB, NT>();
     static_assert(SLOT * 4 <= STAGES * L::stage_bytes, "a warp's partial result fits its ring");
     static_assert(STAGES >= 2 && WARPS <= 16, "");
+    static_assert(attn_smem<NB, NT, PIECES>(kAttnMaxBatch) <= (attn_ctas_per_sm<NB, NT>() == 2 ? 113 : 227) * 1024, "");
     constexpr float kShift = 8.0f, kMost = 15.0f;  // p dV aims at 2^8 and stays below 2^15
     constexpr float kNone = -3.4e38f;              // the reference before any key
     // p is up to 2^15 / dV: 2^125 where the values are tiny (dV is taken as 2^-110 at least here)
     constexpr float kSumScale = 2.3283064365386963e-10f, kSumShift = 32.0f;  // 2^-32
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *rings = smem;
-    int *small = reinterpret_cast<int *>(rings + WARPS * STAGES * L::stage_bytes);  // 32
+    constexpr bool Q_SHARED = attn_q_bytes<NB, NT, PIECES>() > 0;
+    uint2 *q_frags = reinterpret_cast<uint2 *>(rings + WARPS * STAGES * L::stage_bytes);  // [warps][fragments][lanes]
+    int *small = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(q_frags) +
+                                         WARPS * attn_q_bytes<NB, NT, PIECES>());  // 32
     AttnPiece *pieces = reinterpret_cast<AttnPiece *>(small + 32);                  // [warps][head, tail]
     float *piece_r = reinterpret_cast<float *>(pieces + 2 * WARPS);                 // [pieces][COLS]
     float *piece_l = piece_r + 2 * WARPS * COLS;
@@ -579,7 +589,9 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT, PIECES>(), attn_ctas_p
         const int64_t max_begin = a.window ? len - a.nq + 1 + c_last / a.group - a.window : 0;
 
         // q of column g: values 32 n + 8 t4 .. + 7, scaled by a power of two
-        uint32_t qf[NT][NB][2][PARTS][2];
+        uint32_t qf[Q_SHARED ? 1 : NB][2][PARTS][2];
+        uint2 *q_mine = q_frags + warp * (attn_q_bytes<NB, NT, PIECES>() / 8) + lane;
+        const auto q_place = [](int nt, int n, int s, int part) { return (((nt * NB + n) * 2 + s) * PARTS + part) * 32; };
         float col_scale[NT][2];
         int up_most = 0, up_least = 0;
 #pragma unroll
@@ -645,19 +657,31 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT, PIECES>(), attn_ctas_p
             for (int n = 0; n < NB; ++n)
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
+{
+                    uint32_t part[2][2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const float u = v[n][4 * s + 2 * h] * by, w = v[n][4 * s + 2 * h + 1] * by;
                         const uint32_t hi = pack_f16(u, w);
-                        qf[nt][n][s][0][h] = hi;
+                        part[0][h] = hi;
                         if constexpr (WIDE) {
                             const uint32_t lo = rest_f16(hi, u, w);
                             if constexpr (PAIR)
-                                qf[nt][n][s][0][h] = g < 4 ? hi : lo;
+                                part[0][h] = g < 4 ? hi : lo;
                             else
-                                qf[nt][n][s][1][h] = lo;
+                                part[1][h] = lo;
                         }
                     }
+#pragma unroll
+                    for (int i = 0; i < PARTS; ++i) {
+                        if constexpr (Q_SHARED) {
+                            q_mine[q_place(nt, n, s, i)] = make_uint2(part[i][0], part[i][1]);
+                        } else {
+                            qf[n][s][i][0] = part[i][0];
+                            qf[n][s][i][1] = part[i][1];
+                        }
+                    }
+                }
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 col_scale[nt][e] = __uint_as_float(
@@ -753,8 +777,14 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT, PIECES>(), attn_ctas_p
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int piece = PARTS - 1; piece >= 0; --piece)
-                            mma_f16(c[nt], f, qf[nt][n][s][piece][0], qf[nt][n][s][piece][1]);
+                        for (int piece = PARTS - 1; piece >= 0; --piece) {
+                            if constexpr (Q_SHARED) {
+                                const uint2 q = q_mine[q_place(nt, n, s, piece)];
+                                mma_f16(c[nt], f, q.x, q.y);
+                            } else {
+                                mma_f16(c[nt], f, qf[n][s][piece][0], qf[n][s][piece][1]);
+                            }
+                        }
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -1125,17 +1155,20 @@ cudaError_t attn_launch(const AttnArgs &a, int sms, cudaStream_t stream) {
                   dim3(32 * attn_warps<NB, NT, PIECES>()), attn_smem<NB, NT, PIECES>(a.B), stream, true, a);
 }
 
-// Column tiles of 8 or, from 9 columns up, 16 (where the registers hold them).
-template <int NB>
-constexpr int attn_most_columns() { return NB <= 4 ? 16 : 8; }
+// Column tiles of 8 or, from 9 columns up, 16: a tile's codes are converted once
+// for all of them.  (Of heads past 128 values, fp32's two pieces for 16 columns
+// would not fit beside the ring.)
+inline int attn_most_columns(int D, int dtype, int columns) {
+    return columns > 8 && (D <= 128 || dtype != RFP2_F32) ? 16 : 8;
+}
 
 template <int NB>
 cudaError_t attn_by_columns(const AttnArgs &a, int sms, cudaStream_t stream) {
-    if constexpr (attn_most_columns<NB>() == 16)
-        if (a.columns > 8)
-            return a.dtype == RFP2_F32 ? attn_launch<NB, 2, 2>(a, sms, stream)
-                                       : attn_launch<NB, 2, 1>(a, sms, stream);
-    if (a.dtype != RFP2_F32) return attn_launch<NB, 1, 1>(a, sms, stream);
+    const bool two = attn_most_columns(32 * NB, a.dtype, a.columns) == 16;
+    if (a.dtype != RFP2_F32)
+        return two ? attn_launch<NB, 2, 1>(a, sms, stream) : attn_launch<NB, 1, 1>(a, sms, stream);
+    if constexpr (NB <= 4)
+        if (two) return attn_launch<NB, 2, 2>(a, sms, stream);
     return a.columns <= 4 ? attn_launch<NB, 1, kPaired>(a, sms, stream) : attn_launch<NB, 1, 2>(a, sms, stream);
 }
 
