@@ -275,11 +275,10 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT, PIECES>(), attn_ctas_p
         const int len = a.lens[b];
         return len < 0 || len > a.capacity ? -1 : len;
     };
-    const auto tile_low = [&](int len) {
-        if (a.window == 0) return 0;
-        const int64_t low = (int64_t)len - a.nq + 1 - a.window;
-        return low > 0 ? (int)(low / kAttnTile) : 0;
+    const auto first_key = [&](int len) {  // that any query sees
+        return a.window == 0 ? 0 : (int)max((int64_t)0, (int64_t)len - a.nq + 1 - a.window);
     };
+    const auto tile_low = [&](int len) { return first_key(len) / kAttnTile; };
     const auto cost_of = [&](int b) {
         const int len = length_of(b);
         if (len < 0 && blockIdx.x == 0) record_status(a.status, RFP2_EBADID);
@@ -478,12 +477,13 @@ __global__ void __launch_bounds__(32 * attn_warps<NB, NT, PIECES>(), attn_ctas_p
                     }
                 }
             } else {
-                // row of the cache arrays of key `lane`, or -1 (no such key), -2 (no such page)
+                // row of the cache arrays of key `lane`, or -1 (no such key, or out of sight: its page may be
+                // another's by now), -2 (no such page)
                 constexpr uint32_t kNoKey = 0xFFFFFFFFu, kNoPage = 0xFFFFFFFEu;
                 uint32_t row = kNoKey;
                 const int j = key0 + (lane & (kAttnTile - 1));
                 const int32_t own_page = __shfl_sync(0xffffffffu, page, (lt - page_at) * kAttnTile + (lane & (kAttnTile - 1)));
-                if (j < l_len) {
+                if (j < l_len && j >= first_key(l_len)) {
                     if (own_page < 0 || own_page >= a.pages) {
                         row = kNoPage;
                         record_status(a.status, RFP2_EBADID);
