@@ -7,6 +7,11 @@
 // loads of its steps (eight neighbouring values of a head's row, four threads a
 // block of 32); the place of each token in the cache and, for a rotation, each
 // (token, pair)'s cos and sin are computed once into shared memory meanwhile.
+//
+// Measured (one GB300, back to back), 16384 tokens x 8 heads of 128 values, bf16:
+// write 24.6 us, rotated 30.3 (105 MB; the instructions, 169 a warp of 8-value
+// steps, set the pace), read 19.2 us (5.5 TB/s).  Eight fp32 tokens: 2.1 and 1.7.
+// Codes by division took 47 us.
 #include <algorithm>
 
 #include "activation.cuh"

