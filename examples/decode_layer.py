@@ -35,7 +35,9 @@ class Layer:
         self.table = order.view(batch, pages)
         self.lens = torch.zeros(batch, dtype=torch.int32, device="cuda")
         self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
-        self.workspace = g.rfp2_attn_decode_workspace(torch.empty((batch, 1, HEADS, D), device="cuda"), KV_HEADS)
+        # for a prompt's tokens at once, and so for one
+        longest = torch.empty(1, device="cuda").expand(batch, capacity, HEADS, D)
+        self.workspace = g.rfp2_attn_decode_workspace(longest, KV_HEADS)
         self.gemv_workspace = [torch.empty(g.rfp2_gemv_workspace_bytes(batch, K), dtype=torch.uint8, device="cuda")
                                for K in (HIDDEN, HEADS * D)]
 

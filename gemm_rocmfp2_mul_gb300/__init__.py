@@ -461,6 +461,7 @@ def rfp2_debug_wait_timeout(dev_status):
 
 _ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3}
 _ROPE_INTERLEAVED, _ROPE_INVERSE = 1, 2
+_ATTN_ZERO_BYTES = 4096
 _native = None
 
 
@@ -554,12 +555,13 @@ def rfp2_attn_decode_workspace_bytes(B: int, nq: int, Hq: int, heads: int, D: in
 
 
 def rfp2_attn_decode_workspace(q, heads):
-    """A zeroed workspace for rfp2_attn_decode of q [B, nq, Hq, D] over `heads` key heads; calls in
-    one stream may share it."""
-    torch = _torch()
+    """A workspace for rfp2_attn_decode of q [B, nq, Hq, D] over `heads` key heads, its head zeroed;
+    calls in one stream may share it."""
     B, nq, Hq, D = q.shape
-    return torch.zeros(rfp2_attn_decode_workspace_bytes(B, nq, Hq, heads, D), dtype=torch.uint8,
-                       device=q.device)
+    workspace = _empty(max(rfp2_attn_decode_workspace_bytes(B, nq, Hq, heads, D), _ATTN_ZERO_BYTES),
+                       _torch().uint8, q)
+    workspace[:_ATTN_ZERO_BYTES].zero_()
+    return workspace
 
 
 def rfp2_attn_decode(q, cache, table, lens, scale=None, window=0, softcap=0.0, out=None, lse=None,
@@ -568,7 +570,7 @@ def rfp2_attn_decode(q, cache, table, lens, scale=None, window=0, softcap=0.0, o
     [B, width] of pages, lens int32 [B] of keys held (the nq newest among them).  Returns out
     [B, nq, Hq, D] of q's type and lse fp32 [B, nq, Hq].  scale: D**-0.5 unless given; window: only the
     last `window` keys (0: all); softcap: scores become softcap * tanh(s / softcap) (0: as they are).
-    workspace: from rfp2_attn_decode_workspace (zero before its first use)."""
+    workspace: from rfp2_attn_decode_workspace."""
     if out is None or lse is None or workspace is None:
         if q.dim() != 4:
             raise ValueError(f"q must have 4 dimensions, got {q.dim()}")

@@ -6,19 +6,13 @@
 
 using namespace rfp2;
 
-namespace {
-
-// Partial results: two a CTA and one for each of up to 16 warps, of 16 columns'
-// references, sums and values.
-size_t partial_bytes(int64_t D) { return (size_t)(32 + 16 * D) * 4; }
-
-}  // namespace
-
 extern "C" size_t rfp2_attn_decode_workspace_bytes(int64_t B, int64_t nq, int64_t Hq,
                                                    int64_t heads, int64_t D) {
     if (B < 1 || nq < 1 || Hq < 1 || heads < 1 || Hq % heads != 0 || D < 32 || D > 256) return 0;
-    return kAttnCounterBytes +
-           2 * (size_t)sm_count(current_device()) * (2 + 16) * partial_bytes(D);
+    // partial results: two a CTA and one a warp, of as many columns as a tile may have
+    const int NB = (int)(D / 32), NT = nq * (Hq / heads) > 8 ? 2 : 1;
+    const size_t ctas = (size_t)sm_count(current_device()) * attn_ctas_per_sm(NB, NT);
+    return RFP2_ATTN_ZERO_BYTES + ctas * (2 + attn_warps(NB, NT)) * attn_slot(NB, NT) * 4;
 }
 
 extern "C" rfp2_status rfp2_attn_decode(const void *q, int dtype, int64_t B, int64_t nq,
@@ -79,14 +73,14 @@ extern "C" rfp2_status rfp2_attn_decode(const void *q, int dtype, int64_t B, int
     a.softcap = softcap;
     a.window = std::min<int64_t>(window, 1ll << 30);
     a.counters = static_cast<int *>(workspace);
-    a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kAttnCounterBytes);
+    a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + RFP2_ATTN_ZERO_BYTES);
     a.status = dev_status;
     constexpr int64_t kLine = (1ll << 31) - 1;
     const int64_t line = (a.capacity / kAttnTile + 1 + kAttnGap) * a.heads * a.column_tiles;
     if (line > kLine) return RFP2_ESHAPE;
     static const AttnFn kinds[] = {attn_d32,  attn_d64,  attn_d96,  attn_d128,
                                    attn_d160, attn_d192, attn_d224, attn_d256};
-    const int sms = std::min(sm_count(current_device()), kAttnCounterBytes / 8);
+    const int sms = std::min(sm_count(current_device()), RFP2_ATTN_ZERO_BYTES / 8);
     // a launch keeps its sequences' places on the line, 32-bit numbers, in shared memory
     for (int64_t b0 = 0; b0 < B; b0 += a.B) {
         a.B = (int)std::min<int64_t>({B - b0, kAttnMaxBatch, kLine / line});

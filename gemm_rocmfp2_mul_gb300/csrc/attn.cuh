@@ -53,7 +53,6 @@ constexpr int kAttnWholeUnit = 4;
 // stages of 12 warps (64 sequences, 2.4 GB): 373 us, 356 and 368.
 constexpr int kAttnInFlight = 112 * 1024;
 constexpr int kAttnMaxBatch = 1024;  // sequences of one launch
-constexpr int kAttnCounterBytes = 4096;
 
 struct AttnArgs {
     const void *q;
@@ -110,10 +109,8 @@ constexpr int kPaired = 3;
 // head size x columns (what a warp accumulates): 12 up to 128 values x 16 at 168
 // registers, where q's fragments of 16 columns wait in shared memory; beyond that
 // 8.  Small ones run two CTAs of 8.
-template <int NB, int NT, int PIECES>
-constexpr int attn_warps() { return NB * NT <= 2 || NB > 4 ? 8 : 12; }
-template <int NB, int NT>
-constexpr int attn_ctas_per_sm() { return NB * NT <= 2 ? 2 : 1; }
+constexpr int attn_warps(int NB, int NT) { return NB * NT <= 2 || NB > 4 ? 8 : 12; }
+constexpr int attn_ctas_per_sm(int NB, int NT) { return NB * NT <= 2 ? 2 : 1; }
 // Bytes of a warp's q fragments in shared memory: each lane's own, for two column
 // tiles.
 template <int NB, int NT, int PIECES>
@@ -127,24 +124,23 @@ constexpr int attn_small_bytes(int B) {
 }
 template <int NB, int NT, int PIECES>
 constexpr int attn_stages() {
-    constexpr int W = attn_warps<NB, NT, PIECES>();
-    const int budget = (attn_ctas_per_sm<NB, NT>() == 2 ? 113 : 227) * 1024;
+    constexpr int W = attn_warps(NB, NT);
+    const int budget = (attn_ctas_per_sm(NB, NT) == 2 ? 113 : 227) * 1024;
     const int s = (budget - attn_small_bytes<W, NT>(kAttnMaxBatch) - W * attn_q_bytes<NB, NT, PIECES>()) /
                   (W * AttnLayout<NB>::stage_bytes);
     // the tiles on their way to an SM; the last stage is the one that is worked on
-    const int wanted = 1 + kAttnInFlight / (W * attn_ctas_per_sm<NB, NT>() * kAttnTile * NB * 72);
+    const int wanted = 1 + kAttnInFlight / (W * attn_ctas_per_sm(NB, NT) * kAttnTile * NB * 72);
     return s < 2 || wanted < 2 ? 2 : s < wanted ? s : wanted;
 }
 template <int NB, int NT, int PIECES>
 constexpr int attn_smem(int B) {
-    constexpr int W = attn_warps<NB, NT, PIECES>();
+    constexpr int W = attn_warps(NB, NT);
     return W * (attn_stages<NB, NT, PIECES>() * AttnLayout<NB>::stage_bytes + attn_q_bytes<NB, NT, PIECES>()) +
            attn_small_bytes<W, NT>(B);
 }
 // Floats of one partial result: the columns' references and sums, and their
 // values.
-template <int NB, int NT>
-constexpr int attn_slot() { return 8 * NT * (2 + 32 * NB); }
+constexpr int attn_slot(int NB, int NT) { return 8 * NT * (2 + 32 * NB); }
 
 RFP2_DEV void cp_async16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -250,17 +246,17 @@ struct AttnShare {
 };
 
 template <int NB, int NT, int PIECES>
-__global__ void __launch_bounds__(32 * attn_warps<NB, NT, PIECES>(), attn_ctas_per_sm<NB, NT>())
+__global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, NT))
     attn_kernel(const AttnArgs a) {
     using L = AttnLayout<NB>;
-    constexpr int WARPS = attn_warps<NB, NT, PIECES>(), THREADS = 32 * WARPS;
+    constexpr int WARPS = attn_warps(NB, NT), THREADS = 32 * WARPS;
     constexpr bool WIDE = PIECES != 1, PAIR = PIECES == kPaired;  // fp32 activations; their pieces as columns
     constexpr int PARTS = PIECES == 2 ? 2 : 1, PER = PAIR ? 4 : 8;  // fragments of an operand; columns of a tile
     static_assert(!PAIR || NT == 1, "");
-    constexpr int D = L::D, STAGES = attn_stages<NB, NT, PIECES>(), COLS = 8 * NT, SLOT = attn_slot<NB, NT>();
+    constexpr int D = L::D, STAGES = attn_stages<NB, NT, PIECES>(), COLS = 8 * NT, SLOT = attn_slot(NB, NT);
     static_assert(SLOT * 4 <= STAGES * L::stage_bytes, "a warp's partial result fits its ring");
     static_assert(STAGES >= 2 && WARPS <= 16, "");
-    static_assert(attn_smem<NB, NT, PIECES>(kAttnMaxBatch) <= (attn_ctas_per_sm<NB, NT>() == 2 ? 113 : 227) * 1024, "");
+    static_assert(attn_smem<NB, NT, PIECES>(kAttnMaxBatch) <= (attn_ctas_per_sm(NB, NT) == 2 ? 113 : 227) * 1024, "");
     constexpr float kShift = 8.0f, kMost = 15.0f;  // p dV aims at 2^8 and stays below 2^15
     constexpr float kNone = -3.4e38f;              // the reference before any key
     // p is up to 2^15 / dV: 2^125 where the values are tiny (dV is taken as 2^-110 at least here)
@@ -1168,8 +1164,8 @@ cudaError_t attn_launch(const AttnArgs &a, int sms, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         if (device < 64) ready[device].store(1, std::memory_order_relaxed);
     }
-    return launch(attn_kernel<NB, NT, PIECES>, dim3((unsigned)(sms * attn_ctas_per_sm<NB, NT>())),
-                  dim3(32 * attn_warps<NB, NT, PIECES>()), attn_smem<NB, NT, PIECES>(a.B), stream, true, a);
+    return launch(attn_kernel<NB, NT, PIECES>, dim3((unsigned)(sms * attn_ctas_per_sm(NB, NT))),
+                  dim3(32 * attn_warps(NB, NT)), attn_smem<NB, NT, PIECES>(a.B), stream, true, a);
 }
 
 // Column tiles of 8 or, from 9 columns up, 16: a tile's codes are converted once

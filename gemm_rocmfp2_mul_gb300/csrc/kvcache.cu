@@ -9,9 +9,12 @@
 // (token, pair)'s cos and sin are computed once into shared memory meanwhile.
 //
 // Measured (one GB300, back to back), 16384 tokens x 8 heads of 128 values, bf16:
-// write 24.6 us, rotated 30.3 (105 MB; the instructions, 169 a warp of 8-value
-// steps, set the pace), read 19.2 us (5.5 TB/s).  Eight fp32 tokens: 2.1 and 1.7.
-// Codes by division took 47 us.
+// write 25.8 us, rotated 30.7 (105 MB; the instructions, 169 a warp of 8-value
+// steps, set the pace), read 19.0 us (5.5 TB/s).  Eight fp32 tokens: 2.1 and 1.7.
+// Codes by division took 47 us.  Writes at three CTAs of 80 registers an SM against
+// four of 64: 30.7 and 30.3 us, but 6.0 and 7.3 for 4999 tokens of 5 x 96 f16, whose
+// interleaved rotation spills at 64; reads at five against six: 19.0 and 19.2, 3.75
+// and 4.1.
 #include <algorithm>
 
 #include "activation.cuh"
@@ -20,7 +23,7 @@ namespace rfp2 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWriteTokens = 28, kReadTokens = 18;  // of a CTA, at most
+constexpr int kWriteTokens = 36, kReadTokens = 22;  // of a CTA, at most
 constexpr int kMaxTable = 4096;  // (token, pair) entries of a CTA's table
 
 // A token's steps (a head's eight or, reading fp32, four values of key and of
@@ -186,7 +189,7 @@ RFP2_DEV void write_block(const float (&x)[8], int8_t *codes, float *scale, bool
 }
 
 template <typename T, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 4) kv_write_kernel(const WriteArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) kv_write_kernel(const WriteArgs a) {
     constexpr int AHEAD = 4 / sizeof(T);
     extern __shared__ __align__(16) uint8_t smem[];
     float *table = reinterpret_cast<float *>(smem);                                       // [tokens][cos, sin][pairs]
@@ -315,7 +318,7 @@ RFP2_DEV void read_word(const uint32_t (&w)[E / 4], float d, T *out) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 6) kv_read_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) kv_read_kernel(const ReadArgs a) {
     constexpr int E = 16 / sizeof(T), AHEAD = 1;
     extern __shared__ int64_t place[];  // [tokens]
     pdl_wait();
@@ -448,7 +451,7 @@ extern "C" rfp2_status rfp2_kv_write(const void *k, const void *v, int dtype, in
     a.D = (int)D;
     a.pairs = positions ? (int)(R / 2) : 0;
     a.by_pairs = FastDiv(std::max(1, a.pairs));
-    a.deal = deal(T, heads, D / 8, 4, std::min(kWriteTokens, kMaxTable / std::max(1, a.pairs)));
+    a.deal = deal(T, heads, D / 8, 3, std::min(kWriteTokens, kMaxTable / std::max(1, a.pairs)));
     a.interleaved = (flags & RFP2_ROPE_INTERLEAVED) != 0;
     a.factor = factor;
     a.status = dev_status;
@@ -490,7 +493,7 @@ extern "C" rfp2_status rfp2_kv_read(const int8_t *k_codes, const float *k_scales
     a.heads = (int)heads;
     a.D = (int)D;
     a.status = dev_status;
-    a.deal = deal(T, heads, D * dtype_bytes(dtype) / 16, 6, kReadTokens);
+    a.deal = deal(T, heads, D * dtype_bytes(dtype) / 16, 5, kReadTokens);
     const dim3 grid = grid_of(a.deal, T);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const size_t smem = 8 * (size_t)a.deal.tokens;

@@ -9,9 +9,10 @@
 // sin of its (token, pair)s once into shared memory while they travel.
 //
 // Measured (one GB300, back to back): 16383 x 20 heads of 192, f16, 64 rotated:
-// 44.3 us, 5.7 TB/s read and written (copy rate 6.8); 2048 x 40 x 128 bf16: 10.4
-// us; 4 x 32 x 128 fp32: 1.9 us.  Two steps ahead at four CTAs an SM beat four at
-// three (45.9 and 11.3 us); 32-bit angles from fp64 products took twice as long.
+// 41.4 us, 6.1 TB/s read and written (copy rate 6.8); 2048 x 40 x 128 bf16: 9.3
+// us; 4 x 32 x 128 fp32: 1.9 us.  Two steps ahead at five CTAs an SM, a whole number
+// of times, beat two at four (43.2 and 9.8 us), one at eight (41.5 and 9.3) and four at
+// three (45.9 and 11.3); 32-bit angles from fp64 products took twice as long.
 #include <algorithm>
 
 #include "activation.cuh"
@@ -21,6 +22,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kAhead = 2;        // steps of a thread whose loads travel together
+constexpr int kSteps = 8;        // of a thread, about, at most
 constexpr int kMaxPairs = 2048;  // (token, pair) entries of a CTA's table
 
 struct RopeArgs {
@@ -54,7 +56,7 @@ struct alignas(V * sizeof(T)) Runs {
 };
 
 template <typename T, int V, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) rope_kernel(const RopeArgs a) {
     extern __shared__ __align__(16) float table[];  // [tokens][cos, sin][pairs]
     pdl_wait();
     pdl_launch_dependents();
@@ -141,17 +143,20 @@ cudaError_t launch_rope(RopeArgs &a, bool interleaved, bool copy, cudaStream_t s
     const int V = wide ? W : 1;
     a.turned = a.pairs / V;
     a.steps = a.turned + (copy ? (a.D / 2 - a.pairs) / V : 0);
-    // up to 8 steps a thread: tokens share a CTA where a token's heads are fewer, and heads are divided
-    // where they are more.  But a few CTAs for every SM before that, so that none waits for another.
-    constexpr int kSteps = 8 * kThreads;
-    const int64_t ctas = 6 * (int64_t)sm_count(current_device());
-    a.heads = std::max(1, std::min(a.H, kSteps / std::max(1, a.steps)));
-    while (a.heads > 1 && a.heads * a.steps > kThreads && a.T * ((a.H + a.heads - 1) / a.heads) < ctas)
+    // Up to kSteps steps a thread: tokens share a CTA where a token's heads are fewer, and heads are
+    // divided where they are more, or where there are few tokens.  The tokens are dealt so that the CTAs
+    // fill the SMs, five on each, a whole number of times.
+    constexpr int kMost = kSteps * kThreads;
+    const int64_t at_once = 5 * (int64_t)sm_count(current_device());
+    a.heads = std::max(1, std::min(a.H, kMost / std::max(1, a.steps)));
+    while (a.heads > 1 && a.heads * a.steps > kThreads && a.T * ((a.H + a.heads - 1) / a.heads) < at_once)
         a.heads = (a.heads + 1) / 2;
     a.tokens = 1;
     if (a.heads == a.H) {
-        const int64_t most = std::min<int64_t>(kSteps / (a.heads * std::max(1, a.steps)), a.T / ctas);
-        a.tokens = (int)std::max<int64_t>(1, std::min<int64_t>(most, kMaxPairs / std::max(1, a.pairs)));
+        const int64_t most = std::max<int64_t>(
+            1, std::min(kMost / (a.heads * std::max(1, a.steps)), kMaxPairs / std::max(1, a.pairs)));
+        const int64_t waves = (a.T + at_once * most - 1) / (at_once * most);
+        a.tokens = (int)((a.T + at_once * waves - 1) / (at_once * waves));
     }
     a.by_pairs = FastDiv(std::max(1, a.pairs));
     a.by_steps = FastDiv(std::max(1, a.steps));

@@ -470,9 +470,10 @@ rfp2_status rfp2_kv_read(const int8_t *k_codes, const float *k_scales, const int
  *        of that page's keys may stay finite) and stores RFP2_EBADID, as does
  *        a length outside [0, table_width * page_size].
  *   workspace  device, 256-byte aligned, of
- *        rfp2_attn_decode_workspace_bytes(B, nq, Hq, heads, D) bytes, ZERO
- *        before its first use; every call leaves it fit for the next one of
- *        any sizes.  Calls that overlap on the GPU must not share it.
+ *        rfp2_attn_decode_workspace_bytes(B, nq, Hq, heads, D) bytes, the
+ *        first RFP2_ATTN_ZERO_BYTES of them ZERO before its first use; every
+ *        call leaves it fit for the next one, of any sizes that it is large
+ *        enough for.  Calls that overlap on the GPU must not share it.
  * The length is split over the GPU and joined in a fixed order: the same call
  * gives the same bits.
  * Errors: EINVAL, ESHAPE (Hq % heads, D, page_size, B or nq < 1, nq * Hq >
@@ -480,6 +481,7 @@ rfp2_status rfp2_kv_read(const int8_t *k_codes, const float *k_scales, const int
  * ceil(nq * Hq / heads / 8)); table_stride < table_width, pages *
  * heads * page_size >= 2^32), EALIGN, EWORKSPACE, ECUDA.
  */
+#define RFP2_ATTN_ZERO_BYTES 4096
 size_t rfp2_attn_decode_workspace_bytes(int64_t B, int64_t nq, int64_t Hq, int64_t heads,
                                         int64_t D);
 rfp2_status rfp2_attn_decode(const void *q, int dtype, int64_t B, int64_t nq, int64_t Hq,
