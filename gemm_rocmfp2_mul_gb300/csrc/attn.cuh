@@ -18,8 +18,9 @@
 // Products run on f16 matrix instructions (16 keys x 8 columns x 16 values):
 // codes are exact in f16, q goes in scaled by a power of two (one f16 piece is
 // exact for 16-bit q; two pieces leave 2^-22 of fp32 q).  The scores' block sums
-// are scaled by dK in fp32.  p dV goes in as one f16 piece for 16-bit outputs
-// and two for fp32.  Its range: the softmax's reference r is kept near
+// are scaled by dK in fp32.  p dV goes in as one f16 piece for bf16 outputs, whose
+// rounding is eight times coarser, and two for f16 (one alone would cost as much
+// as the output's rounding) and fp32.  Its range: the softmax's reference r is kept near
 // max(s + log2 dV) instead of max s, so p dV stays below 2^15 whatever the
 // scales of the values are, and what is lost lies 2^-33 below the largest.
 //
@@ -100,10 +101,12 @@ struct AttnPiece {
     int unit0;            // the unit's place on the line
 };
 
-// PIECES of the f16 operands: 1 for 16-bit activations; 2 for fp32, taken by two
-// products; kPaired for fp32 of up to four columns, the second pieces being
-// columns 4 .. 7 of the same products.
+// How q and p dV go into the products as f16 pieces.  kPaired is for up to four
+// columns of fp32 or f16: the second pieces are columns 4 .. 7 of the products.
+constexpr int kBf16 = 1;    // one piece each
+constexpr int kF32 = 2;     // two pieces each
 constexpr int kPaired = 3;
+constexpr int kF16 = 4;     // one piece of q, two of p dV
 
 // Warps: the tile's work is a long chain, so as many as the registers hold.  By
 // head size x columns (what a warp accumulates): 12 up to 128 values x 16 at 168
@@ -114,7 +117,7 @@ constexpr int attn_ctas_per_sm(int NB, int NT) { return NB * NT <= 2 ? 2 : 1; }
 // Bytes of a warp's q fragments in shared memory: each lane's own, for two column
 // tiles.
 template <int NB, int NT, int PIECES>
-constexpr int attn_q_bytes() { return NT == 2 ? NB * 2 * (PIECES == 2 ? 2 : 1) * NT * 256 : 0; }
+constexpr int attn_q_bytes() { return NT == 2 ? NB * 2 * (PIECES == kF32 ? 2 : 1) * NT * 256 : 0; }
 
 // The warps' sums of the scan, the pieces and their columns' states, and the
 // line's prefix.
@@ -250,8 +253,10 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
     attn_kernel(const AttnArgs a) {
     using L = AttnLayout<NB>;
     constexpr int WARPS = attn_warps(NB, NT), THREADS = 32 * WARPS;
-    constexpr bool WIDE = PIECES != 1, PAIR = PIECES == kPaired;  // fp32 activations; their pieces as columns
-    constexpr int PARTS = PIECES == 2 ? 2 : 1, PER = PAIR ? 4 : 8;  // fragments of an operand; columns of a tile
+    constexpr bool PAIR = PIECES == kPaired;
+    constexpr int Q_PARTS = PIECES == kF32 ? 2 : 1, P_PARTS = PIECES == kF32 || PIECES == kF16 ? 2 : 1;
+    constexpr int PER = PAIR ? 4 : 8;  // columns of a tile
+    const bool fp32 = PIECES == kF32 || (PAIR && a.dtype == RFP2_F32);  // the activations
     static_assert(!PAIR || NT == 1, "");
     constexpr int D = L::D, STAGES = attn_stages<NB, NT, PIECES>(), COLS = 8 * NT, SLOT = attn_slot(NB, NT);
     static_assert(SLOT * 4 <= STAGES * L::stage_bytes, "a warp's partial result fits its ring");
@@ -435,12 +440,12 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
     enter();
     // a unit's rows of q on their way while the unit before is worked on
     const auto prefetch_q = [&](const AttnPlace &p) {
-        constexpr int LINES = D * (WIDE ? 4 : 2) / 64;  // at least one address of each 128-byte line
+        const int size = fp32 ? 4 : 2, lines = D * size / 64;  // at least one address of each 128-byte line
         const int c0 = p.ct * COLS, live = min(COLS, a.columns - c0);
-        for (int k = lane; k < live * LINES; k += 32) {
-            const int c = c0 + k / LINES, i = c / a.group, h = p.hk * a.group + c - i * a.group;
+        for (int k = lane; k < live * lines; k += 32) {
+            const int cl = k / lines, c = c0 + cl, i = c / a.group, h = p.hk * a.group + c - i * a.group;
             const int64_t at = p.b * a.qb + i * a.qt + h * a.qh;
-            const char *src = static_cast<const char *>(a.q) + at * (WIDE ? 4 : 2) + (k % LINES) * 64;
+            const char *src = static_cast<const char *>(a.q) + at * size + (k - cl * lines) * 64;
             asm volatile("prefetch.global.L1 [%0];" ::"l"(src));
         }
     };
@@ -546,11 +551,11 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
     };
     const auto store_four = [&](int64_t row, int d, const float (&y)[4]) {
         const int64_t at = row * D + d;
-        if (WIDE) {
+        if (fp32) {
             *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
         } else {
             uint2 u;
-            if (a.dtype == RFP2_BF16) {
+            if (PIECES == kBf16) {
                 __nv_bfloat16 v[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = from_f32<__nv_bfloat16>(y[e]);
@@ -602,9 +607,9 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
         const int64_t max_begin = a.window ? len - a.nq + 1 + c_last / a.group - a.window : 0;
 
         // q of column g: values 32 n + 8 t4 .. + 7, scaled by a power of two
-        uint32_t qf[Q_SHARED ? 1 : NB][2][PARTS][2];
+        uint32_t qf[Q_SHARED ? 1 : NB][2][Q_PARTS][2];
         uint2 *q_mine = q_frags + warp * (attn_q_bytes<NB, NT, PIECES>() / 8) + lane;
-        const auto q_place = [](int nt, int n, int s, int part) { return (((nt * NB + n) * 2 + s) * PARTS + part) * 32; };
+        const auto q_place = [](int nt, int n, int s, int part) { return (((nt * NB + n) * 2 + s) * Q_PARTS + part) * 32; };
         float col_scale[NT][2];
         int up_most = 0, up_least = 0;
 #pragma unroll
@@ -618,7 +623,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
             if (c < a.columns) {
                 const int i = c / a.group, h = p.hk * a.group + c - i * a.group;
                 const int64_t at = p.b * a.qb + i * a.qt + h * a.qh + 8 * t4;
-                if (WIDE) {
+                if (fp32) {
                     const float *src = static_cast<const float *>(a.q) + at;
                     if (a.q_words) {
 #pragma unroll
@@ -643,7 +648,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
                         }
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            v[n][e] = a.dtype == RFP2_BF16 ? __uint_as_float((uint32_t)u[e] << 16)
+                            v[n][e] = PIECES == kBf16 ? __uint_as_float((uint32_t)u[e] << 16)
                                                            : __half2float(__ushort_as_half(u[e]));
                     }
                 }
@@ -677,16 +682,11 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
                         const float u = v[n][4 * s + 2 * h] * by, w = v[n][4 * s + 2 * h + 1] * by;
                         const uint32_t hi = pack_f16(u, w);
                         part[0][h] = hi;
-                        if constexpr (WIDE) {
-                            const uint32_t lo = rest_f16(hi, u, w);
-                            if constexpr (PAIR)
-                                part[0][h] = g < 4 ? hi : lo;
-                            else
-                                part[1][h] = lo;
-                        }
+                        if constexpr (PAIR) part[0][h] = g < 4 ? hi : rest_f16(hi, u, w);
+                        if constexpr (Q_PARTS == 2) part[1][h] = rest_f16(hi, u, w);
                     }
 #pragma unroll
-                    for (int i = 0; i < PARTS; ++i) {
+                    for (int i = 0; i < Q_PARTS; ++i) {
                         if constexpr (Q_SHARED) {
                             q_mine[q_place(nt, n, s, i)] = make_uint2(part[i][0], part[i][1]);
                         } else {
@@ -790,7 +790,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int piece = PARTS - 1; piece >= 0; --piece) {
+                        for (int piece = Q_PARTS - 1; piece >= 0; --piece) {
                             if constexpr (Q_SHARED) {
                                 const uint2 q = q_mine[q_place(nt, n, s, piece)];
                                 mma_f16(c[nt], f, q.x, q.y);
@@ -821,7 +821,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        sc[nt][e] = WIDE ? a.softcap * tanhf(sc[nt][e] / a.softcap) * 1.4426950408889634f
+                        sc[nt][e] = fp32 ? a.softcap * tanhf(sc[nt][e] / a.softcap) * 1.4426950408889634f
                                          : tanh_16(sc[nt][e] * cap_in, cap_out);
             if (!whole) {
                 // out of sight: no weight, whatever the value's scale is there
@@ -870,7 +870,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
                 }
 
             // p dV in the layout that the products take it in
-            uint32_t pb[NB][NT][PARTS][2];
+            uint32_t pb[NB][NT][P_PARTS][2];
             const auto weigh = [&](bool odd) {
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
@@ -888,7 +888,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
                                 pb[n][nt][0][k] = transpose8x8(t4 < 2 ? hi : rest_f16(hi, u, w));
                             else
                                 pb[n][nt][0][k] = transpose8x8(hi);
-                            if constexpr (PARTS == 2) pb[n][nt][1][k] = transpose8x8(rest_f16(hi, u, w));
+                            if constexpr (P_PARTS == 2) pb[n][nt][1][k] = transpose8x8(rest_f16(hi, u, w));
                         }
             };
             if (odd)
@@ -915,14 +915,15 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
                                            less_1152(__byte_perm(v, 0x64646464u, 0x4342))};
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        if constexpr (WIDE) {
+                        if constexpr (PIECES == kF32 || PAIR) {
                             // the matrix unit cuts sums off; a long chain of them is kept in fp32 adds
                             float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            if constexpr (PARTS == 2) mma_f16(c, f, pb[n][nt][1][0], pb[n][nt][1][1]);
+                            if constexpr (P_PARTS == 2) mma_f16(c, f, pb[n][nt][1][0], pb[n][nt][1][1]);
                             mma_f16(c, f, pb[n][nt][0][0], pb[n][nt][0][1]);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) o[nt][n][h][e] += c[e];
                         } else {
+                            if constexpr (P_PARTS == 2) mma_f16(o[nt][n][h], f, pb[n][nt][1][0], pb[n][nt][1][1]);
                             mma_f16(o[nt][n][h], f, pb[n][nt][0][0], pb[n][nt][0][1]);
                         }
                     }
@@ -1178,11 +1179,14 @@ inline int attn_most_columns(int D, int dtype, int columns) {
 template <int NB>
 cudaError_t attn_by_columns(const AttnArgs &a, int sms, cudaStream_t stream) {
     const bool two = attn_most_columns(32 * NB, a.dtype, a.columns) == 16;
-    if (a.dtype != RFP2_F32)
-        return two ? attn_launch<NB, 2, 1>(a, sms, stream) : attn_launch<NB, 1, 1>(a, sms, stream);
+    if (a.dtype == RFP2_BF16)
+        return two ? attn_launch<NB, 2, kBf16>(a, sms, stream) : attn_launch<NB, 1, kBf16>(a, sms, stream);
+    if (a.columns <= 4) return attn_launch<NB, 1, kPaired>(a, sms, stream);
+    if (a.dtype == RFP2_F16)
+        return two ? attn_launch<NB, 2, kF16>(a, sms, stream) : attn_launch<NB, 1, kF16>(a, sms, stream);
     if constexpr (NB <= 4)
-        if (two) return attn_launch<NB, 2, 2>(a, sms, stream);
-    return a.columns <= 4 ? attn_launch<NB, 1, kPaired>(a, sms, stream) : attn_launch<NB, 1, 2>(a, sms, stream);
+        if (two) return attn_launch<NB, 2, kF32>(a, sms, stream);
+    return attn_launch<NB, 1, kF32>(a, sms, stream);
 }
 
 // By blocks of 32 values a head; each is instantiated in one translation unit.
