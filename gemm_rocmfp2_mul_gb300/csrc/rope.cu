@@ -211,7 +211,7 @@ extern "C" rfp2_status rfp2_rope(const void *x, int dtype, int64_t T, int64_t H,
         return RFP2_EINVAL;
     if (R < 0 || R % 2 != 0 || D % 2 != 0 || R > D || R > 2 * kMaxPairs) return RFP2_ESHAPE;
     if (T == 0 || H == 0 || D == 0) return RFP2_OK;
-    if (D > 65536 || H > 65536 || T > (1ll << 31) - 1) return RFP2_ESHAPE;
+    if (D > 65536 || H > 65535 || T > (1ll << 31) - 1) return RFP2_ESHAPE;
     if (!x || !out || !positions || (R > 0 && !inv_freq)) return RFP2_EINVAL;
     if (!aligned(x, size) || !aligned(out, size) || !aligned(positions, 4) || !aligned(inv_freq, 4))
         return RFP2_EALIGN;

@@ -411,7 +411,7 @@ rfp2_status rfp2_rope_frequencies(int64_t R, double base, int scaling, double st
  *   positions int32 [T], any value; inv_freq fp32 [R/2], finite; both device.
  *   flags RFP2_ROPE_*.
  * Errors: EINVAL (null, negative size, bad dtype or flags), ESHAPE (R or D
- * odd, R < 0, R > D or R > 4096, D or H > 65536, T > 2^31 - 1), EALIGN (a
+ * odd, R < 0, R > D or R > 4096, D > 65536, H > 65535, T > 2^31 - 1), EALIGN (a
  * pointer not aligned to its type), ECUDA.
  */
 rfp2_status rfp2_rope(const void *x, int dtype, int64_t T, int64_t H, int64_t D,
