@@ -62,9 +62,9 @@ extern "C" rfp2_status rfp2_attn_decode(const void *q, int dtype, int64_t B, int
     const int most = attn_most_columns((int)D, dtype, a.columns);
     a.column_tiles = (a.columns + most - 1) / most;
     a.page_size = (int)page_size;
-    a.page_shift = -1;
-    for (int s = 0; s < 31; ++s)
-        if (page_size == (1ll << s)) a.page_shift = s;
+    a.by_page = FastDiv((uint32_t)page_size);
+    a.by_group = FastDiv((uint32_t)a.group);
+    a.by_tiles = FastDiv((uint32_t)a.column_tiles);
     a.whole_pages = page_size % kAttnTile == 0;
     a.dtype = dtype;
     const int64_t words = 16 / size;

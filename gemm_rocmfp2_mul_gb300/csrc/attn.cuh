@@ -63,9 +63,14 @@ struct AttnArgs {
     const int32_t *table, *lens;
     int64_t pages, table_stride, capacity;
     int B, nq, Hq, heads, group, columns, column_tiles;
-    int page_size, page_shift;  // shift: log2 of page_size, or -1
+    int page_size;
     int whole_pages;            // page_size % 16 == 0: a tile lies in one page
     int dtype, q_words;         // q_words: q can be read as 16-byte words
+    // divisors of the launch, multiplied by: a division by a value only known at
+    // run time is some 25 instructions on the way to the first load, and again at
+    // every unit (12 x 5 tokens of 16 heads over 2, D = 64, pages of 48: 13.5 ->
+    // 12.7 us; 7 x 16 heads of D = 256, pages of 33: 33.2 -> 31.2)
+    FastDiv by_page, by_group, by_tiles;  // page_size, group, column_tiles
     float scale, softcap;
     int64_t window;
     void *out;
@@ -360,7 +365,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
         first.b = b;
         first.tiles = cost - kAttnGap;
         first.unit0 = prefix[b] * units_of + unit * cost;
-        first.hk = a.column_tiles == 1 ? unit : unit / a.column_tiles;
+        first.hk = a.by_tiles(unit);
         first.ct = unit - first.hk * a.column_tiles;
         return cost;
     };
@@ -415,9 +420,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
     int page_at = 0;
     const auto pages_from = [&](int t) {
         const int j = (l_low + t) * kAttnTile + lane * key_step;
-        return j < l_len ? a.table[lp.b * a.table_stride +
-                                   (a.page_shift >= 0 ? j >> a.page_shift : j / a.page_size)]
-                         : -1;
+        return j < l_len ? a.table[lp.b * a.table_stride + a.by_page(j)] : -1;
     };
     // enters units until one has tiles in this stretch
     const auto enter = [&]() {
@@ -440,10 +443,10 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
     enter();
     // a unit's rows of q on their way while the unit before is worked on
     const auto prefetch_q = [&](const AttnPlace &p) {
-        const int size = fp32 ? 4 : 2, lines = D * size / 64;  // at least one address of each 128-byte line
+        const int size = fp32 ? 4 : 2, lines = fp32 ? 2 * NB : NB;  // of 64 bytes: one address at least of each 128
         const int c0 = p.ct * COLS, live = min(COLS, a.columns - c0);
         for (int k = lane; k < live * lines; k += 32) {
-            const int cl = k / lines, c = c0 + cl, i = c / a.group, h = p.hk * a.group + c - i * a.group;
+            const int cl = (fp32 ? k >> 1 : k) / NB, c = c0 + cl, i = a.by_group(c), h = p.hk * a.group + c - i * a.group;
             const int64_t at = p.b * a.qb + i * a.qt + h * a.qh;
             const char *src = static_cast<const char *>(a.q) + at * size + (k - cl * lines) * 64;
             asm volatile("prefetch.global.L1 [%0];" ::"l"(src));
@@ -477,7 +480,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
                     for (int i = 0; i < (kAttnTile * NB + 31) / 32; ++i)
                         if (lane + 32 * i < kAttnTile * NB) p[lane + 32 * i] = CUDART_NAN_F;
                 } else {
-                    const uint32_t off = a.page_shift >= 0 ? key0 & (a.page_size - 1) : key0 % a.page_size;
+                    const uint32_t off = key0 - a.by_page(key0) * a.page_size;
                     const uint32_t row = ((uint32_t)next_page * a.heads + lp.hk) * a.page_size + off;
                     const int8_t *kp = a.k_codes + (int64_t)row * D + 16 * lane;
                     const int8_t *vp = a.v_codes + (int64_t)row * D + 16 * lane;
@@ -506,7 +509,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
                         row = kNoPage;
                         record_status(a.status, RFP2_EBADID);
                     } else {
-                        const uint32_t off = a.page_shift >= 0 ? j & (a.page_size - 1) : j % a.page_size;
+                        const uint32_t off = j - a.by_page(j) * a.page_size;
                         row = ((uint32_t)own_page * a.heads + lp.hk) * a.page_size + off;
                     }
                 }
@@ -546,7 +549,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
 
     // ---- outputs: four values d .. d + 3 of column c of a unit, and its lse ----
     const auto row_of = [&](int b, int hk, int cg) {
-        const int i = cg / a.group;
+        const int i = a.by_group(cg);
         return ((int64_t)b * a.nq + i) * a.Hq + hk * a.group + cg - i * a.group;
     };
     const auto store_four = [&](int64_t row, int d, const float (&y)[4]) {
@@ -600,11 +603,11 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int c = min(p.ct * COLS + column_of(nt, e), a.columns - 1);
-                col_end[nt][e] = len - a.nq + 1 + c / a.group;
+                col_end[nt][e] = len - a.nq + 1 + (int)a.by_group(c);
             }
         const int c_last = min(p.ct * COLS + COLS, a.columns) - 1;
-        const int min_end = len - a.nq + 1 + p.ct * COLS / a.group;
-        const int64_t max_begin = a.window ? len - a.nq + 1 + c_last / a.group - a.window : 0;
+        const int min_end = len - a.nq + 1 + (int)a.by_group(p.ct * COLS);
+        const int64_t max_begin = a.window ? len - a.nq + 1 + (int)a.by_group(c_last) - a.window : 0;
 
         // q of column g: values 32 n + 8 t4 .. + 7, scaled by a power of two
         uint32_t qf[Q_SHARED ? 1 : NB][2][Q_PARTS][2];
@@ -621,7 +624,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[n][e] = 0.0f;
             if (c < a.columns) {
-                const int i = c / a.group, h = p.hk * a.group + c - i * a.group;
+                const int i = a.by_group(c), h = p.hk * a.group + c - i * a.group;
                 const int64_t at = p.b * a.qb + i * a.qt + h * a.qh + 8 * t4;
                 if (fp32) {
                     const float *src = static_cast<const float *>(a.q) + at;
