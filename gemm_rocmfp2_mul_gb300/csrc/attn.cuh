@@ -22,11 +22,11 @@
 // rounding is eight times coarser, and two for f16 (one alone would cost as much
 // as the output's rounding) and fp32.  Its range: the softmax's reference r is kept near
 // max(s + log2 dV) instead of max s, so p dV stays below 2^15 whatever the
-// scales of the values are, and what is lost lies 2^-33 below the largest.
+// scales of the values are, and what is lost lies 2^-32 below the largest.
 //
 // Measured (one GB300, back to back): 64 sequences of up to 32768 keys, 64 heads
 // over 8 of 128, bf16: 351-361 us for 2.39 GB (6.6-6.8 TB/s; copy rate 6.8); one of
-// 131072 keys, 40 over 8: 56 us (5.4 TB/s); 16 of up to 8192, 32 over 8, fp32: 40
+// 131072 keys, 40 over 8: 55 us (5.5 TB/s); 16 of up to 8192, 32 over 8, fp32: 40
 // us (4.7 TB/s); one of 1000 keys: 9.3 us, of 16: 4.9 us.  The start (three
 // dependent reads) and the joins take about 8 us of a long call; on the way the
 // memory sets the pace, with 508 instructions a tile of 8 columns x 128 values
@@ -69,7 +69,7 @@ struct AttnArgs {
     // divisors of the launch, multiplied by: a division by a value only known at
     // run time is some 25 instructions on the way to the first load, and again at
     // every unit (12 x 5 tokens of 16 heads over 2, D = 64, pages of 48: 13.5 ->
-    // 12.7 us; 7 x 16 heads of D = 256, pages of 33: 33.2 -> 31.2)
+    // 12.7 us; 7 x 16 heads of D = 256, pages of 33: 33.2 -> 31.2 us)
     FastDiv by_page, by_group, by_tiles;  // page_size, group, column_tiles
     float scale, softcap;
     int64_t window;
@@ -210,11 +210,6 @@ RFP2_DEV float tanh_16(float x, float cap_out) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(exp2_fast(x) + 1.0f));
     return fmaf(-2.0f * cap_out, r, cap_out);
 }
-RFP2_DEV float log2_fast(float x) {
-    float y;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // A key's NB scales, in the widest words that divide its row.
 template <int NB>
@@ -267,10 +262,14 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
     static_assert(SLOT * 4 <= STAGES * L::stage_bytes, "a warp's partial result fits its ring");
     static_assert(STAGES >= 2 && WARPS <= 16, "");
     static_assert(attn_smem<NB, NT, PIECES>(kAttnMaxBatch) <= (attn_ctas_per_sm(NB, NT) == 2 ? 113 : 227) * 1024, "");
-    constexpr float kShift = 8.0f, kMost = 15.0f;  // p dV aims at 2^8 and stays below 2^15
+    // p = 2^(s - r + 15), with r the largest s + lg so far: lg is 4 floor((e + 8) / 4) for dV of exponent e,
+    // so that p dV lies between 2^7 and 2^11 there and, r staying while s + lg <= r + 4, below 2^15.  lg is 0
+    // for values of ordinary size: r is a score then, and s - r and the lse keep the digits of a score near 0.
+    constexpr float kShift = 15.0f, kSlack = 4.0f;
     constexpr float kNone = -3.4e38f;              // the reference before any key
-    // p is up to 2^15 / dV: 2^125 where the values are tiny (dV is taken as 2^-110 at least here)
-    constexpr float kSumScale = 2.3283064365386963e-10f, kSumShift = 32.0f;  // 2^-32
+    // p is up to 2^(19 - lg): 2^127 where the values are tiny (lg is -108 at least)
+    constexpr int kLeast = -108;
+    constexpr float kSumScale = 2.3283064365386963e-10f;  // 2^-32
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *rings = smem;
     constexpr bool Q_SHARED = attn_q_bytes<NB, NT, PIECES>() > 0;
@@ -573,7 +572,10 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
         }
     };
     const auto lse_of = [&](float m, float l) {
-        return l == 0.0f ? -CUDART_INF_F : (m + kSumShift) * 0.6931471805599453f + logf(l);
+        const float whole = l * 131072.0f;  // sum of 2^(s - r): 2^(32 - 15) l
+        return l == 0.0f ? -CUDART_INF_F
+                         : m * 0.6931471805599453f +
+                               (whole <= 3.4e38f ? logf(whole) : logf(l) + 11.783502069519070f);
     };
 
     // four values d .. d + 3 of column c of a unit that is joined: references and sums m and l
@@ -717,7 +719,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
             }
 
         float o[NT][NB][2][4];          // [column tile][block][pair of values][accumulator]
-        float ref[NT][2], sum[NT][2];   // r - 8, and this lane's share of the sum of p, times 2^-32
+        float ref[NT][2], sum[NT][2];   // r, and this lane's share of the sum of p, times 2^-32
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -762,8 +764,8 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
                     }
                 }
             }
-            const float lg[2] = {fmaxf(log2_fast(__uint_as_float(top_d[0])), -110.0f),
-                                 fmaxf(log2_fast(__uint_as_float(top_d[1])), -110.0f)};
+            const float lg[2] = {(float)max((int)((top_d[0] >> 23) - 119u) & ~3, kLeast),
+                                 (float)max((int)((top_d[1] >> 23) - 119u) & ~3, kLeast)};
             if (far)
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
@@ -839,14 +841,14 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) more |= sc[nt][e] - ref[nt][e & 1] + lg[e >> 1] > kMost;
+                for (int e = 0; e < 4; ++e) more |= sc[nt][e] - ref[nt][e & 1] + lg[e >> 1] > kSlack;
             if (__any_sync(0xffffffffu, more)) {
                 // a larger reference for the columns that need one
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float m = fmaxf(sc[nt][e] + lg[0], sc[nt][e + 2] + lg[1]) - kShift;
+                        float m = fmaxf(sc[nt][e] + lg[0], sc[nt][e + 2] + lg[1]);
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
@@ -868,7 +870,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    pr[nt][e] = exp2_fast(sc[nt][e] - ref[nt][e & 1]);
+                    pr[nt][e] = exp2_fast(sc[nt][e] - ref[nt][e & 1] + kShift);
                     sum[nt][e & 1] += pr[nt][e] * kSumScale;
                 }
 

@@ -185,6 +185,21 @@ def test_value_scales_of_any_size(g, dtype):
     c.check(*_run(g, c))
 
 
+def test_lse_of_one_key_is_its_score(g):
+    """Near 0 as well: no constant of the kernel's own may round it.  The score's own bound ds (above) and
+    the roundings of the way to base 2 and back, 2^-21 of it."""
+    for D, Hq, Hkv, small in ((128, 4, 4, 2.0 ** -10), (64, 16, 2, 2.0 ** -14), (256, 5, 1, 1.0)):
+        c = Case(3, 1, Hq, Hkv, D, 16, 1, seed=11)
+        c.vs[:] = np.float32(1 / 60)
+        c.q = c.q * small
+        _, lse = _run(g, c)
+        q = c.q.double().numpy()[:, 0].reshape(3, Hkv, Hq // Hkv, D)
+        k = np.stack([k[0] for k in c.k])[:, :, None]
+        s, size = ((x * k).sum(-1).reshape(3, Hq) * c.scale for x in (q, np.abs(q) * np.sign(k)))
+        err = np.abs(lse.double().cpu().numpy()[:, 0] - s)
+        assert (err <= 2.0 ** -19 * size + 2.0 ** -21 * np.abs(s)).all(), (err / np.abs(s)).max()
+
+
 def test_queries_of_any_size(g):
     import torch
     for size in (2.0 ** -120, 2.0 ** 100):
