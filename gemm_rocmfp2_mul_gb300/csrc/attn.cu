@@ -70,7 +70,8 @@ extern "C" rfp2_status rfp2_attn_decode(const void *q, int dtype, int64_t B, int
     const int64_t words = 16 / size;
     a.q_words = aligned(q, 16) && a.qb % words == 0 && a.qt % words == 0 && a.qh % words == 0;
     a.scale = scale;
-    a.softcap = softcap;
+    // a cap so far off moves no score below 2^48; its reciprocal's products would be subnormal
+    a.softcap = softcap < 0x1p60f ? softcap : 0.0f;
     a.window = std::min<int64_t>(window, 1ll << 30);
     a.counters = static_cast<int *>(workspace);
     a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + RFP2_ATTN_ZERO_BYTES);

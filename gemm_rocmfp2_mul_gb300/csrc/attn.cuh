@@ -203,14 +203,6 @@ RFP2_DEV float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// cap_out tanh(x / 2 log2 e) = cap_out (1 - 2 / (2^x + 1)): off by 2e-7 cap_out,
-// far below the rounding of 16-bit outputs.
-RFP2_DEV float tanh_16(float x, float cap_out) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(exp2_fast(x) + 1.0f));
-    return fmaf(-2.0f * cap_out, r, cap_out);
-}
-
 // A key's NB scales, in the widest words that divide its row.
 template <int NB>
 RFP2_DEV void load_scales(const float *p, float (&d)[NB]) {
@@ -590,7 +582,9 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
 
     // ---- the units of this stretch ----
     const float cap_out = a.softcap * 1.4426950408889634f;
-    const float cap_in = 2.8853900817779268f / a.softcap;  // 2 log2 e / softcap
+    // tanhf for 16-bit types too, 13.0 -> 13.4 us of 12 x 5 tokens: the lse of few keys shows an error of
+    // 2e-7 of the cap, as 1 - 2 / (e^2x + 1) has it near 0
+    const float cap_in = fminf(1.0f / a.softcap, 3.402823466e38f);
     int stage = 0;
     bool filled = false;
     for (AttnPlace p = first; p.unit0 + kAttnGap < y1; next_unit(p)) {
@@ -826,8 +820,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        sc[nt][e] = fp32 ? a.softcap * tanhf(sc[nt][e] / a.softcap) * 1.4426950408889634f
-                                         : tanh_16(sc[nt][e] * cap_in, cap_out);
+                        sc[nt][e] = cap_out * tanhf(sc[nt][e] * cap_in);
             if (!whole) {
                 // out of sight: no weight, whatever the value's scale is there
 #pragma unroll

@@ -460,6 +460,7 @@ rfp2_status rfp2_kv_read(const int8_t *k_codes, const float *k_scales, const int
  * sees the keys j < lens[b] - nq + 1 + i, and with window > 0 only the last
  * `window` of those.  Query head h reads key head h / (Hq / heads):
  *   s = scale * q . k,  with softcap > 0: s = softcap * tanh(s / softcap)
+ *   (a softcap of 2^60 or more is none)
  *   out = sum_j softmax(s)_j v_j,  lse = log sum_j exp(s_j) (natural).
  * A query that sees no key gets out = 0 and lse = -infinity.
  *   q    `dtype` [B, nq, Hq, D] device: D contiguous, any other strides.

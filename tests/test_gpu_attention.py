@@ -200,6 +200,28 @@ def test_lse_of_one_key_is_its_score(g):
         assert (err <= 2.0 ** -19 * size + 2.0 ** -21 * np.abs(s)).all(), (err / np.abs(s)).max()
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+def test_lse_of_one_key_under_a_cap(g, dtype):
+    """cap tanh(s / cap): the score's bound ds, and 2^-20 of the result for the reciprocal, the products, the
+    tangent's two units in the last place and the way to base 2 and back.  A cap of 2^60 and more is none."""
+    import torch
+    c = Case(3, 1, 8, 4, 128, 16, 1, seed=12, dtype=dtype)
+    c.vs[:] = np.float32(1 / 60)
+    c.q = c.q * torch.tensor([2.0 ** -12, 2.0 ** -4, 1, 8, 2.0 ** -12, 2.0 ** -4, 1, 8]).to(c.q.dtype).view(8, 1)
+    q = c.q.double().numpy()[:, 0].reshape(3, 4, 2, 128)
+    k = np.stack([k[0] for k in c.k])[:, :, None]
+    s, size = ((x * k).sum(-1).reshape(3, 8) * c.scale for x in (q, np.abs(q) * np.sign(k)))
+    for cap in (30.0, 0.5, 1000.0):
+        _, lse = _run(g, c, softcap=cap)
+        want = cap * np.tanh(s / cap)
+        err = np.abs(lse.double().cpu().numpy()[:, 0] - want)
+        assert (err <= 2.0 ** -19 * size + 2.0 ** -20 * np.abs(want)).all(), (cap, (err / np.abs(want)).max())
+    plain_out, plain_lse = _run(g, c)
+    for cap in (2.0 ** 60, 3e38, float("inf")):
+        out, lse = _run(g, c, softcap=cap)
+        assert torch.equal(out, plain_out) and torch.equal(lse, plain_lse)
+
+
 def test_queries_of_any_size(g):
     import torch
     for size in (2.0 ** -120, 2.0 ** 100):
