@@ -25,7 +25,7 @@
 // scales of the values are, and what is lost lies 2^-32 below the largest.
 //
 // Measured (one GB300, back to back): 64 sequences of up to 32768 keys, 64 heads
-// over 8 of 128, bf16: 351-361 us for 2.39 GB (6.6-6.8 TB/s; copy rate 6.8); one of
+// over 8 of 128, bf16: 351-357 us for 2.39 GB (6.7-6.8 TB/s; copy rate 6.8); one of
 // 131072 keys, 40 over 8: 55 us (5.5 TB/s); 16 of up to 8192, 32 over 8, fp32: 40
 // us (4.7 TB/s); one of 1000 keys: 9.3 us, of 16: 4.9 us.  The start (three
 // dependent reads) and the joins take about 8 us of a long call; on the way the
