@@ -15,22 +15,24 @@
 // at the end: within the CTA through shared memory, between CTAs through the
 // workspace by the last of them to arrive, always in the order of the keys.
 //
-// Products run on f16 matrix instructions (16 keys x 8 columns x 16 values):
-// codes are exact in f16, q goes in scaled by a power of two (one f16 piece is
-// exact for 16-bit q; two pieces leave 2^-22 of fp32 q).  The scores' block sums
-// are scaled by dK in fp32.  p dV goes in as one f16 piece for bf16 outputs, whose
-// rounding is eight times coarser, and two for f16 (one alone would cost as much
-// as the output's rounding) and fp32.  Its range: the softmax's reference r is kept near
-// max(s + log2 dV) instead of max s, so p dV stays below 2^15 whatever the
-// scales of the values are, and what is lost lies 2^-32 below the largest.
+// Products run on 16-bit matrix instructions (16 keys x 8 columns x 16 values).
+// Scores: codes are exact in f16, q goes in scaled by a power of two (one f16
+// piece is exact for 16-bit q down to 2^-28 of its row's largest value; two leave
+// 2^-22 of fp32 q; neither less than 2^-39 of the largest), and the block sums are
+// scaled by dK in fp32.  Outputs: codes are exact in bf16 as well, and p dV goes in
+// as bf16 pieces, which have fp32's range: however far apart the weights of the
+// keys and the scales of a row's blocks are, each product keeps its own digits.
+// Two pieces (the first 8 bits of p dV, and the rest rounded to 8) leave 2^-15 of
+// it for 16-bit outputs, three are all 24 bits for fp32.  (f16 pieces, one for bf16
+// outputs, took 353 us where these take 386, 55 where 60 and 40.5 where 45 below,
+// but needed one exponent for all blocks of a key and lost what lay far below.)
 //
 // Measured (one GB300, back to back): 64 sequences of up to 32768 keys, 64 heads
-// over 8 of 128, bf16: 351-357 us for 2.39 GB (6.7-6.8 TB/s; copy rate 6.8); one of
-// 131072 keys, 40 over 8: 55 us (5.5 TB/s); 16 of up to 8192, 32 over 8, fp32: 40
-// us (4.7 TB/s); one of 1000 keys: 9.3 us, of 16: 4.9 us.  The start (three
-// dependent reads) and the joins take about 8 us of a long call; on the way the
-// memory sets the pace, with 508 instructions a tile of 8 columns x 128 values
-// in 54 % of the issue slots.
+// over 8 of 128, bf16: 386 us for 2.39 GB (6.2 TB/s; copy rate 6.7); one of 131072
+// keys, 40 over 8: 60 us (5.0 TB/s); 16 of up to 8192, 32 over 8, fp32: 45 us (4.2
+// TB/s); one of 1000 keys: 9.4 us.  The start (three dependent reads) and the joins
+// take about 8 us of a long call; on the way the instructions of three warps a
+// scheduler set the pace: 580 a tile of 8 columns x 128 values, 716 for fp32.
 #pragma once
 
 #include <atomic>
@@ -106,12 +108,12 @@ struct AttnPiece {
     int unit0;            // the unit's place on the line
 };
 
-// How q and p dV go into the products as f16 pieces.  kPaired is for up to four
-// columns of fp32 or f16: the second pieces are columns 4 .. 7 of the products.
-constexpr int kBf16 = 1;    // one piece each
-constexpr int kF32 = 2;     // two pieces each
-constexpr int kPaired = 3;
-constexpr int kF16 = 4;     // one piece of q, two of p dV
+// How q and p dV go into the products as pieces.  The kinds for up to four columns
+// have second pieces as columns 4 .. 7 of the products.
+constexpr int kHalf = 1;      // 16-bit activations: one piece of q, two of p dV
+constexpr int kF32 = 2;       // two of q, three of p dV
+constexpr int kPairHalf = 3;  // up to four columns
+constexpr int kPairF32 = 4;
 
 // Warps: the tile's work is a long chain, so as many as the registers hold.  By
 // head size x columns (what a warp accumulates): 12 up to 128 values x 16 at 168
@@ -173,6 +175,13 @@ RFP2_DEV void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The same with bf16 in.
+RFP2_DEV void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 RFP2_DEV uint32_t transpose8x8(uint32_t a) {
     uint32_t d;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -197,6 +206,27 @@ RFP2_DEV uint32_t rest_f16(uint32_t h, float lo, float hi) {
         : "=f"(u), "=f"(v)
         : "r"(h), "f"(lo), "f"(hi));
     return pack_f16(-u, -v);
+}
+// Two codes, bytes 0 and 2 of h, as two bf16 of a 64th of them, exact: a byte u as the bits of a bf16 is u 2^-133 (up
+// to the smallest normal binade they are linear), u = code + 128, and a fused product with 2^127 takes 2 off.
+RFP2_DEV uint32_t codes_bf16(uint32_t h) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;"
+        : "=r"(d)
+        : "r"((h & 0x00FF00FFu) ^ 0x00800080u), "r"(0x7F007F00u), "r"(0xC000C000u));
+    return d;
+}
+// The first 8 bits of (lo, hi) as two bf16, and what is left of them, exact.
+RFP2_DEV uint32_t first_bf16(float &lo, float &hi) {
+    const uint32_t u = __float_as_uint(lo), w = __float_as_uint(hi);
+    lo -= __uint_as_float(u & 0xFFFF0000u);
+    hi -= __uint_as_float(w & 0xFFFF0000u);
+    return __byte_perm(u, w, 0x7632);
+}
+RFP2_DEV uint32_t pack_bf16(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
 }
 RFP2_DEV float exp2_fast(float x) {
     float y;
@@ -245,23 +275,20 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
     attn_kernel(const AttnArgs a) {
     using L = AttnLayout<NB>;
     constexpr int WARPS = attn_warps(NB, NT), THREADS = 32 * WARPS;
-    constexpr bool PAIR = PIECES == kPaired;
-    constexpr int Q_PARTS = PIECES == kF32 ? 2 : 1, P_PARTS = PIECES == kF32 || PIECES == kF16 ? 2 : 1;
+    constexpr bool PAIR = PIECES == kPairHalf || PIECES == kPairF32;
+    constexpr bool fp32 = PIECES == kF32 || PIECES == kPairF32;  // the activations
+    constexpr int Q_PARTS = PIECES == kF32 ? 2 : 1, P_PARTS = PIECES == kPairHalf ? 1 : PIECES == kF32 ? 3 : 2;
     constexpr int PER = PAIR ? 4 : 8;  // columns of a tile
-    const bool fp32 = PIECES == kF32 || (PAIR && a.dtype == RFP2_F32);  // the activations
     static_assert(!PAIR || NT == 1, "");
     constexpr int D = L::D, STAGES = attn_stages<NB, NT, PIECES>(), COLS = 8 * NT, SLOT = attn_slot(NB, NT);
     static_assert(SLOT * 4 <= STAGES * L::stage_bytes, "a warp's partial result fits its ring");
     static_assert(STAGES >= 2 && WARPS <= 16, "");
     static_assert(attn_smem<NB, NT, PIECES>(kAttnMaxBatch) <= (attn_ctas_per_sm(NB, NT) == 2 ? 113 : 227) * 1024, "");
-    // p = 2^(s - r + 15), with r the largest s + lg so far: lg is 4 floor((e + 8) / 4) for dV of exponent e,
-    // so that p dV lies between 2^7 and 2^11 there and, r staying while s + lg <= r + 4, below 2^15.  lg is 0
-    // for values of ordinary size: r is a score then, and s - r and the lse keep the digits of a score near 0.
-    constexpr float kShift = 15.0f, kSlack = 4.0f;
+    // p = 64 * 2^(s - r - 4), with r the largest s but for at most 4: it goes with a 64th of the codes, so that their
+    // product is a value at most
+    constexpr float kShift = 2.0f, kSlack = 4.0f;
+    constexpr float kCodes = 64.0f;                // the products' codes are 64ths
     constexpr float kNone = -3.4e38f;              // the reference before any key
-    // p is up to 2^(19 - lg): 2^127 where the values are tiny (lg is -108 at least)
-    constexpr int kLeast = -108;
-    constexpr float kSumScale = 2.3283064365386963e-10f;  // 2^-32
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *rings = smem;
     constexpr bool Q_SHARED = attn_q_bytes<NB, NT, PIECES>() > 0;
@@ -549,7 +576,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
             *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
         } else {
             uint2 u;
-            if (PIECES == kBf16) {
+            if (a.dtype == RFP2_BF16) {
                 __nv_bfloat16 v[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = from_f32<__nv_bfloat16>(y[e]);
@@ -564,15 +591,12 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
         }
     };
     const auto lse_of = [&](float m, float l) {
-        const float whole = l * 131072.0f;  // sum of 2^(s - r): 2^(32 - 15) l
-        return l == 0.0f ? -CUDART_INF_F
-                         : m * 0.6931471805599453f +
-                               (whole <= 3.4e38f ? logf(whole) : logf(l) + 11.783502069519070f);
+        return l == 0.0f ? -CUDART_INF_F : m * 0.6931471805599453f + logf(l * 0.25f);
     };
 
     // four values d .. d + 3 of column c of a unit that is joined: references and sums m and l
     const auto finish = [&](const AttnPiece &u, int c, int d, float (&y)[4], float m, float l) {
-        const float inv = l == 0.0f ? 0.0f : kSumScale / l;
+        const float inv = l == 0.0f ? 0.0f : kCodes / l;
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] *= inv;
         const int64_t row = row_of(u.b, u.hk, u.ct * COLS + c);
@@ -647,7 +671,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
                         }
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            v[n][e] = PIECES == kBf16 ? __uint_as_float((uint32_t)u[e] << 16)
+                            v[n][e] = a.dtype == RFP2_BF16 ? __uint_as_float((uint32_t)u[e] << 16)
                                                            : __half2float(__ushort_as_half(u[e]));
                     }
                 }
@@ -681,7 +705,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
                         const float u = v[n][4 * s + 2 * h] * by, w = v[n][4 * s + 2 * h + 1] * by;
                         const uint32_t hi = pack_f16(u, w);
                         part[0][h] = hi;
-                        if constexpr (PAIR) part[0][h] = g < 4 ? hi : rest_f16(hi, u, w);
+                        if constexpr (PIECES == kPairF32) part[0][h] = g < 4 ? hi : rest_f16(hi, u, w);
                         if constexpr (Q_PARTS == 2) part[1][h] = rest_f16(hi, u, w);
                     }
 #pragma unroll
@@ -713,7 +737,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
             }
 
         float o[NT][NB][2][4];          // [column tile][block][pair of values][accumulator]
-        float ref[NT][2], sum[NT][2];   // r, and this lane's share of the sum of p, times 2^-32
+        float ref[NT][2], sum[NT][2];   // r, and this lane's share of the sum of p
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -737,29 +761,11 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
 
             // scales of keys g and g + 8
             float dk[2][NB], dv[2][NB];
-            uint32_t top_d[2] = {0u, 0u};
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 load_scales<NB>(ks + (g + 8 * k) * NB, dk[k]);
                 load_scales<NB>(vs + (g + 8 * k) * NB, dv[k]);
-#pragma unroll
-                for (int n = 0; n < NB; ++n) top_d[k] = max(top_d[k], __float_as_uint(dv[k][n]));
             }
-            // an infinite, NaN or negative scale is no measure of range
-            const bool odd = __any_sync(0xffffffffu, max(top_d[0], top_d[1]) >= 0x7F800000u);
-            if (odd) {
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    top_d[k] = 0u;
-#pragma unroll
-                    for (int n = 0; n < NB; ++n) {
-                        const uint32_t u = __float_as_uint(dv[k][n]) & 0x7FFFFFFFu;
-                        top_d[k] = max(top_d[k], u < 0x7F800000u ? u : 0u);
-                    }
-                }
-            }
-            const float lg[2] = {(float)max((int)((top_d[0] >> 23) - 119u) & ~3, kLeast),
-                                 (float)max((int)((top_d[1] >> 23) - 119u) & ~3, kLeast)};
             if (far)
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
@@ -805,7 +811,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
                         sc[nt][e] = n ? sc[nt][e] + dk[e >> 1][n] * c[nt][e] : dk[e >> 1][n] * c[nt][e];
             }
 
-            if constexpr (PAIR)
+            if constexpr (PIECES == kPairF32)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sc[0][e] += __shfl_xor_sync(0xffffffffu, sc[0][e], 2);
 
@@ -821,8 +827,8 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         sc[nt][e] = cap_out * tanhf(sc[nt][e] * cap_in);
+            bool odd = false;  // a scale that is not finite, where some column may not see its key
             if (!whole) {
-                // out of sight: no weight, whatever the value's scale is there
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -830,18 +836,22 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
                         const int j = key0 + g + 8 * (e >> 1), end = col_end[nt][e & 1];
                         if (j >= end || (a.window && j < end - a.window)) sc[nt][e] = -CUDART_INF_F;
                     }
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+                    odd |= !(fabsf(dv[0][n]) <= 3.402823466e38f) || !(fabsf(dv[1][n]) <= 3.402823466e38f);
+                odd = __any_sync(0xffffffffu, odd);
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) more |= sc[nt][e] - ref[nt][e & 1] + lg[e >> 1] > kSlack;
+                for (int e = 0; e < 4; ++e) more |= sc[nt][e] - ref[nt][e & 1] > kSlack;
             if (__any_sync(0xffffffffu, more)) {
                 // a larger reference for the columns that need one
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float m = fmaxf(sc[nt][e] + lg[0], sc[nt][e + 2] + lg[1]);
+                        float m = fmaxf(sc[nt][e], sc[nt][e + 2]);
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
@@ -864,14 +874,15 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     pr[nt][e] = exp2_fast(sc[nt][e] - ref[nt][e & 1] + kShift);
-                    sum[nt][e & 1] += pr[nt][e] * kSumScale;
+                    sum[nt][e & 1] += pr[nt][e];
                 }
 
-            // p dV in the layout that the products take it in
-            uint32_t pb[NB][NT][P_PARTS][2];
-            const auto weigh = [&](bool odd) {
+            // values: out^T += V^T (p dV), keys 2 t4, + 1, + 8, + 9
+            const auto values = [&](bool odd) {
 #pragma unroll
-                for (int n = 0; n < NB; ++n)
+                for (int n = 0; n < NB; ++n) {
+                    // p dV in the layout that the products take it in
+                    uint32_t pb[NT][P_PARTS][2];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -881,52 +892,57 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
                                 if (sc[nt][2 * k] == -CUDART_INF_F) u = 0.0f;
                                 if (sc[nt][2 * k + 1] == -CUDART_INF_F) w = 0.0f;
                             }
-                            const uint32_t hi = pack_f16(u, w);
-                            if constexpr (PAIR)
-                                pb[n][nt][0][k] = transpose8x8(t4 < 2 ? hi : rest_f16(hi, u, w));
-                            else
-                                pb[n][nt][0][k] = transpose8x8(hi);
-                            if constexpr (P_PARTS == 2) pb[n][nt][1][k] = transpose8x8(rest_f16(hi, u, w));
+                            const uint32_t hi = first_bf16(u, w);
+                            if constexpr (PIECES == kHalf) {
+                                pb[nt][0][k] = transpose8x8(hi);
+                                pb[nt][1][k] = transpose8x8(pack_bf16(u, w));
+                            } else if constexpr (PIECES == kPairHalf) {
+                                pb[nt][0][k] = transpose8x8(t4 < 2 ? hi : pack_bf16(u, w));
+                            } else {
+                                const uint32_t mid = first_bf16(u, w), lo = first_bf16(u, w);
+                                if constexpr (PIECES == kF32) {
+                                    pb[nt][0][k] = transpose8x8(hi);
+                                    pb[nt][1][k] = transpose8x8(mid);
+                                    pb[nt][2][k] = transpose8x8(lo);
+                                } else {
+                                    pb[nt][0][k] = transpose8x8(t4 < 2 ? hi : mid);
+                                    pb[nt][1][k] = transpose8x8(t4 < 2 ? lo : 0u);
+                                }
+                            }
                         }
-            };
-            if (odd)
-                weigh(true);
-            else
-                weigh(false);
-
-            // values: out^T += V^T (p dV), keys 2 t4, + 1, + 8, + 9
+                    const uint8_t *vp = vt + 2 * t4 * L::v_stride + 32 * (n ^ L::v_order(2 * t4)) + 4 * g;
+                    uint32_t w[4];
 #pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                const uint8_t *vp = vt + 2 * t4 * L::v_stride + 32 * (n ^ L::v_order(2 * t4)) + 4 * g;
-                uint32_t w[4];
+                    for (int k = 0; k < 4; ++k)
+                        w[k] = *reinterpret_cast<const uint32_t *>(vp + ((k & 1) + 8 * (k >> 1)) * L::v_stride);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    w[k] = *reinterpret_cast<const uint32_t *>(vp + ((k & 1) + 8 * (k >> 1)) * L::v_stride);
+                    for (int h = 0; h < 2; ++h) {  // values 4 g + 2 h and 4 g + 2 h + 1 of the block
+                        const uint32_t at0 = h ? 0x0602 : 0x0400, at1 = h ? 0x0703 : 0x0501;
+                        const uint32_t f[4] = {
+                            codes_bf16(__byte_perm(w[0], w[1], at0)), codes_bf16(__byte_perm(w[0], w[1], at1)),
+                            codes_bf16(__byte_perm(w[2], w[3], at0)), codes_bf16(__byte_perm(w[2], w[3], at1))};
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {  // values 4 g + 2 h and 4 g + 2 h + 1 of the block
-                    const uint32_t sel = h ? 0x7362 : 0x5140;
-                    const uint32_t u = __byte_perm(w[0], w[1], sel) ^ 0x80808080u;
-                    const uint32_t v = __byte_perm(w[2], w[3], sel) ^ 0x80808080u;
-                    const uint32_t f[4] = {less_1152(__byte_perm(u, 0x64646464u, 0x4140)),
-                                           less_1152(__byte_perm(u, 0x64646464u, 0x4342)),
-                                           less_1152(__byte_perm(v, 0x64646464u, 0x4140)),
-                                           less_1152(__byte_perm(v, 0x64646464u, 0x4342))};
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if constexpr (fp32 || PAIR) {
+                                // the matrix unit cuts sums off; a long chain of them is kept in fp32 adds
+                                float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        if constexpr (PIECES == kF32 || PAIR) {
-                            // the matrix unit cuts sums off; a long chain of them is kept in fp32 adds
-                            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            if constexpr (P_PARTS == 2) mma_f16(c, f, pb[n][nt][1][0], pb[n][nt][1][1]);
-                            mma_f16(c, f, pb[n][nt][0][0], pb[n][nt][0][1]);
+                                for (int i = P_PARTS - 1; i >= 0; --i) mma_bf16(c, f, pb[nt][i][0], pb[nt][i][1]);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) o[nt][n][h][e] += c[e];
-                        } else {
-                            if constexpr (P_PARTS == 2) mma_f16(o[nt][n][h], f, pb[n][nt][1][0], pb[n][nt][1][1]);
-                            mma_f16(o[nt][n][h], f, pb[n][nt][0][0], pb[n][nt][0][1]);
+                                for (int e = 0; e < 4; ++e) o[nt][n][h][e] += c[e];
+                            } else {
+#pragma unroll
+                                for (int i = P_PARTS - 1; i >= 0; --i)
+                                    mma_bf16(o[nt][n][h], f, pb[nt][i][0], pb[nt][i][1]);
+                            }
                         }
                     }
                 }
-            }
+            };
+            if (odd)
+                values(true);
+            else
+                values(false);
         }
 
         // ---- the end of the unit, or of the stretch ----
@@ -953,7 +969,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
                     const int cg = p.ct * COLS + column_of(nt, e);
                     if (!writes || cg >= a.columns) continue;
                     const int64_t row = row_of(p.b, p.hk, cg);
-                    const float l = sum[nt][e], inv = l == 0.0f ? 0.0f : kSumScale / l;
+                    const float l = sum[nt][e], inv = l == 0.0f ? 0.0f : kCodes / l;
 #pragma unroll
                     for (int n = 0; n < NB; ++n) {
                         float y[4] = {o[nt][n][0][e] * inv, o[nt][n][0][e + 2] * inv, o[nt][n][1][e] * inv,
@@ -1066,7 +1082,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
         } else {
             // a unit of several CTAs
             float *mine = a.partials + (2 * (int64_t)blockIdx.x + u.starts) * SLOT;
-            const float inv = l == 0.0f ? 0.0f : kSumScale / l;
+            const float inv = l == 0.0f ? 0.0f : kCodes / l;
             *reinterpret_cast<float4 *>(mine + 2 * COLS + c * D + d) =
                 make_float4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
             if (d == 0) *reinterpret_cast<float2 *>(mine + 2 * c) = make_float2(m, l);
@@ -1177,11 +1193,11 @@ inline int attn_most_columns(int D, int dtype, int columns) {
 template <int NB>
 cudaError_t attn_by_columns(const AttnArgs &a, int sms, cudaStream_t stream) {
     const bool two = attn_most_columns(32 * NB, a.dtype, a.columns) == 16;
-    if (a.dtype == RFP2_BF16)
-        return two ? attn_launch<NB, 2, kBf16>(a, sms, stream) : attn_launch<NB, 1, kBf16>(a, sms, stream);
-    if (a.columns <= 4) return attn_launch<NB, 1, kPaired>(a, sms, stream);
-    if (a.dtype == RFP2_F16)
-        return two ? attn_launch<NB, 2, kF16>(a, sms, stream) : attn_launch<NB, 1, kF16>(a, sms, stream);
+    if (a.dtype != RFP2_F32) {
+        if (a.columns <= 4) return attn_launch<NB, 1, kPairHalf>(a, sms, stream);
+        return two ? attn_launch<NB, 2, kHalf>(a, sms, stream) : attn_launch<NB, 1, kHalf>(a, sms, stream);
+    }
+    if (a.columns <= 4) return attn_launch<NB, 1, kPairF32>(a, sms, stream);
     if constexpr (NB <= 4)
         if (two) return attn_launch<NB, 2, kF32>(a, sms, stream);
     return attn_launch<NB, 1, kF32>(a, sms, stream);

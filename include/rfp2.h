@@ -369,7 +369,7 @@ rfp2_status rfp2_debug_wait_timeout(int32_t *dev_status, rfp2_stream_t stream);
  * Attention between the products of a decoder layer: rotary positions, a paged
  * key-value cache held in Q8 blocks, and the attention of the newest tokens
  * over it.  Values of activations may be fp32 (what the GEMVs return), bf16 or
- * f16; all arithmetic is fp32, rounded once at the end.
+ * f16; sums and softmax states are fp32, and results are rounded once at the end.
  */
 typedef enum { RFP2_F32 = 0, RFP2_BF16 = 1, RFP2_F16 = 2 } rfp2_dtype;
 
@@ -462,6 +462,10 @@ rfp2_status rfp2_kv_read(const int8_t *k_codes, const float *k_scales, const int
  *   s = scale * q . k,  with softcap > 0: s = softcap * tanh(s / softcap)
  *   (a softcap of 2^60 or more is none)
  *   out = sum_j softmax(s)_j v_j,  lse = log sum_j exp(s_j) (natural).
+ * Roundings on the way: q counts to 2^-22 of itself (16-bit q exactly) or
+ * 2^-39 of the largest value of its row; a weight times its value to 24 bits
+ * for fp32 outputs, to 2^-15 of itself for 16-bit ones; a weight below 2^-126
+ * of its row's largest is nothing.
  * A query that sees no key gets out = 0 and lse = -infinity.
  *   q    `dtype` [B, nq, Hq, D] device: D contiguous, any other strides.
  *   out  `dtype` [B, nq, Hq, D] contiguous; lse fp32 [B, nq, Hq] or NULL.
