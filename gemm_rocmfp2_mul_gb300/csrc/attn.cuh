@@ -28,11 +28,11 @@
 // but needed one exponent for all blocks of a key and lost what lay far below.)
 //
 // Measured (one GB300, back to back): 64 sequences of up to 32768 keys, 64 heads
-// over 8 of 128, bf16: 386 us for 2.39 GB (6.2 TB/s; copy rate 6.7); one of 131072
-// keys, 40 over 8: 60 us (5.0 TB/s); 16 of up to 8192, 32 over 8, fp32: 45 us (4.2
-// TB/s); one of 1000 keys: 9.4 us.  The start (three dependent reads) and the joins
+// over 8 of 128, bf16: 385 us for 2.39 GB (6.2 TB/s; copy rate 6.7); one of 131072
+// keys, 40 over 8: 60 us (5.0 TB/s); 16 of up to 8192, 32 over 8, fp32: 44 us (4.2
+// TB/s); one of 1000 keys: 9.5 us.  The start (three dependent reads) and the joins
 // take about 8 us of a long call; on the way the instructions of three warps a
-// scheduler set the pace: 580 a tile of 8 columns x 128 values, 716 for fp32.
+// scheduler set the pace, some 600 a tile of 8 columns x 128 values.
 #pragma once
 
 #include <atomic>
@@ -56,6 +56,10 @@ constexpr int kAttnWholeUnit = 4;
 // stages of 12 warps (64 sequences, 2.4 GB): 373 us, 356 and 368.
 constexpr int kAttnInFlight = 112 * 1024;
 constexpr int kAttnMaxBatch = 1024;  // sequences of one launch
+// Tiles whose weights are summed by themselves before they join the unit's sum: one
+// by one, small weights round off beside what a large one has left (lse of 131072
+// keys, 1700 tiles a warp: 4.5e-6 off, so 6e-7).
+constexpr int kAttnSums = 32;
 
 struct AttnArgs {
     const void *q;
@@ -750,135 +754,166 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
             sum[nt][0] = sum[nt][1] = 0.0f;
         }
 
-        for (int t = from; t < to; ++t) {
-            cp_async_wait<STAGES - 2>();
-            __syncwarp();
-            load_tile(stage == 0 ? STAGES - 1 : stage - 1);
-            const uint8_t *kt = rings + (warp * STAGES + stage) * L::stage_bytes, *vt = kt + L::k_bytes;
-            const float *ks = reinterpret_cast<const float *>(vt + L::v_bytes), *vs = ks + kAttnTile * NB;
-            stage = stage + 1 == STAGES ? 0 : stage + 1;
-            const int key0 = (low + t) * kAttnTile;
-
-            // scales of keys g and g + 8
-            float dk[2][NB], dv[2][NB];
+        const auto sum_of_keys = [](float l) {
+            l += __shfl_xor_sync(0xffffffffu, l, 4);
+            l += __shfl_xor_sync(0xffffffffu, l, 8);
+            return l + __shfl_xor_sync(0xffffffffu, l, 16);
+        };
+#pragma unroll 1
+        for (int t = from; t < to;) {
+            const int stop = min(to, t + kAttnSums);
+            float part[NT][2];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                load_scales<NB>(ks + (g + 8 * k) * NB, dk[k]);
-                load_scales<NB>(vs + (g + 8 * k) * NB, dv[k]);
-            }
-            if (far)
+            for (int nt = 0; nt < NT; ++nt) part[nt][0] = part[nt][1] = 0.0f;
+#pragma unroll 1
+            for (; t < stop; ++t) {
+                cp_async_wait<STAGES - 2>();
+                __syncwarp();
+                load_tile(stage == 0 ? STAGES - 1 : stage - 1);
+                const uint8_t *kt = rings + (warp * STAGES + stage) * L::stage_bytes, *vt = kt + L::k_bytes;
+                const float *ks = reinterpret_cast<const float *>(vt + L::v_bytes), *vs = ks + kAttnTile * NB;
+                stage = stage + 1 == STAGES ? 0 : stage + 1;
+                const int key0 = (low + t) * kAttnTile;
+
+                // scales of keys g and g + 8
+                float dk[2][NB], dv[2][NB];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    load_scales<NB>(ks + (g + 8 * k) * NB, dk[k]);
+                    load_scales<NB>(vs + (g + 8 * k) * NB, dv[k]);
+                }
+                if (far)
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) {
+                        dk[0][n] *= near_by;
+                        dk[1][n] *= near_by;
+                    }
+
+                // scores of keys g and g + 8
+                float sc[NT][4];
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
-                    dk[0][n] *= near_by;
-                    dk[1][n] *= near_by;
-                }
-
-            // scores of keys g and g + 8
-            float sc[NT][4];
-#pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                const int at = 32 * (n ^ L::k_order(g)) + 8 * t4;
-                const uint2 lo = *reinterpret_cast<const uint2 *>(kt + g * L::k_stride + at);
-                const uint2 hi = *reinterpret_cast<const uint2 *>(kt + (g + 8) * L::k_stride + at);
-                float c[NT][4];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) c[nt][e] = 0.0f;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const uint32_t w0 = (s ? lo.y : lo.x) ^ 0x80808080u, w1 = (s ? hi.y : hi.x) ^ 0x80808080u;
-                    const uint32_t f[4] = {less_1152(__byte_perm(w0, 0x64646464u, 0x4140)),
-                                           less_1152(__byte_perm(w1, 0x64646464u, 0x4140)),
-                                           less_1152(__byte_perm(w0, 0x64646464u, 0x4342)),
-                                           less_1152(__byte_perm(w1, 0x64646464u, 0x4342))};
+                    const int at = 32 * (n ^ L::k_order(g)) + 8 * t4;
+                    const uint2 lo = *reinterpret_cast<const uint2 *>(kt + g * L::k_stride + at);
+                    const uint2 hi = *reinterpret_cast<const uint2 *>(kt + (g + 8) * L::k_stride + at);
+                    float c[NT][4];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int piece = Q_PARTS - 1; piece >= 0; --piece) {
-                            if constexpr (Q_SHARED) {
-                                const uint2 q = q_mine[q_place(nt, n, s, piece)];
-                                mma_f16(c[nt], f, q.x, q.y);
-                            } else {
-                                mma_f16(c[nt], f, qf[n][s][piece][0], qf[n][s][piece][1]);
+                        for (int e = 0; e < 4; ++e) c[nt][e] = 0.0f;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const uint32_t w0 = (s ? lo.y : lo.x) ^ 0x80808080u, w1 = (s ? hi.y : hi.x) ^ 0x80808080u;
+                        const uint32_t f[4] = {less_1152(__byte_perm(w0, 0x64646464u, 0x4140)),
+                                               less_1152(__byte_perm(w1, 0x64646464u, 0x4140)),
+                                               less_1152(__byte_perm(w0, 0x64646464u, 0x4342)),
+                                               less_1152(__byte_perm(w1, 0x64646464u, 0x4342))};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int piece = Q_PARTS - 1; piece >= 0; --piece) {
+                                if constexpr (Q_SHARED) {
+                                    const uint2 q = q_mine[q_place(nt, n, s, piece)];
+                                    mma_f16(c[nt], f, q.x, q.y);
+                                } else {
+                                    mma_f16(c[nt], f, qf[n][s][piece][0], qf[n][s][piece][1]);
+                                }
                             }
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            sc[nt][e] = n ? sc[nt][e] + dk[e >> 1][n] * c[nt][e] : dk[e >> 1][n] * c[nt][e];
+                }
+
+                if constexpr (PIECES == kPairF32)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[0][e] += __shfl_xor_sync(0xffffffffu, sc[0][e], 2);
+
+                const bool whole = key0 + kAttnTile <= min_end && key0 >= max_begin;
+                bool more = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[nt][e] *= col_scale[nt][e & 1];
+                if (a.softcap > 0.0f)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            sc[nt][e] = cap_out * tanhf(sc[nt][e] * cap_in);
+                if (!whole) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = key0 + g + 8 * (e >> 1), end = col_end[nt][e & 1];
+                            if (j >= end || (a.window && j < end - a.window)) sc[nt][e] = -CUDART_INF_F;
+                        }
+                    // a value's scale that is not finite counts where its key is seen, and there alone
+                    bool odd = false;
+#pragma unroll
+                    for (int n = 0; n < NB; ++n)
+                        odd |= !(fabsf(dv[0][n]) <= 3.402823466e38f) || !(fabsf(dv[1][n]) <= 3.402823466e38f);
+                    if (__any_sync(0xffffffffu, odd))
+#pragma unroll
+                        for (int n = 0; n < NB; ++n) {
+                            const bool bad[2] = {!(fabsf(dv[0][n]) <= 3.402823466e38f),
+                                                 !(fabsf(dv[1][n]) <= 3.402823466e38f)};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const bool seen = (bad[0] && sc[nt][e] != -CUDART_INF_F) ||
+                                                      (bad[1] && sc[nt][e + 2] != -CUDART_INF_F);
+                                    // by any of the lanes of this column
+                                    if (__ballot_sync(0xffffffffu, seen) & 0x11111111u << t4)
+#pragma unroll
+                                        for (int h = 0; h < 2; ++h) o[nt][n][h][e] = o[nt][n][h][e + 2] = CUDART_NAN_F;
+                                }
+                            if (bad[0]) dv[0][n] = 0.0f;
+                            if (bad[1]) dv[1][n] = 0.0f;
                         }
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        sc[nt][e] = n ? sc[nt][e] + dk[e >> 1][n] * c[nt][e] : dk[e >> 1][n] * c[nt][e];
-            }
-
-            if constexpr (PIECES == kPairF32)
+                    for (int e = 0; e < 4; ++e) more |= sc[nt][e] - ref[nt][e & 1] > kSlack;
+                if (__any_sync(0xffffffffu, more)) {
+                    // a larger reference for the columns that need one
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sc[0][e] += __shfl_xor_sync(0xffffffffu, sc[0][e], 2);
-
-            const bool whole = key0 + kAttnTile <= min_end && key0 >= max_begin;
-            bool more = false;
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                        for (int e = 0; e < 2; ++e) {
+                            float m = fmaxf(sc[nt][e], sc[nt][e + 2]);
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                            m = fmaxf(m, ref[nt][e]);
+                            const float keep = exp2_fast(ref[nt][e] - m);
+                            ref[nt][e] = m;
+                            sum[nt][e] *= keep;
+                            part[nt][e] *= keep;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sc[nt][e] *= col_scale[nt][e & 1];
-            if (a.softcap > 0.0f)
+                            for (int n = 0; n < NB; ++n)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        sc[nt][e] = cap_out * tanhf(sc[nt][e] * cap_in);
-            bool odd = false;  // a scale that is not finite, where some column may not see its key
-            if (!whole) {
+                                for (int h = 0; h < 2; ++h) {
+                                    o[nt][n][h][e] *= keep;
+                                    o[nt][n][h][e + 2] *= keep;
+                                }
+                        }
+                }
+                float pr[NT][4];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int j = key0 + g + 8 * (e >> 1), end = col_end[nt][e & 1];
-                        if (j >= end || (a.window && j < end - a.window)) sc[nt][e] = -CUDART_INF_F;
+                        pr[nt][e] = exp2_fast(sc[nt][e] - ref[nt][e & 1] + kShift);
+                        part[nt][e & 1] += pr[nt][e];
                     }
-#pragma unroll
-                for (int n = 0; n < NB; ++n)
-                    odd |= !(fabsf(dv[0][n]) <= 3.402823466e38f) || !(fabsf(dv[1][n]) <= 3.402823466e38f);
-                odd = __any_sync(0xffffffffu, odd);
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) more |= sc[nt][e] - ref[nt][e & 1] > kSlack;
-            if (__any_sync(0xffffffffu, more)) {
-                // a larger reference for the columns that need one
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float m = fmaxf(sc[nt][e], sc[nt][e + 2]);
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                        m = fmaxf(m, ref[nt][e]);
-                        const float keep = exp2_fast(ref[nt][e] - m);
-                        ref[nt][e] = m;
-                        sum[nt][e] *= keep;
-#pragma unroll
-                        for (int n = 0; n < NB; ++n)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                o[nt][n][h][e] *= keep;
-                                o[nt][n][h][e + 2] *= keep;
-                            }
-                    }
-            }
-            float pr[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    pr[nt][e] = exp2_fast(sc[nt][e] - ref[nt][e & 1] + kShift);
-                    sum[nt][e & 1] += pr[nt][e];
-                }
 
-            // values: out^T += V^T (p dV), keys 2 t4, + 1, + 8, + 9
-            const auto values = [&](bool odd) {
+                // values: out^T += V^T (p dV), keys 2 t4, + 1, + 8, + 9
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
                     // p dV in the layout that the products take it in
@@ -888,10 +923,6 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             float u = pr[nt][2 * k] * dv[k][n], w = pr[nt][2 * k + 1] * dv[k][n];
-                            if (odd) {  // a key out of sight has no weight, whatever its scale is
-                                if (sc[nt][2 * k] == -CUDART_INF_F) u = 0.0f;
-                                if (sc[nt][2 * k + 1] == -CUDART_INF_F) w = 0.0f;
-                            }
                             const uint32_t hi = first_bf16(u, w);
                             if constexpr (PIECES == kHalf) {
                                 pb[nt][0][k] = transpose8x8(hi);
@@ -923,26 +954,21 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
                             codes_bf16(__byte_perm(w[2], w[3], at0)), codes_bf16(__byte_perm(w[2], w[3], at1))};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            if constexpr (fp32 || PAIR) {
-                                // the matrix unit cuts sums off; a long chain of them is kept in fp32 adds
-                                float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                            // the matrix unit cuts its sums off: 1.4e-7 of them a tile, were they kept there.  (As the
+                            // accumulators of the products: 368 us of 64 sequences, so 384.)
+                            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                                for (int i = P_PARTS - 1; i >= 0; --i) mma_bf16(c, f, pb[nt][i][0], pb[nt][i][1]);
+                            for (int i = P_PARTS - 1; i >= 0; --i) mma_bf16(c, f, pb[nt][i][0], pb[nt][i][1]);
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) o[nt][n][h][e] += c[e];
-                            } else {
-#pragma unroll
-                                for (int i = P_PARTS - 1; i >= 0; --i)
-                                    mma_bf16(o[nt][n][h], f, pb[nt][i][0], pb[nt][i][1]);
-                            }
+                            for (int e = 0; e < 4; ++e) o[nt][n][h][e] += c[e];
                         }
                     }
                 }
-            };
-            if (odd)
-                values(true);
-            else
-                values(false);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) sum[nt][e] += part[nt][e];
         }
 
         // ---- the end of the unit, or of the stretch ----
