@@ -28,9 +28,9 @@
 // but needed one exponent for all blocks of a key and lost what lay far below.)
 //
 // Measured (one GB300, back to back): 64 sequences of up to 32768 keys, 64 heads
-// over 8 of 128, bf16: 385 us for 2.39 GB (6.2 TB/s; copy rate 6.7); one of 131072
-// keys, 40 over 8: 60 us (5.0 TB/s); 16 of up to 8192, 32 over 8, fp32: 44 us (4.2
-// TB/s); one of 1000 keys: 9.5 us.  The start (three dependent reads) and the joins
+// over 8 of 128, bf16: 388 us for 2.39 GB (6.2 TB/s; copy rate 6.7); one of 131072
+// keys, 40 over 8: 60 us (5.0 TB/s); 16 of up to 8192, 32 over 8, fp32: 44 us (4.3
+// TB/s); one of 1000 keys: 9.4 us.  The start (three dependent reads) and the joins
 // take about 8 us of a long call; on the way the instructions of three warps a
 // scheduler set the pace, some 600 a tile of 8 columns x 128 values.
 #pragma once
@@ -191,10 +191,11 @@ RFP2_DEV uint32_t transpose8x8(uint32_t a) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
-// Two f16 of 1024 + u (u a byte) less 1152: the codes u - 128, exact.
-RFP2_DEV uint32_t less_1152(uint32_t h) {
+// Two bytes u = code + 128, bytes 0 and 2 of h, as two f16 of 2^-24 of the codes, exact: as the bits of an f16 a byte
+// is u 2^-24.
+RFP2_DEV uint32_t codes_f16(uint32_t h) {
     uint32_t d;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(h), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(h), "r"(0x00800080u));
     return d;
 }
 RFP2_DEV uint32_t pack_f16(float lo, float hi) {
@@ -613,6 +614,9 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
     // tanhf for 16-bit types too, 13.0 -> 13.4 us of 12 x 5 tokens: the lse of few keys shows an error of
     // 2e-7 of the cap, as 1 - 2 / (e^2x + 1) has it near 0
     const float cap_in = fminf(1.0f / a.softcap, 3.402823466e38f);
+    // Queries of any size on keys of any size: 2^-24 of the codes and q below 2^15 make a block's sum 8 at most, so that
+    // no scale of fp32's takes a score's sum out of its range; what q was scaled by comes off first, these last.
+    const float to_score = 16777216.0f * a.scale * (a.softcap > 0.0f ? 1.0f : 1.4426950408889634f);
     int stage = 0;
     bool filled = false;
     for (AttnPlace p = first; p.unit0 + kAttnGap < y1; next_unit(p)) {
@@ -638,7 +642,6 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
         uint2 *q_mine = q_frags + warp * (attn_q_bytes<NB, NT, PIECES>() / 8) + lane;
         const auto q_place = [](int nt, int n, int s, int part) { return (((nt * NB + n) * 2 + s) * Q_PARTS + part) * 32; };
         float col_scale[NT][2];
-        int up_most = 0, up_least = 0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int c = p.ct * COLS + nt * 8 + (g & (PER - 1));
@@ -695,8 +698,6 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             // 2^up brings the largest value to [2^14, 2^15); a zero row stays as it is
             const int up = top > 0.0f ? min(141 - (int)(__float_as_uint(top) >> 23), 126) : 0;
-            up_most = max(up_most, up);
-            up_least = min(up_least, up);
             const float by = __uint_as_float((uint32_t)(127 + up) << 23);
 #pragma unroll
             for (int n = 0; n < NB; ++n)
@@ -727,18 +728,6 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
                 col_scale[nt][e] = __uint_as_float(
                     (uint32_t)(127 - __shfl_sync(0xffffffffu, up, 4 * column_of(0, e))) << 23);
         }
-        // q far from 1 is for keys as far on the other side: their scales are brought 2^60 nearer, so
-        // that no sum on the way leaves fp32's range
-        const bool tiny = __any_sync(0xffffffffu, up_most > 60);
-        const bool far = tiny || __any_sync(0xffffffffu, up_least < -60);
-        const float near_by = tiny ? 8.673617379884035e-19f : 1.152921504606847e18f;  // 2^-60, 2^60
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                if (far) col_scale[nt][e] *= tiny ? 1.152921504606847e18f : 8.673617379884035e-19f;
-                col_scale[nt][e] *= a.scale * (a.softcap > 0.0f ? 1.0f : 1.4426950408889634f);
-            }
 
         float o[NT][NB][2][4];          // [column tile][block][pair of values][accumulator]
         float ref[NT][2], sum[NT][2];   // r, and this lane's share of the sum of p
@@ -782,12 +771,6 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
                     load_scales<NB>(ks + (g + 8 * k) * NB, dk[k]);
                     load_scales<NB>(vs + (g + 8 * k) * NB, dv[k]);
                 }
-                if (far)
-#pragma unroll
-                    for (int n = 0; n < NB; ++n) {
-                        dk[0][n] *= near_by;
-                        dk[1][n] *= near_by;
-                    }
 
                 // scores of keys g and g + 8
                 float sc[NT][4];
@@ -804,10 +787,10 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
                         const uint32_t w0 = (s ? lo.y : lo.x) ^ 0x80808080u, w1 = (s ? hi.y : hi.x) ^ 0x80808080u;
-                        const uint32_t f[4] = {less_1152(__byte_perm(w0, 0x64646464u, 0x4140)),
-                                               less_1152(__byte_perm(w1, 0x64646464u, 0x4140)),
-                                               less_1152(__byte_perm(w0, 0x64646464u, 0x4342)),
-                                               less_1152(__byte_perm(w1, 0x64646464u, 0x4342))};
+                        const uint32_t f[4] = {codes_f16(__byte_perm(w0, 0u, 0x4140)),
+                                               codes_f16(__byte_perm(w1, 0u, 0x4140)),
+                                               codes_f16(__byte_perm(w0, 0u, 0x4342)),
+                                               codes_f16(__byte_perm(w1, 0u, 0x4342))};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -836,7 +819,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[nt][e] *= col_scale[nt][e & 1];
+                    for (int e = 0; e < 4; ++e) sc[nt][e] = sc[nt][e] * col_scale[nt][e & 1] * to_score;
                 if (a.softcap > 0.0f)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)

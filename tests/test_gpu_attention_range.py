@@ -111,3 +111,18 @@ def test_values_of_extreme_size(g, Hq):
         c = Case(2, 1, Hq, 1, 64, 16, [50, 200], seed=4)
         rescale(c, np.float32(2.0 ** e))
         judge(c, *_run(g, c))
+
+
+@pytest.mark.parametrize("keys", [-100, 0, 100])
+@pytest.mark.parametrize("dtype,tiny,huge", [("float32", -120, 100), ("float32", -60, 90), ("bfloat16", -120, 115)])
+def test_tiny_and_huge_queries_of_one_key_head(g, dtype, tiny, huge, keys):
+    """Rows of q far below 1 beside rows far above it, on keys of any size: scores of 0, of order 1, and as large
+    as fp32 holds, side by side."""
+    import torch
+    c = Case(1, 2, 8, 2, 64, 16, 90, dtype=dtype, seed=7)
+    size = torch.tensor([tiny, huge, 0, tiny, 0, huge, tiny, huge]).double().exp2().view(1, 1, 8, 1)
+    size = torch.minimum(size, torch.tensor(2.0 ** (120 - keys)).double())     # whose scores stay finite
+    c.q = (c.q.double() * size).to(c.q.dtype)
+    c.ks *= np.float32(2.0 ** keys)
+    c.k = [k * 2.0 ** keys for k in c.k]
+    judge(c, *_run(g, c))
