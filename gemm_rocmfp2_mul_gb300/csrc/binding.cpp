@@ -178,6 +178,10 @@ int kv_write(PyObject *const *a) {
         inv_freq = f.data_ptr<float>();
         R = 2 * f.numel();
     }
+    if (R == 0 && a[4] != Py_None && a[5] != Py_None) {  // no pairs to turn
+        positions = nullptr;
+        inv_freq = nullptr;
+    }
     return rfp2_kv_write(k.data_ptr(), v.data_ptr(), type, k.size(0), k.stride(0), k.stride(1), v.stride(0),
                          v.stride(1), slots.data_ptr<int64_t>(), positions, inv_freq, R, (float)number(a[7]),
                          (int)whole(a[6]), c.k_codes, c.k_scales, c.v_codes, c.v_scales, c.pages, c.heads,

@@ -419,14 +419,13 @@ extern "C" rfp2_status rfp2_kv_write(const void *k, const void *v, int dtype, in
                                      int64_t page_size, int64_t D, int32_t *dev_status,
                                      rfp2_stream_t stream) {
     const int size = dtype_bytes(dtype);
-    if (T < 0 || !size || (flags & ~RFP2_ROPE_INTERLEAVED) || !positions != !inv_freq)
-        return RFP2_EINVAL;
+    if (T < 0 || !size || (flags & ~RFP2_ROPE_INTERLEAVED)) return RFP2_EINVAL;
     if (T > (1ll << 31) - 1 || (positions && (R < 0 || R % 2 != 0 || R > D))) return RFP2_ESHAPE;
     const rfp2_status st =
         check_cache(k_codes, k_scales, v_codes, v_scales, pages, heads, page_size, D);
     if (st != RFP2_OK) return st;
     if (T == 0) return RFP2_OK;
-    if (!k || !v || !slots) return RFP2_EINVAL;
+    if (!k || !v || !slots || !positions != !inv_freq) return RFP2_EINVAL;
     if (!aligned(k, size) || !aligned(v, size) || !aligned(slots, 8) || !aligned(positions, 4) ||
         !aligned(inv_freq, 4))
         return RFP2_EALIGN;
