@@ -7,8 +7,9 @@ torch when the caller does not pass them, passes raw device pointers and the
 current torch stream to the library, and raises :class:`RFP2Error` on a
 non-zero status.  All arithmetic runs in the library's CUDA kernels; there is
 no CPU or PyTorch fallback: if the library is not built or cannot be loaded,
-every call raises.  Most calls go through ctypes; those of the attention
-operators, small and many, through a compiled binding.
+every call raises.  Tensors have to be on the current device, where the library
+launches.  Most calls go through ctypes; those of the attention operators, small
+and many, through a compiled binding.
 
 Build the library with :func:`build` (nvcc, sm_103a).
 """
@@ -139,13 +140,16 @@ def _ptr(t):
 
 
 def _stream():
-    return C.c_void_p(_torch().cuda.current_stream().cuda_stream)
+    cuda = _torch()._C
+    return C.c_void_p(cuda._cuda_getCurrentRawStream(cuda._cuda_getDevice()))
 
 
 def _need(t, dtype, name, device=None):
     torch = _torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} must be on the current device")  # where the library launches
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
@@ -557,6 +561,8 @@ def rfp2_attn_decode_workspace_bytes(B: int, nq: int, Hq: int, heads: int, D: in
 def rfp2_attn_decode_workspace(q, heads):
     """A workspace for rfp2_attn_decode of q [B, nq, Hq, D] over `heads` key heads, its head zeroed;
     calls in one stream may share it."""
+    if q.get_device() != _torch().cuda.current_device():
+        raise ValueError("q must be on the current device")
     B, nq, Hq, D = q.shape
     workspace = _empty(max(rfp2_attn_decode_workspace_bytes(B, nq, Hq, heads, D), _ATTN_ZERO_BYTES),
                        _torch().uint8, q)

@@ -8,6 +8,7 @@
 
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <algorithm>
@@ -29,14 +30,17 @@ struct Refused {};
     throw Refused{};
 }
 
-// The tensor behind `o`, on the GPU that `device` names (-1: any, and it does so
-// from then on).
+// The tensor behind `o`, on the GPU that `device` names (-1: none yet, and then it
+// has to be the current one, where the library launches).
 const at::Tensor &tensor(PyObject *o, const char *name, int &device) {
     if (!THPVariable_Check(o)) refuse(PyExc_TypeError, name, "must be a CUDA tensor");
     const at::Tensor &t = THPVariable_Unpack(o);
     if (!t.is_cuda()) refuse(PyExc_TypeError, name, "must be a CUDA tensor");
     const int index = t.get_device();
-    if (device < 0) device = index;
+    if (device < 0) {
+        if (index != c10::cuda::current_device()) refuse(PyExc_ValueError, name, "must be on the current device");
+        device = index;
+    }
     if (index != device) refuse(PyExc_ValueError, name, "must be on the other tensors' device");
     return t;
 }

@@ -30,3 +30,37 @@ def test_no_tokens_and_no_pairs_to_write(g):
         cache[0].zero_()
         g.rfp2_kv_write(cache, k, v, slots, positions, no_frequencies)
         assert all(torch.equal(a, b) for a, b in zip(cache, same)) and bool(cache[0].any())
+
+
+def test_tensors_of_another_device_are_refused(g):
+    """The library launches on the current device: tensors elsewhere would be read there by their addresses.
+    (Tensors without memory stand for those of a second GPU: no call below can come to a launch.)"""
+    import torch
+
+    class Elsewhere(torch.Tensor):
+        @staticmethod
+        def __new__(cls, *shape, dtype=torch.float32):
+            strides = [1]
+            for n in shape[:0:-1]:
+                strides.insert(0, strides[0] * n)
+            return torch.Tensor._make_wrapper_subclass(cls, shape, strides=strides, dtype=dtype,
+                                                       device=f"cuda:{torch.cuda.current_device() + 1}")
+
+        @classmethod
+        def __torch_dispatch__(cls, func, types, args=(), kwargs=None):
+            raise AssertionError(f"{func} of a tensor without memory")
+
+    x = Elsewhere(3, 2, 64)
+    positions, f, slots = Elsewhere(3, dtype=torch.int32), Elsewhere(32), Elsewhere(3, dtype=torch.int64)
+    cache = tuple(Elsewhere(2, 2, 4, n, dtype=t) for n, t in ((64, torch.int8), (2, torch.float32)) * 2)
+    q, lse = Elsewhere(3, 1, 2, 64), Elsewhere(3, 1, 2)
+    table, lens, workspace = Elsewhere(3, 2, dtype=torch.int32), positions, Elsewhere(1 << 20, dtype=torch.uint8)
+    W, y = Elsewhere(16, 20, dtype=torch.uint8), Elsewhere(3, 16)
+    calls = [lambda: g.rfp2_rope(x, positions, f, out=x), lambda: g.rfp2_kv_write(cache, x, x, slots),
+             lambda: g.rfp2_kv_read(cache, slots, k=x, v=x), lambda: g.rfp2_attn_decode_workspace(q, 2),
+             lambda: g.rfp2_attn_decode(q, cache, table, lens, out=q, lse=lse, workspace=workspace),
+             lambda: g.rfp2_gemv(W, 16, 64, y, y=y, workspace=workspace),
+             lambda: g.rfp2_pack_weights(y, out=W)]
+    for call in calls:
+        with pytest.raises(ValueError, match="current device"):
+            call()
