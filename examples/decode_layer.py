@@ -77,6 +77,8 @@ class Layer:
 
 def run(prompt=300, new=20, batch=2, seed=0):
     """Outputs of the layer for a prompt and `new` tokens, one replayed step each, and their inputs."""
+    if min(prompt, new, batch) < 1:
+        raise ValueError(f"a prompt, new tokens and sequences are needed, got {prompt}, {new} and {batch}")
     import torch
     layer = Layer(batch, prompt + new, seed)
     r = torch.Generator(device="cuda").manual_seed(seed + 1)
