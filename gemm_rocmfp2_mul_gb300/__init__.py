@@ -467,6 +467,7 @@ _ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3}
 _ROPE_INTERLEAVED, _ROPE_INVERSE = 1, 2
 _ATTN_ZERO_BYTES = 4096
 _native = None
+_rope_function = None
 
 
 class KVCache(NamedTuple):
@@ -510,7 +511,12 @@ def rfp2_rope_frequencies(R, base=10000.0, scaling="plain", stretch=1.0, trained
 def rfp2_rope(x, positions, inv_freq, out=None, interleaved=False, inverse=False, factor=1.0):
     """Rotary positions: x [T, H, D] (any token and head strides) with the first 2*len(inv_freq)
     values of each head rotated by positions int32 [T]; out=x rotates in place.  inverse=True
-    negates the angles (the gradient)."""
+    negates the angles (the gradient).  A gradient of x goes through the call, unless `out` is given:
+    that is refused where x requires one."""
+    if x.requires_grad and _torch().is_grad_enabled():
+        if out is not None:
+            raise RuntimeError("rfp2_rope with out= has no gradient, and x requires one")
+        return _rope_with_gradient().apply(x, positions, inv_freq, interleaved, inverse, factor)
     if out is None:
         out = _empty(x.shape, x.dtype, x)
     rc = (_native or _binding()).rope(
@@ -519,6 +525,29 @@ def rfp2_rope(x, positions, inv_freq, out=None, interleaved=False, inverse=False
     if rc:
         raise RFP2Error(rc, "rfp2_rope")
     return out
+
+
+def _rope_with_gradient():
+    """rfp2_rope as a function of autograd: the gradient turns back."""
+    global _rope_function
+    if _rope_function is None:
+        class RotaryPositions(_torch().autograd.Function):
+            @staticmethod
+            def forward(ctx, x, positions, inv_freq, interleaved, inverse, factor):
+                ctx.save_for_backward(positions, inv_freq)
+                ctx.how = interleaved, inverse, factor
+                return rfp2_rope(x, positions, inv_freq, None, interleaved, inverse, factor)
+
+            @staticmethod
+            def backward(ctx, gy):
+                positions, inv_freq = ctx.saved_tensors
+                interleaved, inverse, factor = ctx.how
+                if gy.stride(-1) != 1:
+                    gy = gy.contiguous()
+                return rfp2_rope(gy, positions, inv_freq, None, interleaved, not inverse, factor), *[None] * 5
+
+        _rope_function = RotaryPositions
+    return _rope_function
 
 
 def rfp2_kv_alloc(pages, heads, page_size, D, device="cuda"):
@@ -531,7 +560,8 @@ def rfp2_kv_alloc(pages, heads, page_size, D, device="cuda"):
 def rfp2_kv_write(cache, k, v, slots, positions=None, inv_freq=None, interleaved=False, factor=1.0,
                   dev_status=None):
     """Quantise k, v [T, heads, D] into the cache at slots int64 [T] (page * page_size + offset;
-    -1 leaves a token out).  With positions and inv_freq, k is rotated on the way in."""
+    -1 leaves a token out).  With positions and inv_freq, k is rotated on the way in.  Like the other calls
+    over the cache, it has no gradient."""
     rc = (_native or _binding()).kv_write(cache, k, v, slots, positions, inv_freq,
                                           _ROPE_INTERLEAVED if interleaved else 0, factor, dev_status)
     if rc:
@@ -576,7 +606,7 @@ def rfp2_attn_decode(q, cache, table, lens, scale=None, window=0, softcap=0.0, o
     [B, width] of pages, lens int32 [B] of keys held (the nq newest among them).  Returns out
     [B, nq, Hq, D] of q's type and lse fp32 [B, nq, Hq].  scale: D**-0.5 unless given; window: only the
     last `window` keys (0: all); softcap: scores become softcap * tanh(s / softcap) (0: as they are).
-    workspace: from rfp2_attn_decode_workspace."""
+    workspace: from rfp2_attn_decode_workspace.  There is no gradient."""
     if out is None or lse is None or workspace is None:
         if q.dim() != 4:
             raise ValueError(f"q must have 4 dimensions, got {q.dim()}")

@@ -12,6 +12,7 @@
 #include <c10/cuda/CUDAStream.h>
 
 #include <algorithm>
+#include <array>
 #include <cmath>
 
 #include "rfp2.h"
@@ -76,6 +77,11 @@ int type_code(const at::Tensor &t, const char *name) {
     }
 }
 
+// A tensor that a call writes to: what autograd has kept of it is out of date.
+void wrote(const at::Tensor &t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 bool same_shape(const at::Tensor &a, const at::Tensor &b) { return a.sizes() == b.sizes(); }
 
 int32_t *status_of(PyObject *o, int &device) {
@@ -94,6 +100,7 @@ struct Cache {
     int8_t *k_codes, *v_codes;
     float *k_scales, *v_scales;
     int64_t pages, heads, page_size, D;
+    std::array<const at::Tensor *, 4> arrays;
 
     Cache(PyObject *o, int &device) : held(PySequence_Fast(o, "cache must be four tensors")) {
         if (!held) throw Refused{};
@@ -112,6 +119,7 @@ struct Cache {
                 refuse(PyExc_ValueError,
                        "the cache's codes must be [pages, heads, page_size, D], its scales "
                        "[pages, heads, page_size, D/32]");
+            arrays = {&kc, &ks, &vc, &vs};
             k_codes = kc.data_ptr<int8_t>();
             k_scales = ks.data_ptr<float>();
             v_codes = vc.data_ptr<int8_t>();
@@ -152,6 +160,7 @@ int rope(PyObject *const *a) {
     const at::Tensor &out = rows(a[3], "out", 3, device);
     if (!same_shape(out, x) || out.scalar_type() != x.scalar_type())
         refuse(PyExc_ValueError, "out must have x's shape and type");
+    wrote(out);
     return rfp2_rope(x.data_ptr(), type, x.size(0), x.size(1), x.size(2), x.stride(0), x.stride(1),
                      positions.data_ptr<int32_t>(), inv_freq.data_ptr<float>(), 2 * inv_freq.numel(),
                      (float)number(a[5]), (int)whole(a[4]), out.data_ptr(), out.stride(0), out.stride(1),
@@ -186,6 +195,7 @@ int kv_write(PyObject *const *a) {
         positions = nullptr;
         inv_freq = nullptr;
     }
+    for (const at::Tensor *t : c.arrays) wrote(*t);
     return rfp2_kv_write(k.data_ptr(), v.data_ptr(), type, k.size(0), k.stride(0), k.stride(1), v.stride(0),
                          v.stride(1), slots.data_ptr<int64_t>(), positions, inv_freq, R, (float)number(a[7]),
                          (int)whole(a[6]), c.k_codes, c.k_scales, c.v_codes, c.v_scales, c.pages, c.heads,
@@ -204,6 +214,8 @@ int kv_read(PyObject *const *a) {
     if (v.scalar_type() != k.scalar_type()) refuse(PyExc_TypeError, "v must have k's type");
     if (!k.is_contiguous() || !v.is_contiguous() || k.sizes() != at::IntArrayRef(shape, 3) || !same_shape(k, v))
         refuse(PyExc_ValueError, "k and v must be [T, heads, D] and contiguous");
+    wrote(k);
+    wrote(v);
     return rfp2_kv_read(c.k_codes, c.k_scales, c.v_codes, c.v_scales, c.pages, c.heads, c.page_size, c.D,
                         slots.data_ptr<int64_t>(), slots.numel(), type, k.data_ptr(), v.data_ptr(),
                         status_of(a[4], device), stream_of(device));
@@ -230,6 +242,8 @@ int attn_decode(PyObject *const *a) {
     const at::Tensor &workspace = array(a[9], "workspace", at::kByte, "torch.uint8", device);
     const int64_t width = table.size(1), stride = B > 1 ? table.stride(0) : std::max(table.stride(0), width);
     const double scale = a[4] == Py_None ? 1.0 / std::sqrt((double)c.D) : number(a[4]);
+    wrote(out);
+    wrote(lse);
     return rfp2_attn_decode(q.data_ptr(), type, B, nq, Hq, c.D, q.stride(0), q.stride(1), q.stride(2), c.k_codes,
                             c.k_scales, c.v_codes, c.v_scales, c.pages, c.heads, c.page_size,
                             table.data_ptr<int32_t>(), width, stride, lens.data_ptr<int32_t>(), (float)scale,

@@ -64,3 +64,65 @@ def test_tensors_of_another_device_are_refused(g):
     for call in calls:
         with pytest.raises(ValueError, match="current device"):
             call()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("inverse", [False, True])
+def test_a_gradient_goes_through_the_rotation(g, interleaved, inverse):
+    """The rotation is linear: its gradient is the transpose, which is the rotation back by the same factor; the
+    gradient's gradient is the rotation itself.  Against the call itself (its own tests check it against the
+    formula) and against a difference, exact for a linear map up to the rounding of 256 terms of up to 8 in
+    fp32."""
+    import torch
+    r = torch.Generator(device="cuda").manual_seed(3)
+    x, gy, step = (torch.randn((5, 2, 64), generator=r, device="cuda") for _ in range(3))
+    positions = torch.arange(5, dtype=torch.int32, device="cuda") * 77
+    f, _ = g.rfp2_rope_frequencies(48)
+    how = dict(interleaved=interleaved, inverse=inverse, factor=1.25)
+    leaf = x.clone().requires_grad_()
+    y = g.rfp2_rope(leaf, positions, f, **how)
+    assert torch.equal(y.detach(), g.rfp2_rope(x, positions, f, **how))
+    grad_out = gy.clone().requires_grad_()
+    (gx,) = torch.autograd.grad(y, leaf, grad_out, create_graph=True)
+    assert torch.equal(gx.detach(), g.rfp2_rope(gy, positions, f, **{**how, "inverse": not inverse}))
+    difference = ((g.rfp2_rope(x + step, positions, f, **how).double() - g.rfp2_rope(x, positions, f, **how).double()) * gy).sum()
+    assert abs(float(difference - (gx.detach().double() * step).sum())) <= 640 * 8 * 2.0 ** -22
+    (ggx,) = torch.autograd.grad(gx, grad_out, x)
+    assert torch.equal(ggx, g.rfp2_rope(x, positions, f, **how))
+    # of a sum: a gradient without strides of its own
+    y = g.rfp2_rope(leaf, positions, f, **how)
+    y.sum().backward()
+    assert torch.equal(leaf.grad, g.rfp2_rope(torch.ones_like(x), positions, f, **{**how, "inverse": not inverse}))
+
+
+def test_in_place_and_gradients(g):
+    """out= drops no gradient in silence; a tensor that a call writes has another version, so that autograd knows."""
+    import torch
+    f, _ = g.rfp2_rope_frequencies(64)
+    positions = torch.arange(3, dtype=torch.int32, device="cuda")
+    leaf = torch.randn((3, 2, 64), device="cuda", requires_grad=True)
+    for out in (leaf, torch.empty((3, 2, 64), device="cuda")):
+        with pytest.raises(RuntimeError, match="gradient"):
+            g.rfp2_rope(leaf, positions, f, out=out)
+        with torch.no_grad():
+            g.rfp2_rope(leaf, positions, f, out=out)
+    x = leaf.detach().clone()
+    kept = leaf * x                      # autograd keeps x
+    g.rfp2_rope(x, positions, f, out=x)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        kept.sum().backward()
+    cache = g.rfp2_kv_alloc(2, 2, 4, 64)
+    slots = torch.arange(3, device="cuda")
+    q, lse = torch.randn((1, 1, 2, 64), device="cuda"), torch.empty((1, 1, 2), device="cuda")
+    out, k, v = torch.empty_like(q), torch.empty_like(x), torch.empty_like(x)
+    table, lens = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda")
+    written = (*cache, k, v, out, lse)
+    before = [t._version for t in written]
+    g.rfp2_kv_write(cache, x, x, slots)
+    g.rfp2_kv_read(cache, slots, k=k, v=v)
+    g.rfp2_attn_decode(q, cache, table, lens, out=out, lse=lse)
+    assert all(t._version > n for t, n in zip(written, before))
+    with torch.inference_mode():         # where versions are not kept
+        inside = x.clone()
+        g.rfp2_rope(inside, positions, f, out=inside)
+    g.rfp2_rope(inside, positions, f, out=inside)
