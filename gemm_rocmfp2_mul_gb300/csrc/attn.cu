@@ -6,6 +6,37 @@
 
 using namespace rfp2;
 
+namespace {
+
+// A call's queries: rows of D values, `qb`, `qt` and `qh` values apart.
+struct Queries {
+    uintptr_t at;
+    int64_t B, nq, Hq, D, qb, qt, qh;
+    int size;
+    bool contiguous() const {
+        return (Hq == 1 || qh == D) && (nq == 1 || qt == Hq * D) && (B == 1 || qb == nq * Hq * D);
+    }
+    // Does any row share memory with [from, from + bytes)?
+    bool meet(uintptr_t from, int64_t bytes) const {
+        const auto apart = [&](int64_t low, int64_t high) {  // values before the first row, and after
+            return (int64_t)(from - at) >= high * size || (int64_t)(from + bytes - at) <= low * size;
+        };
+        const int64_t b = (B - 1) * qb, t = (nq - 1) * qt, h = (Hq - 1) * qh;
+        if (apart(std::min<int64_t>(b, 0) + std::min<int64_t>(t, 0) + std::min<int64_t>(h, 0),
+                  std::max<int64_t>(b, 0) + std::max<int64_t>(t, 0) + std::max<int64_t>(h, 0) + D))
+            return false;
+        // between the rows, perhaps
+        for (int64_t i = 0; i < B * nq; ++i)
+            for (int64_t j = 0; j < Hq; ++j) {
+                const int64_t row = i / nq * qb + i % nq * qt + j * qh;
+                if (!apart(row, row + D)) return true;
+            }
+        return false;
+    }
+};
+
+}  // namespace
+
 extern "C" size_t rfp2_attn_decode_workspace_bytes(int64_t B, int64_t nq, int64_t Hq,
                                                    int64_t heads, int64_t D) {
     if (B < 1 || nq < 1 || Hq < 1 || heads < 1 || Hq % heads != 0 || D < 32 || D > 256) return 0;
@@ -43,6 +74,14 @@ extern "C" rfp2_status rfp2_attn_decode(const void *q, int dtype, int64_t B, int
         !aligned(lens, 4) || !aligned(k_codes, 16) || !aligned(k_scales, 16) ||
         !aligned(v_codes, 16) || !aligned(v_scales, 16) || !aligned(workspace, 256))
         return RFP2_EALIGN;
+    // Each row of q is read before the same row of out is written, and at any time to another's.
+    const uintptr_t q_at = reinterpret_cast<uintptr_t>(q), out_at = reinterpret_cast<uintptr_t>(out),
+                    lse_at = reinterpret_cast<uintptr_t>(lse);
+    const int64_t rows = B * nq * Hq;
+    const Queries queries = {q_at, B, nq, Hq, D, q_batch_stride, q_token_stride, q_head_stride, size};
+    if (!(q_at == out_at && queries.contiguous()) && queries.meet(out_at, rows * D * size)) return RFP2_EINVAL;
+    if (lse && (queries.meet(lse_at, rows * 4) || (lse_at < out_at + rows * D * size && out_at < lse_at + rows * 4)))
+        return RFP2_EINVAL;
     AttnArgs a;
     a.qb = q_batch_stride;
     a.qt = q_token_stride;

@@ -469,6 +469,8 @@ rfp2_status rfp2_kv_read(const int8_t *k_codes, const float *k_scales, const int
  * A query that sees no key gets out = 0 and lse = -infinity.
  *   q    `dtype` [B, nq, Hq, D] device: D contiguous, any other strides.
  *   out  `dtype` [B, nq, Hq, D] contiguous; lse fp32 [B, nq, Hq] or NULL.
+ *        out == q, with q contiguous, writes in place; any other overlap of q,
+ *        out and lse is not allowed.
  *   table int32 [B, table_width] device (rows table_stride apart), lens int32
  *        [B] device.  Only the entries that hold visible keys are read; one
  *        outside [0, pages) makes its sequence's rows NaN (rows that see none
@@ -481,7 +483,7 @@ rfp2_status rfp2_kv_read(const int8_t *k_codes, const float *k_scales, const int
  *        enough for.  Calls that overlap on the GPU must not share it.
  * The length is split over the GPU and joined in a fixed order: the same call
  * gives the same bits.
- * Errors: EINVAL, ESHAPE (Hq % heads, D, page_size, B or nq < 1, nq * Hq >
+ * Errors: EINVAL (also such an overlap), ESHAPE (Hq % heads, D, page_size, B or nq < 1, nq * Hq >
  * 65536, table_width * page_size > 2^30, or > 2^35 / (heads *
  * ceil(nq * Hq / heads / 8)); table_stride < table_width, pages *
  * heads * page_size >= 2^32), EALIGN, EWORKSPACE, ECUDA.

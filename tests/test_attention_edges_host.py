@@ -32,3 +32,26 @@ def test_the_example_needs_a_prompt_and_new_tokens(kw):
     spec.loader.exec_module(example)
     with pytest.raises(ValueError, match="are needed"):
         example.run(**{**dict(prompt=4, new=4), **kw})
+
+
+def attn_decode(g, q, out, lse, B=2, nq=3, Hq=4, D=64, strides=None, dtype=0, page=16, width=4, heads=2):
+    """The status of a call whose arrays are addresses that nothing looks at."""
+    p = C.c_void_p(1 << 40)
+    strides = strides or (nq * Hq * D, Hq * D, D)
+    return g.lib().rfp2_attn_decode(C.c_void_p(q), dtype, B, nq, Hq, D, *strides, p, p, p, p, 8, heads, page, p, width, width, p, 1.0, 0,
+                                    0.0, C.c_void_p(out), C.c_void_p(lse), p, 1 << 40, None, None)
+
+
+def test_overlaps_of_queries_and_outputs_are_refused(g):
+    """A row of q is read before the same row of out is written, but not before any other."""
+    q, row = 1 << 30, 64 * 4
+    rows = 2 * 3 * 4
+    far = 1 << 35
+    assert attn_decode(g, q, q + 16, far) == 1                                  # the same rows, moved
+    assert attn_decode(g, q, q + (rows - 1) * row, far) == 1                    # the last row of q
+    assert attn_decode(g, q, q - (rows - 1) * row, far) == 1                    # the first
+    assert attn_decode(g, q, q, far, strides=(64, 2 * 4 * 64, 2 * 64)) == 1     # the same memory in another order
+    assert attn_decode(g, q, q, far, nq=1, strides=(8 * 64, 0, 64)) == 1        # out runs into the second sequence's q
+    assert attn_decode(g, q, far, q + rows * row - 4) == 1                      # lse over q
+    assert attn_decode(g, q, far, far + 4 * rows) == 1                          # and over out
+    assert attn_decode(g, q, far, far - 4) == 1

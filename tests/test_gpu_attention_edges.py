@@ -126,3 +126,34 @@ def test_in_place_and_gradients(g):
         inside = x.clone()
         g.rfp2_rope(inside, positions, f, out=inside)
     g.rfp2_rope(inside, positions, f, out=inside)
+
+
+def test_queries_and_outputs_in_common_memory(g):
+    """In place, row by row, and in the gaps between the rows of q: the same results as apart."""
+    import torch
+    r = torch.Generator(device="cuda").manual_seed(5)
+    B, nq, Hq, Hkv, D, page, pages = 3, 2, 8, 2, 64, 16, 400
+    cache = g.rfp2_kv_alloc(pages, Hkv, page, D)
+    for t in cache:
+        t.copy_(torch.randint(-127, 128, t.shape, generator=r, device="cuda") if t.dtype == torch.int8 else
+                torch.rand(t.shape, generator=r, device="cuda") / 60)
+    table = torch.randperm(pages - 1, generator=r, device="cuda").int().view(B, -1)
+    lens = torch.tensor([2100, 17, 0], dtype=torch.int32, device="cuda")
+    for dtype in (torch.float32, torch.bfloat16):
+        q = torch.randn((B, nq, Hq, D), generator=r, device="cuda").to(dtype)
+        out, lse = g.rfp2_attn_decode(q, cache, table, lens)
+        here = q.clone()
+        for _ in range(3):
+            here.copy_(q)
+            same, lse2 = g.rfp2_attn_decode(here, cache, table, lens, out=here)
+            assert same.data_ptr() == here.data_ptr() and torch.equal(same, out) and torch.equal(lse2, lse)
+        n = nq * Hq * D
+        arena = torch.zeros((B, 5 * n), device="cuda", dtype=dtype)
+        between = arena[:, :n].unflatten(1, (nq, Hq, D))
+        between.copy_(q)
+        gap = arena[0, n: 4 * n].view(B, nq, Hq, D)
+        inside, _ = g.rfp2_attn_decode(between, cache, table, lens, out=gap)
+        assert inside.data_ptr() == gap.data_ptr() and torch.equal(inside, out) and torch.equal(between, q)
+        with pytest.raises(g.RFP2Error) as e:
+            g.rfp2_attn_decode(between, cache, table, lens, out=arena.view(-1)[2 * n + D: 5 * n + D].view(B, nq, Hq, D))
+        assert e.value.status == 1
