@@ -115,7 +115,7 @@ extern "C" rfp2_status rfp2_attn_decode(const void *q, int dtype, int64_t B, int
     a.counters = static_cast<int *>(workspace);
     a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + RFP2_ATTN_ZERO_BYTES);
     a.status = dev_status;
-    constexpr int64_t kLine = (1ll << 31) - 1;
+    constexpr int64_t kLine = (1ll << 31) - 1 - kAttnGap;  // the kernel adds a gap to its places
     const int64_t line = (a.capacity / kAttnTile + 1 + kAttnGap) * a.heads * a.column_tiles;
     if (line > kLine) return RFP2_ESHAPE;
     static const AttnFn kinds[] = {attn_d32,  attn_d64,  attn_d96,  attn_d128,

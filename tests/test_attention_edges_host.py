@@ -55,3 +55,11 @@ def test_overlaps_of_queries_and_outputs_are_refused(g):
     assert attn_decode(g, q, far, q + rows * row - 4) == 1                      # lse over q
     assert attn_decode(g, q, far, far + 4 * rows) == 1                          # and over out
     assert attn_decode(g, q, far, far - 4) == 1
+
+
+def test_the_line_ends_before_32_bits_do(g):
+    """Places on the line of tiles are 32-bit numbers, to which a unit's gap of 4 is added on the way: a line of
+    2^31 - 4 places and more is refused (it is (table_width + 5) * heads for pages of 16)."""
+    for line, heads in ((2 ** 31 - 2, 33), (2 ** 31 - 3, 95), (2 ** 31 - 4, 932)):
+        assert line % heads == 0
+        assert attn_decode(g, 1 << 30, 1 << 35, 1 << 36, B=1, nq=1, Hq=heads, heads=heads, page=16, width=line // heads - 5) == 2
