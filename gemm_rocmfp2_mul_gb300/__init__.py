@@ -604,7 +604,8 @@ def rfp2_attn_decode(q, cache, table, lens, scale=None, window=0, softcap=0.0, o
                      workspace=None, dev_status=None):
     """Attention of each sequence's newest tokens over the paged cache: q [B, nq, Hq, D], table int32
     [B, width] of pages, lens int32 [B] of keys held (the nq newest among them).  Returns out
-    [B, nq, Hq, D] of q's type (out=q, contiguous, writes in place) and lse fp32 [B, nq, Hq].  scale: D**-0.5 unless given; window: only the
+    [B, nq, Hq, D] of q's type (out=q, contiguous, writes in place) and lse fp32 [B, nq, Hq].
+    scale: D**-0.5 unless given; window: only the
     last `window` keys (0: all); softcap: scores become softcap * tanh(s / softcap) (0: as they are).
     workspace: from rfp2_attn_decode_workspace.  There is no gradient."""
     if out is None or lse is None or workspace is None:
