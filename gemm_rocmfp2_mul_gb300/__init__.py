@@ -486,8 +486,8 @@ def _binding():
         _torch()
         lib()
         from . import buildlib as _b
-        if not os.path.exists(_b.BINDING):
-            raise RuntimeError(f"the binding is not built ({_b.BINDING}); run gemm_rocmfp2_mul_gb300.build()")
+        if not os.path.exists(_b.BINDING) or not _b.binding_fits():
+            raise RuntimeError(f"no binding is built for {_b.binding_for()} ({_b.BINDING}); run gemm_rocmfp2_mul_gb300.build()")
         spec = importlib.util.spec_from_file_location("_rfp2_binding", _b.BINDING)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)

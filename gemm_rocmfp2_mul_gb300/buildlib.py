@@ -2,9 +2,11 @@
 
 Every ``csrc/*.cu`` file is one translation unit; they are compiled in
 parallel and linked into ``_build/librfp2.so`` (git-ignored).
-``csrc/binding.cpp`` is compiled beside them against the installed torch and
-linked to that library as ``_build/_rfp2_binding.so``.  ptxas resource
-reports (registers, spills, shared memory) go to ``_build/ptxas.log``.
+That needs nvcc alone.  Where torch is installed, ``csrc/binding.cpp`` is
+compiled beside them against it and linked to that library as
+``_build/_rfp2_binding.so``, for that torch and Python alone
+(``_build/binding.txt``).  ptxas resource reports (registers, spills, shared
+memory) go to ``_build/ptxas.log``.
 
 Run ``python -m gemm_rocmfp2_mul_gb300.buildlib`` or call :func:`build`.
 """
@@ -12,6 +14,8 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -43,15 +47,43 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps_mtime():
-    files = _sources() + glob.glob(os.path.join(CSRC, "*.c*h")) + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(
-        os.path.join(os.path.dirname(HERE), "include", "*.h")) + [os.path.abspath(__file__)]
-    return max(os.path.getmtime(f) for f in files)
+def _newer(built: str, sources) -> bool:
+    headers = glob.glob(os.path.join(os.path.dirname(HERE), "include", "*.h"))
+    newest = max(os.path.getmtime(f) for f in [*sources, *headers, os.path.abspath(__file__)])
+    return os.path.exists(built) and os.path.getmtime(built) >= newest
+
+
+def _library_up_to_date() -> bool:
+    return _newer(LIB, _sources() + glob.glob(os.path.join(CSRC, "*.cuh")))
+
+
+def binding_for() -> str | None:
+    """What a binding built here is for; None without torch."""
+    if importlib.util.find_spec("torch") is None:
+        return None
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        import torch
+        version = torch.__version__
+    return f"torch {version}, {sys.implementation.cache_tag}"
+
+
+def binding_fits() -> bool:
+    """Is the binding that is there for the torch and the Python that run?"""
+    stamp = os.path.join(BUILD, "binding.txt")
+    if not os.path.exists(stamp):
+        return False
+    with open(stamp) as f:
+        return f.read() == binding_for()
+
+
+def _binding_up_to_date() -> bool:
+    return binding_for() is None or (binding_fits() and _newer(BINDING, [os.path.join(CSRC, "binding.cpp")]))
 
 
 def up_to_date() -> bool:
-    newest = _deps_mtime()
-    return all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, BINDING))
+    return _library_up_to_date() and _binding_up_to_date()
 
 
 def _compile(src: str) -> tuple[str, str]:
@@ -94,29 +126,31 @@ def _link_binding(obj: str) -> None:
     _run(["g++", "-shared", "-o", tmp, obj, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
           "-L" + BUILD, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib], "linking the binding")
     os.replace(tmp, BINDING)
+    with open(os.path.join(BUILD, "binding.txt"), "w") as f:
+        f.write(binding_for())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link librfp2.so; returns its path."""
-    if not force and up_to_date():
-        return LIB
+    """Compile and link librfp2.so, and the binding where torch is installed; returns the library's path."""
+    library = force or not _library_up_to_date()
+    binding = binding_for() is not None and (force or not _binding_up_to_date())
     os.makedirs(BUILD, exist_ok=True)
-    srcs = _sources()
-    logs = []
+    srcs = _sources() if library else []
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = ex.submit(_compile_binding) if binding else None
         results = list(ex.map(_compile, srcs))
-        binding = binding.result()
-    objs = [o for o, _ in results]
-    logs = [l for _, l in results]
-    tmp = LIB + f".tmp{os.getpid()}"
-    _run([_nvcc()] + ARCH + ["-shared", "-Xlinker", "-soname=" + os.path.basename(LIB), "-o", tmp] + objs, "link")
-    os.replace(tmp, LIB)
-    _link_binding(binding)
-    with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
-        f.write("\n".join(logs))
-    if verbose:
-        print("\n".join(logs))
+    if library:
+        tmp = LIB + f".tmp{os.getpid()}"
+        _run([_nvcc()] + ARCH + ["-shared", "-Xlinker", "-soname=" + os.path.basename(LIB), "-o", tmp]
+             + [obj for obj, _ in results], "link")
+        os.replace(tmp, LIB)
+        logs = "\n".join(log for _, log in results)
+        with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
+            f.write(logs)
+        if verbose:
+            print(logs)
+    if binding:
+        _link_binding(binding.result())
     return LIB
 
 
