@@ -157,3 +157,30 @@ def test_queries_and_outputs_in_common_memory(g):
         with pytest.raises(g.RFP2Error) as e:
             g.rfp2_attn_decode(between, cache, table, lens, out=arena.view(-1)[2 * n + D: 5 * n + D].view(B, nq, Hq, D))
         assert e.value.status == 1
+
+
+@pytest.mark.parametrize("T,H,D,turned", [(3000, 1, 32, 0), (3000, 1, 32, 32), (16417, 2, 64, 64), (200001, 1, 32, 0), (1500001, 1, 32, 2)])
+def test_many_tokens_to_write_and_read(g, T, H, D, turned):
+    """More tokens than a CTA's table holds, than the CTAs take at once, odd ones: each is where its slot says, the
+    same as when it is written by itself."""
+    import torch
+    r = torch.Generator(device="cuda").manual_seed(T)
+    page = 16
+    whole, parts = (g.rfp2_kv_alloc(-(-T // page) + 1, H, page, D) for _ in range(2))
+    k, v = torch.randn((2, T, H, D), generator=r, device="cuda")
+    slots = torch.randperm(T, generator=r, device="cuda")
+    slots[:: 97] = -1
+    rotation = ()
+    if turned:
+        rotation = (torch.randint(0, 9999, (T,), generator=r, device="cuda", dtype=torch.int32), g.rfp2_rope_frequencies(turned)[0])
+    g.rfp2_kv_write(whole, k, v, slots, *rotation)
+    for a in range(0, T, 999):
+        b = min(a + 999, T)
+        g.rfp2_kv_write(parts, k[a:b], v[a:b], slots[a:b], *(t if t.numel() != T else t[a:b] for t in rotation))
+    assert all(torch.equal(x, y) for x, y in zip(whole, parts))
+    kept = slots >= 0
+    rk, rv = g.rfp2_kv_read(whole, slots)
+    if not turned:
+        assert float((rk - k)[kept].abs().max()) <= float(k.abs().max()) / 253
+    assert float((rv - v)[kept].abs().max()) <= float(v.abs().max()) / 253
+    assert not rk[~kept].any() and not rv[~kept].any()
