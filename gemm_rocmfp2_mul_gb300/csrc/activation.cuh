@@ -87,14 +87,16 @@ RFP2_DEV uint64_t turn_fraction(float f) {
 }
 
 // (cos, sin) of position turns of `fraction`: the top 32 bits as a signed
-// share of a turn (2^-32 turn = 1.5e-9 rad), then sincospi, exact in its
-// argument.
+// share of a turn (2^-32 turn = 1.5e-9 rad), of which sincospi, exact in its
+// argument, takes what a float holds; the rest, up to 9.4e-8 rad, turns the result.
 RFP2_DEV float2 rotary_cos_sin(int position, uint64_t fraction) {
     const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(position)) * fraction;
-    const float half_turns = static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f;
+    const int share = static_cast<int>(turn >> 32);
+    const float held = static_cast<float>(share);
+    const float rest = static_cast<float>(share - static_cast<int>(held)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
     float s, c;
-    sincospif(half_turns, &s, &c);
-    return make_float2(c, s);
+    sincospif(held * 4.656612873077393e-10f, &s, &c);
+    return make_float2(fmaf(-s, rest, c), fmaf(c, rest, s));
 }
 
 // The place of pair p in a table of `pairs` cosines or sines that is read four
