@@ -607,7 +607,7 @@ def rfp2_attn_decode(q, cache, table, lens, scale=None, window=0, softcap=0.0, o
     [B, nq, Hq, D] of q's type (out=q, contiguous, writes in place) and lse fp32 [B, nq, Hq].
     scale: D**-0.5 unless given; window: only the
     last `window` keys (0: all); softcap: scores become softcap * tanh(s / softcap) (0: as they are).
-    workspace: from rfp2_attn_decode_workspace.  There is no gradient."""
+    workspace: from rfp2_attn_decode_workspace.  No sequence (B = 0) is nothing to do.  There is no gradient."""
     if out is None or lse is None or workspace is None:
         if q.dim() != 4:
             raise ValueError(f"q must have 4 dimensions, got {q.dim()}")

@@ -242,6 +242,7 @@ int attn_decode(PyObject *const *a) {
     const at::Tensor &workspace = array(a[9], "workspace", at::kByte, "torch.uint8", device);
     const int64_t width = table.size(1), stride = B > 1 ? table.stride(0) : std::max(table.stride(0), width);
     const double scale = a[4] == Py_None ? 1.0 / std::sqrt((double)c.D) : number(a[4]);
+    if (B == 0) return RFP2_OK;  // no sequence, as rotation and cache take no token
     wrote(out);
     wrote(lse);
     return rfp2_attn_decode(q.data_ptr(), type, B, nq, Hq, c.D, q.stride(0), q.stride(1), q.stride(2), c.k_codes,

@@ -184,3 +184,18 @@ def test_many_tokens_to_write_and_read(g, T, H, D, turned):
         assert float((rk - k)[kept].abs().max()) <= float(k.abs().max()) / 253
     assert float((rv - v)[kept].abs().max()) <= float(v.abs().max()) / 253
     assert not rk[~kept].any() and not rv[~kept].any()
+
+
+def test_no_sequences(g):
+    """A batch of none, as a server between requests has, is nothing to do; what else is wrong is still said."""
+    import torch
+    cache = g.rfp2_kv_alloc(2, 2, 4, 64)
+    q = torch.empty((0, 1, 4, 64), device="cuda")
+    table, lens = (torch.empty(s, dtype=torch.int32, device="cuda") for s in ((0, 3), (0,)))
+    for workspace in (None, torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")):
+        out, lse = g.rfp2_attn_decode(q, cache, table, lens, workspace=workspace)
+        assert out.shape == (0, 1, 4, 64) and lse.shape == (0, 1, 4)
+    with pytest.raises(ValueError):
+        g.rfp2_attn_decode(q, cache, table, torch.zeros(1, dtype=torch.int32, device="cuda"))
+    with pytest.raises(TypeError):
+        g.rfp2_attn_decode(q, cache, table.long(), lens)
