@@ -1,6 +1,8 @@
 """Edges of the attention operators' arguments that the host decides, without a GPU."""
 import ctypes as C
+import math
 
+import numpy as np
 import pytest
 
 
@@ -63,3 +65,19 @@ def test_the_line_ends_before_32_bits_do(g):
     for line, heads in ((2 ** 31 - 2, 33), (2 ** 31 - 3, 95), (2 ** 31 - 4, 932)):
         assert line % heads == 0
         assert attn_decode(g, 1 << 30, 1 << 35, 1 << 36, B=1, nq=1, Hq=heads, heads=heads, page=16, width=line // heads - 5) == 2
+
+
+@pytest.mark.parametrize("R,base,stretch,trained,fast,slow", [(128, 10000.0, 8.0, 4096.0, 32.0, 1.0), (64, 500000.0, 4.0, 8192.0, 32.0, 1.0),
+                                                              (96, 10000.0, 16.0, 2048.0, 20.0, 2.5)])
+def test_the_ramp_between_its_ends(g, R, base, stretch, trained, fast, slow):
+    """f (keep + (1 - keep) / stretch), keep = (trained f / 2 pi - slow) / (fast - slow) within [0, 1], in double and
+    rounded once: libm's last places may fall either way at a float's boundary, so half a float's place and 1e-14."""
+    got, _ = g.rfp2_rope_frequencies(R, base, "ramp", stretch=stretch, trained=trained, fast=fast, slow=slow, device="cpu")
+    between = 0
+    for i, x in enumerate(got.tolist()):
+        f = base ** (-2 * i / R)
+        keep = min(1.0, max(0.0, (trained * f / (2 * math.pi) - slow) / (fast - slow)))
+        between += 0.0 < keep < 1.0
+        want = f * (keep + (1 - keep) / stretch)
+        assert abs(x - want) <= 0.5 * float(np.spacing(np.float32(want))) + 1e-14 * want
+    assert between >= 5         # the case has a ramp
