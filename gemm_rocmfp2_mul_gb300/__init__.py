@@ -513,11 +513,9 @@ def rfp2_rope(x, positions, inv_freq, out=None, interleaved=False, inverse=False
     values of each head rotated by positions int32 [T]; out=x rotates in place.  inverse=True
     negates the angles (the gradient).  A gradient of x goes through the call, unless `out` is given:
     that is refused where x requires one."""
-    if x.requires_grad and _torch().is_grad_enabled():
-        if out is not None:
-            raise RuntimeError("rfp2_rope with out= has no gradient, and x requires one")
-        return _rope_with_gradient().apply(x, positions, inv_freq, interleaved, inverse, factor)
     if out is None:
+        if x.requires_grad and _torch().is_grad_enabled():
+            return _rope_with_gradient().apply(x, positions, inv_freq, interleaved, inverse, factor)
         out = _empty(x.shape, x.dtype, x)
     rc = (_native or _binding()).rope(
         x, positions, inv_freq, out,

@@ -289,9 +289,9 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
     static_assert(SLOT * 4 <= STAGES * L::stage_bytes, "a warp's partial result fits its ring");
     static_assert(STAGES >= 2 && WARPS <= 16, "");
     static_assert(attn_smem<NB, NT, PIECES>(kAttnMaxBatch) <= (attn_ctas_per_sm(NB, NT) == 2 ? 113 : 227) * 1024, "");
-    // p = 64 * 2^(s - r - 4), with r the largest s but for at most 4: it goes with a 64th of the codes, so that their
-    // product is a value at most
-    constexpr float kShift = 2.0f, kSlack = 4.0f;
+    // p = 2^(s - r), with r the largest s but for at most 4: 16 at most, and it goes with a 64th of the codes, so that
+    // their product is a quarter of a value at most
+    constexpr float kSlack = 4.0f;
     constexpr float kCodes = 64.0f;                // the products' codes are 64ths
     constexpr float kNone = -3.4e38f;              // the reference before any key
     extern __shared__ __align__(128) uint8_t smem[];
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
         }
     };
     const auto lse_of = [&](float m, float l) {
-        return l == 0.0f ? -CUDART_INF_F : m * 0.6931471805599453f + logf(l * 0.25f);
+        return l == 0.0f ? -CUDART_INF_F : m * 0.6931471805599453f + logf(l);
     };
 
     // four values d .. d + 3 of column c of a unit that is joined: references and sums m and l
@@ -892,7 +892,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        pr[nt][e] = exp2_fast(sc[nt][e] - ref[nt][e & 1] + kShift);
+                        pr[nt][e] = exp2_fast(sc[nt][e] - ref[nt][e & 1]);
                         part[nt][e & 1] += pr[nt][e];
                     }
 

@@ -8,6 +8,7 @@
 
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <ATen/core/grad_mode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -39,7 +40,9 @@ const at::Tensor &tensor(PyObject *o, const char *name, int &device) {
     if (!t.is_cuda()) refuse(PyExc_TypeError, name, "must be a CUDA tensor");
     const int index = t.get_device();
     if (device < 0) {
-        if (index != c10::cuda::current_device()) refuse(PyExc_ValueError, name, "must be on the current device");
+        // (with one GPU there, that is 0)
+        if ((index != 0 || c10::cuda::device_count() > 1) && index != c10::cuda::current_device())
+            refuse(PyExc_ValueError, name, "must be on the current device");
         device = index;
     }
     if (index != device) refuse(PyExc_ValueError, name, "must be on the other tensors' device");
@@ -160,6 +163,8 @@ int rope(PyObject *const *a) {
     const at::Tensor &out = rows(a[3], "out", 3, device);
     if (!same_shape(out, x) || out.scalar_type() != x.scalar_type())
         refuse(PyExc_ValueError, "out must have x's shape and type");
+    if (x.requires_grad() && at::GradMode::is_enabled())
+        refuse(PyExc_RuntimeError, "x", "requires a gradient, which a call with out= does not give");
     wrote(out);
     return rfp2_rope(x.data_ptr(), type, x.size(0), x.size(1), x.size(2), x.stride(0), x.stride(1),
                      positions.data_ptr<int32_t>(), inv_freq.data_ptr<float>(), 2 * inv_freq.numel(),
