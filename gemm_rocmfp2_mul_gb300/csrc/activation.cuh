@@ -107,7 +107,7 @@ RFP2_DEV int table_place(int p, int pairs) {
     return V == 8 ? ((p >> 2 & 1) * (pairs >> 3) + (p >> 3)) * 4 + (p & 3) : p;
 }
 
-// n / d for 0 <= n < 2^31 by a multiplication: with 2^(s-1) < d <= 2^s and
+// n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery 1994): with 2^(s-1) < d <= 2^s and
 // mul = floor(2^32 (2^s - d) / d) + 1, n / d = (mulhi(n, mul) + n) >> s.
 struct FastDiv {
     uint32_t d, mul, shift;

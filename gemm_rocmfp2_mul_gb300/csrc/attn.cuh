@@ -24,15 +24,16 @@
 // keys and the scales of a row's blocks are, each product keeps its own digits.
 // Two pieces (the first 8 bits of p dV, and the rest rounded to 8) leave 2^-15 of
 // it for 16-bit outputs, three are all 24 bits for fp32.  (f16 pieces, one for bf16
-// outputs, took 353 us where these take 386, 55 where 60 and 40.5 where 45 below,
+// outputs, took 350 us where these take 385, 55 where 60 and 40.5 where 44 below,
 // but needed one exponent for all blocks of a key and lost what lay far below.)
 //
 // Measured (one GB300, back to back): 64 sequences of up to 32768 keys, 64 heads
-// over 8 of 128, bf16: 388 us for 2.39 GB (6.2 TB/s; copy rate 6.7); one of 131072
+// over 8 of 128, bf16: 385 us for 2.39 GB (6.2 TB/s; copy rate 6.7); one of 131072
 // keys, 40 over 8: 60 us (5.0 TB/s); 16 of up to 8192, 32 over 8, fp32: 44 us (4.3
-// TB/s); one of 1000 keys: 9.4 us.  The start (three dependent reads) and the joins
-// take about 8 us of a long call; on the way the instructions of three warps a
-// scheduler set the pace, some 600 a tile of 8 columns x 128 values.
+// TB/s); one of 1000 keys: 9.4 us, of 16: 4.5 us.  The start (three dependent reads)
+// and the joins take about 8 us of a long call; on the way the instructions of three
+// warps a scheduler set the pace, 607 a tile of 8 columns x 128 values, in 60 % of the
+// issue slots.
 #pragma once
 
 #include <atomic>
@@ -42,18 +43,19 @@
 namespace rfp2 {
 
 constexpr int kAttnTile = 16;        // keys
-// A unit's fixed cost, in tiles.  1, 2 and 4: 37.8, 34.2 and 34.4 us for 7 sequences
-// of 16 heads of 256 values, 27.8, 26.1 and 23.7 us for 53 of up to 926 keys.
+// A unit's fixed cost, in tiles.  1, 2 and 4: 38.4, 33.4 and 33.3 us for 7 sequences
+// of 16 heads of 256 values, 26.8, 24.4 and 24.2 us for 53 of up to 926 keys.
 constexpr int kAttnGap = 4;
 // The shortest stretch of a warp, in tiles: 1 tile against 2, one sequence of 1000
-// keys: 9.2 and 10.4 us.
+// keys: 9.4 and 10.6 us.
 constexpr int kAttnMinStretch = 1;
 // Tiles a warp (gap included) up to which a unit stays in one CTA where the CTAs
-// suffice: 8 heads of 256 keys 7.5 us in one CTA each and 10.0 joined, 512 keys 8.9
-// and 9.9, 1000 keys 12.5 and 9.3.
+// suffice: 8 heads of 256 keys 7.3 us in one CTA each and 8.7 joined, 512 keys 9.0
+// and 9.1, 1000 keys 13.0 and 9.4.
 constexpr int kAttnWholeUnit = 4;
-// Bytes of the cache on their way to an SM, at most.  74 KB, 110 and 147, by the
-// stages of 12 warps (64 sequences, 2.4 GB): 373 us, 356 and 368.
+// Bytes of the cache on their way to an SM, at most.  55 KB, 110 and 166, by the
+// stages of 12 warps (64 sequences, 2.4 GB): 386 us, 386 and 388; 8 heads of 1000 keys:
+// 9.5, 9.4 and 9.4; 53 sequences of up to 926: 23.8, 24.2 and 25.2.
 constexpr int kAttnInFlight = 112 * 1024;
 constexpr int kAttnMaxBatch = 1024;  // sequences of one launch
 // Tiles whose weights are summed by themselves before they join the unit's sum: one
@@ -74,8 +76,8 @@ struct AttnArgs {
     int dtype, q_words;         // q_words: q can be read as 16-byte words
     // divisors of the launch, multiplied by: a division by a value only known at
     // run time is some 25 instructions on the way to the first load, and again at
-    // every unit (12 x 5 tokens of 16 heads over 2, D = 64, pages of 48: 13.5 ->
-    // 12.7 us; 7 x 16 heads of D = 256, pages of 33: 33.2 -> 31.2 us)
+    // every unit (12 x 5 tokens of 16 heads over 2, D = 64, pages of 48: 14.0 ->
+    // 13.4 us; 7 x 16 heads of D = 256, pages of 33: 34.7 -> 33.3 us)
     FastDiv by_page, by_group, by_tiles;  // page_size, group, column_tiles
     float scale, softcap;
     int64_t window;
@@ -121,8 +123,9 @@ constexpr int kPairF32 = 4;
 
 // Warps: the tile's work is a long chain, so as many as the registers hold.  By
 // head size x columns (what a warp accumulates): 12 up to 128 values x 16 at 168
-// registers, where q's fragments of 16 columns wait in shared memory; beyond that
-// 8.  Small ones run two CTAs of 8.
+// registers, where q's fragments of 16 columns wait in shared memory (8: 436 us for 12's
+// 386 of 64 sequences); beyond that 8.  Small ones run two CTAs of 8.  (Spilled to hold that: of 16 columns 16-20 bytes
+// at 128 values, 24 at 256; of 8 columns of 256 values 8, fp32.)
 constexpr int attn_warps(int NB, int NT) { return NB * NT <= 2 || NB > 4 ? 8 : 12; }
 constexpr int attn_ctas_per_sm(int NB, int NT) { return NB * NT <= 2 ? 2 : 1; }
 // Bytes of a warp's q fragments in shared memory: each lane's own, for two column
@@ -611,7 +614,7 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
 
     // ---- the units of this stretch ----
     const float cap_out = a.softcap * 1.4426950408889634f;
-    // tanhf for 16-bit types too, 13.0 -> 13.4 us of 12 x 5 tokens: the lse of few keys shows an error of
+    // tanhf for 16-bit types too, 0.4 us of 13.4 for 12 x 5 tokens: the lse of few keys shows an error of
     // 2e-7 of the cap, as 1 - 2 / (e^2x + 1) has it near 0
     const float cap_in = fminf(1.0f / a.softcap, 3.402823466e38f);
     // Queries of any size on keys of any size: 2^-24 of the codes and q below 2^15 make a block's sum 8 at most, so that

@@ -9,12 +9,13 @@
 // (token, pair)'s cos and sin are computed once into shared memory meanwhile.
 //
 // Measured (one GB300, back to back), 16384 tokens x 8 heads of 128 values, bf16:
-// write 25.8 us, rotated 30.7 (105 MB; the instructions, 169 a warp of 8-value
-// steps, set the pace), read 19.0 us (5.5 TB/s).  Eight fp32 tokens: 2.1 and 1.7.
-// Codes by division took 47 us.  Writes at three CTAs of 80 registers an SM against
-// four of 64: 30.7 and 30.3 us, but 6.0 and 7.3 for 4999 tokens of 5 x 96 f16, whose
-// interleaved rotation spills at 64; reads at five against six: 19.0 and 19.2, 3.75
-// and 4.1.
+// write 24.6 us, rotated 30.2 (105 MB; the instructions, 172 a warp of 8-value
+// steps, set the pace), read 15.2 us, written and read in turn 48.8.  Eight fp32
+// tokens: 2.2 and 2.2.  Codes by division took 47 us.  Writes at three CTAs of 80
+// registers an SM against four of 64: 30.7 and 30.3 us, but 6.0 and 7.3 for 4999
+// tokens of 5 x 96 f16, whose interleaved rotation spills at 64 (rows of 16 bits at
+// any alignment spill 48 bytes at 80 too); reads at five against six: 19.0 and 19.2,
+// 3.75 and 4.1.
 #include <algorithm>
 
 #include "activation.cuh"
