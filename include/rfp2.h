@@ -385,7 +385,8 @@ typedef enum {
     RFP2_ROPE_RAMP = 3     /* by turns over the trained length (YaRN, Peng et al.
                               2023): kept from `fast` turns up, divided by
                               `stretch` below `slow` turns, linear in the turns'
-                              share of [slow, fast] between */
+                              share of [slow, fast] between (not, as some
+                              implementations, in the pair's index) */
 } rfp2_rope_scaling;
 
 /* Rotary frequencies, host memory: inv_freq[i], i < R/2, computed in double
