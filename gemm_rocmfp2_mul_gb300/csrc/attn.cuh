@@ -746,11 +746,6 @@ __global__ void __launch_bounds__(32 * attn_warps(NB, NT), attn_ctas_per_sm(NB, 
             sum[nt][0] = sum[nt][1] = 0.0f;
         }
 
-        const auto sum_of_keys = [](float l) {
-            l += __shfl_xor_sync(0xffffffffu, l, 4);
-            l += __shfl_xor_sync(0xffffffffu, l, 8);
-            return l + __shfl_xor_sync(0xffffffffu, l, 16);
-        };
 #pragma unroll 1
         for (int t = from; t < to;) {
             const int stop = min(to, t + kAttnSums);
