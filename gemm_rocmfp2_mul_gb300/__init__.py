@@ -8,8 +8,8 @@ current torch stream to the library, and raises :class:`RFP2Error` on a
 non-zero status.  All arithmetic runs in the library's CUDA kernels; there is
 no CPU or PyTorch fallback: if the library is not built or cannot be loaded,
 every call raises.  Tensors have to be on the current device, where the library
-launches.  Most calls go through ctypes; those of the attention operators, small
-and many, through a compiled binding.
+launches.  Most calls go through ctypes; those of the attention and feed-forward
+operators, small and many, through a compiled binding.
 
 Build the library with :func:`build` (nvcc, sm_103a).
 """
@@ -34,6 +34,8 @@ __all__ = [
     "rfp2_set_weight_prefetch", "rfp2_weight_prefetch",
     "KVCache", "rfp2_rope_frequencies", "rfp2_rope", "rfp2_kv_alloc", "rfp2_kv_write", "rfp2_kv_read",
     "rfp2_attn_decode", "rfp2_attn_decode_workspace", "rfp2_attn_decode_workspace_bytes",
+    "Norm", "rfp2_rms_norm", "rfp2_moe_route", "rfp2_moe_gemm", "rfp2_moe_gemm_workspace",
+    "rfp2_moe_gemm_workspace_bytes", "rfp2_moe_combine",
 ]
 
 MAX_BATCH = 8
@@ -100,6 +102,12 @@ _SIGNATURES = {
     "rfp2_attn_decode_workspace_bytes": (_SZ, [_I64] * 5),
     "rfp2_attn_decode": (_I32, [_P, _I32] + [_I64] * 7 + [_P] * 4 + [_I64] * 3
                          + [_P, _I64, _I64, _P, _F32, _I64, _F32, _P, _P, _P, _SZ, _P, _P]),
+    "rfp2_rms_norm": (_I32, [_P, _I32, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I32, _F32, _P, _I32,
+                             _I64, _P, _P, _P]),
+    "rfp2_moe_route": (_I32, [_P, _I32, _I64, _I64, _I64, _I32, _P] + [_I64] * 4 + [_I32, _F32, _P, _P, _P]),
+    "rfp2_moe_combine": (_I32, [_P, _I32] + [_I64] * 5 + [_P, _P, _P, _I64, _P, _I32, _I64, _P]),
+    "rfp2_moe_gemm_workspace_bytes": (_SZ, [_I64] * 3),
+    "rfp2_moe_gemm": (_I32, [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _I32, _P, _I32, _P, _P, _SZ, _P, _P]),
 }
 
 
@@ -617,3 +625,106 @@ def rfp2_attn_decode(q, cache, table, lens, scale=None, window=0, softcap=0.0, o
     if rc:
         raise RFP2Error(rc, "rfp2_attn_decode")
     return out, lse
+
+
+# -- the feed-forward half around the (routed) experts' products ----------------------------
+
+_SCORINGS = {"softmax": 0, "sigmoid": 1}
+_ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}
+
+
+class Norm(NamedTuple):
+    """What rfp2_rms_norm returns: y [T, K]; its Q8 blocks, codes q int8 [T, K] and scales d fp32
+    [T, K/32]; total = x + residual.  What was not asked for is None."""
+    y: Any
+    q: Any
+    d: Any
+    total: Any
+
+
+def rfp2_rms_norm(x, weight, eps=1e-6, residual=None, want="y", dtype=None, y=None, q=None, d=None, total=None):
+    """Root-mean-square norm of x [T, K] (any row stride), after adding `residual` where there is one:
+    s / sqrt(mean(s^2) + eps) * weight.  want: "y" (values, of `dtype`, x's unless given), "q8" (the Q8
+    blocks that rfp2_gemv_q8 reads, K % 32 == 0) or "both".  Buffers that are passed are filled; total and y may be
+    x or residual.  There is no gradient."""
+    if want not in ("y", "q8", "both"):
+        raise ValueError(f"want must be 'y', 'q8' or 'both', got {want!r}")
+    torch = _torch()
+    if want == "q8":
+        y = None
+    elif y is None:
+        y = _empty(x.shape, dtype or x.dtype, x)
+    if want == "y":
+        q = d = None
+    else:
+        q = _empty(x.shape, torch.int8, x) if q is None else q
+        d = _empty((*x.shape[:-1], x.shape[-1] // 32), torch.float32, x) if d is None else d
+    if residual is None:
+        total = None
+    elif total is None:
+        total = _empty(x.shape, x.dtype, x)
+    rc = (_native or _binding()).rms_norm(x, weight, eps, residual, total, y, q, d)
+    if rc:
+        raise RFP2Error(rc, "rfp2_rms_norm")
+    return Norm(y, q, d, total)
+
+
+def rfp2_moe_route(logits, top_k, scoring="softmax", bias=None, groups=1, keep=1, group_top=1, renormalise=True,
+                   scale=1.0, ids=None, weights=None):
+    """The experts of each token, from the router's logits [T, E]: (ids int32 [T, top_k], largest first, and
+    weights fp32 [T, top_k]).  scoring: "softmax" or "sigmoid"; bias fp32 [E] is added for the choice alone; with
+    groups > 1 only the `keep` groups are chosen from whose group_top largest values sum to most.  A logit of
+    -infinity masks its expert; where none is left the id is -1 and the weight 0.  There is no gradient."""
+    if ids is None or weights is None:
+        torch = _torch()
+        if logits.dim() != 2:
+            raise ValueError(f"logits must have 2 dimensions, got {logits.dim()}")
+        shape = (logits.shape[0], top_k)
+        ids = _empty(shape, torch.int32, logits) if ids is None else ids
+        weights = _empty(shape, torch.float32, logits) if weights is None else weights
+    if ids.shape[-1] != top_k:
+        raise ValueError(f"ids must be [T, {top_k}], got {tuple(ids.shape)}")
+    rc = (_native or _binding()).moe_route(logits, _SCORINGS[scoring], bias, groups, keep, group_top,
+                                           1 if renormalise else 0, scale, ids, weights)
+    if rc:
+        raise RFP2Error(rc, "rfp2_moe_route")
+    return ids, weights
+
+
+def rfp2_moe_gemm_workspace_bytes(T: int, top_k: int, E: int) -> int:
+    return int(lib().rfp2_moe_gemm_workspace_bytes(T, top_k, E))
+
+
+def rfp2_moe_gemm_workspace(ids, E):
+    """A workspace for rfp2_moe_gemm of ids [T, top_k] over E experts, any M and K; calls in one stream may share it."""
+    T, top_k = ids.shape
+    return _empty(max(rfp2_moe_gemm_workspace_bytes(T, top_k, E), 1), _torch().uint8, ids)
+
+
+def rfp2_moe_gemm(W, E, M, K, ids, X, bias=None, activation="none", Y=None, workspace=None, dev_status=None):
+    """The routed experts' products on the tensor cores, for any number of tokens: bf16 [T, top_k, M] =
+    W[ids[t, j]] x + bias[ids[t, j]] with X bf16 [T, K], or [T, top_k, K] (a row for every slot), ids int32
+    [T, top_k] and bias fp32 [E, M].  activation "silu" or "gelu": [T, top_k, M/2] = act(gate) * up, W's first M/2 rows
+    being the gate's.  An id of -1 is no expert: its row becomes zeros.  There is no gradient."""
+    if Y is None:
+        Y = _empty((*ids.shape, M if activation == "none" else M // 2), _torch().bfloat16, X)
+    if workspace is None:
+        workspace = rfp2_moe_gemm_workspace(ids, E)
+    rc = (_native or _binding()).moe_gemm(W, E, M, K, ids, X, bias, _ACTIVATIONS[activation], Y, workspace, dev_status)
+    if rc:
+        raise RFP2Error(rc, "rfp2_moe_gemm")
+    return Y
+
+
+def rfp2_moe_combine(y, weights, ids=None, residual=None, out=None, dtype=None):
+    """The sum of a token's experts: [T, M] = sum_j weights[t, j] * y[t, j] + residual[t], of y [T, top_k, M] (any
+    token and slot strides) and weights fp32 [T, top_k].  ids: slots with a negative id are not read.  The result has
+    the residual's type, else `dtype`, else y's; out may be residual.  There is no gradient."""
+    if out is None:
+        if y.dim() != 3:
+            raise ValueError(f"y must have 3 dimensions, got {y.dim()}")
+        out = _empty((y.shape[0], y.shape[2]), residual.dtype if residual is not None else dtype or y.dtype, y)
+    rc = (_native or _binding()).moe_combine(y, weights, ids, residual, out)
+    if rc:
+        raise RFP2Error(rc, "rfp2_moe_combine")
+    return out

@@ -139,6 +139,24 @@ RFP2_DEV void rotary_table(float *table, const int32_t *positions, const float *
     }
 }
 
+// Host: T rows in memory, `bytes` of each read or written, `stride` bytes apart.
+struct Rows {
+    uintptr_t at;
+    int64_t T, bytes, stride;
+    Rows(const void *p, int64_t rows, int64_t row_bytes, int64_t stride_bytes)
+        : at(reinterpret_cast<uintptr_t>(p)), T(p ? rows : 0), bytes(row_bytes), stride(rows > 1 ? stride_bytes : row_bytes) {}
+    // Have the two a byte in common?  (Rows of different strides in one stretch of memory: taken as yes.)
+    bool meet(const Rows &o) const {
+        if (T == 0 || o.T == 0) return false;
+        const uintptr_t end = at + (T - 1) * stride + bytes, o_end = o.at + (o.T - 1) * o.stride + o.bytes;
+        if (end <= o.at || o_end <= at) return false;
+        if (T == 1 || o.T == 1 || stride != o.stride || stride < bytes || stride < o.bytes) return true;
+        const int64_t d = (int64_t)((at < o.at ? o.at - at : stride - (at - o.at) % stride) % stride);
+        return d < bytes || d + o.bytes > stride;
+    }
+    bool same(const Rows &o) const { return at == o.at && bytes == o.bytes && stride == o.stride; }
+};
+
 // Host: bytes of one value, 0 for an unknown type.
 inline int dtype_bytes(int dtype) {
     return dtype == RFP2_F32 ? 4 : dtype == RFP2_BF16 || dtype == RFP2_F16 ? 2 : 0;

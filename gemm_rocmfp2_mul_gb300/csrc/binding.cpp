@@ -258,6 +258,144 @@ int attn_decode(PyObject *const *a) {
                             stream_of(device));
 }
 
+// An input of a call that has no gradient.
+const at::Tensor &no_gradient(const at::Tensor &t, const char *name) {
+    if (t.requires_grad() && at::GradMode::is_enabled())
+        refuse(PyExc_RuntimeError, name, "requires a gradient, which the call does not give");
+    return t;
+}
+
+// rms_norm(x, weight, eps, residual, total, y, q, d)
+int rms_norm(PyObject *const *a) {
+    int device = -1;
+    const at::Tensor &x = no_gradient(rows(a[0], "x", 2, device), "x");
+    const int type = type_code(x, "x");
+    const int64_t T = x.size(0), K = x.size(1);
+    const at::Tensor &weight = no_gradient(rows(a[1], "weight", 1, device), "weight");
+    const int weight_type = type_code(weight, "weight");
+    if (weight.size(0) != K) refuse(PyExc_ValueError, "weight needs one value per column");
+    const auto like_x = [&](PyObject *o, const char *name) -> const at::Tensor * {
+        if (o == Py_None) return nullptr;
+        const at::Tensor &t = rows(o, name, 2, device);
+        if (!same_shape(t, x) || t.scalar_type() != x.scalar_type()) refuse(PyExc_ValueError, name, "must have x's shape and type");
+        return &t;
+    };
+    const at::Tensor *residual = like_x(a[3], "residual"), *total = like_x(a[4], "total");
+    if (residual) no_gradient(*residual, "residual");
+    const at::Tensor *y = nullptr;
+    int y_type = RFP2_F32;
+    if (a[5] != Py_None) {
+        y = &rows(a[5], "y", 2, device);
+        y_type = type_code(*y, "y");
+        if (!same_shape(*y, x)) refuse(PyExc_ValueError, "y must have x's shape");
+    }
+    int8_t *q = nullptr;
+    float *d = nullptr;
+    if (a[6] != Py_None && a[7] != Py_None) {
+        const at::Tensor &qt = array(a[6], "q", at::kChar, "torch.int8", device);
+        const at::Tensor &dt = array(a[7], "d", at::kFloat, "torch.float32", device);
+        if (!same_shape(qt, x) || dt.dim() != 2 || dt.size(0) != T || dt.size(1) != K / 32)
+            refuse(PyExc_ValueError, "q must be [T, K] and d [T, K/32]");
+        q = qt.data_ptr<int8_t>();
+        d = dt.data_ptr<float>();
+        wrote(qt);
+        wrote(dt);
+    }
+    const double eps = number(a[2]);
+    if (total) wrote(*total);
+    if (y) wrote(*y);
+    return rfp2_rms_norm(x.data_ptr(), type, T, K, x.stride(0), residual ? residual->data_ptr() : nullptr,
+                         residual ? residual->stride(0) : 0, total ? total->data_ptr() : nullptr,
+                         total ? total->stride(0) : 0, weight.data_ptr(), weight_type, (float)eps,
+                         y ? y->data_ptr() : nullptr, y_type, y ? y->stride(0) : 0, q, d, stream_of(device));
+}
+
+// moe_route(logits, scoring, bias, groups, keep, group_top, renormalise, scale, ids, weights)
+int moe_route(PyObject *const *a) {
+    int device = -1;
+    const at::Tensor &logits = no_gradient(rows(a[0], "logits", 2, device), "logits");
+    const int type = type_code(logits, "logits");
+    const int64_t T = logits.size(0), E = logits.size(1);
+    const float *bias = nullptr;
+    if (a[2] != Py_None) {
+        const at::Tensor &b = no_gradient(array(a[2], "bias", at::kFloat, "torch.float32", device), "bias");
+        if (b.numel() != E) refuse(PyExc_ValueError, "bias needs one value per expert");
+        bias = b.data_ptr<float>();
+    }
+    const at::Tensor &ids = array(a[8], "ids", at::kInt, "torch.int32", device);
+    const at::Tensor &weights = array(a[9], "weights", at::kFloat, "torch.float32", device);
+    if (ids.dim() != 2 || ids.size(0) != T || !same_shape(ids, weights))
+        refuse(PyExc_ValueError, "ids and weights must be [T, top_k]");
+    wrote(ids);
+    wrote(weights);
+    return rfp2_moe_route(logits.data_ptr(), type, T, E, logits.stride(0), (int)whole(a[1]), bias, whole(a[3]),
+                          whole(a[4]), whole(a[5]), ids.size(1), (int)whole(a[6]), (float)number(a[7]),
+                          ids.data_ptr<int32_t>(), weights.data_ptr<float>(), stream_of(device));
+}
+
+// moe_combine(y, weights, ids, residual, out)
+int moe_combine(PyObject *const *a) {
+    int device = -1;
+    const at::Tensor &y = no_gradient(rows(a[0], "y", 3, device), "y");
+    const int type = type_code(y, "y");
+    const int64_t T = y.size(0), top_k = y.size(1), M = y.size(2);
+    const at::Tensor &weights = no_gradient(array(a[1], "weights", at::kFloat, "torch.float32", device), "weights");
+    const auto per_slot = [&](const at::Tensor &t) { return t.dim() == 2 && t.size(0) == T && t.size(1) == top_k; };
+    if (!per_slot(weights)) refuse(PyExc_ValueError, "weights must be [T, top_k]");
+    const int32_t *ids = nullptr;
+    if (a[2] != Py_None) {
+        const at::Tensor &i = array(a[2], "ids", at::kInt, "torch.int32", device);
+        if (!per_slot(i)) refuse(PyExc_ValueError, "ids must be [T, top_k]");
+        ids = i.data_ptr<int32_t>();
+    }
+    const at::Tensor &out = rows(a[4], "out", 2, device);
+    const int out_type = type_code(out, "out");
+    if (out.size(0) != T || out.size(1) != M) refuse(PyExc_ValueError, "out must be [T, M]");
+    const at::Tensor *residual = nullptr;
+    if (a[3] != Py_None) {
+        residual = &no_gradient(rows(a[3], "residual", 2, device), "residual");
+        if (!same_shape(*residual, out) || residual->scalar_type() != out.scalar_type())
+            refuse(PyExc_ValueError, "residual must have out's shape and type");
+    }
+    wrote(out);
+    return rfp2_moe_combine(y.data_ptr(), type, T, top_k, M, y.stride(0), y.stride(1), weights.data_ptr<float>(),
+                            ids, residual ? residual->data_ptr() : nullptr, residual ? residual->stride(0) : 0,
+                            out.data_ptr(), out_type, out.stride(0), stream_of(device));
+}
+
+// moe_gemm(W, E, M, K, ids, X, bias, activation, Y, workspace, dev_status)
+int moe_gemm(PyObject *const *a) {
+    int device = -1;
+    const at::Tensor &W = array(a[0], "W", at::kByte, "torch.uint8", device);
+    const int64_t E = whole(a[1]), M = whole(a[2]), K = whole(a[3]);
+    if (E < 1 || M < 1 || K < 1 || E > 65536 || M > (1 << 30) || K > (1 << 30) || W.numel() / E / M != K / 32 * 10 ||
+        W.numel() % (E * M) != 0)
+        refuse(PyExc_ValueError, "W must be the blocks [E, M, K/32, 10]");
+    const at::Tensor &ids = array(a[4], "ids", at::kInt, "torch.int32", device);
+    if (ids.dim() != 2) refuse(PyExc_ValueError, "ids must be [T, top_k]");
+    const int64_t T = ids.size(0), top_k = ids.size(1);
+    const at::Tensor &X = no_gradient(array(a[5], "X", at::kBFloat16, "torch.bfloat16", device), "X");
+    const bool each = X.dim() == 3;
+    if (X.dim() < 2 || X.dim() > 3 || X.size(0) != T || X.size(-1) != K || (each && X.size(1) != top_k))
+        refuse(PyExc_ValueError, "X must be [T, K] or [T, top_k, K]");
+    const float *bias = nullptr;
+    if (a[6] != Py_None) {
+        const at::Tensor &b = no_gradient(array(a[6], "bias", at::kFloat, "torch.float32", device), "bias");
+        if (b.dim() != 2 || b.size(0) != E || b.size(1) != M) refuse(PyExc_ValueError, "bias must be [E, M]");
+        bias = b.data_ptr<float>();
+    }
+    const int activation = (int)whole(a[7]);
+    const at::Tensor &Y = array(a[8], "Y", at::kBFloat16, "torch.bfloat16", device);
+    if (Y.dim() != 3 || Y.size(0) != T || Y.size(1) != top_k || Y.size(2) != (activation == RFP2_ACT_NONE ? M : M / 2))
+        refuse(PyExc_ValueError, "Y must be [T, top_k, M], M/2 when gated");
+    const at::Tensor &workspace = array(a[9], "workspace", at::kByte, "torch.uint8", device);
+    wrote(Y);
+    return rfp2_moe_gemm(W.data_ptr<uint8_t>(), E, M, K, ids.data_ptr<int32_t>(), T, top_k,
+                         static_cast<const uint16_t *>(X.data_ptr()), each, bias, activation,
+                         static_cast<uint16_t *>(Y.data_ptr()), workspace.data_ptr(), (size_t)workspace.numel(),
+                         status_of(a[10], device), stream_of(device));
+}
+
 template <int (*F)(PyObject *const *), int N>
 PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != N) {
@@ -276,7 +414,8 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n) {
 
 #define RFP2_METHOD(name, n) {#name, reinterpret_cast<PyCFunction>(call<name, n>), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {RFP2_METHOD(rope, 6), RFP2_METHOD(kv_write, 9), RFP2_METHOD(kv_read, 5),
-                         RFP2_METHOD(attn_decode, 11), {nullptr, nullptr, 0, nullptr}};
+                         RFP2_METHOD(attn_decode, 11), RFP2_METHOD(rms_norm, 8), RFP2_METHOD(moe_route, 10),
+                         RFP2_METHOD(moe_combine, 5), RFP2_METHOD(moe_gemm, 11), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_rfp2_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

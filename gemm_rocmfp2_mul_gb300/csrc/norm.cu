@@ -1,0 +1,341 @@
+// Root-mean-square norm after the residual's addition:
+//   s = x + residual (rounded to the activations' type), r = 1 / sqrt(mean s^2 + eps), y = s r weight,
+// as values and / or in Q8 blocks.  Bound by memory: a value is read once (twice with a residual) and
+// written once to three times, against about ten operations.
+//
+// A row belongs to a CTA, or to a warp where it is short; it stays in registers between its sum and its
+// outputs.  Q8 codes are those of the formula, not of its fp32 roundings: code = round-half-away(127 u / U)
+// with u = |s weight| and U a block's largest, in which r drops out.  In fp32 the quotient is off by
+// 4e-7 of itself at most; where a half-integer is that near, u and U, exact in fp64 (48 bits), decide.
+#include <algorithm>
+
+#include "activation.cuh"
+
+namespace rfp2 {
+namespace {
+
+struct NormArgs {
+    const void *x, *residual, *weight;
+    void *total, *y;
+    int8_t *q;
+    float *d;
+    int64_t T, xs, rs, ts, ys;
+    int K, weight_type, y_type;
+    float eps;
+};
+
+// V values of `type` (a uniform branch) at element `at`; four of 16 bits as one word of 8 bytes.
+template <typename T, int V>
+RFP2_DEV void load_run(const T *p, float (&v)[V]) {
+    if constexpr (V * sizeof(T) == 8) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p);
+        T t[V];
+        memcpy(t, &u, 8);
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = to_f32(t[e]);
+    } else {
+        load_values(p, v);
+    }
+}
+template <typename T, int V>
+RFP2_DEV void store_run(T *p, const float (&v)[V]) {
+    if constexpr (V * sizeof(T) == 8) {
+        T t[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) t[e] = from_f32<T>(v[e]);
+        uint2 u;
+        memcpy(&u, t, 8);
+        *reinterpret_cast<uint2 *>(p) = u;
+    } else {
+        store_values(p, v);
+    }
+}
+template <int V>
+RFP2_DEV void load_typed(const void *p, int type, int64_t at, float (&v)[V]) {
+    if (type == RFP2_F32)
+        load_run(static_cast<const float *>(p) + at, v);
+    else if (type == RFP2_BF16)
+        load_run(static_cast<const __nv_bfloat16 *>(p) + at, v);
+    else
+        load_run(static_cast<const __half *>(p) + at, v);
+}
+template <int V>
+RFP2_DEV void store_typed(void *p, int type, int64_t at, const float (&v)[V]) {
+    if (type == RFP2_F32)
+        store_run(static_cast<float *>(p) + at, v);
+    else if (type == RFP2_BF16)
+        store_run(static_cast<__nv_bfloat16 *>(p) + at, v);
+    else
+        store_run(static_cast<__half *>(p) + at, v);
+}
+
+// Sum (or maximum) over the warps that share a row; `part` has 32 places, and successive calls take
+// turns between two of them.
+template <bool MAX>
+RFP2_DEV float over_row(float v, int warps, float *part) {
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) {
+        const float o = __shfl_xor_sync(0xffffffffu, v, off);
+        v = MAX ? fmaxf(v, o) : v + o;
+    }
+    if (warps == 1) return v;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = lane < warps ? part[lane] : 0.0f;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) {
+        const float o = __shfl_xor_sync(0xffffffffu, v, off);
+        v = MAX ? fmaxf(v, o) : v + o;
+    }
+    return v;
+}
+
+// Is 254 u >= m U?  Exactly: u and U have 48 bits, the factors 8, and what a product loses is added back.
+RFP2_DEV bool reaches(double u, double m, double U) {
+    const double p = 254.0 * u, q = m * U;
+    return (p - q) + (fma(254.0, u, -p) - fma(m, U, -q)) >= 0.0;
+}
+
+// The codes of V values of a block that 32 / V neighbouring lanes share; s and w as they are, y = s r w in
+// fp32.  Returns the block's scale.
+template <int V>
+RFP2_DEV float block_codes(const float (&s)[V], const float (&w)[V], const float (&y)[V], int8_t (&code)[V]) {
+    constexpr int kLanes = 32 / V;
+    uint32_t top = 0;  // of |y|'s bits: NaN above infinity above all else
+#pragma unroll
+    for (int e = 0; e < V; ++e) top = max(top, __float_as_uint(y[e]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int off = 1; off < kLanes; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+    const float most = __uint_as_float(top);
+    const bool finite = top < 0x7F800000u, tiny = most < 0x1p-90f;
+    const float by = 127.0f / most;
+    bool near = finite && tiny && top != 0;
+    float c[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        const float t = fabsf(y[e]) * by;
+        c[e] = floorf(t + 0.5f);
+        near |= finite && fabsf(t - floorf(t) - 0.5f) <= t * 5e-7f;
+    }
+    if (__any_sync(0xffffffffu, near)) {
+        double U = 0.0;
+#pragma unroll
+        for (int e = 0; e < V; ++e) U = fmax(U, fabs((double)s[e] * (double)w[e]));
+#pragma unroll
+        for (int off = 1; off < kLanes; off <<= 1) U = fmax(U, __shfl_xor_sync(0xffffffffu, U, off));
+        if (near && U > 0.0 && U < CUDART_INF) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const double u = fabs((double)s[e] * (double)w[e]);
+                double k = tiny ? floor(127.0 * (u / U) + 0.5) : (double)c[e];
+                if (reaches(u, 2.0 * k + 1.0, U))
+                    k += 1.0;
+                else if (!reaches(u, 2.0 * k - 1.0, U))
+                    k -= 1.0;
+                c[e] = (float)k;
+            }
+        }
+    }
+    const float d = __fdiv_rn(most, 127.0f);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        const int k = finite && d != 0.0f ? (int)fminf(c[e], 127.0f) : 0;
+        code[e] = (int8_t)(__float_as_uint(y[e]) >> 31 ? -k : k);
+    }
+    return finite ? d : CUDART_NAN_F;
+}
+
+// A row's values: N runs of V a thread, run i of thread t at V (i threads + t).
+template <typename T, int V, int N>
+__global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a, int warps) {
+    __shared__ float part[2][32];
+    pdl_wait();
+    pdl_launch_dependents();
+    // warps == 1: each warp of the CTA has a row of its own
+    const int lanes = warps == 1 ? 32 : blockDim.x;
+    const int tid = warps == 1 ? threadIdx.x & 31 : threadIdx.x;
+    const int rows = warps == 1 ? blockDim.x >> 5 : 1;
+    for (int64_t row = (int64_t)blockIdx.x * rows + (warps == 1 ? threadIdx.x >> 5 : 0); row < a.T;
+         row += (int64_t)gridDim.x * rows) {
+        float s[N][V];
+        const T *x = static_cast<const T *>(a.x) + row * a.xs;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int at = V * (i * lanes + tid);
+#pragma unroll
+            for (int e = 0; e < V; ++e) s[i][e] = 0.0f;
+            if (at < a.K) load_values(x + at, s[i]);
+        }
+        if (a.residual) {
+            const T *rest = static_cast<const T *>(a.residual) + row * a.rs;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int at = V * (i * lanes + tid);
+                if (at < a.K) {
+                    float b[V];
+                    load_values(rest + at, b);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) s[i][e] = to_f32(from_f32<T>(s[i][e] + b[e]));
+                }
+            }
+        }
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int e = 0; e < V; ++e) sum = fmaf(s[i][e], s[i][e], sum);
+        sum = over_row<false>(sum, warps, part[0]);
+        float r = 1.0f / sqrtf(sum / (float)a.K + a.eps);
+        if (!(sum < 0x1p126f) || sum < 0x1p-90f) {
+            // squares out of range: of values below 1 in size, by a power of two
+            float most = 0.0f;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int e = 0; e < V; ++e) most = fmaxf(most, fabsf(s[i][e]));
+            most = over_row<true>(most, warps, part[1]);
+            if (most > 0.0f && most < CUDART_INF_F && sum == sum) {
+                int ex;
+                frexpf(most, &ex);
+                const float down = ldexpf(1.0f, -ex / 2), down2 = ldexpf(1.0f, -ex - -ex / 2);
+                float part_sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        const float v = s[i][e] * down * down2;
+                        part_sum = fmaf(v, v, part_sum);
+                    }
+                if (warps > 1) __syncthreads();
+                part_sum = over_row<false>(part_sum, warps, part[0]);
+                // r = 2^-ex / sqrt(mean + eps 2^-2ex)
+                const float mean = part_sum / (float)a.K + a.eps * down * down * down2 * down2;
+                r = mean < CUDART_INF_F ? down * (down2 / sqrtf(mean)) : r;
+            }
+        }
+        if (warps > 1) __syncthreads();  // part[] is written again for the next row
+        if (a.total && a.residual) {
+            T *to = static_cast<T *>(a.total) + row * a.ts;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int at = V * (i * lanes + tid);
+                if (at < a.K) store_values(to + at, s[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int at = V * (i * lanes + tid);
+            if (a.q == nullptr && at >= a.K) continue;
+            float w[V], y[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) w[e] = 0.0f;
+            if (at < a.K) load_typed(a.weight, a.weight_type, at, w);
+#pragma unroll
+            for (int e = 0; e < V; ++e) y[e] = s[i][e] * r * w[e];
+            if (a.y && at < a.K) store_typed(a.y, a.y_type, row * a.ys + at, y);
+            if (a.q) {
+                int8_t code[V];
+                const float d = block_codes<V>(s[i], w, y, code);
+                if (at < a.K) {
+                    int8_t *q = a.q + row * a.K + at;
+                    if constexpr (V == 8)
+                        *reinterpret_cast<uint2 *>(q) = *reinterpret_cast<const uint2 *>(code);
+                    else if constexpr (V == 4)
+                        *reinterpret_cast<uint32_t *>(q) = *reinterpret_cast<const uint32_t *>(code);
+                    else
+                        *q = code[0];
+                    if ((at & 31) == 0) a.d[row * (a.K >> 5) + (at >> 5)] = d;
+                }
+            }
+        }
+    }
+}
+
+template <typename T>
+cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream) {
+    constexpr int W = 16 / sizeof(T);
+    const auto fits = [&](const void *p, int64_t stride, int size) {
+        return !p || (aligned(p, 16) && stride * size % 16 == 0);
+    };
+    const int ysize = a.y ? dtype_bytes(a.y_type) : 4;
+    const bool wide = a.K % W == 0 && fits(a.x, a.xs, sizeof(T)) && fits(a.residual, a.rs, sizeof(T)) &&
+                      fits(a.total, a.ts, sizeof(T)) && aligned(a.weight, 16) && fits(a.y, a.ys, ysize);
+    const int V = wide ? W : 1;
+    const int runs = (a.K + V - 1) / V;
+    // Few rows: a run a thread, for the shortest wait.  Many: four, so that a row's loads travel together
+    // and few warps wait for its sum.
+    const int sms = sm_count(current_device());
+    const int most = wide ? (a.T <= 2 * sms ? 1 : 4) : 8;
+    int warps = 1;
+    while (warps < 32 && warps * 32 * most < runs) warps *= 2;
+    const int n = (runs + warps * 32 - 1) / (warps * 32);
+    const int threads = warps == 1 ? 128 : warps * 32, rows = warps == 1 ? 4 : 1;
+    const int64_t ctas = (a.T + rows - 1) / rows;
+    const dim3 grid((unsigned)std::min<int64_t>(ctas, (int64_t)sms * std::max(1, 2048 / threads)));
+    void (*k)(NormArgs, int);
+    if (wide)
+        k = n <= 1 ? norm_kernel<T, W, 1> : n <= 2 ? norm_kernel<T, W, 2> : n <= 4 ? norm_kernel<T, W, 4> : norm_kernel<T, W, 8>;
+    else
+        k = n <= 8 ? norm_kernel<T, 1, 8> : norm_kernel<T, 1, 32>;
+    return launch(k, grid, dim3(threads), 0, stream, true, a, warps);
+}
+
+}  // namespace
+}  // namespace rfp2
+
+using namespace rfp2;
+
+extern "C" rfp2_status rfp2_rms_norm(const void *x, int dtype, int64_t T, int64_t K, int64_t x_stride,
+                                     const void *residual, int64_t residual_stride, void *total,
+                                     int64_t total_stride, const void *weight, int weight_dtype, float eps,
+                                     void *y, int y_dtype, int64_t y_stride, int8_t *q, float *d,
+                                     rfp2_stream_t stream) {
+    const int size = dtype_bytes(dtype), wsize = dtype_bytes(weight_dtype), ysize = y ? dtype_bytes(y_dtype) : 1;
+    if (T < 0 || K < 0 || !size || !wsize || !ysize || !(eps > 0.0f && isfinite(eps))) return RFP2_EINVAL;
+    if (K > 32768 || T > (1ll << 31) - 1 || (q && K % 32 != 0)) return RFP2_ESHAPE;
+    if (T == 0 || K == 0) return RFP2_OK;
+    if (!x || !weight || (!y && !q) || !q != !d || (total && !residual)) return RFP2_EINVAL;
+    const auto strided = [&](const void *p, int64_t stride, int64_t least) { return !p || T == 1 || stride >= least; };
+    if (!strided(x, x_stride, 0) || !strided(residual, residual_stride, 0) || !strided(total, total_stride, K) ||
+        !strided(y, y_stride, K))
+        return RFP2_ESHAPE;
+    if (!aligned(x, size) || !aligned(residual, size) || !aligned(total, size) || !aligned(weight, wsize) ||
+        !aligned(y, ysize) || !aligned(q, 16) || !aligned(d, 4))
+        return RFP2_EALIGN;
+    // A value is read before its place in total and y is written, and by the same thread.
+    const Rows in[] = {{x, T, K * size, x_stride * size},
+                       {residual, T, K * size, residual_stride * size},
+                       {weight, 1, K * wsize, 0}};
+    const Rows out[] = {{total, T, K * size, total_stride * size},
+                        {y, T, K * ysize, y_stride * ysize},
+                        {q, 1, T * K, 0},
+                        {d, 1, T * (K / 32) * 4, 0}};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < 3; ++j)
+            if (out[i].meet(in[j]) && !(i < 2 && j < 2 && out[i].same(in[j]))) return RFP2_EINVAL;
+        for (int j = 0; j < i; ++j)
+            if (out[i].meet(out[j])) return RFP2_EINVAL;
+    }
+    NormArgs a;
+    a.x = x;
+    a.residual = residual;
+    a.weight = weight;
+    a.total = total;
+    a.y = y;
+    a.q = q;
+    a.d = d;
+    a.T = T;
+    a.xs = x_stride;
+    a.rs = residual_stride;
+    a.ts = total_stride;
+    a.ys = y_stride;
+    a.K = (int)K;
+    a.weight_type = weight_dtype;
+    a.y_type = y_dtype;
+    a.eps = eps;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return from_cuda(dtype == RFP2_F32    ? launch_norm<float>(a, st)
+                     : dtype == RFP2_BF16 ? launch_norm<__nv_bfloat16>(a, st)
+                                          : launch_norm<__half>(a, st));
+}

@@ -1,0 +1,394 @@
+// The router: the top_k experts of each token and their weights, from its logits.
+//   score = softmax(x) or 1 / (1 + exp(-x));  value = score + bias;  groups of experts by the sum of their
+//   group_top largest values;  the top_k largest values of the kept groups;  weights = scores.
+//
+// A warp has a token, lane l its experts l, l + 32, ...; a pick is the largest value over the warp (one
+// redux of order-preserving integers) and the lowest index that has it (another).
+//
+// What is chosen is what the formula in 64 bits chooses.  Without a bias values are compared by their
+// logits, exactly.  With one, fp32 values are off by `slack` at most (below), so picks further apart than
+// twice that are in their true order; a run of nearer ones is taken to its end, past top_k, and put in
+// order by values in fp64, one of them a lane.  What that cannot settle (a run of more than a warp's
+// lanes; groups too near to tell apart) is done in fp64 from the start.
+#include <algorithm>
+
+#include "activation.cuh"
+
+namespace rfp2 {
+namespace {
+
+constexpr int kWarps = 4;  // tokens of a CTA at a time
+constexpr unsigned kAll = 0xffffffffu;
+
+struct RouteArgs {
+    const void *logits;
+    const float *bias;
+    int32_t *ids;
+    float *weights;
+    int64_t T, stride;
+    int E, top_k, groups, keep, group_top, group_size, renormalise;
+    float scale;
+};
+
+// fp32 as integers in the same order; -infinity is 0x007FFFFF, and 0 is below all of them.
+RFP2_DEV uint32_t ordered(float v) {
+    const uint32_t b = __float_as_uint(v);
+    return b >> 31 ? ~b : b | 0x80000000u;
+}
+RFP2_DEV float unordered(uint32_t k) { return __uint_as_float(k >> 31 ? k & 0x7FFFFFFFu : ~k); }
+
+RFP2_DEV float sigmoid(float x) {
+    const float e = expf(-fabsf(x));
+    return (x >= 0.0f ? 1.0f : e) / (1.0f + e);
+}
+RFP2_DEV double sigmoid(double x) { return 1.0 / (1.0 + exp(-x)); }
+
+RFP2_DEV float warp_sum(float v) {
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
+    return v;
+}
+RFP2_DEV double warp_sum(double v) {
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(kAll, v, off);
+    return v;
+}
+
+// Twice how far a value in fp32 may be off: a score is at most 1 and off by 1e-6 of itself (expf 2 ulp, the
+// difference before it half a one of at most its own size, ten levels of a sum, a quotient), and its sum
+// with the bias is rounded.
+RFP2_DEV float slack(float v) { return 2e-6f + 1.3e-7f * fabsf(v); }
+
+// Does pair (v, i) come before (w, j)?
+template <typename F>
+RFP2_DEV bool before(F v, int i, F w, int j) {
+    return v > w || (v == w && i < j);
+}
+
+// The token's choice in fp64, without any storage: every value is computed anew wherever it is compared.
+// Slow, and reached by rows with near ties that the fast way cannot settle.  Returns lane j's pick j, -1: none.
+template <typename T, bool SOFTMAX>
+__device__ __noinline__ int choose_exactly(const RouteArgs &a, const T *x, int lane) {
+    double top = 0.0, total = 1.0;
+    if (SOFTMAX) {
+        float m = -CUDART_INF_F;
+        for (int e = lane; e < a.E; e += 32) m = fmaxf(m, to_f32(x[e]));
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, off));
+        top = m;
+        total = 0.0;
+        for (int e = lane; e < a.E; e += 32)
+            if (to_f32(x[e]) > -CUDART_INF_F) total += exp((double)to_f32(x[e]) - top);
+        total = warp_sum(total);
+    }
+    // what expert e's score is, and what it is chosen by (-infinity: it is not)
+    const auto score = [&](int e) {
+        return SOFTMAX ? exp((double)to_f32(x[e]) - top) / total : sigmoid((double)to_f32(x[e]));
+    };
+    const auto value = [&](int e) {
+        const float v = to_f32(x[e]);
+        if (!(v > -CUDART_INF_F)) return -CUDART_INF;
+        return a.bias ? score(e) + (double)a.bias[e] : (double)v;
+    };
+    unsigned kept = kAll;
+    if (a.groups > 1) {
+        double mine = -CUDART_INF;  // lane g: what group g counts
+        for (int g = 0; g < a.groups; ++g) {
+            double b1 = -CUDART_INF, b2 = -CUDART_INF;
+            for (int e = g * a.group_size + lane; e < (g + 1) * a.group_size; e += 32) {
+                double v = value(e);
+                if (v > -CUDART_INF && !a.bias && a.group_top > 1) v = score(e);
+                if (v > b1) {
+                    b2 = b1;
+                    b1 = v;
+                } else if (v > b2) {
+                    b2 = v;
+                }
+            }
+#pragma unroll
+            for (int off = 16; off >= 1; off >>= 1) {
+                const double o1 = __shfl_xor_sync(kAll, b1, off), o2 = __shfl_xor_sync(kAll, b2, off);
+                b2 = fmax(fmin(b1, o1), fmax(b2, o2));
+                b1 = fmax(b1, o1);
+            }
+            if (a.group_top > 1 && b2 > -CUDART_INF) b1 += b2;
+            if (lane == g) mine = b1;
+        }
+        int rank = 0;
+        for (int g = 0; g < a.groups; ++g) {
+            const double o = __shfl_sync(kAll, mine, g);
+            rank += before(o, g, mine, lane);
+        }
+        kept = __ballot_sync(kAll, lane < a.groups && rank < a.keep && mine > -CUDART_INF);
+    }
+    double last = CUDART_INF;
+    int last_e = -1, pick = -1;
+    for (int p = 0; p < a.top_k; ++p) {
+        double best = -CUDART_INF;
+        int at = -1;
+        for (int e = lane; e < a.E; e += 32) {
+            if (a.groups > 1 && !(kept >> (e / a.group_size) & 1)) continue;
+            const double v = value(e);
+            if (v > -CUDART_INF && (last_e < 0 || before(last, last_e, v, e)) && (at < 0 || v > best)) {
+                best = v;
+                at = e;
+            }
+        }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) {
+            const double v = __shfl_xor_sync(kAll, best, off);
+            const int e = __shfl_xor_sync(kAll, at, off);
+            if (e >= 0 && (at < 0 || before(v, e, best, at))) {
+                best = v;
+                at = e;
+            }
+        }
+        if (at < 0) break;
+        if (lane == p) pick = at;
+        last = best;
+        last_e = at;
+    }
+    return pick;
+}
+
+// V experts a lane.
+template <typename T, int V, bool SOFTMAX>
+__global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    for (int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); t < a.T; t += (int64_t)gridDim.x * kWarps) {
+        const T *row = static_cast<const T *>(a.logits) + t * a.stride;
+        float x[V];
+        bool bad = false;
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = j * 32 + lane < a.E ? to_f32(row[j * 32 + lane]) : -CUDART_INF_F;
+        float bias[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            bias[j] = a.bias && j * 32 + lane < a.E ? a.bias[j * 32 + lane] : 0.0f;
+            bad |= x[j] != x[j] || bias[j] != bias[j] || (SOFTMAX && x[j] == CUDART_INF_F);
+        }
+        if (__any_sync(kAll, bad)) {
+            if (lane < a.top_k) {
+                a.ids[t * a.top_k + lane] = -1;
+                a.weights[t * a.top_k + lane] = CUDART_NAN_F;
+            }
+            continue;
+        }
+        float top = 0.0f, total = 1.0f;
+        if (SOFTMAX) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int j = 0; j < V; ++j) m = max(m, ordered(x[j]));
+            top = unordered(__reduce_max_sync(kAll, m));
+            if (top == -CUDART_INF_F) top = 0.0f;  // all are masked
+            float e[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) e[j] = expf(x[j] - top);
+#pragma unroll
+            for (int w = V / 2; w >= 1; w /= 2)
+#pragma unroll
+                for (int j = 0; j < w; ++j) e[j] += e[j + w];
+            total = warp_sum(e[0]);
+        }
+        const bool by_sum = a.groups > 1 && a.group_top > 1;
+        // keys: what experts are chosen by; `part`: what groups are
+        uint32_t key[V], part[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            float score = 0.0f;
+            if (a.bias || by_sum) score = SOFTMAX ? expf(x[j] - top) / total : sigmoid(x[j]);
+            const float value = a.bias ? score + bias[j] : x[j];
+            key[j] = x[j] > -CUDART_INF_F && value > -CUDART_INF_F ? ordered(value) : 0u;
+            part[j] = key[j] == 0 ? 0u : by_sum && !a.bias ? ordered(score) : key[j];
+        }
+        bool unsure = false;
+        if (a.groups > 1) {
+            float mine = -CUDART_INF_F;  // lane g: what group g counts
+            float room = 0.0f;           // how far any of them may be off
+            for (int g = 0; g < a.groups; ++g) {
+                const int from = g * a.group_size, to = from + a.group_size;
+                uint32_t b1 = 0, b2 = 0;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const int e = j * 32 + lane;
+                    const uint32_t k = e >= from && e < to ? part[j] : 0u;
+                    b2 = max(b2, min(b1, k));
+                    b1 = max(b1, k);
+                }
+                const uint32_t m1 = __reduce_max_sync(kAll, b1);
+                float v = m1 ? unordered(m1) : -CUDART_INF_F;
+                if (by_sum) {
+                    const int owner = __ffs(__ballot_sync(kAll, b1 == m1)) - 1;
+                    const uint32_t m2 = __reduce_max_sync(kAll, lane == owner ? b2 : b1);
+                    room = fmaxf(room, slack(v) + (m2 ? slack(unordered(m2)) : 0.0f));
+                    if (m2) v += unordered(m2);
+                } else if (m1) {
+                    room = fmaxf(room, slack(v));
+                }
+                if (lane == g) mine = v;
+            }
+            int rank = 0;
+            for (int g = 0; g < a.groups; ++g) {
+                const float o = __shfl_sync(kAll, mine, g);
+                rank += before(o, g, mine, lane);
+            }
+            const unsigned kept = __ballot_sync(kAll, lane < a.groups && rank < a.keep && mine > -CUDART_INF_F);
+            if (a.keep < a.groups && (a.bias || by_sum)) {
+                // Are the last group that is kept and the first that is not far enough apart?
+                const unsigned in = __ballot_sync(kAll, lane < a.groups && rank == a.keep - 1);
+                const unsigned out = __ballot_sync(kAll, lane < a.groups && rank == a.keep);
+                const float u = __shfl_sync(kAll, mine, __ffs(in) - 1), w = __shfl_sync(kAll, mine, __ffs(out) - 1);
+                unsure = w > -CUDART_INF_F && !(u - w > 2.0f * room);
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int e = j * 32 + lane;
+                if (e < a.E && !(kept >> (e / a.group_size) & 1)) key[j] = 0;
+            }
+        }
+        int pick = -1;
+        if (!unsure) {
+            int n = 0;           // picks so far
+            bool near = false;   // are two neighbours too near to tell apart?
+            float last = 0.0f;
+            while (true) {
+                uint32_t best = 0, at = ~0u;
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (key[j] > best) {
+                        best = key[j];
+                        at = j * 32 + lane;
+                    }
+                const uint32_t m = __reduce_max_sync(kAll, best);
+                if (m == 0) break;
+                if (a.bias) {
+                    const float v = unordered(m);
+                    const bool apart = last - v > slack(last);
+                    if (n >= a.top_k && apart) break;
+                    near |= n > 0 && !apart;
+                    last = v;
+                }
+                if (n == 32) {
+                    unsure = true;  // the run goes on past the lanes
+                    break;
+                }
+                const uint32_t e = __reduce_min_sync(kAll, best == m ? at : ~0u);
+                if (lane == n) pick = e;
+                ++n;
+                if (n >= a.top_k && !a.bias) break;
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if ((uint32_t)(j * 32 + lane) == e) key[j] = 0;
+            }
+            if (near && !unsure) {
+                double denominator = 1.0;
+                if (SOFTMAX) {
+                    denominator = 0.0;
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        if (x[j] > -CUDART_INF_F) denominator += exp((double)x[j] - (double)top);
+                    denominator = warp_sum(denominator);
+                }
+                double v = -CUDART_INF;
+                if (lane < n) {
+                    const double l = to_f32(row[pick]);
+                    v = (SOFTMAX ? exp(l - (double)top) / denominator : sigmoid(l)) + (double)a.bias[pick];
+                }
+                int rank = 0;
+                for (int o = 0; o < n; ++o) {
+                    const double w = __shfl_sync(kAll, v, o);
+                    const int e = __shfl_sync(kAll, pick, o);
+                    rank += before(w, e, v, pick);
+                }
+                int mine = -1;
+                for (int o = 0; o < n; ++o) {
+                    const int r = __shfl_sync(kAll, rank, o), e = __shfl_sync(kAll, pick, o);
+                    if (r == lane) mine = e;
+                }
+                pick = mine;
+            }
+        }
+        if (unsure) pick = choose_exactly<T, SOFTMAX>(a, row, lane);
+        if (lane >= a.top_k) pick = -1;
+        // Scores of the picks.  Their shares of one another are formed from the logits, so that they hold
+        // where the scores themselves underflow.
+        const float l = pick >= 0 ? to_f32(row[pick]) : -CUDART_INF_F;
+        float w = 0.0f;
+        if (a.renormalise) {
+            float most = l;
+#pragma unroll
+            for (int off = 16; off >= 1; off >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, off));
+            if (!SOFTMAX) most = fminf(most, 0.0f);
+            if (pick >= 0) w = SOFTMAX ? expf(l - most) : expf(fminf(l, 0.0f) - most) / (1.0f + expf(-fabsf(l)));
+            const float sum = warp_sum(w);
+            w = sum > 0.0f ? w / sum : 0.0f;
+        } else if (pick >= 0) {
+            w = SOFTMAX ? expf(l - top) / total : sigmoid(l);
+        }
+        if (lane < a.top_k) {
+            a.ids[t * a.top_k + lane] = pick;
+            a.weights[t * a.top_k + lane] = w * a.scale;
+        }
+    }
+}
+
+template <typename T, bool SOFTMAX>
+cudaError_t launch_route(const RouteArgs &a, cudaStream_t stream) {
+    void (*const kinds[])(RouteArgs) = {route_kernel<T, 1, SOFTMAX>, route_kernel<T, 2, SOFTMAX>,
+                                        route_kernel<T, 4, SOFTMAX>, route_kernel<T, 8, SOFTMAX>,
+                                        route_kernel<T, 16, SOFTMAX>, route_kernel<T, 32, SOFTMAX>};
+    int k = 0;
+    while (32 << k < a.E) ++k;
+    const int64_t ctas = (a.T + kWarps - 1) / kWarps;
+    return launch(kinds[k], dim3((unsigned)ctas), dim3(kWarps * 32), 0, stream, true, a);
+}
+
+template <typename T>
+cudaError_t launch_scoring(const RouteArgs &a, int scoring, cudaStream_t s) {
+    return scoring == RFP2_SOFTMAX ? launch_route<T, true>(a, s) : launch_route<T, false>(a, s);
+}
+
+}  // namespace
+}  // namespace rfp2
+
+using namespace rfp2;
+
+extern "C" rfp2_status rfp2_moe_route(const void *logits, int dtype, int64_t T, int64_t E, int64_t logits_stride,
+                                      int scoring, const float *bias, int64_t groups, int64_t keep,
+                                      int64_t group_top, int64_t top_k, int renormalise, float scale,
+                                      int32_t *ids, float *weights, rfp2_stream_t stream) {
+    const int size = dtype_bytes(dtype);
+    if (T < 0 || !size || (scoring != RFP2_SOFTMAX && scoring != RFP2_SIGMOID) || !isfinite(scale))
+        return RFP2_EINVAL;
+    if (E < 1 || E > 1024 || top_k < 1 || top_k > 32 || top_k > E || groups < 1 || groups > 32 || E % groups != 0 ||
+        keep < 1 || keep > groups || group_top < 1 || group_top > 2 || T > (1ll << 31) - 1)
+        return RFP2_ESHAPE;
+    if (T == 0) return RFP2_OK;
+    if (!logits || !ids || !weights) return RFP2_EINVAL;
+    if (T > 1 && logits_stride < 0) return RFP2_ESHAPE;
+    if (!aligned(logits, size) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4)) return RFP2_EALIGN;
+    const Rows in[] = {{logits, T, E * size, logits_stride * size}, {bias, 1, E * 4, E * 4}};
+    const Rows to(ids, 1, T * top_k * 4, 0), other(weights, 1, T * top_k * 4, 0);
+    if (to.meet(other) || to.meet(in[0]) || to.meet(in[1]) || other.meet(in[0]) || other.meet(in[1])) return RFP2_EINVAL;
+    RouteArgs a;
+    a.logits = logits;
+    a.bias = bias;
+    a.ids = ids;
+    a.weights = weights;
+    a.T = T;
+    a.stride = logits_stride;
+    a.E = (int)E;
+    a.top_k = (int)top_k;
+    a.groups = (int)groups;
+    a.keep = (int)keep;
+    a.group_top = (int)group_top;
+    a.group_size = (int)(E / groups);
+    a.renormalise = renormalise;
+    a.scale = scale;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return from_cuda(dtype == RFP2_F32    ? launch_scoring<float>(a, scoring, s)
+                     : dtype == RFP2_BF16 ? launch_scoring<__nv_bfloat16>(a, scoring, s)
+                                          : launch_scoring<__half>(a, scoring, s));
+}

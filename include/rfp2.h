@@ -502,6 +502,123 @@ rfp2_status rfp2_attn_decode(const void *q, int dtype, int64_t B, int64_t nq, in
                              void *workspace, size_t workspace_bytes, int32_t *dev_status,
                              rfp2_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The feed-forward half of a decoder layer, around the products of its
+ * (routed) experts: the norm before them, the router that chooses the experts,
+ * their products for any number of tokens, and the sum of a token's experts.
+ * Values of activations are fp32, bf16 or f16 (rfp2_dtype); sums and softmax
+ * states are fp32, and results are rounded once at the end.
+ */
+
+/* Root-mean-square norm, after the residual's addition if there is one:
+ *   s = x + residual, rounded to `dtype` (the sum that is kept is the one that
+ *   is normalised);  r = 1 / sqrt(mean(s^2) + eps);  y = s * r * weight.
+ *   x, residual, total  `dtype` [T, K] device, rows *_stride elements apart;
+ *        residual may be NULL, and total (the sums, output) is NULL without it
+ *        or where they are not wanted.
+ *   weight  `weight_dtype` [K] device, contiguous.
+ *   y    `y_dtype` [T, K] device (output) or NULL.
+ *   q, d (output, both or neither): y in Q8_1-style blocks as
+ *        rfp2_quantize_act's, int8 [T, K] and fp32 [T, K/32] contiguous, of y
+ *        before any rounding: with U the largest |s * weight| of a block, code
+ *        = round-half-away(127 s weight / U), exactly, and d = r U / 127.  A
+ *        block that is not finite has codes 0 and a scale that is not finite.
+ *        K % 32 == 0.
+ *   total and y may each be x or residual, with the same type and stride; any
+ *   other overlap is not allowed.
+ * Squares that leave fp32's range are taken of values scaled by a power of two,
+ * so rows of any finite size have their norm.
+ * Errors: EINVAL (null, negative size, bad dtype, no output, q without d, eps
+ * not positive and finite, such an overlap), ESHAPE (K > 32768, K % 32 with q, T > 2^31 - 1, an
+ * output's row stride below K, an input's below 0), EALIGN (a pointer not aligned to its type, q not to 16
+ * bytes), ECUDA.
+ */
+rfp2_status rfp2_rms_norm(const void *x, int dtype, int64_t T, int64_t K, int64_t x_stride,
+                          const void *residual, int64_t residual_stride, void *total,
+                          int64_t total_stride, const void *weight, int weight_dtype, float eps,
+                          void *y, int y_dtype, int64_t y_stride, int8_t *q, float *d,
+                          rfp2_stream_t stream);
+
+typedef enum { RFP2_SOFTMAX = 0, RFP2_SIGMOID = 1 } rfp2_scoring;
+
+/* The experts of each token, from the router's logits: what rfp2_moe_gemv and
+ * rfp2_moe_gemm take as ids, and rfp2_moe_combine as weights.
+ *   score = softmax(logits) over the E experts, or sigmoid(logit);
+ *   value = score + bias[e] (bias fp32 [E] device, or NULL): what is chosen by;
+ *   with groups > 1 the experts are `groups` runs of E / groups; a group counts
+ *   the sum of its group_top (1 or 2) largest values, and only experts of the
+ *   `keep` groups that count most are chosen from;
+ *   ids int32 [T, top_k] (output): the top_k largest values, largest first;
+ *   weights fp32 [T, top_k] (output): their scores (without the bias), divided
+ *   by their sum if `renormalise` is not 0, times `scale`.
+ * Ties go to the lowest index.  The choice is that of the formula in 64 bits,
+ * whatever the fp32 scores round to; without a bias scores are compared by
+ * their logits.
+ * A logit of -infinity masks its expert: it is never chosen (nor is one whose
+ * value is -infinity), and a group of none is never kept.  Where fewer than
+ * top_k experts are left, the last ids are -1 and their weights 0.  A row with a
+ * NaN (one in the bias is in every row), or with +infinity under softmax, has
+ * ids -1 and weights NaN.
+ *   logits  `dtype` [T, E] device, rows logits_stride elements apart.
+ * Errors: EINVAL (null, negative size, bad dtype or scoring, scale not
+ * finite, an output over another array), ESHAPE (E < 1 or > 1024, top_k < 1, > 32 or > E, groups < 1 or > 32
+ * or not a divisor of E, keep < 1 or > groups, group_top not 1 or 2, T > 2^31 -
+ * 1, logits_stride < 0), EALIGN, ECUDA.
+ */
+rfp2_status rfp2_moe_route(const void *logits, int dtype, int64_t T, int64_t E,
+                           int64_t logits_stride, int scoring, const float *bias, int64_t groups,
+                           int64_t keep, int64_t group_top, int64_t top_k, int renormalise,
+                           float scale, int32_t *ids, float *weights, rfp2_stream_t stream);
+
+/* The sum of a token's experts:
+ *   out[t] = sum_j weights[t, j] * y[t, j] + residual[t].
+ *   y    `dtype` [T, top_k, M] device, M contiguous, tokens y_token_stride and
+ *        slots y_slot_stride elements apart.
+ *   weights fp32 [T, top_k] device; ids int32 [T, top_k] device or NULL: the
+ *        row of a slot with a negative id is not read (its weight times 0 is
+ *        added).
+ *   residual  `out_dtype` [T, M] device or NULL; out the same type (output),
+ *        rows *_stride elements apart; out may be residual with the same stride.
+ * Errors: EINVAL (null, negative size, bad dtype, out over another
+ * array), ESHAPE (top_k < 1 or > 1024,
+ * T or M > 2^31 - 1, out's row stride below M, another below 0), EALIGN, ECUDA.
+ */
+rfp2_status rfp2_moe_combine(const void *y, int dtype, int64_t T, int64_t top_k, int64_t M,
+                             int64_t y_token_stride, int64_t y_slot_stride, const float *weights,
+                             const int32_t *ids, const void *residual, int64_t residual_stride,
+                             void *out, int out_dtype, int64_t out_stride, rfp2_stream_t stream);
+
+typedef enum { RFP2_ACT_NONE = 0, RFP2_ACT_SILU = 1, RFP2_ACT_GELU = 2 } rfp2_activation;
+
+/* The routed experts' products for any number of tokens, on the tensor cores
+ * (rfp2_moe_gemv is for a few):  z = W[ids[t, j]] x + bias[ids[t, j]], and
+ *   y[t, j] = z                                     (RFP2_ACT_NONE), or
+ *   y[t, j] = act(z[0 .. M/2)) * z[M/2 .. M)        (gate rows, then up rows)
+ * with act(a) = a / (1 + exp(-a)) (SILU) or a (1 + tanh(sqrt(2/pi) (a + 0.044715
+ * a^3))) / 2 (GELU).  Weights are decoded exactly to bf16, sums and activations
+ * are fp32, and y is rounded once.
+ *   W    uint8 [E, M, K/32, 10] device, 16-byte aligned.
+ *   ids  int32 [T, top_k] device.  -1 is no expert: its row becomes zeros.  Any
+ *        other id outside [0, E) gives a row of NaN and RFP2_EBADID.
+ *   X    bf16 bit patterns device, 16-byte aligned: [T, K], or with each != 0
+ *        [T, top_k, K], a row for every slot (the second product of an expert).
+ *   bias fp32 [E, M] device or NULL.
+ *   Y    bf16 bit patterns [T, top_k, M] (or M/2 when gated) device (output).
+ *   workspace  device, 256-byte aligned, rfp2_moe_gemm_workspace_bytes(T, top_k,
+ *        E) bytes; it needs no clearing.  Calls that overlap on the GPU must not
+ *        share it.
+ * T = 0 is nothing to do.
+ * Errors: EINVAL (also Y or the workspace over another array), ESHAPE (E < 1 or > 1024, M, K or top_k < 1, T * top_k > 2^24,
+ * E * M > 2^30), EUNSUPPORTED (K % 256, M % 16, or M % 32 when gated), EALIGN,
+ * EWORKSPACE, ECUDA; a bounded device wait that ran out stores ETIMEOUT in
+ * dev_status.
+ */
+size_t rfp2_moe_gemm_workspace_bytes(int64_t T, int64_t top_k, int64_t E);
+rfp2_status rfp2_moe_gemm(const uint8_t *W, int64_t E, int64_t M, int64_t K, const int32_t *ids,
+                          int64_t T, int64_t top_k, const uint16_t *X, int each, const float *bias,
+                          int activation, uint16_t *Y, void *workspace, size_t workspace_bytes,
+                          int32_t *dev_status, rfp2_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
