@@ -2,14 +2,17 @@
 //   z = W[e] x + bias[e];  y = z, or act(z[gate rows]) * z[up rows];  a row of y for each (token, slot) pair.
 //
 // Two launches:
-//  1. plan (one CTA): the pairs sorted by expert, and each expert's run cut into tiles of tokens.
-//  2. the product: units of (tile, block of weight rows).
+//  1. plan (one CTA): the pairs sorted by expert, and each expert's run cut into tiles of at most 256 tokens.
+//  2. the product on the tensor cores: units of a tile and 256 weight rows (128 gate rows and the 128 up rows
+//     that go with them).
 #include <algorithm>
 #include <mutex>
 
 #include "activation.cuh"
 #include "expand.cuh"
 #include "rfp2_decode.cuh"
+#include "tcgen05.cuh"
+#include "tma.cuh"
 
 namespace rfp2 {
 namespace {
@@ -160,66 +163,343 @@ RFP2_DEV void fill_rest(const GemmArgs &a, int64_t thread, int64_t threads) {
     }
 }
 
-// The plain form on CUDA cores: 32 output columns x 32 tokens of a tile at a time, 64 of K per step.
-constexpr int kRows = 32, kCols = 32, kStep = 64, kThreads = 256;
+// ---- the product --------------------------------------------------------------
+constexpr int kRows = 128;   // weight rows of a CTA (TMEM lanes), 256 of a pair (UMMA M)
+constexpr int kStep = 64;    // K of a stage: one 128-byte swizzle row
+constexpr int kUmmaK = 16;   // K of an instruction
+constexpr int kABytes = kRows * kStep * 2;
+constexpr int kBBytes = kTileTokens / 2 * kStep * 2;
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kStages = 5;
+constexpr int kBoxRowBytes = 80;  // eight 10-byte blocks: four steps of K
+constexpr int kBoxBytes = kRows * kBoxRowBytes;
+constexpr int kBoxes = 4;
+constexpr int kGroups = 4;      // decoders: group i takes steps i, i + 4, ...
+constexpr int kGroupWarps = 4;  // a weight row a thread
+constexpr int kDecodeWarps = kGroups * kGroupWarps;
+constexpr int kThreads = (7 + kDecodeWarps) * 32;
+constexpr uint32_t kTmemCols = 512;  // two accumulators of 256 columns
+constexpr size_t kRingOff = (size_t)kStages * kStageBytes;
+constexpr size_t kBarOff = kRingOff + (size_t)kBoxes * kBoxBytes;
+constexpr size_t kSmemBytes = 1024 + kBarOff + 256;
 
-__global__ void __launch_bounds__(kThreads) product_kernel(const GemmArgs a) {
-    __shared__ float w[2][kRows][kStep + 1], x[kCols][kStep + 1];
-    pdl_wait();
-    pdl_launch_dependents();
-    fill_rest(a, (int64_t)blockIdx.x * kThreads + threadIdx.x, (int64_t)gridDim.x * kThreads);
-    const int ntiles = a.plan.header[0], blocks = (a.out + kRows - 1) / kRows;
-    const int parts = a.activation == RFP2_ACT_NONE ? 1 : 2;
-    const int row = threadIdx.x >> 3, col0 = (threadIdx.x & 7) * 4;
-    for (int64_t u = blockIdx.x; u < (int64_t)ntiles * blocks; u += gridDim.x) {
-        const int4 tile = a.plan.tiles[u / blocks];
-        const int row0 = (int)(u % blocks) * kRows;
-        for (int c0 = 0; c0 < tile.z; c0 += kCols) {
-            float sum[2][4] = {};
-            for (int k0 = 0; k0 < a.K; k0 += kStep) {
-                for (int i = threadIdx.x; i < kCols * kStep; i += kThreads) {
-                    const int c = i / kStep, k = i % kStep;
-                    float v = 0.0f;
-                    if (c0 + c < tile.z) {
-                        const int p = a.plan.pairs[tile.y + c0 + c];
-                        v = __bfloat162float(a.X[(int64_t)(a.each ? p : p / a.top_k) * a.K + k0 + k]);
-                    }
-                    x[c][k] = v;
-                }
-                for (int i = threadIdx.x; i < parts * kRows * (kStep / 16); i += kThreads) {
-                    const int h = i % (kStep / 16), r = i / (kStep / 16) % kRows, part = i / (kStep / 16) / kRows;
-                    const int m = row0 + r;
-                    const int half = k0 / 16 + h;
-                    const uint8_t *b = a.W + ((int64_t)tile.x * a.M + part * a.out + m) * (a.K / 32 * 10) + half / 2 * 10;
-                    for (int j = 0; j < 16; ++j) {
-                        float v = 0.0f;
-                        if (m < a.out) {
-                            float s0, s1;
-                            decode_scale_pair(b[8] | b[9] << 8, s0, s1);
-                            const int c = b[(half & 1) * 4 + j / 4] >> (2 * (j % 4)) & 3;
-                            v = (half & 1 ? s1 : s0) * (c == 0 ? -4.0f : c == 1 ? -1.0f : c == 2 ? 1.0f : 4.0f);
-                        }
-                        w[part][r][h * 16 + j] = v;
-                    }
-                }
-                __syncthreads();
-                for (int k = 0; k < kStep; ++k)
-                    for (int part = 0; part < parts; ++part)
+// A unit of work of a CTA pair: a tile of tokens and a block of 256 weight rows.
+struct Unit {
+    int4 tile;
+    int block, width;  // columns of the MMA: the tile's tokens, rounded up to 32
+};
+RFP2_DEV Unit unit_at(const GemmArgs &a, int u, int blocks) {
+    Unit r;
+    const int t = u / blocks;
+    r.tile = a.plan.tiles[t];
+    r.block = u - t * blocks;
+    r.width = (r.tile.z + 31) & ~31;
+    return r;
+}
+
+// Four rows of a K step (x = its first column) into four rows of shared memory, signalled on a barrier of
+// either CTA of the pair.
+RFP2_DEV void tma_gather4_pair(void *smem_dst, const CUtensorMap *map, int x, const int (&row)[4], uint32_t bar_cluster) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_addr(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]),
+        "r"(bar_cluster)
+        : "memory");
+}
+
+// Persistent over CTA pairs (clusters of two): pair p takes units p, p + pairs, ...  The weights are the MMAs'
+// A operand, so that a tile has as many columns as it has tokens.  In each CTA
+//   warp 0        gathers its half of the tile's tokens, four rows to a TMA copy, a copy a lane, into the
+//                 B half of a ring of stages;
+//   warp 6        streams the packed rows of its 128 weight rows, 256 of K to a box, into a ring of boxes;
+//   warps 7-22    decode them exactly to bf16 into the A half of the stages, a row a thread;
+//   warp 1        (even CTA) issues M = 256 pair MMAs over both CTAs' stages;
+//   warps 2-5     read one of two accumulators back while the MMAs fill the other: a lane has a weight row, a
+//                 register a token.
+// Gated: lanes 0-15 of a warp have gate rows, lanes 16-31 the up rows that go with them, and a shuffle brings
+// the two together.  Every wait is bounded; tensor memory is always freed.
+template <int ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap, const GemmArgs a,
+                   int32_t *status) {
+    constexpr bool kGated = ACT != RFP2_ACT_NONE;
+    constexpr int kOut = kGated ? kRows / 2 : kRows;  // outputs of a CTA's rows
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *ring = smem + kRingOff;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kBarOff);  // (even CTA) a stage of both CTAs is there
+    uint64_t *empty = full + kStages;       // its MMAs are done
+    uint64_t *accf = empty + kStages;       // [2] an accumulator is complete
+    uint64_t *acce = accf + 2;              // [2] (even CTA) it has been read back
+    uint64_t *pfull = acce + 2;             // a box is there
+    uint64_t *pempty = pfull + kBoxes;      // it has been decoded
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(pempty + kBoxes);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const int nk = a.K / kStep;
+
+    if (threadIdx.x == 0) {
+        prefetch_tensor_map(&xmap);
+        prefetch_tensor_map(&wmap);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1 + 2 * kGroupWarps);  // the gathers, and the decoders of both CTAs
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&accf[b], 1);
+            mbar_init(&acce[b], 8);
+        }
+        for (int s = 0; s < kBoxes; ++s) {
+            mbar_init(&pfull[s], 1);
+            mbar_init(&pempty[s], kDecodeWarps);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, kTmemCols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    pdl_wait();  // the plan comes from the launch before, X and W perhaps from earlier ones
+    const int blocks = (a.out + 2 * kOut - 1) / (2 * kOut);
+    const int units = a.plan.header[0] * blocks;
+
+    int g = 0;  // stages filled by this CTA
+    if (warp == 0) {
+        // ---- gathers
+        const uint32_t full0 = cluster_map(&full[0], 0);
+        bool ok = true;
+        for (int u = pair; u < units && ok; u += npairs) {
+            const Unit un = unit_at(a, u, blocks);
+            const int half = un.width / 2;
+            int row[4];
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) sum[part][c] = fmaf(w[part][row][k], x[col0 + c][k], sum[part][c]);
-                __syncthreads();
+            for (int i = 0; i < 4; ++i) {
+                // columns past the tile's tokens repeat its last
+                const int c = min((int)rank * half + 4 * lane + i, un.tile.z - 1);
+                const int p = a.plan.pairs[un.tile.y + c];
+                row[i] = a.each ? p : p / a.top_k;
             }
-            const int m = row0 + row;
+            for (int kb = 0; kb < nk; ++kb, ++g) {
+                const int s = g % kStages;
+                const bool free = !*abort_flag && (g < kStages || mbar_wait(&empty[s], ((g / kStages) - 1) & 1));
+                if (!__all_sync(0xffffffffu, free)) {
+                    if (lane == 0) record_status(status, RFP2_ETIMEOUT);
+                    *abort_flag = 1;
+                    ok = false;
+                    break;
+                }
+                if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(un.width * kStep * 2));
+                if (4 * lane < half)
+                    tma_gather4_pair(smem + (size_t)s * kStageBytes + kABytes + lane * 512, &xmap, kb * kStep, row, full0 + 8u * s);
+            }
+        }
+    } else if (warp == 1 && rank == 0 && lane == 0) {
+        // ---- MMAs
+        int gm = 0, it = 0;
+        bool ok = true;
+        for (int u = pair; u < units && ok; u += npairs, ++it) {
+            const int b = it & 1;
+            if (*abort_flag || (it >= 2 && !mbar_wait(&acce[b], ((it >> 1) - 1) & 1))) {
+                record_status(status, RFP2_ETIMEOUT);
+                *abort_flag = 1;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t idesc = idesc_bf16_f32(2 * kRows, unit_at(a, u, blocks).width);
+            const uint32_t d = tmem + (uint32_t)(b * kTileTokens);
+            for (int kb = 0; kb < nk; ++kb, ++gm) {
+                const int s = gm % kStages;
+                if (*abort_flag || !mbar_wait(&full[s], (gm / kStages) & 1)) {
+                    record_status(status, RFP2_ETIMEOUT);
+                    *abort_flag = 1;
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t at = smem_addr(smem + (size_t)s * kStageBytes);
+                const uint64_t adesc = smem_desc_sw128(at), bdesc = smem_desc_sw128(at + kABytes);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (c0 + col0 + c >= tile.z || m >= a.out) continue;
-                const float *bias = a.bias ? a.bias + (int64_t)tile.x * a.M + m : nullptr;
-                float z = sum[0][c] + (bias ? bias[0] : 0.0f);
-                if (parts == 2) z = activated(a.activation, z, sum[1][c] + (bias ? bias[a.out] : 0.0f));
-                a.Y[(int64_t)a.plan.pairs[tile.y + c0 + col0 + c] * a.out + m] = __float2bfloat16(z);
+                for (int k = 0; k < kStep / kUmmaK; ++k)
+                    umma_bf16_pair(d, adesc + 2 * k, bdesc + 2 * k, idesc, (kb > 0 || k > 0) ? 1u : 0u);
+                umma_commit_pair_both(&empty[s]);
+            }
+            umma_commit_pair_both(&accf[b]);  // complete, or idle after an abort
+        }
+    } else if (warp >= 2 && warp < 6) {
+        // ---- epilogue
+        fill_rest(a, (int64_t)blockIdx.x * 128 + threadIdx.x - 64, (int64_t)gridDim.x * 128);
+        const int q = warp & 3;  // lanes 32 q ... of the accumulators
+        const uint32_t acce0 = cluster_map(&acce[0], 0);
+        int it = 0;
+        for (int u = pair; u < units; u += npairs, ++it) {
+            const int b = it & 1;
+            const Unit un = unit_at(a, u, blocks);
+            const int m = (2 * un.block + (int)rank) * kOut + (kGated ? q * 16 + (lane & 15) : q * 32 + lane);
+            float bias = 0.0f;
+            if (a.bias && m < a.out) bias = a.bias[(int64_t)un.tile.x * a.M + m + (kGated && lane >= 16 ? a.out : 0)];
+            if (*abort_flag || !mbar_wait(&accf[b], (it >> 1) & 1)) {
+                record_status(status, RFP2_ETIMEOUT);
+                *abort_flag = 1;
+                break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < un.width; c0 += 32) {
+                uint32_t r[32];
+                tmem_ld_32cols(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kTileTokens + c0), r);
+                const int mine = a.plan.pairs[un.tile.y + min(c0 + lane, un.tile.z - 1)];
+                tmem_ld_wait();
+                const int n = un.tile.z - c0;
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                    if constexpr (kGated) {
+                        // lanes 0-15 finish column c, lanes 16-31 column c + 1
+                        const bool low = lane < 16;
+                        const float own = __uint_as_float(low ? r[c] : r[c + 1]) + bias;
+                        const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float(low ? r[c + 1] : r[c]) + bias, 16);
+                        const int p = __shfl_sync(0xffffffffu, mine, c + (lane >> 4));
+                        const float y = activated(ACT, low ? own : other, low ? other : own);
+                        if (c + (lane >> 4) < n && m < a.out) a.Y[(int64_t)p * a.out + m] = __float2bfloat16(y);
+                    } else {
+                        // even lanes take two rows of column c, odd lanes of column c + 1
+                        const bool odd = lane & 1;
+                        const float own = __uint_as_float(odd ? r[c + 1] : r[c]) + bias;
+                        const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float(odd ? r[c] : r[c + 1]) + bias, 1);
+                        const int p = __shfl_sync(0xffffffffu, mine, c + odd);
+                        const __nv_bfloat162 y = __floats2bfloat162_rn(odd ? other : own, odd ? own : other);
+                        if (c + odd < n && m < a.out)  // out is even, so both rows are there or neither
+                            *reinterpret_cast<__nv_bfloat162 *>(a.Y + (int64_t)p * a.out + (m & ~1)) = y;
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(acce0 + 8u * b);
+        }
+    } else if (warp == 6 && lane == 0) {
+        // ---- packed boxes, in the decoders' order; gated: 64 gate rows, then 64 up rows
+        int n = 0;
+        bool ok = true;
+        for (int u = pair; u < units && ok; u += npairs) {
+            const Unit un = unit_at(a, u, blocks);
+            const int row = un.tile.x * a.M + (2 * un.block + (int)rank) * kOut;
+            for (int kq = 0; kq < nk / 4; ++kq, ++n) {
+                const int s = n % kBoxes;
+                if (*abort_flag || (n >= kBoxes && !mbar_wait(&pempty[s], ((n / kBoxes) - 1) & 1))) {
+                    record_status(status, RFP2_ETIMEOUT);
+                    *abort_flag = 1;
+                    ok = false;
+                    break;
+                }
+                mbar_arrive_expect_tx(&pfull[s], kBoxBytes);
+                uint8_t *to = ring + (size_t)s * kBoxBytes;
+                tma_load_2d(to, &wmap, kq * kBoxRowBytes, row, &pfull[s]);
+                tma_load_2d(to + kBoxBytes / 2, &wmap, kq * kBoxRowBytes, row + (kGated ? a.out : kRows / 2), &pfull[s]);
+            }
+        }
+        for (int i = max(0, n - kBoxes); i < n; ++i)  // none in flight when the CTA retires
+            if (!mbar_wait(&pfull[i % kBoxes], (i / kBoxes) & 1)) record_status(status, RFP2_ETIMEOUT);
+    } else if (warp >= 7) {
+        // ---- decoders: two blocks of a row at byte 20 gi of its 80-byte box row, in a window of 32 bytes
+        const int gi = (warp - 7) / kGroupWarps;
+        const int quarter = (warp - 7) % kGroupWarps;
+        const int row = quarter * 32 + lane;  // of the A operand
+        const int from = kGated ? (lane < 16 ? quarter * 16 + lane : 64 + quarter * 16 + lane - 16) : row;  // of the box
+        const int wq = (20 * gi & 15) >> 2;
+        const uint32_t full0 = cluster_map(&full[0], 0);
+        int gbase = 0, nd = 0;
+        bool ok = true;
+        for (int u = pair; u < units && ok; u += npairs, gbase += nk) {
+            for (int kb = gi; kb < nk; kb += kGroups, ++nd) {
+                const int gd = gbase + kb, s = gd % kStages, ps = nd % kBoxes;
+                bool there = !*abort_flag && mbar_wait(&pfull[ps], (nd / kBoxes) & 1);
+                if (gd >= kStages) there = there && mbar_wait(&empty[s], ((gd / kStages) - 1) & 1);
+                if (!__all_sync(0xffffffffu, there)) {
+                    if (lane == 0) record_status(status, RFP2_ETIMEOUT);
+                    *abort_flag = 1;
+                    ok = false;
+                    break;
+                }
+                const uint4 *win = reinterpret_cast<const uint4 *>(ring + (size_t)ps * kBoxBytes + from * kBoxRowBytes + ((20 * gi) & ~15));
+                const uint4 q0 = win[0], q1 = win[1];
+                const uint32_t wv[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+                uint32_t w[5];
+#pragma unroll
+                for (int i = 0; i < 5; ++i)
+                    w[i] = wq == 0 ? wv[i] : wq == 1 ? wv[i + 1] : wq == 2 ? wv[i + 2] : wv[i + 3];
+                // block 0: codes w0, w1, scales in the low half of w2; block 1: from byte 10
+                const uint32_t code[4] = {w[0], w[1], __funnelshift_r(w[2], w[3], 16), __funnelshift_r(w[3], w[4], 16)};
+                float sc[4];
+                decode_scale_pair(w[2] & 0xFFFFu, sc[0], sc[1]);
+                decode_scale_pair(w[4] >> 16, sc[2], sc[3]);
+                uint8_t *to = smem + (size_t)s * kStageBytes + row * 128;
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t o[8];
+                    decode_half_bf16(code[h], sc[h], o);
+                    *reinterpret_cast<uint4 *>(to + (((2 * h) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4 *>(to + (((2 * h + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive_remote(full0 + 8u * s);
+                    mbar_arrive(&pempty[ps]);
+                }
             }
         }
     }
+    if (warp == 0 && lane == 0) {
+        // Neither CTA leaves before the commits of the last stages have arrived here (after an abort, before its
+        // copies have, where it can see them).
+        for (int i = max(0, g - kStages); i < g; ++i) {
+            const bool done = *abort_flag && rank == 0 ? mbar_wait(&full[i % kStages], (i / kStages) & 1)
+                                                       : mbar_wait(&empty[i % kStages], (i / kStages) & 1);
+            if (!done) record_status(status, RFP2_ETIMEOUT);
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, kTmemCols);
+    }
+}
+
+using ProductFn = void (*)(CUtensorMap, CUtensorMap, GemmArgs, int32_t *);
+
+// Sets the kernels up on a device; returns how many pairs it holds at a time (0: an error).
+int pairs_of(int dev) {
+    static std::mutex mu;
+    static int held[64] = {};
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 64 && held[dev]) return held[dev];
+    int pairs = 0;
+    const ProductFn kinds[] = {product_kernel<RFP2_ACT_NONE>, product_kernel<RFP2_ACT_SILU>, product_kernel<RFP2_ACT_GELU>};
+    if (set_smem_limit(plan_kernel, 32 * (kMaxExperts + 1) * 4) != cudaSuccess) return 0;
+    for (const ProductFn k : kinds) {
+        if (set_smem_limit(k, (int)kSmemBytes) != cudaSuccess) return 0;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmemBytes;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void *>(k), &cfg) != cudaSuccess || n <= 0) return 0;
+        pairs = pairs ? std::min(pairs, n) : n;
+    }
+    if (dev < 64) held[dev] = pairs;
+    return pairs;
 }
 
 }  // namespace
@@ -237,8 +517,8 @@ extern "C" rfp2_status rfp2_moe_gemm(const uint8_t *W, int64_t E, int64_t M, int
                                      uint16_t *Y, void *workspace, size_t workspace_bytes, int32_t *dev_status,
                                      rfp2_stream_t stream) {
     if (T < 0 || activation < RFP2_ACT_NONE || activation > RFP2_ACT_GELU) return RFP2_EINVAL;
-    if (E < 1 || E > kMaxExperts || M < 1 || K < 1 || top_k < 1 || T > kMaxPairs / top_k || E * M > (1 << 30) ||
-        M > (1 << 30) || K > (1 << 20))
+    if (E < 1 || E > kMaxExperts || M < 1 || K < 1 || top_k < 1 || T > kMaxPairs / top_k || M > (1 << 30) || E * M > (1 << 30) ||
+        K > (1 << 20) || T * top_k > (1ll << 40) / M)
         return RFP2_ESHAPE;
     const bool gated = activation != RFP2_ACT_NONE;
     if (K % 256 != 0 || M % (gated ? 32 : 16) != 0) return RFP2_EUNSUPPORTED;
@@ -255,16 +535,15 @@ extern "C" rfp2_status rfp2_moe_gemm(const uint8_t *W, int64_t E, int64_t M, int
     bool meet = y.meet(ws);
     for (const Rows &r : in) meet |= r.meet(y) || r.meet(ws);
     if (meet) return RFP2_EINVAL;
-    static std::mutex mu;
-    static bool configured[64] = {};
-    const int dev = current_device();
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        if (dev >= 64 || !configured[dev]) {
-            if (set_smem_limit(plan_kernel, 32 * (kMaxExperts + 1) * 4) != cudaSuccess) return RFP2_ECUDA;
-            if (dev < 64) configured[dev] = true;
-        }
-    }
+    const int pairs = pairs_of(current_device());
+    CUtensorMap xmap, wmap;
+    const uint64_t row_bytes = (uint64_t)(K / 32) * 10;
+    if (pairs <= 0 ||
+        !encode_tensor_map_2d(&xmap, X, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (uint64_t)K, (uint64_t)(each ? P : T), (uint64_t)K * 2,
+                              kStep, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tensor_map_2d(&wmap, W, CU_TENSOR_MAP_DATA_TYPE_UINT8, row_bytes, (uint64_t)(E * M), row_bytes, kBoxRowBytes,
+                              kRows / 2, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return RFP2_ECUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     GemmArgs a;
     a.W = W;
@@ -284,5 +563,11 @@ extern "C" rfp2_status rfp2_moe_gemm(const uint8_t *W, int64_t E, int64_t M, int
     cudaError_t e = launch(plan_kernel, dim3(1), dim3(kPlanThreads), (size_t)warps * (E + 1) * 4, s, true, ids, (int)P,
                            (int)E, warps, a.plan, dev_status);
     if (e != cudaSuccess) return RFP2_ECUDA;
-    return from_cuda(launch(product_kernel, dim3(4 * sm_count(dev)), dim3(kThreads), 0, s, true, a));
+    // at most a pair for every unit there can be
+    const int64_t blocks = (out + (gated ? kRows : 2 * kRows) - 1) / (gated ? kRows : 2 * kRows);
+    const dim3 grid((unsigned)(2 * std::min<int64_t>(pairs, most_tiles(P, E) * blocks)));
+    const ProductFn k = activation == RFP2_ACT_NONE   ? product_kernel<RFP2_ACT_NONE>
+                        : activation == RFP2_ACT_SILU ? product_kernel<RFP2_ACT_SILU>
+                                                      : product_kernel<RFP2_ACT_GELU>;
+    return from_cuda(launch(k, grid, dim3(kThreads), kSmemBytes, s, true, xmap, wmap, a, dev_status));
 }

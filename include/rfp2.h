@@ -609,7 +609,7 @@ typedef enum { RFP2_ACT_NONE = 0, RFP2_ACT_SILU = 1, RFP2_ACT_GELU = 2 } rfp2_ac
  *        share it.
  * T = 0 is nothing to do.
  * Errors: EINVAL (also Y or the workspace over another array), ESHAPE (E < 1 or > 1024, M, K or top_k < 1, T * top_k > 2^24,
- * E * M > 2^30), EUNSUPPORTED (K % 256, M % 16, or M % 32 when gated), EALIGN,
+ * E * M > 2^30, K > 2^20, T * top_k * M > 2^40), EUNSUPPORTED (K % 256, M % 16, or M % 32 when gated), EALIGN,
  * EWORKSPACE, ECUDA; a bounded device wait that ran out stores ETIMEOUT in
  * dev_status.
  */
