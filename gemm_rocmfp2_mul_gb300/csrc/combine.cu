@@ -1,6 +1,9 @@
 // The sum of a token's experts: out[t] = sum_j weights[t, j] y[t, j] + residual[t], summed in fp32 in the
-// order of the slots.  Bound by memory: each of a token's top_k rows is read once.  A thread takes a run of
-// 16 bytes of the output's row and sends off the loads of up to eight slots before it adds.
+// order of the slots.  Bound by memory: each of a token's top_k rows is read once.
+//
+// A thread has a run of 16 bytes or more of a token's row (or four single values, a CTA's width apart, where
+// rows have no such alignment) and sends off the loads of up to eight slots before it adds any; they
+// stay as they were loaded until then, which is half the registers of fp32 values.
 #include <algorithm>
 
 #include "activation.cuh"
@@ -9,7 +12,6 @@ namespace rfp2 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 8;  // slots whose loads travel together
 
 struct CombineArgs {
     const void *y, *residual;
@@ -17,59 +19,101 @@ struct CombineArgs {
     const float *weights;
     const int32_t *ids;
     int64_t T, yt, yj, rs, os;
-    int top_k, M, runs;  // runs of V values of a row
+    int top_k, M, runs;   // runs of V values of a row
+    int lanes, tokens;    // threads of a token, tokens of a CTA
+    FastDiv by_lanes;
 };
 
-template <typename Ty, typename To, int V>
+// V values as they are in memory, in words of 16 bytes where V > 1.
+template <typename T, int V>
+struct Held {
+    T v[V];
+    RFP2_DEV void load(const T *p) {
+        if constexpr (V == 1) {
+            v[0] = *p;
+        } else {
+#pragma unroll
+            for (int w = 0; w < V * (int)sizeof(T) / 16; ++w) {
+                const uint4 u = reinterpret_cast<const uint4 *>(p)[w];
+                memcpy(v + w * (16 / sizeof(T)), &u, 16);
+            }
+        }
+    }
+};
+
+// C runs a thread, a.lanes apart.
+template <typename Ty, typename To, int V, int C>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const CombineArgs a) {
+    constexpr int kAhead = 8 / C;  // slots whose loads travel together
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t n = a.T * a.runs;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
-        const int64_t t = i / a.runs;
-        const int at = (int)(i - t * a.runs) * V;
-        const Ty *y = static_cast<const Ty *>(a.y) + t * a.yt + at;
-        float sum[V];
+    const int tt = (int)a.by_lanes(threadIdx.x);
+    const int64_t t = (int64_t)blockIdx.x * a.tokens + tt;
+    if (tt >= a.tokens || t >= a.T) return;
+    const int r0 = blockIdx.y * a.lanes * C + (threadIdx.x - tt * a.lanes);
+    const Ty *y = static_cast<const Ty *>(a.y) + t * a.yt;
+    const float *weights = a.weights + t * a.top_k;
+    const int32_t *ids = a.ids ? a.ids + t * a.top_k : nullptr;
+    float sum[C][V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) sum[e] = 0.0f;
-        for (int j0 = 0; j0 < a.top_k; j0 += kAhead) {
-            float v[kAhead][V], w[kAhead];
+    for (int c = 0; c < C; ++c)
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                const bool in = j0 + j < a.top_k;
-                w[j] = in ? a.weights[t * a.top_k + j0 + j] : 0.0f;
+        for (int e = 0; e < V; ++e) sum[c][e] = 0.0f;
+    for (int j0 = 0; j0 < a.top_k; j0 += kAhead) {
+        Held<Ty, V> v[kAhead][C];
+        float w[kAhead];
+        bool read[kAhead];
 #pragma unroll
-                for (int e = 0; e < V; ++e) v[j][e] = 0.0f;
-                if (in && (!a.ids || a.ids[t * a.top_k + j0 + j] >= 0)) load_values(y + (j0 + j) * a.yj, v[j]);
-            }
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j)
-#pragma unroll
-                for (int e = 0; e < V; ++e) sum[e] = fmaf(w[j], v[j][e], sum[e]);
+        for (int j = 0; j < kAhead; ++j) {
+            const bool in = j0 + j < a.top_k;
+            w[j] = in ? weights[j0 + j] : 0.0f;
+            read[j] = in && (!ids || ids[j0 + j] >= 0);
         }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                if (read[j] && r0 + c * a.lanes < a.runs) v[j][c].load(y + (j0 + j) * a.yj + (int64_t)(r0 + c * a.lanes) * V);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int e = 0; e < V; ++e) sum[c][e] = fmaf(w[j], read[j] ? to_f32(v[j][c].v[e]) : 0.0f, sum[c][e]);
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int64_t at = (int64_t)(r0 + c * a.lanes) * V;
+        if (r0 + c * a.lanes >= a.runs) continue;
         if (a.residual) {
             float r[V];
             load_values(static_cast<const To *>(a.residual) + t * a.rs + at, r);
 #pragma unroll
-            for (int e = 0; e < V; ++e) sum[e] += r[e];
+            for (int e = 0; e < V; ++e) sum[c][e] += r[e];
         }
-        store_values(static_cast<To *>(a.out) + t * a.os + at, sum);
+        store_values(static_cast<To *>(a.out) + t * a.os + at, sum[c]);
     }
 }
 
 template <typename Ty, typename To>
 cudaError_t launch_combine(CombineArgs &a, cudaStream_t stream) {
-    // V: 16 bytes of y's type, whatever the output's
-    constexpr int W = 16 / sizeof(Ty) * sizeof(To) % 16 == 0 ? 16 / sizeof(Ty) : 16 / sizeof(To);
+    // 16 bytes of y or of out, whichever has fewer values to them is two words of the other
+    constexpr int W = 16 / (sizeof(Ty) < sizeof(To) ? sizeof(Ty) : sizeof(To));
     const auto fits = [](const void *p, int64_t stride, size_t size) {
         return !p || (aligned(p, 16) && stride * (int64_t)size % 16 == 0);
     };
     const bool wide = a.M % W == 0 && fits(a.y, a.yt, sizeof(Ty)) && fits(a.y, a.yj, sizeof(Ty)) &&
                       fits(a.residual, a.rs, sizeof(To)) && fits(a.out, a.os, sizeof(To));
+    constexpr int C = 4;  // single values a thread
     a.runs = wide ? a.M / W : a.M;
-    const int64_t ctas = (a.T * a.runs + kThreads - 1) / kThreads;
-    const dim3 grid((unsigned)std::min<int64_t>(ctas, 1 << 30));
-    return launch(wide ? combine_kernel<Ty, To, W> : combine_kernel<Ty, To, 1>, grid, dim3(kThreads), 0, stream, true, a);
+    const int each = wide ? 1 : C;
+    a.lanes = std::min(kThreads, (a.runs + each - 1) / each);
+    a.tokens = kThreads / a.lanes;
+    a.by_lanes = FastDiv((uint32_t)a.lanes);
+    const int64_t ctas = (a.T + a.tokens - 1) / a.tokens, parts = (a.runs + (int64_t)a.lanes * each - 1) / ((int64_t)a.lanes * each);
+    if (parts > 65535) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)ctas, (unsigned)parts);
+    return launch(wide ? combine_kernel<Ty, To, W, 1> : combine_kernel<Ty, To, 1, C>, grid, dim3(kThreads), 0, stream, true, a);
 }
 
 template <typename Ty>
@@ -90,7 +134,7 @@ extern "C" rfp2_status rfp2_moe_combine(const void *y, int dtype, int64_t T, int
                                         void *out, int out_dtype, int64_t out_stride, rfp2_stream_t stream) {
     const int size = dtype_bytes(dtype), osize = dtype_bytes(out_dtype);
     if (T < 0 || M < 0 || !size || !osize) return RFP2_EINVAL;
-    if (top_k < 1 || top_k > 1024 || T > (1ll << 31) - 1 || M > (1ll << 31) - 1 || y_token_stride < 0 ||
+    if (top_k < 1 || top_k > 1024 || T > (1ll << 31) - 1 || M > 1 << 24 || y_token_stride < 0 ||
         y_slot_stride < 0)
         return RFP2_ESHAPE;
     if (T == 0 || M == 0) return RFP2_OK;

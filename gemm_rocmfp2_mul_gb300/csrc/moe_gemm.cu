@@ -145,7 +145,8 @@ struct GemmArgs {
     __nv_bfloat16 *Y;
     const int32_t *ids;
     Plan plan;
-    int E, M, K, top_k, each, activation, out;
+    int E, M, K, each, out;
+    FastDiv by_top_k;
 };
 
 RFP2_DEV float activated(int activation, float gate, float up) {
@@ -177,7 +178,9 @@ constexpr int kBoxes = 4;
 constexpr int kGroups = 4;      // decoders: group i takes steps i, i + 4, ...
 constexpr int kGroupWarps = 4;  // a weight row a thread
 constexpr int kDecodeWarps = kGroups * kGroupWarps;
-constexpr int kThreads = (7 + kDecodeWarps) * 32;
+constexpr int kLoadWarps = 2;  // gather the tokens
+constexpr int kThreads = (7 + kDecodeWarps + kLoadWarps) * 32;
+constexpr int kLoads = kTileTokens / 2 / (4 * kLoadWarps);  // of a thread for a stage, at most
 constexpr uint32_t kTmemCols = 512;  // two accumulators of 256 columns
 constexpr size_t kRingOff = (size_t)kStages * kStageBytes;
 constexpr size_t kBarOff = kRingOff + (size_t)kBoxes * kBoxBytes;
@@ -197,21 +200,19 @@ RFP2_DEV Unit unit_at(const GemmArgs &a, int u, int blocks) {
     return r;
 }
 
-// Four rows of a K step (x = its first column) into four rows of shared memory, signalled on a barrier of
-// either CTA of the pair.
-RFP2_DEV void tma_gather4_pair(void *smem_dst, const CUtensorMap *map, int x, const int (&row)[4], uint32_t bar_cluster) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_addr(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]),
-        "r"(bar_cluster)
-        : "memory");
+// 16 bytes to shared memory, and an arrival of this thread on `bar` when all its copies so far have landed.
+RFP2_DEV void copy16(uint32_t smem_dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(src) : "memory");
+}
+RFP2_DEV void arrive_after_copies(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
 // Persistent over CTA pairs (clusters of two): pair p takes units p, p + pairs, ...  The weights are the MMAs'
 // A operand, so that a tile has as many columns as it has tokens.  In each CTA
-//   warp 0        gathers its half of the tile's tokens, four rows to a TMA copy, a copy a lane, into the
-//                 B half of a ring of stages;
+//   warps 23, 24  gather their CTA's half of the tile's tokens into the B half of a ring of stages, swizzled,
+//                 16 bytes a lane and copy (TMA's four-row gathers took 2400 cycles for the 128 rows of a stage);
+//   warp 0        hands each gathered stage over to the even CTA;
 //   warp 6        streams the packed rows of its 128 weight rows, 256 of K to a box, into a ring of boxes;
 //   warps 7-22    decode them exactly to bf16 into the A half of the stages, a row a thread;
 //   warp 1        (even CTA) issues M = 256 pair MMAs over both CTAs' stages;
@@ -221,8 +222,7 @@ RFP2_DEV void tma_gather4_pair(void *smem_dst, const CUtensorMap *map, int x, co
 // the two together.  Every wait is bounded; tensor memory is always freed.
 template <int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    product_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap, const GemmArgs a,
-                   int32_t *status) {
+    product_kernel(const __grid_constant__ CUtensorMap wmap, const GemmArgs a, int32_t *status) {
     constexpr bool kGated = ACT != RFP2_ACT_NONE;
     constexpr int kOut = kGated ? kRows / 2 : kRows;  // outputs of a CTA's rows
     extern __shared__ uint8_t smem_raw[];
@@ -234,7 +234,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint64_t *acce = accf + 2;              // [2] (even CTA) it has been read back
     uint64_t *pfull = acce + 2;             // a box is there
     uint64_t *pempty = pfull + kBoxes;      // it has been decoded
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(pempty + kBoxes);
+    uint64_t *bfull = pempty + kBoxes;      // this CTA's tokens of a stage are there
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bfull + kStages);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -243,11 +244,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int nk = a.K / kStep;
 
     if (threadIdx.x == 0) {
-        prefetch_tensor_map(&xmap);
         prefetch_tensor_map(&wmap);
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], 1 + 2 * kGroupWarps);  // the gathers, and the decoders of both CTAs
+            mbar_init(&full[s], 2 * (1 + kGroupWarps));  // both CTAs' tokens and decoders
             mbar_init(&empty[s], 1);
+            mbar_init(&bfull[s], kLoadWarps * 32);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&accf[b], 1);
@@ -273,67 +274,110 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int blocks = (a.out + 2 * kOut - 1) / (2 * kOut);
     const int units = a.plan.header[0] * blocks;
 
-    int g = 0;  // stages filled by this CTA
-    if (warp == 0) {
-        // ---- gathers
+    int g = 0;  // stages handed over by this CTA
+    if (warp == 0 && lane == 0) {
+        // ---- the gathered stages, made visible to the tensor cores
         const uint32_t full0 = cluster_map(&full[0], 0);
-        bool ok = true;
-        for (int u = pair; u < units && ok; u += npairs) {
-            const Unit un = unit_at(a, u, blocks);
-            const int half = un.width / 2;
-            int row[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // columns past the tile's tokens repeat its last
-                const int c = min((int)rank * half + 4 * lane + i, un.tile.z - 1);
-                const int p = a.plan.pairs[un.tile.y + c];
-                row[i] = a.each ? p : p / a.top_k;
+        const int n = (units - pair + npairs - 1) / npairs * nk;
+        for (; g < n; ++g) {
+            const int s = g % kStages;
+            if (*abort_flag || !mbar_wait(&bfull[s], (g / kStages) & 1)) {
+                record_status(status, RFP2_ETIMEOUT);
+                *abort_flag = 1;
+                break;
             }
-            for (int kb = 0; kb < nk; ++kb, ++g) {
-                const int s = g % kStages;
-                const bool free = !*abort_flag && (g < kStages || mbar_wait(&empty[s], ((g / kStages) - 1) & 1));
+            fence_proxy_async_smem();
+            mbar_arrive_remote(full0 + 8u * s);
+        }
+    } else if (warp >= 7 + kDecodeWarps) {
+        // ---- gathers: lane l copies chunk l % 8 of rows l / 8, l / 8 + 8, ... of its warp's
+        const int w = warp - 7 - kDecodeWarps, at = 4 * w + (lane >> 3);
+        const uint32_t to = smem_addr(smem) + kABytes + at * 128 + (((lane & 7) ^ (at & 7)) << 4);
+        const auto rows_of = [&](int u, const Unit &un, int (&row)[kLoads]) {
+            const int half = un.width / 2;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                // columns past the tile's tokens repeat its last
+                const int c = min((int)rank * half + 8 * i + at, un.tile.z - 1);
+                if (8 * i < half) {
+                    const int p = a.plan.pairs[un.tile.y + c];
+                    row[i] = a.each ? p : (int)a.by_top_k(p);
+                }
+            }
+        };
+        int row[kLoads], next[kLoads], gl = 0;
+        bool ok = true;
+        Unit un;
+        if (pair < units) {
+            un = unit_at(a, pair, blocks);
+            rows_of(pair, un, row);
+        }
+        for (int u = pair; u < units && ok; u += npairs) {
+            const int half = un.width / 2;
+            // the next unit's rows are fetched while this one's steps go by
+            const bool more = u + npairs < units;
+            Unit un2 = un;
+            for (int kb = 0; kb < nk; ++kb, ++gl) {
+                const int s = gl % kStages;
+                const bool free = !*abort_flag && (gl < kStages || mbar_wait(&empty[s], ((gl / kStages) - 1) & 1));
                 if (!__all_sync(0xffffffffu, free)) {
                     if (lane == 0) record_status(status, RFP2_ETIMEOUT);
                     *abort_flag = 1;
                     ok = false;
                     break;
                 }
-                if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(un.width * kStep * 2));
-                if (4 * lane < half)
-                    tma_gather4_pair(smem + (size_t)s * kStageBytes + kABytes + lane * 512, &xmap, kb * kStep, row, full0 + 8u * s);
+                const __nv_bfloat16 *x = a.X + kb * kStep + (lane & 7) * 8;
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i)
+                    if (8 * i < half) copy16(to + s * kStageBytes + i * 1024, x + (int64_t)row[i] * a.K);
+                arrive_after_copies(&bfull[s]);
+                if (more && kb == 0) un2 = unit_at(a, u + npairs, blocks);
+                if (more && kb == 1) rows_of(u + npairs, un2, next);
             }
+            un = un2;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) row[i] = next[i];
         }
-    } else if (warp == 1 && rank == 0 && lane == 0) {
-        // ---- MMAs
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == 1 && rank == 0) {
+        // ---- MMAs: the whole warp waits, one lane issues (operands stay warp-uniform)
         int gm = 0, it = 0;
         bool ok = true;
+        int width = pair < units ? unit_at(a, pair, blocks).width : 0;
         for (int u = pair; u < units && ok; u += npairs, ++it) {
             const int b = it & 1;
-            if (*abort_flag || (it >= 2 && !mbar_wait(&acce[b], ((it >> 1) - 1) & 1))) {
-                record_status(status, RFP2_ETIMEOUT);
+            const bool free = !*abort_flag && (it < 2 || mbar_wait(&acce[b], ((it >> 1) - 1) & 1));
+            if (!__all_sync(0xffffffffu, free)) {
+                if (lane == 0) record_status(status, RFP2_ETIMEOUT);
                 *abort_flag = 1;
                 break;
             }
             tc_fence_after();
-            const uint32_t idesc = idesc_bf16_f32(2 * kRows, unit_at(a, u, blocks).width);
+            const uint32_t idesc = idesc_bf16_f32(2 * kRows, width);
             const uint32_t d = tmem + (uint32_t)(b * kTileTokens);
+            if (u + npairs < units) width = unit_at(a, u + npairs, blocks).width;
             for (int kb = 0; kb < nk; ++kb, ++gm) {
                 const int s = gm % kStages;
-                if (*abort_flag || !mbar_wait(&full[s], (gm / kStages) & 1)) {
-                    record_status(status, RFP2_ETIMEOUT);
+                const bool there = !*abort_flag && mbar_wait(&full[s], (gm / kStages) & 1);
+                if (!__all_sync(0xffffffffu, there)) {
+                    if (lane == 0) record_status(status, RFP2_ETIMEOUT);
                     *abort_flag = 1;
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t at = smem_addr(smem + (size_t)s * kStageBytes);
-                const uint64_t adesc = smem_desc_sw128(at), bdesc = smem_desc_sw128(at + kABytes);
+                if (elect_one()) {
+                    const uint32_t at = smem_addr(smem) + s * kStageBytes;
+                    const uint64_t adesc = smem_desc_sw128(at), bdesc = smem_desc_sw128(at + kABytes);
 #pragma unroll
-                for (int k = 0; k < kStep / kUmmaK; ++k)
-                    umma_bf16_pair(d, adesc + 2 * k, bdesc + 2 * k, idesc, (kb > 0 || k > 0) ? 1u : 0u);
-                umma_commit_pair_both(&empty[s]);
+                    for (int k = 0; k < kStep / kUmmaK; ++k)
+                        umma_bf16_pair(d, adesc + 2 * k, bdesc + 2 * k, idesc, (kb > 0 || k > 0) ? 1u : 0u);
+                    umma_commit_pair_both(&empty[s]);
+                }
+                __syncwarp();
             }
-            umma_commit_pair_both(&accf[b]);  // complete, or idle after an abort
+            if (elect_one()) umma_commit_pair_both(&accf[b]);  // complete, or idle after an abort
+            __syncwarp();
         }
     } else if (warp >= 2 && warp < 6) {
         // ---- epilogue
@@ -409,7 +453,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = max(0, n - kBoxes); i < n; ++i)  // none in flight when the CTA retires
             if (!mbar_wait(&pfull[i % kBoxes], (i / kBoxes) & 1)) record_status(status, RFP2_ETIMEOUT);
-    } else if (warp >= 7) {
+    } else if (warp >= 7 && warp < 7 + kDecodeWarps) {
         // ---- decoders: two blocks of a row at byte 20 gi of its 80-byte box row, in a window of 32 bytes
         const int gi = (warp - 7) / kGroupWarps;
         const int quarter = (warp - 7) % kGroupWarps;
@@ -423,6 +467,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int kb = gi; kb < nk; kb += kGroups, ++nd) {
                 const int gd = gbase + kb, s = gd % kStages, ps = nd % kBoxes;
                 bool there = !*abort_flag && mbar_wait(&pfull[ps], (nd / kBoxes) & 1);
+                // decoded before the wait for a free stage, so that only the stores come after it
+                uint32_t o[4][8];
+                if (there) {
+                    const uint4 *win = reinterpret_cast<const uint4 *>(ring + (size_t)ps * kBoxBytes + from * kBoxRowBytes + ((20 * gi) & ~15));
+                    const uint4 q0 = win[0], q1 = win[1];
+                    const uint32_t wv[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+                    uint32_t w[5];
+#pragma unroll
+                    for (int i = 0; i < 5; ++i)
+                        w[i] = wq == 0 ? wv[i] : wq == 1 ? wv[i + 1] : wq == 2 ? wv[i + 2] : wv[i + 3];
+                    // block 0: codes w0, w1, scales in the low half of w2; block 1: from byte 10
+                    const uint32_t code[4] = {w[0], w[1], __funnelshift_r(w[2], w[3], 16), __funnelshift_r(w[3], w[4], 16)};
+                    float sc[4];
+                    decode_scale_pair(w[2] & 0xFFFFu, sc[0], sc[1]);
+                    decode_scale_pair(w[4] >> 16, sc[2], sc[3]);
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) decode_half_bf16(code[h], sc[h], o[h]);
+                }
                 if (gd >= kStages) there = there && mbar_wait(&empty[s], ((gd / kStages) - 1) & 1);
                 if (!__all_sync(0xffffffffu, there)) {
                     if (lane == 0) record_status(status, RFP2_ETIMEOUT);
@@ -430,25 +492,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                const uint4 *win = reinterpret_cast<const uint4 *>(ring + (size_t)ps * kBoxBytes + from * kBoxRowBytes + ((20 * gi) & ~15));
-                const uint4 q0 = win[0], q1 = win[1];
-                const uint32_t wv[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-                uint32_t w[5];
-#pragma unroll
-                for (int i = 0; i < 5; ++i)
-                    w[i] = wq == 0 ? wv[i] : wq == 1 ? wv[i + 1] : wq == 2 ? wv[i + 2] : wv[i + 3];
-                // block 0: codes w0, w1, scales in the low half of w2; block 1: from byte 10
-                const uint32_t code[4] = {w[0], w[1], __funnelshift_r(w[2], w[3], 16), __funnelshift_r(w[3], w[4], 16)};
-                float sc[4];
-                decode_scale_pair(w[2] & 0xFFFFu, sc[0], sc[1]);
-                decode_scale_pair(w[4] >> 16, sc[2], sc[3]);
                 uint8_t *to = smem + (size_t)s * kStageBytes + row * 128;
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
-                    uint32_t o[8];
-                    decode_half_bf16(code[h], sc[h], o);
-                    *reinterpret_cast<uint4 *>(to + (((2 * h) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4 *>(to + (((2 * h + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    *reinterpret_cast<uint4 *>(to + (((2 * h) ^ (row & 7)) << 4)) = make_uint4(o[h][0], o[h][1], o[h][2], o[h][3]);
+                    *reinterpret_cast<uint4 *>(to + (((2 * h + 1) ^ (row & 7)) << 4)) = make_uint4(o[h][4], o[h][5], o[h][6], o[h][7]);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -460,13 +508,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     }
     if (warp == 0 && lane == 0) {
-        // Neither CTA leaves before the commits of the last stages have arrived here (after an abort, before its
-        // copies have, where it can see them).
-        for (int i = max(0, g - kStages); i < g; ++i) {
-            const bool done = *abort_flag && rank == 0 ? mbar_wait(&full[i % kStages], (i / kStages) & 1)
-                                                       : mbar_wait(&empty[i % kStages], (i / kStages) & 1);
-            if (!done) record_status(status, RFP2_ETIMEOUT);
-        }
+        // Neither CTA leaves before the commits of the last stages have arrived here.
+        for (int i = max(0, g - kStages); i < g; ++i)
+            if (!mbar_wait(&empty[i % kStages], (i / kStages) & 1)) record_status(status, RFP2_ETIMEOUT);
     }
     tc_fence_before();
     __syncwarp();
@@ -477,7 +521,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
-using ProductFn = void (*)(CUtensorMap, CUtensorMap, GemmArgs, int32_t *);
+using ProductFn = void (*)(CUtensorMap, GemmArgs, int32_t *);
 
 // Sets the kernels up on a device; returns how many pairs it holds at a time (0: an error).
 int pairs_of(int dev) {
@@ -536,11 +580,9 @@ extern "C" rfp2_status rfp2_moe_gemm(const uint8_t *W, int64_t E, int64_t M, int
     for (const Rows &r : in) meet |= r.meet(y) || r.meet(ws);
     if (meet) return RFP2_EINVAL;
     const int pairs = pairs_of(current_device());
-    CUtensorMap xmap, wmap;
+    CUtensorMap wmap;
     const uint64_t row_bytes = (uint64_t)(K / 32) * 10;
     if (pairs <= 0 ||
-        !encode_tensor_map_2d(&xmap, X, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (uint64_t)K, (uint64_t)(each ? P : T), (uint64_t)K * 2,
-                              kStep, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_tensor_map_2d(&wmap, W, CU_TENSOR_MAP_DATA_TYPE_UINT8, row_bytes, (uint64_t)(E * M), row_bytes, kBoxRowBytes,
                               kRows / 2, CU_TENSOR_MAP_SWIZZLE_NONE))
         return RFP2_ECUDA;
@@ -555,9 +597,8 @@ extern "C" rfp2_status rfp2_moe_gemm(const uint8_t *W, int64_t E, int64_t M, int
     a.E = (int)E;
     a.M = (int)M;
     a.K = (int)K;
-    a.top_k = (int)top_k;
+    a.by_top_k = FastDiv((uint32_t)top_k);
     a.each = each;
-    a.activation = activation;
     a.out = (int)out;
     const int warps = (int)std::min<int64_t>(32, (P + 31) / 32);
     cudaError_t e = launch(plan_kernel, dim3(1), dim3(kPlanThreads), (size_t)warps * (E + 1) * 4, s, true, ids, (int)P,
@@ -569,5 +610,5 @@ extern "C" rfp2_status rfp2_moe_gemm(const uint8_t *W, int64_t E, int64_t M, int
     const ProductFn k = activation == RFP2_ACT_NONE   ? product_kernel<RFP2_ACT_NONE>
                         : activation == RFP2_ACT_SILU ? product_kernel<RFP2_ACT_SILU>
                                                       : product_kernel<RFP2_ACT_GELU>;
-    return from_cuda(launch(k, grid, dim3(kThreads), kSmemBytes, s, true, xmap, wmap, a, dev_status));
+    return from_cuda(launch(k, grid, dim3(kThreads), kSmemBytes, s, true, wmap, a, dev_status));
 }

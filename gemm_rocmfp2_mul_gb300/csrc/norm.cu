@@ -8,6 +8,7 @@
 // with u = |s weight| and U a block's largest, in which r drops out.  In fp32 the quotient is off by
 // 4e-7 of itself at most; where a half-integer is that near, u and U, exact in fp64 (48 bits), decide.
 #include <algorithm>
+#include <type_traits>
 
 #include "activation.cuh"
 
@@ -69,6 +70,21 @@ RFP2_DEV void store_typed(void *p, int type, int64_t at, const float (&v)[V]) {
         store_run(static_cast<__half *>(p) + at, v);
 }
 
+// V values as they are in memory, in words of 16 bytes where V > 1.
+template <typename T, int V>
+struct Held {
+    T v[V];
+    RFP2_DEV void load(const T *p) {
+        if constexpr (V == 1) {
+            v[0] = *p;
+        } else {
+            static_assert(V * sizeof(T) == 16, "one word");
+            const uint4 u = *reinterpret_cast<const uint4 *>(p);
+            memcpy(v, &u, 16);
+        }
+    }
+};
+
 // Sum (or maximum) over the warps that share a row; `part` has 32 places, and successive calls take
 // turns between two of them.
 template <bool MAX>
@@ -97,58 +113,78 @@ RFP2_DEV bool reaches(double u, double m, double U) {
     return (p - q) + (fma(254.0, u, -p) - fma(m, U, -q)) >= 0.0;
 }
 
-// The codes of V values of a block that 32 / V neighbouring lanes share; s and w as they are, y = s r w in
-// fp32.  Returns the block's scale.
+// The codes of the values s w of a block that 32 / V neighbouring lanes share, where they are `near` a border;
+// right but for one step before, unless the block is `tiny`.
 template <int V>
-RFP2_DEV float block_codes(const float (&s)[V], const float (&w)[V], const float (&y)[V], int8_t (&code)[V]) {
+__device__ __noinline__ void exact_codes(const float *s, const float *w, int8_t *code, bool near, bool tiny) {
+    double U = 0.0;
+#pragma unroll 1
+    for (int e = 0; e < V; ++e) U = fmax(U, fabs((double)s[e] * (double)w[e]));
+#pragma unroll
+    for (int off = 1; off < 32 / V; off <<= 1) U = fmax(U, __shfl_xor_sync(0xffffffffu, U, off));
+    if (!near || !(U > 0.0 && U < CUDART_INF)) return;
+#pragma unroll 1
+    for (int e = 0; e < V; ++e) {
+        const double v = (double)s[e] * (double)w[e], u = fabs(v);
+        double k = tiny ? floor(127.0 * (u / U) + 0.5) : (double)abs(code[e]);
+        if (reaches(u, 2.0 * k + 1.0, U))
+            k += 1.0;
+        else if (!reaches(u, 2.0 * k - 1.0, U))
+            k -= 1.0;
+        code[e] = (int8_t)(v < 0.0 ? -(int)k : (int)k);
+    }
+}
+
+// The codes of V values of a block that 32 / V neighbouring lanes share, as bytes; s and w as they are, y = s r w
+// in fp32.  Returns the block's scale.  A quotient t + 1.5 2^23 has the nearest whole number, two's complement,
+// in its low byte; where t is a half-integer but for its error, which one is decided exactly.
+template <int V>
+RFP2_DEV float block_codes(const float (&s)[V], const float (&w)[V], const float (&y)[V], uint32_t (&code)[V]) {
     constexpr int kLanes = 32 / V;
+    constexpr float kWhole = 12582912.0f;
     uint32_t top = 0;  // of |y|'s bits: NaN above infinity above all else
 #pragma unroll
     for (int e = 0; e < V; ++e) top = max(top, __float_as_uint(y[e]) & 0x7FFFFFFFu);
 #pragma unroll
     for (int off = 1; off < kLanes; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-    const float most = __uint_as_float(top);
-    const bool finite = top < 0x7F800000u, tiny = most < 0x1p-90f;
-    const float by = 127.0f / most;
-    bool near = finite && tiny && top != 0;
-    float c[V];
+    const float most = __uint_as_float(top), d = __fdiv_rn(most, 127.0f);
+    const bool finite = top < 0x7F800000u, any = finite && d != 0.0f, tiny = most < 0x1p-90f;
+    const float by = __fdiv_rn(127.0f, most);
+    bool near = any && tiny;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        const float t = fabsf(y[e]) * by;
-        c[e] = floorf(t + 0.5f);
-        near |= finite && fabsf(t - floorf(t) - 0.5f) <= t * 5e-7f;
+        const float t = y[e] * by, m = t + kWhole;
+        code[e] = __float_as_uint(m);
+        near |= any && fabsf(t - (m - kWhole)) >= fmaf(fabsf(t), -6e-7f, 0.5f);
     }
     if (__any_sync(0xffffffffu, near)) {
-        double U = 0.0;
+        // (copies, so that the values themselves stay in registers)
+        float cs[V], cw[V];
+        int8_t k[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) U = fmax(U, fabs((double)s[e] * (double)w[e]));
+        for (int e = 0; e < V; ++e) cs[e] = s[e], cw[e] = w[e], k[e] = (int8_t)code[e];
+        exact_codes<V>(cs, cw, k, near, tiny);
 #pragma unroll
-        for (int off = 1; off < kLanes; off <<= 1) U = fmax(U, __shfl_xor_sync(0xffffffffu, U, off));
-        if (near && U > 0.0 && U < CUDART_INF) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const double u = fabs((double)s[e] * (double)w[e]);
-                double k = tiny ? floor(127.0 * (u / U) + 0.5) : (double)c[e];
-                if (reaches(u, 2.0 * k + 1.0, U))
-                    k += 1.0;
-                else if (!reaches(u, 2.0 * k - 1.0, U))
-                    k -= 1.0;
-                c[e] = (float)k;
-            }
-        }
+        for (int e = 0; e < V; ++e) code[e] = (uint8_t)k[e];
     }
-    const float d = __fdiv_rn(most, 127.0f);
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        const int k = finite && d != 0.0f ? (int)fminf(c[e], 127.0f) : 0;
-        code[e] = (int8_t)(__float_as_uint(y[e]) >> 31 ? -k : k);
-    }
+    for (int e = 0; e < V; ++e) code[e] = any ? code[e] : 0;
     return finite ? d : CUDART_NAN_F;
 }
 
+// Low bytes of four words.
+RFP2_DEV uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
 // A row's values: N runs of V a thread, run i of thread t at V (i threads + t).
-template <typename T, int V, int N>
-__global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a, int warps) {
+// At most so many threads, for the registers that their values take.
+template <int V, int N>
+constexpr int most_threads() {
+    return (V > 1 && N == 4) || N * V > 32 || (V == 1 && N == 8) ? 512 : 1024;
+}
+template <typename T, int V, int N, bool Q8>
+__global__ void __launch_bounds__(most_threads<V, N>(), 1) norm_kernel(const NormArgs a, int warps) {
     __shared__ float part[2][32];
     pdl_wait();
     pdl_launch_dependents();
@@ -156,97 +192,113 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a, int war
     const int lanes = warps == 1 ? 32 : blockDim.x;
     const int tid = warps == 1 ? threadIdx.x & 31 : threadIdx.x;
     const int rows = warps == 1 ? blockDim.x >> 5 : 1;
-    for (int64_t row = (int64_t)blockIdx.x * rows + (warps == 1 ? threadIdx.x >> 5 : 0); row < a.T;
-         row += (int64_t)gridDim.x * rows) {
-        float s[N][V];
-        const T *x = static_cast<const T *>(a.x) + row * a.xs;
+    const int64_t row = (int64_t)blockIdx.x * rows + (warps == 1 ? threadIdx.x >> 5 : 0);
+    if (row >= a.T) return;
+    const T *x = static_cast<const T *>(a.x) + row * a.xs;
+    const T *rest = a.residual ? static_cast<const T *>(a.residual) + row * a.rs : nullptr;
+    // all loads of a row that is not too long travel together
+    constexpr bool kHeld = N <= (V > 1 ? 4 : 8);
+    Held<T, V> hx[N], hr[kHeld ? N : 1];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int at = V * (i * lanes + tid);
+        if (at < a.K) hx[i].load(x + at);
+        if constexpr (kHeld)
+            if (rest && at < a.K) hr[i].load(rest + at);
+    }
+    float s[N][V];
+    constexpr bool kEarly = N * V <= 8;  // few values: their weights are fetched before the sum, not after it
+    float early[kEarly ? N : 1][V];
+    if constexpr (kEarly) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int at = V * (i * lanes + tid);
-#pragma unroll
-            for (int e = 0; e < V; ++e) s[i][e] = 0.0f;
-            if (at < a.K) load_values(x + at, s[i]);
+            if (at < a.K) load_typed(a.weight, a.weight_type, at, early[i]);
         }
-        if (a.residual) {
-            const T *rest = static_cast<const T *>(a.residual) + row * a.rs;
+    }
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int at = V * (i * lanes + tid);
-                if (at < a.K) {
-                    float b[V];
-                    load_values(rest + at, b);
+    for (int i = 0; i < N; ++i) {
+        const int at = V * (i * lanes + tid);
+        const bool in = at < a.K;
+        if constexpr (!kHeld)
+            if (rest && in) hr[0].load(rest + at);
 #pragma unroll
-                    for (int e = 0; e < V; ++e) s[i][e] = to_f32(from_f32<T>(s[i][e] + b[e]));
-                }
-            }
+        for (int e = 0; e < V; ++e) {
+            s[i][e] = in ? to_f32(hx[i].v[e]) : 0.0f;
+            if (rest && in) s[i][e] = to_f32(from_f32<T>(s[i][e] + to_f32(hr[kHeld ? i : 0].v[e])));
         }
-        float sum = 0.0f;
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int e = 0; e < V; ++e) sum = fmaf(s[i][e], s[i][e], sum);
+    sum = over_row<false>(sum, warps, part[0]);
+    float r = 1.0f / sqrtf(sum / (float)a.K + a.eps);
+    if (!(sum < 0x1p126f) || sum < 0x1p-90f) {
+        // squares out of range: of values below 1 in size, by a power of two
+        float most = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
-            for (int e = 0; e < V; ++e) sum = fmaf(s[i][e], s[i][e], sum);
-        sum = over_row<false>(sum, warps, part[0]);
-        float r = 1.0f / sqrtf(sum / (float)a.K + a.eps);
-        if (!(sum < 0x1p126f) || sum < 0x1p-90f) {
-            // squares out of range: of values below 1 in size, by a power of two
-            float most = 0.0f;
+            for (int e = 0; e < V; ++e) most = fmaxf(most, fabsf(s[i][e]));
+        most = over_row<true>(most, warps, part[1]);
+        if (most > 0.0f && most < CUDART_INF_F && sum == sum) {
+            int ex;
+            frexpf(most, &ex);
+            const float down = ldexpf(1.0f, -ex / 2), down2 = ldexpf(1.0f, -ex - -ex / 2);
+            float part_sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < N; ++i)
 #pragma unroll
-                for (int e = 0; e < V; ++e) most = fmaxf(most, fabsf(s[i][e]));
-            most = over_row<true>(most, warps, part[1]);
-            if (most > 0.0f && most < CUDART_INF_F && sum == sum) {
-                int ex;
-                frexpf(most, &ex);
-                const float down = ldexpf(1.0f, -ex / 2), down2 = ldexpf(1.0f, -ex - -ex / 2);
-                float part_sum = 0.0f;
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-#pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        const float v = s[i][e] * down * down2;
-                        part_sum = fmaf(v, v, part_sum);
-                    }
-                if (warps > 1) __syncthreads();
-                part_sum = over_row<false>(part_sum, warps, part[0]);
-                // r = 2^-ex / sqrt(mean + eps 2^-2ex)
-                const float mean = part_sum / (float)a.K + a.eps * down * down * down2 * down2;
-                r = mean < CUDART_INF_F ? down * (down2 / sqrtf(mean)) : r;
-            }
+                for (int e = 0; e < V; ++e) {
+                    const float v = s[i][e] * down * down2;
+                    part_sum = fmaf(v, v, part_sum);
+                }
+            if (warps > 1) __syncthreads();
+            part_sum = over_row<false>(part_sum, warps, part[0]);
+            // r = 2^-ex / sqrt(mean + eps 2^-2ex)
+            const float mean = part_sum / (float)a.K + a.eps * down * down * down2 * down2;
+            r = mean < CUDART_INF_F ? down * (down2 / sqrtf(mean)) : r;
         }
-        if (warps > 1) __syncthreads();  // part[] is written again for the next row
-        if (a.total && a.residual) {
-            T *to = static_cast<T *>(a.total) + row * a.ts;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int at = V * (i * lanes + tid);
-                if (at < a.K) store_values(to + at, s[i]);
-            }
-        }
+    }
+    if (a.total && a.residual) {
+        T *to = static_cast<T *>(a.total) + row * a.ts;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int at = V * (i * lanes + tid);
-            if (a.q == nullptr && at >= a.K) continue;
-            float w[V], y[V];
+            if (at < a.K) store_values(to + at, s[i]);
+        }
+    }
 #pragma unroll
-            for (int e = 0; e < V; ++e) w[e] = 0.0f;
-            if (at < a.K) load_typed(a.weight, a.weight_type, at, w);
+    for (int i = 0; i < N; ++i) {
+        const int at = V * (i * lanes + tid);
+        if (!Q8 && at >= a.K) continue;
+        float w[V], y[V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) y[e] = s[i][e] * r * w[e];
-            if (a.y && at < a.K) store_typed(a.y, a.y_type, row * a.ys + at, y);
-            if (a.q) {
-                int8_t code[V];
-                const float d = block_codes<V>(s[i], w, y, code);
-                if (at < a.K) {
-                    int8_t *q = a.q + row * a.K + at;
-                    if constexpr (V == 8)
-                        *reinterpret_cast<uint2 *>(q) = *reinterpret_cast<const uint2 *>(code);
-                    else if constexpr (V == 4)
-                        *reinterpret_cast<uint32_t *>(q) = *reinterpret_cast<const uint32_t *>(code);
-                    else
-                        *q = code[0];
-                    if ((at & 31) == 0) a.d[row * (a.K >> 5) + (at >> 5)] = d;
-                }
+        for (int e = 0; e < V; ++e) w[e] = 0.0f;
+        if (at < a.K) {
+            if constexpr (kEarly)
+                memcpy(w, early[i], sizeof(w));
+            else
+                load_typed(a.weight, a.weight_type, at, w);
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) y[e] = s[i][e] * r * w[e];
+        if (a.y && at < a.K) store_typed(a.y, a.y_type, row * a.ys + at, y);
+        if constexpr (Q8) {
+            uint32_t code[V];
+            const float d = block_codes<V>(s[i], w, y, code);
+            if (at < a.K) {
+                int8_t *q = a.q + row * a.K + at;
+                if constexpr (V == 8)
+                    *reinterpret_cast<uint2 *>(q) = make_uint2(low_bytes(code[0], code[1], code[2], code[3]),
+                                                               low_bytes(code[4], code[5], code[6], code[7]));
+                else if constexpr (V == 4)
+                    *reinterpret_cast<uint32_t *>(q) = low_bytes(code[0], code[1], code[2], code[3]);
+                else
+                    *q = (int8_t)code[0];
+                if ((at & 31) == 0) a.d[row * (a.K >> 5) + (at >> 5)] = d;
             }
         }
     }
@@ -266,18 +318,31 @@ cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream) {
     // Few rows: a run a thread, for the shortest wait.  Many: four, so that a row's loads travel together
     // and few warps wait for its sum.
     const int sms = sm_count(current_device());
-    const int most = wide ? (a.T <= 2 * sms ? 1 : 4) : 8;
-    int warps = 1;
-    while (warps < 32 && warps * 32 * most < runs) warps *= 2;
-    const int n = (runs + warps * 32 - 1) / (warps * 32);
+    const auto warps_for = [&](int n) { return (runs + 32 * n - 1) / (32 * n); };
+    int n = !wide ? 8 : a.T <= 2 * sms ? 1 : 4;
+    if (wide && n == 1 && warps_for(1) > 32) n = 2;
+    if (wide && n == 2 && warps_for(2) > 32) n = 4;
+    if (wide && n == 4 && warps_for(4) > 16) n = 8;
+    if (!wide && warps_for(8) > 16) n = 32;
+    const int warps = warps_for(n);
     const int threads = warps == 1 ? 128 : warps * 32, rows = warps == 1 ? 4 : 1;
     const int64_t ctas = (a.T + rows - 1) / rows;
-    const dim3 grid((unsigned)std::min<int64_t>(ctas, (int64_t)sms * std::max(1, 2048 / threads)));
+    const dim3 grid((unsigned)ctas);
     void (*k)(NormArgs, int);
-    if (wide)
-        k = n <= 1 ? norm_kernel<T, W, 1> : n <= 2 ? norm_kernel<T, W, 2> : n <= 4 ? norm_kernel<T, W, 4> : norm_kernel<T, W, 8>;
+    const auto pick = [&](auto q8) {
+        constexpr bool Q8 = decltype(q8)::value;
+        if (wide)
+            k = n == 1   ? norm_kernel<T, W, 1, Q8>
+                : n == 2 ? norm_kernel<T, W, 2, Q8>
+                : n == 4 ? norm_kernel<T, W, 4, Q8>
+                         : norm_kernel<T, W, 8, Q8>;
+        else
+            k = n == 8 ? norm_kernel<T, 1, 8, Q8> : norm_kernel<T, 1, 32, Q8>;
+    };
+    if (a.q)
+        pick(std::true_type());
     else
-        k = n <= 8 ? norm_kernel<T, 1, 8> : norm_kernel<T, 1, 32>;
+        pick(std::false_type());
     return launch(k, grid, dim3(threads), 0, stream, true, a, warps);
 }
 

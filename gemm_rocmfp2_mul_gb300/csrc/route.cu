@@ -65,10 +65,11 @@ RFP2_DEV bool before(F v, int i, F w, int j) {
     return v > w || (v == w && i < j);
 }
 
-// The token's choice in fp64, without any storage: every value is computed anew wherever it is compared.
-// Slow, and reached by rows with near ties that the fast way cannot settle.  Returns lane j's pick j, -1: none.
+// The token's choice in fp64, for rows with near ties that the fast way cannot settle.  `values`: a place for E
+// numbers.  Returns lane j's pick j, -1: none.  (Values computed anew wherever they were compared took 60 us of
+// a row, which a grid of 16384 rows waited for; once each, about 3 us.)
 template <typename T, bool SOFTMAX>
-__device__ __noinline__ int choose_exactly(const RouteArgs &a, const T *x, int lane) {
+__device__ __noinline__ int choose_exactly(const RouteArgs &a, const T *x, double *values, int lane) {
     double top = 0.0, total = 1.0;
     if (SOFTMAX) {
         float m = -CUDART_INF_F;
@@ -81,23 +82,22 @@ __device__ __noinline__ int choose_exactly(const RouteArgs &a, const T *x, int l
             if (to_f32(x[e]) > -CUDART_INF_F) total += exp((double)to_f32(x[e]) - top);
         total = warp_sum(total);
     }
-    // what expert e's score is, and what it is chosen by (-infinity: it is not)
-    const auto score = [&](int e) {
-        return SOFTMAX ? exp((double)to_f32(x[e]) - top) / total : sigmoid((double)to_f32(x[e]));
-    };
-    const auto value = [&](int e) {
-        const float v = to_f32(x[e]);
-        if (!(v > -CUDART_INF_F)) return -CUDART_INF;
-        return a.bias ? score(e) + (double)a.bias[e] : (double)v;
-    };
+    __syncwarp();
+    for (int e = lane; e < a.E; e += 32) {
+        const double v = to_f32(x[e]);
+        const double score = SOFTMAX ? exp(v - top) / total : sigmoid(v);
+        values[e] = v > -CUDART_INF ? (a.bias ? score + (double)a.bias[e] : score) : -CUDART_INF;
+    }
+    __syncwarp();
+    // what expert e is chosen by (-infinity: it is not)
+    const auto value = [&](int e) { return a.bias ? values[e] : (double)to_f32(x[e]); };
     unsigned kept = kAll;
     if (a.groups > 1) {
         double mine = -CUDART_INF;  // lane g: what group g counts
         for (int g = 0; g < a.groups; ++g) {
             double b1 = -CUDART_INF, b2 = -CUDART_INF;
             for (int e = g * a.group_size + lane; e < (g + 1) * a.group_size; e += 32) {
-                double v = value(e);
-                if (v > -CUDART_INF && !a.bias && a.group_top > 1) v = score(e);
+                const double v = a.group_top > 1 ? values[e] : value(e);
                 if (v > b1) {
                     b2 = b1;
                     b1 = v;
@@ -154,6 +154,7 @@ __device__ __noinline__ int choose_exactly(const RouteArgs &a, const T *x, int l
 // V experts a lane.
 template <typename T, int V, bool SOFTMAX>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
+    extern __shared__ double values[];  // [kWarps][E], of rows that need them
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
                 pick = mine;
             }
         }
-        if (unsure) pick = choose_exactly<T, SOFTMAX>(a, row, lane);
+        if (unsure) pick = choose_exactly<T, SOFTMAX>(a, row, values + (threadIdx.x >> 5) * a.E, lane);
         if (lane >= a.top_k) pick = -1;
         // Scores of the picks.  Their shares of one another are formed from the logits, so that they hold
         // where the scores themselves underflow.
@@ -342,7 +343,7 @@ cudaError_t launch_route(const RouteArgs &a, cudaStream_t stream) {
     int k = 0;
     while (32 << k < a.E) ++k;
     const int64_t ctas = (a.T + kWarps - 1) / kWarps;
-    return launch(kinds[k], dim3((unsigned)ctas), dim3(kWarps * 32), 0, stream, true, a);
+    return launch(kinds[k], dim3((unsigned)ctas), dim3(kWarps * 32), (size_t)kWarps * a.E * 8, stream, true, a);
 }
 
 template <typename T>

@@ -581,7 +581,7 @@ rfp2_status rfp2_moe_route(const void *logits, int dtype, int64_t T, int64_t E,
  *        rows *_stride elements apart; out may be residual with the same stride.
  * Errors: EINVAL (null, negative size, bad dtype, out over another
  * array), ESHAPE (top_k < 1 or > 1024,
- * T or M > 2^31 - 1, out's row stride below M, another below 0), EALIGN, ECUDA.
+ * T > 2^31 - 1, M > 2^24, out's row stride below M, another below 0), EALIGN, ECUDA.
  */
 rfp2_status rfp2_moe_combine(const void *y, int dtype, int64_t T, int64_t top_k, int64_t M,
                              int64_t y_token_stride, int64_t y_slot_stride, const float *weights,
