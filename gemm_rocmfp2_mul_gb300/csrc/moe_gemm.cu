@@ -178,13 +178,21 @@ constexpr int kBoxes = 4;
 constexpr int kGroups = 4;      // decoders: group i takes steps i, i + 4, ...
 constexpr int kGroupWarps = 4;  // a weight row a thread
 constexpr int kDecodeWarps = kGroups * kGroupWarps;
-constexpr int kLoadWarps = 2;  // gather the tokens
-constexpr int kThreads = (7 + kDecodeWarps + kLoadWarps) * 32;
-constexpr int kLoads = kTileTokens / 2 / (4 * kLoadWarps);  // of a thread for a stage, at most
+constexpr int kLoadWarps = 4;  // gather the tokens: warp i of them steps i, i + 4, ...
+constexpr int kThreads = (6 + kDecodeWarps + kLoadWarps) * 32;
+constexpr int kLoads = kTileTokens / 2 / 4;  // copies of a lane for a step, at most
 constexpr uint32_t kTmemCols = 512;  // two accumulators of 256 columns
 constexpr size_t kRingOff = (size_t)kStages * kStageBytes;
 constexpr size_t kBarOff = kRingOff + (size_t)kBoxes * kBoxBytes;
 constexpr size_t kSmemBytes = 1024 + kBarOff + 256;
+
+// mbar_wait, which reads the GPU's timer once a probe has failed, after probes without it.
+RFP2_DEV bool wait_for(uint64_t *bar, uint32_t parity) {
+#pragma unroll 1
+    for (int i = 0; i < 1024; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait(bar, parity);
+}
 
 // A unit of work of a CTA pair: a tile of tokens and a block of 256 weight rows.
 struct Unit {
@@ -200,19 +208,15 @@ RFP2_DEV Unit unit_at(const GemmArgs &a, int u, int blocks) {
     return r;
 }
 
-// 16 bytes to shared memory, and an arrival of this thread on `bar` when all its copies so far have landed.
 RFP2_DEV void copy16(uint32_t smem_dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(src) : "memory");
 }
-RFP2_DEV void arrive_after_copies(uint64_t *bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
+RFP2_DEV void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Persistent over CTA pairs (clusters of two): pair p takes units p, p + pairs, ...  The weights are the MMAs'
 // A operand, so that a tile has as many columns as it has tokens.  In each CTA
-//   warps 23, 24  gather their CTA's half of the tile's tokens into the B half of a ring of stages, swizzled,
-//                 16 bytes a lane and copy (TMA's four-row gathers took 2400 cycles for the 128 rows of a stage);
-//   warp 0        hands each gathered stage over to the even CTA;
+//   warps 0, 23-25 gather their CTA's half of the tile's tokens into the B half of a ring of stages, swizzled,
+//                 16 bytes a lane and copy, a step of K a warp at a time;
 //   warp 6        streams the packed rows of its 128 weight rows, 256 of K to a box, into a ring of boxes;
 //   warps 7-22    decode them exactly to bf16 into the A half of the stages, a row a thread;
 //   warp 1        (even CTA) issues M = 256 pair MMAs over both CTAs' stages;
@@ -234,8 +238,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint64_t *acce = accf + 2;              // [2] (even CTA) it has been read back
     uint64_t *pfull = acce + 2;             // a box is there
     uint64_t *pempty = pfull + kBoxes;      // it has been decoded
-    uint64_t *bfull = pempty + kBoxes;      // this CTA's tokens of a stage are there
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bfull + kStages);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(pempty + kBoxes);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -248,7 +251,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 2 * (1 + kGroupWarps));  // both CTAs' tokens and decoders
             mbar_init(&empty[s], 1);
-            mbar_init(&bfull[s], kLoadWarps * 32);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&accf[b], 1);
@@ -274,52 +276,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int blocks = (a.out + 2 * kOut - 1) / (2 * kOut);
     const int units = a.plan.header[0] * blocks;
 
-    int g = 0;  // stages handed over by this CTA
-    if (warp == 0 && lane == 0) {
-        // ---- the gathered stages, made visible to the tensor cores
+    if (warp == 0 || warp >= 7 + kDecodeWarps) {
+        // ---- gathers: lane l copies chunk l % 8 of rows l / 8, l / 8 + 4, ...  Each warp waits for its own copies
+        // before it hands the stage over; the other three have theirs on their way meanwhile.
+        const int wl = warp == 0 ? 0 : warp - 6 - kDecodeWarps, at = lane >> 3;
+        const uint32_t base = smem_addr(smem) + kABytes + at * 128;
+        const uint32_t even = base + (((lane & 7) ^ at) << 4), odd = base + (((lane & 7) ^ (at + 4)) << 4);  // rows % 8
         const uint32_t full0 = cluster_map(&full[0], 0);
-        const int n = (units - pair + npairs - 1) / npairs * nk;
-        for (; g < n; ++g) {
-            const int s = g % kStages;
-            if (*abort_flag || !mbar_wait(&bfull[s], (g / kStages) & 1)) {
-                record_status(status, RFP2_ETIMEOUT);
-                *abort_flag = 1;
-                break;
-            }
-            fence_proxy_async_smem();
-            mbar_arrive_remote(full0 + 8u * s);
-        }
-    } else if (warp >= 7 + kDecodeWarps) {
-        // ---- gathers: lane l copies chunk l % 8 of rows l / 8, l / 8 + 8, ... of its warp's
-        const int w = warp - 7 - kDecodeWarps, at = 4 * w + (lane >> 3);
-        const uint32_t to = smem_addr(smem) + kABytes + at * 128 + (((lane & 7) ^ (at & 7)) << 4);
-        const auto rows_of = [&](int u, const Unit &un, int (&row)[kLoads]) {
+        int gbase = 0;
+        bool ok = true;
+        for (int u = pair; u < units && ok; u += npairs, gbase += nk) {
+            const Unit un = unit_at(a, u, blocks);
             const int half = un.width / 2;
+            int row[kLoads];
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
                 // columns past the tile's tokens repeat its last
-                const int c = min((int)rank * half + 8 * i + at, un.tile.z - 1);
-                if (8 * i < half) {
-                    const int p = a.plan.pairs[un.tile.y + c];
-                    row[i] = a.each ? p : (int)a.by_top_k(p);
-                }
+                const int c = min((int)rank * half + 4 * i + at, un.tile.z - 1);
+                if (4 * i < half) row[i] = a.plan.pairs[un.tile.y + c];
             }
-        };
-        int row[kLoads], next[kLoads], gl = 0;
-        bool ok = true;
-        Unit un;
-        if (pair < units) {
-            un = unit_at(a, pair, blocks);
-            rows_of(pair, un, row);
-        }
-        for (int u = pair; u < units && ok; u += npairs) {
-            const int half = un.width / 2;
-            // the next unit's rows are fetched while this one's steps go by
-            const bool more = u + npairs < units;
-            Unit un2 = un;
-            for (int kb = 0; kb < nk; ++kb, ++gl) {
-                const int s = gl % kStages;
-                const bool free = !*abort_flag && (gl < kStages || mbar_wait(&empty[s], ((gl / kStages) - 1) & 1));
+            if (!a.each)
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) row[i] = (int)a.by_top_k(row[i]);
+            for (int kb = wl; kb < nk; kb += kLoadWarps) {
+                const int g = gbase + kb, s = g % kStages;
+                const bool free = !*abort_flag && (g < kStages || wait_for(&empty[s], ((g / kStages) - 1) & 1));
                 if (!__all_sync(0xffffffffu, free)) {
                     if (lane == 0) record_status(status, RFP2_ETIMEOUT);
                     *abort_flag = 1;
@@ -329,16 +310,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const __nv_bfloat16 *x = a.X + kb * kStep + (lane & 7) * 8;
 #pragma unroll
                 for (int i = 0; i < kLoads; ++i)
-                    if (8 * i < half) copy16(to + s * kStageBytes + i * 1024, x + (int64_t)row[i] * a.K);
-                arrive_after_copies(&bfull[s]);
-                if (more && kb == 0) un2 = unit_at(a, u + npairs, blocks);
-                if (more && kb == 1) rows_of(u + npairs, un2, next);
+                    if (4 * i < half) copy16((i & 1 ? odd : even) + s * kStageBytes + i * 512, x + (int64_t)row[i] * a.K);
+                copies_wait();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(full0 + 8u * s);
             }
-            un = un2;
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) row[i] = next[i];
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == 1 && rank == 0) {
         // ---- MMAs: the whole warp waits, one lane issues (operands stay warp-uniform)
         int gm = 0, it = 0;
@@ -346,7 +324,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int width = pair < units ? unit_at(a, pair, blocks).width : 0;
         for (int u = pair; u < units && ok; u += npairs, ++it) {
             const int b = it & 1;
-            const bool free = !*abort_flag && (it < 2 || mbar_wait(&acce[b], ((it >> 1) - 1) & 1));
+            const bool free = !*abort_flag && (it < 2 || wait_for(&acce[b], ((it >> 1) - 1) & 1));
             if (!__all_sync(0xffffffffu, free)) {
                 if (lane == 0) record_status(status, RFP2_ETIMEOUT);
                 *abort_flag = 1;
@@ -358,7 +336,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (u + npairs < units) width = unit_at(a, u + npairs, blocks).width;
             for (int kb = 0; kb < nk; ++kb, ++gm) {
                 const int s = gm % kStages;
-                const bool there = !*abort_flag && mbar_wait(&full[s], (gm / kStages) & 1);
+                const bool there = !*abort_flag && wait_for(&full[s], (gm / kStages) & 1);
                 if (!__all_sync(0xffffffffu, there)) {
                     if (lane == 0) record_status(status, RFP2_ETIMEOUT);
                     *abort_flag = 1;
@@ -391,7 +369,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int m = (2 * un.block + (int)rank) * kOut + (kGated ? q * 16 + (lane & 15) : q * 32 + lane);
             float bias = 0.0f;
             if (a.bias && m < a.out) bias = a.bias[(int64_t)un.tile.x * a.M + m + (kGated && lane >= 16 ? a.out : 0)];
-            if (*abort_flag || !mbar_wait(&accf[b], (it >> 1) & 1)) {
+            if (*abort_flag || !wait_for(&accf[b], (it >> 1) & 1)) {
                 record_status(status, RFP2_ETIMEOUT);
                 *abort_flag = 1;
                 break;
@@ -439,7 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int row = un.tile.x * a.M + (2 * un.block + (int)rank) * kOut;
             for (int kq = 0; kq < nk / 4; ++kq, ++n) {
                 const int s = n % kBoxes;
-                if (*abort_flag || (n >= kBoxes && !mbar_wait(&pempty[s], ((n / kBoxes) - 1) & 1))) {
+                if (*abort_flag || (n >= kBoxes && !wait_for(&pempty[s], ((n / kBoxes) - 1) & 1))) {
                     record_status(status, RFP2_ETIMEOUT);
                     *abort_flag = 1;
                     ok = false;
@@ -452,7 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         }
         for (int i = max(0, n - kBoxes); i < n; ++i)  // none in flight when the CTA retires
-            if (!mbar_wait(&pfull[i % kBoxes], (i / kBoxes) & 1)) record_status(status, RFP2_ETIMEOUT);
+            if (!wait_for(&pfull[i % kBoxes], (i / kBoxes) & 1)) record_status(status, RFP2_ETIMEOUT);
     } else if (warp >= 7 && warp < 7 + kDecodeWarps) {
         // ---- decoders: two blocks of a row at byte 20 gi of its 80-byte box row, in a window of 32 bytes
         const int gi = (warp - 7) / kGroupWarps;
@@ -466,7 +444,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int u = pair; u < units && ok; u += npairs, gbase += nk) {
             for (int kb = gi; kb < nk; kb += kGroups, ++nd) {
                 const int gd = gbase + kb, s = gd % kStages, ps = nd % kBoxes;
-                bool there = !*abort_flag && mbar_wait(&pfull[ps], (nd / kBoxes) & 1);
+                bool there = !*abort_flag && wait_for(&pfull[ps], (nd / kBoxes) & 1);
                 // decoded before the wait for a free stage, so that only the stores come after it
                 uint32_t o[4][8];
                 if (there) {
@@ -485,7 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int h = 0; h < 4; ++h) decode_half_bf16(code[h], sc[h], o[h]);
                 }
-                if (gd >= kStages) there = there && mbar_wait(&empty[s], ((gd / kStages) - 1) & 1);
+                if (gd >= kStages) there = there && wait_for(&empty[s], ((gd / kStages) - 1) & 1);
                 if (!__all_sync(0xffffffffu, there)) {
                     if (lane == 0) record_status(status, RFP2_ETIMEOUT);
                     *abort_flag = 1;
@@ -509,8 +487,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (warp == 0 && lane == 0) {
         // Neither CTA leaves before the commits of the last stages have arrived here.
-        for (int i = max(0, g - kStages); i < g; ++i)
-            if (!mbar_wait(&empty[i % kStages], (i / kStages) & 1)) record_status(status, RFP2_ETIMEOUT);
+        const int n = (units - pair + npairs - 1) / npairs * nk;
+        for (int i = max(0, n - kStages); i < n; ++i)
+            if (!wait_for(&empty[i % kStages], (i / kStages) & 1)) record_status(status, RFP2_ETIMEOUT);
     }
     tc_fence_before();
     __syncwarp();
