@@ -21,6 +21,7 @@ struct CombineArgs {
     int64_t T, yt, yj, rs, os;
     int top_k, M, runs;   // runs of V values of a row
     int lanes, tokens;    // threads of a token, tokens of a CTA
+    int eights;           // weights and ids of eight slots are aligned words
     FastDiv by_lanes;
 };
 
@@ -59,15 +60,34 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const CombineArgs a) 
     for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int e = 0; e < V; ++e) sum[c][e] = 0.0f;
+    Held<To, V> rest[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+        if (a.residual && r0 + c * a.lanes < a.runs)
+            rest[c].load(static_cast<const To *>(a.residual) + t * a.rs + (int64_t)(r0 + c * a.lanes) * V);
     for (int j0 = 0; j0 < a.top_k; j0 += kAhead) {
         Held<Ty, V> v[kAhead][C];
         float w[kAhead];
         bool read[kAhead];
+        if (kAhead == 8 && a.eights) {
+            const float4 *fw = reinterpret_cast<const float4 *>(weights + j0);
+            const float4 w0 = fw[0], w1 = fw[1];
+            const float ws[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+            int4 i0 = make_int4(0, 0, 0, 0), i1 = i0;
+            if (ids) {
+                i0 = reinterpret_cast<const int4 *>(ids + j0)[0];
+                i1 = reinterpret_cast<const int4 *>(ids + j0)[1];
+            }
+            const int is[8] = {i0.x, i0.y, i0.z, i0.w, i1.x, i1.y, i1.z, i1.w};
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const bool in = j0 + j < a.top_k;
-            w[j] = in ? weights[j0 + j] : 0.0f;
-            read[j] = in && (!ids || ids[j0 + j] >= 0);
+            for (int j = 0; j < kAhead; ++j) w[j] = ws[j & 7], read[j] = is[j & 7] >= 0;
+        } else {
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const bool in = j0 + j < a.top_k;
+                w[j] = in ? weights[j0 + j] : 0.0f;
+                read[j] = in && (!ids || ids[j0 + j] >= 0);
+            }
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
@@ -85,12 +105,9 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const CombineArgs a) 
     for (int c = 0; c < C; ++c) {
         const int64_t at = (int64_t)(r0 + c * a.lanes) * V;
         if (r0 + c * a.lanes >= a.runs) continue;
-        if (a.residual) {
-            float r[V];
-            load_values(static_cast<const To *>(a.residual) + t * a.rs + at, r);
+        if (a.residual)
 #pragma unroll
-            for (int e = 0; e < V; ++e) sum[c][e] += r[e];
-        }
+            for (int e = 0; e < V; ++e) sum[c][e] += to_f32(rest[c].v[e]);
         store_values(static_cast<To *>(a.out) + t * a.os + at, sum[c]);
     }
 }
@@ -162,6 +179,7 @@ extern "C" rfp2_status rfp2_moe_combine(const void *y, int dtype, int64_t T, int
     a.os = out_stride;
     a.top_k = (int)top_k;
     a.M = (int)M;
+    a.eights = top_k % 8 == 0 && aligned(weights, 16) && aligned(ids, 16);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return from_cuda(dtype == RFP2_F32    ? launch_to<float>(a, out_dtype, s)
                      : dtype == RFP2_BF16 ? launch_to<__nv_bfloat16>(a, out_dtype, s)

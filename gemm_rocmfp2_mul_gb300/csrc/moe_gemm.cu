@@ -186,6 +186,19 @@ constexpr size_t kRingOff = (size_t)kStages * kStageBytes;
 constexpr size_t kBarOff = kRingOff + (size_t)kBoxes * kBoxBytes;
 constexpr size_t kSmemBytes = 1024 + kBarOff + 256;
 
+// Has the phase with `parity` completed?  (No waiting.)
+RFP2_DEV bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // mbar_wait, which reads the GPU's timer once a probe has failed, after probes without it.
 RFP2_DEV bool wait_for(uint64_t *bar, uint32_t parity) {
 #pragma unroll 1
@@ -282,7 +295,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int wl = warp == 0 ? 0 : warp - 6 - kDecodeWarps, at = lane >> 3;
         const uint32_t base = smem_addr(smem) + kABytes + at * 128;
         const uint32_t even = base + (((lane & 7) ^ at) << 4), odd = base + (((lane & 7) ^ (at + 4)) << 4);  // rows % 8
-        const uint32_t full0 = cluster_map(&full[0], 0);
+        const uint32_t full0 = cluster_map(&full[0], 0), pitch = (uint32_t)a.K * 2;
         int gbase = 0;
         bool ok = true;
         for (int u = pair; u < units && ok; u += npairs, gbase += nk) {
@@ -307,10 +320,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                const __nv_bfloat16 *x = a.X + kb * kStep + (lane & 7) * 8;
+                // (few instructions a copy, and none for the rows that a narrow tile lacks: the decoders keep the
+                // schedulers busy)
+                const uint8_t *x = reinterpret_cast<const uint8_t *>(a.X + kb * kStep + (lane & 7) * 8);
+                const uint32_t to0 = even + s * kStageBytes, to1 = odd + s * kStageBytes;
 #pragma unroll
-                for (int i = 0; i < kLoads; ++i)
-                    if (4 * i < half) copy16((i & 1 ? odd : even) + s * kStageBytes + i * 512, x + (int64_t)row[i] * a.K);
+                for (int j = 0; j < kLoads; j += 4) {
+                    if (4 * j >= half) break;  // half is a multiple of 16 rows
+#pragma unroll
+                    for (int i = j; i < j + 4; ++i)
+                        copy16((i & 1 ? to1 : to0) + i * 512, x + (uint64_t)(uint32_t)row[i] * pitch);
+                }
                 copies_wait();
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -319,9 +339,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1 && rank == 0) {
         // ---- MMAs: the whole warp waits, one lane issues (operands stay warp-uniform)
-        int gm = 0, it = 0;
-        bool ok = true;
+        // The warp's own instructions are on the critical path: the next stage is looked at while this one's MMAs are
+        // issued, and nothing but a vote stands between a stage that is there and its MMAs.
+        int it = 0, s = 0;
+        uint32_t phase = 0;
+        bool ok = true, ready = false;
         int width = pair < units ? unit_at(a, pair, blocks).width : 0;
+        const uint64_t adesc0 = smem_desc_sw128(smem_addr(smem)), bdesc0 = smem_desc_sw128(smem_addr(smem) + kABytes);
         for (int u = pair; u < units && ok; u += npairs, ++it) {
             const int b = it & 1;
             const bool free = !*abort_flag && (it < 2 || wait_for(&acce[b], ((it >> 1) - 1) & 1));
@@ -334,25 +358,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t idesc = idesc_bf16_f32(2 * kRows, width);
             const uint32_t d = tmem + (uint32_t)(b * kTileTokens);
             if (u + npairs < units) width = unit_at(a, u + npairs, blocks).width;
-            for (int kb = 0; kb < nk; ++kb, ++gm) {
-                const int s = gm % kStages;
-                const bool there = !*abort_flag && wait_for(&full[s], (gm / kStages) & 1);
-                if (!__all_sync(0xffffffffu, there)) {
-                    if (lane == 0) record_status(status, RFP2_ETIMEOUT);
-                    *abort_flag = 1;
-                    ok = false;
-                    break;
+            for (int kb = 0; kb < nk; ++kb) {
+                if (!__all_sync(0xffffffffu, ready)) {
+                    const bool there = !*abort_flag && wait_for(&full[s], phase);
+                    if (!__all_sync(0xffffffffu, there)) {
+                        if (lane == 0) record_status(status, RFP2_ETIMEOUT);
+                        *abort_flag = 1;
+                        ok = false;
+                        break;
+                    }
                 }
                 tc_fence_after();
+                const int s1 = s + 1 == kStages ? 0 : s + 1;
+                const uint32_t phase1 = s1 ? phase : phase ^ 1;
+                ready = mbar_test(&full[s1], phase1);
                 if (elect_one()) {
-                    const uint32_t at = smem_addr(smem) + s * kStageBytes;
-                    const uint64_t adesc = smem_desc_sw128(at), bdesc = smem_desc_sw128(at + kABytes);
+                    const uint64_t at = (uint64_t)((s * kStageBytes) >> 4);
 #pragma unroll
                     for (int k = 0; k < kStep / kUmmaK; ++k)
-                        umma_bf16_pair(d, adesc + 2 * k, bdesc + 2 * k, idesc, (kb > 0 || k > 0) ? 1u : 0u);
+                        umma_bf16_pair(d, adesc0 + at + 2 * k, bdesc0 + at + 2 * k, idesc, (kb > 0 || k > 0) ? 1u : 0u);
                     umma_commit_pair_both(&empty[s]);
                 }
-                __syncwarp();
+                s = s1;
+                phase = phase1;
             }
             if (elect_one()) umma_commit_pair_both(&accf[b]);  // complete, or idle after an abort
             __syncwarp();

@@ -316,10 +316,10 @@ cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream) {
     const int V = wide ? W : 1;
     const int runs = (a.K + V - 1) / V;
     // Few rows: a run a thread, for the shortest wait.  Many: four, so that a row's loads travel together
-    // and few warps wait for its sum.
+    // and few warps wait for its sum; two where there are codes to make, whose registers cost more in rows at once.
     const int sms = sm_count(current_device());
     const auto warps_for = [&](int n) { return (runs + 32 * n - 1) / (32 * n); };
-    int n = !wide ? 8 : a.T <= 2 * sms ? 1 : 4;
+    int n = !wide ? 8 : a.T <= 2 * sms ? 1 : a.q ? 2 : 4;
     if (wide && n == 1 && warps_for(1) > 32) n = 2;
     if (wide && n == 2 && warps_for(2) > 32) n = 4;
     if (wide && n == 4 && warps_for(4) > 16) n = 8;

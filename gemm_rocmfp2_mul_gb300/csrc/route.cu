@@ -28,11 +28,12 @@ struct RouteArgs {
     int64_t T, stride;
     int E, top_k, groups, keep, group_top, group_size, renormalise;
     float scale;
+    FastDiv by_size;  // experts of a group
 };
 
-// fp32 as integers in the same order; -infinity is 0x007FFFFF, and 0 is below all of them.
+// fp32 as integers in the same order, -0 as 0; -infinity is 0x007FFFFF, and 0 is below all of them.
 RFP2_DEV uint32_t ordered(float v) {
-    const uint32_t b = __float_as_uint(v);
+    const uint32_t b = __float_as_uint(v + 0.0f);
     return b >> 31 ? ~b : b | 0x80000000u;
 }
 RFP2_DEV float unordered(uint32_t k) { return __uint_as_float(k >> 31 ? k & 0x7FFFFFFFu : ~k); }
@@ -65,11 +66,19 @@ RFP2_DEV bool before(F v, int i, F w, int j) {
     return v > w || (v == w && i < j);
 }
 
+// fp64 as integers in the same order (fp64 comparisons are as slow as fp64 sums here); 0: not to be chosen.
+RFP2_DEV uint64_t ordered(double v) {
+    const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);  // -0 is 0
+    return v == -CUDART_INF ? 0ull : b >> 63 ? ~b : b | 1ull << 63;
+}
+RFP2_DEV double unordered(uint64_t k) {
+    return k ? __longlong_as_double((long long)(k >> 63 ? k & ~(1ull << 63) : ~k)) : -CUDART_INF;
+}
+
 // The token's choice in fp64, for rows with near ties that the fast way cannot settle.  `values`: a place for E
-// numbers.  Returns lane j's pick j, -1: none.  (Values computed anew wherever they were compared took 60 us of
-// a row, which a grid of 16384 rows waited for; once each, about 3 us.)
+// numbers.  Returns lane j's pick j, -1: none.  Each value is computed once, and compared as an integer.
 template <typename T, bool SOFTMAX>
-__device__ __noinline__ int choose_exactly(const RouteArgs &a, const T *x, double *values, int lane) {
+__device__ __noinline__ int choose_exactly(const RouteArgs &a, const T *x, uint64_t *values, int lane) {
     double top = 0.0, total = 1.0;
     if (SOFTMAX) {
         float m = -CUDART_INF_F;
@@ -84,66 +93,70 @@ __device__ __noinline__ int choose_exactly(const RouteArgs &a, const T *x, doubl
     }
     __syncwarp();
     for (int e = lane; e < a.E; e += 32) {
-        const double v = to_f32(x[e]);
-        const double score = SOFTMAX ? exp(v - top) / total : sigmoid(v);
-        values[e] = v > -CUDART_INF ? (a.bias ? score + (double)a.bias[e] : score) : -CUDART_INF;
+        const float l = to_f32(x[e]);
+        double v = -CUDART_INF;
+        if (l > -CUDART_INF_F) {
+            v = SOFTMAX ? exp((double)l - top) / total : sigmoid((double)l);
+            if (a.bias) v += (double)a.bias[e];
+        }
+        values[e] = ordered(v);
     }
     __syncwarp();
-    // what expert e is chosen by (-infinity: it is not)
-    const auto value = [&](int e) { return a.bias ? values[e] : (double)to_f32(x[e]); };
+    // what expert e is chosen by
+    const auto value = [&](int e) -> uint64_t {
+        if (a.bias) return values[e];
+        const float l = to_f32(x[e]);
+        return l > -CUDART_INF_F ? (uint64_t)ordered(l) : 0ull;
+    };
     unsigned kept = kAll;
     if (a.groups > 1) {
-        double mine = -CUDART_INF;  // lane g: what group g counts
+        uint64_t mine = 0;  // lane g: what group g counts
         for (int g = 0; g < a.groups; ++g) {
-            double b1 = -CUDART_INF, b2 = -CUDART_INF;
+            uint64_t b1 = 0, b2 = 0;
             for (int e = g * a.group_size + lane; e < (g + 1) * a.group_size; e += 32) {
-                const double v = a.group_top > 1 ? values[e] : value(e);
-                if (v > b1) {
-                    b2 = b1;
-                    b1 = v;
-                } else if (v > b2) {
-                    b2 = v;
-                }
+                const uint64_t v = a.group_top > 1 ? values[e] : value(e);
+                b2 = max(b2, min(b1, v));
+                b1 = max(b1, v);
             }
 #pragma unroll
             for (int off = 16; off >= 1; off >>= 1) {
-                const double o1 = __shfl_xor_sync(kAll, b1, off), o2 = __shfl_xor_sync(kAll, b2, off);
-                b2 = fmax(fmin(b1, o1), fmax(b2, o2));
-                b1 = fmax(b1, o1);
+                const uint64_t o1 = __shfl_xor_sync(kAll, b1, off), o2 = __shfl_xor_sync(kAll, b2, off);
+                b2 = max(min(b1, o1), max(b2, o2));
+                b1 = max(b1, o1);
             }
-            if (a.group_top > 1 && b2 > -CUDART_INF) b1 += b2;
+            if (a.group_top > 1 && b2) b1 = ordered(unordered(b1) + unordered(b2));
             if (lane == g) mine = b1;
         }
         int rank = 0;
         for (int g = 0; g < a.groups; ++g) {
-            const double o = __shfl_sync(kAll, mine, g);
+            const uint64_t o = __shfl_sync(kAll, mine, g);
             rank += before(o, g, mine, lane);
         }
-        kept = __ballot_sync(kAll, lane < a.groups && rank < a.keep && mine > -CUDART_INF);
+        kept = __ballot_sync(kAll, lane < a.groups && rank < a.keep && mine);
     }
-    double last = CUDART_INF;
+    uint64_t last = ~0ull;
     int last_e = -1, pick = -1;
     for (int p = 0; p < a.top_k; ++p) {
-        double best = -CUDART_INF;
-        int at = -1;
+        uint64_t best = 0;
+        int at = a.E;
         for (int e = lane; e < a.E; e += 32) {
-            if (a.groups > 1 && !(kept >> (e / a.group_size) & 1)) continue;
-            const double v = value(e);
-            if (v > -CUDART_INF && (last_e < 0 || before(last, last_e, v, e)) && (at < 0 || v > best)) {
+            if (a.groups > 1 && !(kept >> a.by_size(e) & 1)) continue;
+            const uint64_t v = value(e);
+            if (v > best && before(last, last_e, v, e)) {
                 best = v;
                 at = e;
             }
         }
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) {
-            const double v = __shfl_xor_sync(kAll, best, off);
+            const uint64_t v = __shfl_xor_sync(kAll, best, off);
             const int e = __shfl_xor_sync(kAll, at, off);
-            if (e >= 0 && (at < 0 || before(v, e, best, at))) {
+            if (before(v, e, best, at)) {
                 best = v;
                 at = e;
             }
         }
-        if (at < 0) break;
+        if (best == 0) break;
         if (lane == p) pick = at;
         last = best;
         last_e = at;
@@ -154,7 +167,7 @@ __device__ __noinline__ int choose_exactly(const RouteArgs &a, const T *x, doubl
 // V experts a lane.
 template <typename T, int V, bool SOFTMAX>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
-    extern __shared__ double values[];  // [kWarps][E], of rows that need them
+    extern __shared__ uint64_t values[];  // [kWarps][E], of rows that need them
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
@@ -208,16 +221,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
         if (a.groups > 1) {
             float mine = -CUDART_INF_F;  // lane g: what group g counts
             float room = 0.0f;           // how far any of them may be off
-            for (int g = 0; g < a.groups; ++g) {
-                const int from = g * a.group_size, to = from + a.group_size;
-                uint32_t b1 = 0, b2 = 0;
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const int e = j * 32 + lane;
-                    const uint32_t k = e >= from && e < to ? part[j] : 0u;
-                    b2 = max(b2, min(b1, k));
-                    b1 = max(b1, k);
-                }
+            // group g's largest values, from each lane's two largest
+            const auto count = [&](int g, uint32_t b1, uint32_t b2) {
                 const uint32_t m1 = __reduce_max_sync(kAll, b1);
                 float v = m1 ? unordered(m1) : -CUDART_INF_F;
                 if (by_sum) {
@@ -229,6 +234,33 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
                     room = fmaxf(room, slack(v));
                 }
                 if (lane == g) mine = v;
+            };
+            if ((a.group_size & 31) == 0) {  // a group is the same values of every lane
+                uint32_t b1 = 0, b2 = 0;
+                int g = 0, end = a.group_size;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    b2 = max(b2, min(b1, part[j]));
+                    b1 = max(b1, part[j]);
+                    if ((j + 1) * 32 == end) {
+                        count(g++, b1, b2);
+                        b1 = b2 = 0;
+                        end += a.group_size;
+                    }
+                }
+            } else {
+                for (int g = 0; g < a.groups; ++g) {
+                    const int from = g * a.group_size, to = from + a.group_size;
+                    uint32_t b1 = 0, b2 = 0;
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const int e = j * 32 + lane;
+                        const uint32_t k = e >= from && e < to ? part[j] : 0u;
+                        b2 = max(b2, min(b1, k));
+                        b1 = max(b1, k);
+                    }
+                    count(g, b1, b2);
+                }
             }
             int rank = 0;
             for (int g = 0; g < a.groups; ++g) {
@@ -246,7 +278,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int e = j * 32 + lane;
-                if (e < a.E && !(kept >> (e / a.group_size) & 1)) key[j] = 0;
+                if (e < a.E && !(kept >> a.by_size(e) & 1)) key[j] = 0;
             }
         }
         int pick = -1;
@@ -292,14 +324,14 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
                         if (x[j] > -CUDART_INF_F) denominator += exp((double)x[j] - (double)top);
                     denominator = warp_sum(denominator);
                 }
-                double v = -CUDART_INF;
+                uint64_t v = 0;
                 if (lane < n) {
                     const double l = to_f32(row[pick]);
-                    v = (SOFTMAX ? exp(l - (double)top) / denominator : sigmoid(l)) + (double)a.bias[pick];
+                    v = ordered((SOFTMAX ? exp(l - (double)top) / denominator : sigmoid(l)) + (double)a.bias[pick]);
                 }
                 int rank = 0;
                 for (int o = 0; o < n; ++o) {
-                    const double w = __shfl_sync(kAll, v, o);
+                    const uint64_t w = __shfl_sync(kAll, v, o);
                     const int e = __shfl_sync(kAll, pick, o);
                     rank += before(w, e, v, pick);
                 }
@@ -386,6 +418,7 @@ extern "C" rfp2_status rfp2_moe_route(const void *logits, int dtype, int64_t T, 
     a.keep = (int)keep;
     a.group_top = (int)group_top;
     a.group_size = (int)(E / groups);
+    a.by_size = FastDiv((uint32_t)(E / groups));
     a.renormalise = renormalise;
     a.scale = scale;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -70,7 +70,8 @@ def test_ties_go_to_the_lowest_index(g, scoring, groups):
         flat = torch.zeros((3, E), device="cuda")
         few = torch.randint(0, 3, (40, E), device="cuda", generator=torch.Generator(device="cuda").manual_seed(3)).float()
         for bias in (None, np.zeros(E, np.float32), np.full(E, 0.25, np.float32)):
-            for x in (flat, few, logits(60, E, "bfloat16", 4)):
+            zeros = torch.where(few > 0, 0.0, -0.0)   # both zeros are one value
+            for x in (flat, few, zeros, logits(60, E, "bfloat16", 4)):
                 check(g, x, 8, bias, **kw)
 
 
