@@ -12,6 +12,7 @@ namespace rfp2 {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kResident = 4;  // CTAs of an SM
 
 struct CombineArgs {
     const void *y, *residual;
@@ -42,73 +43,87 @@ struct Held {
     }
 };
 
-// C runs a thread, a.lanes apart.
+// Weights of up to N slots, and which of them are read.
+template <int N>
+struct Slots {
+    float w[N];
+    int id[N];
+    RFP2_DEV void load(const CombineArgs &a, int64_t t, int j0) {
+        const float *weights = a.weights + t * a.top_k + j0;
+        const int32_t *ids = a.ids ? a.ids + t * a.top_k + j0 : nullptr;
+        if (N == 8 && a.eights) {
+            const float4 w0 = reinterpret_cast<const float4 *>(weights)[0], w1 = reinterpret_cast<const float4 *>(weights)[1];
+            const float ws[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+            int4 i0 = make_int4(0, 0, 0, 0), i1 = i0;
+            if (ids) i0 = reinterpret_cast<const int4 *>(ids)[0], i1 = reinterpret_cast<const int4 *>(ids)[1];
+            const int is[8] = {i0.x, i0.y, i0.z, i0.w, i1.x, i1.y, i1.z, i1.w};
+#pragma unroll
+            for (int j = 0; j < N; ++j) w[j] = ws[j & 7], id[j] = is[j & 7];
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const bool in = j0 + j < a.top_k;
+                w[j] = in ? weights[j] : 0.0f;
+                id[j] = !in ? -1 : ids ? ids[j] : 0;
+            }
+        }
+    }
+};
+
+// C runs a thread, a.lanes apart, of one token after another: the next one's slots are fetched while this one's
+// rows are on their way.
 template <typename Ty, typename To, int V, int C>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const CombineArgs a) {
     constexpr int kAhead = 8 / C;  // slots whose loads travel together
     pdl_wait();
     pdl_launch_dependents();
     const int tt = (int)a.by_lanes(threadIdx.x);
-    const int64_t t = (int64_t)blockIdx.x * a.tokens + tt;
+    int64_t t = (int64_t)blockIdx.x * a.tokens + tt;
     if (tt >= a.tokens || t >= a.T) return;
     const int r0 = blockIdx.y * a.lanes * C + (threadIdx.x - tt * a.lanes);
-    const Ty *y = static_cast<const Ty *>(a.y) + t * a.yt;
-    const float *weights = a.weights + t * a.top_k;
-    const int32_t *ids = a.ids ? a.ids + t * a.top_k : nullptr;
-    float sum[C][V];
+    const int64_t step = (int64_t)gridDim.x * a.tokens;
+    Slots<kAhead> slots;
+    slots.load(a, t, 0);
+    for (; t < a.T; t += step) {
+        const Ty *y = static_cast<const Ty *>(a.y) + t * a.yt;
+        Held<To, V> rest[C];
+        float sum[C][V];
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+        for (int c = 0; c < C; ++c) {
+            if (a.residual && r0 + c * a.lanes < a.runs)
+                rest[c].load(static_cast<const To *>(a.residual) + t * a.rs + (int64_t)(r0 + c * a.lanes) * V);
 #pragma unroll
-        for (int e = 0; e < V; ++e) sum[c][e] = 0.0f;
-    Held<To, V> rest[C];
+            for (int e = 0; e < V; ++e) sum[c][e] = 0.0f;
+        }
+        for (int j0 = 0; j0 < a.top_k; j0 += kAhead) {
+            Held<Ty, V> v[kAhead][C];
+            const Slots<kAhead> now = slots;
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-        if (a.residual && r0 + c * a.lanes < a.runs)
-            rest[c].load(static_cast<const To *>(a.residual) + t * a.rs + (int64_t)(r0 + c * a.lanes) * V);
-    for (int j0 = 0; j0 < a.top_k; j0 += kAhead) {
-        Held<Ty, V> v[kAhead][C];
-        float w[kAhead];
-        bool read[kAhead];
-        if (kAhead == 8 && a.eights) {
-            const float4 *fw = reinterpret_cast<const float4 *>(weights + j0);
-            const float4 w0 = fw[0], w1 = fw[1];
-            const float ws[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-            int4 i0 = make_int4(0, 0, 0, 0), i1 = i0;
-            if (ids) {
-                i0 = reinterpret_cast<const int4 *>(ids + j0)[0];
-                i1 = reinterpret_cast<const int4 *>(ids + j0)[1];
-            }
-            const int is[8] = {i0.x, i0.y, i0.z, i0.w, i1.x, i1.y, i1.z, i1.w};
+            for (int j = 0; j < kAhead; ++j)
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) w[j] = ws[j & 7], read[j] = is[j & 7] >= 0;
-        } else {
+                for (int c = 0; c < C; ++c)
+                    if (now.id[j] >= 0 && r0 + c * a.lanes < a.runs)
+                        v[j][c].load(y + (j0 + j) * a.yj + (int64_t)(r0 + c * a.lanes) * V);
+            if (j0 + kAhead < a.top_k)
+                slots.load(a, t, j0 + kAhead);
+            else if (t + step < a.T)
+                slots.load(a, t + step, 0);
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                const bool in = j0 + j < a.top_k;
-                w[j] = in ? weights[j0 + j] : 0.0f;
-                read[j] = in && (!ids || ids[j0 + j] >= 0);
-            }
+            for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        sum[c][e] = fmaf(now.w[j], now.id[j] >= 0 ? to_f32(v[j][c].v[e]) : 0.0f, sum[c][e]);
         }
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j)
+        for (int c = 0; c < C; ++c) {
+            if (r0 + c * a.lanes >= a.runs) continue;
+            if (a.residual)
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-                if (read[j] && r0 + c * a.lanes < a.runs) v[j][c].load(y + (j0 + j) * a.yj + (int64_t)(r0 + c * a.lanes) * V);
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-#pragma unroll
-                for (int e = 0; e < V; ++e) sum[c][e] = fmaf(w[j], read[j] ? to_f32(v[j][c].v[e]) : 0.0f, sum[c][e]);
-    }
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int64_t at = (int64_t)(r0 + c * a.lanes) * V;
-        if (r0 + c * a.lanes >= a.runs) continue;
-        if (a.residual)
-#pragma unroll
-            for (int e = 0; e < V; ++e) sum[c][e] += to_f32(rest[c].v[e]);
-        store_values(static_cast<To *>(a.out) + t * a.os + at, sum[c]);
+                for (int e = 0; e < V; ++e) sum[c][e] += to_f32(rest[c].v[e]);
+            store_values(static_cast<To *>(a.out) + t * a.os + (int64_t)(r0 + c * a.lanes) * V, sum[c]);
+        }
     }
 }
 
@@ -129,7 +144,9 @@ cudaError_t launch_combine(CombineArgs &a, cudaStream_t stream) {
     a.by_lanes = FastDiv((uint32_t)a.lanes);
     const int64_t ctas = (a.T + a.tokens - 1) / a.tokens, parts = (a.runs + (int64_t)a.lanes * each - 1) / ((int64_t)a.lanes * each);
     if (parts > 65535) return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)ctas, (unsigned)parts);
+    // as many CTAs as the SMs hold, so that most tokens have their slots fetched beforehand
+    const int64_t held = std::max<int64_t>(1, (int64_t)kResident * sm_count(current_device()) / parts);
+    const dim3 grid((unsigned)std::min(ctas, held), (unsigned)parts);
     return launch(wide ? combine_kernel<Ty, To, W, 1> : combine_kernel<Ty, To, 1, C>, grid, dim3(kThreads), 0, stream, true, a);
 }
 

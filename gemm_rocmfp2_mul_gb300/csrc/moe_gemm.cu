@@ -68,7 +68,9 @@ RFP2_DEV int2 scan_pairs(int2 v, int2 *sums, int2 &total) {
 }
 
 // Each warp counts a stretch of the pairs by expert in a row of shared memory of its own, the rows become
-// places, and each warp puts its stretch there: every pair's place is a function of the ids alone.
+// places, and each warp puts its stretch there.  Lanes that meet in one expert are in no fixed order, which
+// changes nothing: a column's sums do not depend on its place in a tile.  (Ranks by matching lanes, in a
+// fixed order, took 35 us of 16376 pairs over 256 experts.)
 __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const int32_t *__restrict__ ids, int P, int E, int warps,
                                                                Plan plan, int32_t *status) {
     extern __shared__ int count[];  // [warps][E + 1], the last for pairs without an expert
@@ -82,17 +84,26 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const int32_t *__
     const int chunk = ((P + warps - 1) / warps + 31) / 32 * 32;
     const int from = min(P, warp * chunk), to = warp < warps ? min(P, from + chunk) : from;
     int *mine = count + warp * bins;
-    const auto bin_of = [&](int p) {
-        const int e = ids[p];
-        return e >= 0 && e < E ? e : E;
+    // the ids are fetched eight words at a time, all on their way together
+    constexpr int kAhead = 8;
+    int id[kAhead];
+    const auto fetch = [&](int p0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int p = p0 + 32 * i + lane;
+            id[i] = p < to ? ids[p] : 0;
+        }
     };
-    for (int p0 = from; p0 < to; p0 += 32) {
-        const int p = p0 + lane;
-        const int b = p < to ? bin_of(p) : -1;
-        if (b == E && ids[p] != -1) record_status(status, RFP2_EBADID);
-        const unsigned same = __match_any_sync(0xffffffffu, b);
-        if (b >= 0 && lane == __ffs(same) - 1) mine[b] += __popc(same);
-        __syncwarp();
+    for (int p0 = from; p0 < to; p0 += 32 * kAhead) {
+        fetch(p0);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (p0 + 32 * i >= to) break;
+            const bool in = p0 + 32 * i + lane < to;
+            const int b = !in ? -1 : (unsigned)id[i] < (unsigned)E ? id[i] : E;
+            if (b == E && id[i] != -1) record_status(status, RFP2_EBADID);
+            if (b >= 0) atomicAdd(&mine[b], 1);
+        }
     }
     __syncthreads();
     // thread e: the places of expert e's pairs and tiles
@@ -126,14 +137,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const int32_t *__
         }
     }
     __syncthreads();
-    for (int p0 = from; p0 < to; p0 += 32) {
-        const int p = p0 + lane;
-        const int b = p < to ? bin_of(p) : -1;
-        const unsigned same = __match_any_sync(0xffffffffu, b);
-        if (b >= 0) plan.pairs[mine[b] + __popc(same & ((1u << lane) - 1))] = p;
-        __syncwarp();
-        if (b >= 0 && lane == __ffs(same) - 1) mine[b] += __popc(same);
-        __syncwarp();
+    for (int p0 = from; p0 < to; p0 += 32 * kAhead) {
+        if (to - from > 32 * kAhead) fetch(p0);  // a short stretch is still there
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (p0 + 32 * i >= to) break;
+            const int p = p0 + 32 * i + lane;
+            const int b = p >= to ? -1 : (unsigned)id[i] < (unsigned)E ? id[i] : E;
+            if (b >= 0) plan.pairs[atomicAdd(&mine[b], 1)] = p;
+        }
     }
 }
 
@@ -201,8 +213,17 @@ RFP2_DEV bool mbar_test(uint64_t *bar, uint32_t parity) {
 // mbar_wait, which reads the GPU's timer once a probe has failed, after probes without it.
 RFP2_DEV bool wait_for(uint64_t *bar, uint32_t parity) {
 #pragma unroll 1
-    for (int i = 0; i < 1024; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
+    for (int i = 0; i < 64; ++i) {
+        uint32_t ok;  // sleeps for up to 20 us at a time: probes would take the decoders' issue slots
+        asm volatile(
+            "{\n .reg .pred p;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+    }
     return mbar_wait(bar, parity);
 }
 
