@@ -660,7 +660,8 @@ def rfp2_rms_norm(x, weight, eps=1e-6, residual=None, want="y", dtype=None, y=No
         q = _empty(x.shape, torch.int8, x) if q is None else q
         d = _empty((*x.shape[:-1], x.shape[-1] // 32), torch.float32, x) if d is None else d
     if residual is None:
-        total = None
+        if total is not None:
+            raise ValueError("total is x + residual: there is no residual")
     elif total is None:
         total = _empty(x.shape, x.dtype, x)
     rc = (_native or _binding()).rms_norm(x, weight, eps, residual, total, y, q, d)

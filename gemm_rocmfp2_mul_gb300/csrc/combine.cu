@@ -143,7 +143,6 @@ cudaError_t launch_combine(CombineArgs &a, cudaStream_t stream) {
     a.tokens = kThreads / a.lanes;
     a.by_lanes = FastDiv((uint32_t)a.lanes);
     const int64_t ctas = (a.T + a.tokens - 1) / a.tokens, parts = (a.runs + (int64_t)a.lanes * each - 1) / ((int64_t)a.lanes * each);
-    if (parts > 65535) return cudaErrorInvalidValue;
     // as many CTAs as the SMs hold, so that most tokens have their slots fetched beforehand
     const int64_t held = std::max<int64_t>(1, (int64_t)kResident * sm_count(current_device()) / parts);
     const dim3 grid((unsigned)std::min(ctas, held), (unsigned)parts);

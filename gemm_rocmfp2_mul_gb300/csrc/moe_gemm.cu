@@ -16,7 +16,7 @@
 namespace rfp2 {
 namespace {
 
-constexpr int kTileTokens = 256;
+constexpr int kTileTokens = 256;  // of a tile at most, and 64 at least where tiles are narrow
 constexpr int kMaxExperts = 1024;
 constexpr int64_t kMaxPairs = 1 << 24;
 constexpr int kPlanThreads = 1024;
@@ -30,7 +30,7 @@ struct Plan {
 };
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
-int64_t most_tiles(int64_t P, int64_t E) { return P / kTileTokens + std::min(P, E); }
+int64_t most_tiles(int64_t P, int64_t E) { return P / 64 + std::min(P, E); }  // of any width
 size_t plan_bytes(int64_t P, int64_t E) {
     return 256 + align256((size_t)P * 4) + align256((size_t)most_tiles(P, E) * 16);
 }
@@ -72,7 +72,7 @@ RFP2_DEV int2 scan_pairs(int2 v, int2 *sums, int2 &total) {
 // changes nothing: a column's sums do not depend on its place in a tile.  (Ranks by matching lanes, in a
 // fixed order, took 35 us of 16376 pairs over 256 experts.)
 __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const int32_t *__restrict__ ids, int P, int E, int warps,
-                                                               Plan plan, int32_t *status) {
+                                                               int tile, Plan plan, int32_t *status) {
     extern __shared__ int count[];  // [warps][E + 1], the last for pairs without an expert
     __shared__ int2 sums[33];
     pdl_wait();
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const int32_t *__
     int n = 0;
     if (tid < E)
         for (int w = 0; w < warps; ++w) n += count[w * bins + tid];
-    const int tiles = (n + kTileTokens - 1) / kTileTokens;
+    const int tiles = (n + tile - 1) / tile;
     int2 total;
     const int2 at = scan_pairs(make_int2(n, tiles), sums, total);
     if (tid < E) {
@@ -180,9 +180,6 @@ constexpr int kRows = 128;   // weight rows of a CTA (TMEM lanes), 256 of a pair
 constexpr int kStep = 64;    // K of a stage: one 128-byte swizzle row
 constexpr int kUmmaK = 16;   // K of an instruction
 constexpr int kABytes = kRows * kStep * 2;
-constexpr int kBBytes = kTileTokens / 2 * kStep * 2;
-constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kStages = 5;
 constexpr int kBoxRowBytes = 80;  // eight 10-byte blocks: four steps of K
 constexpr int kBoxBytes = kRows * kBoxRowBytes;
 constexpr int kBoxes = 4;
@@ -191,11 +188,21 @@ constexpr int kGroupWarps = 4;  // a weight row a thread
 constexpr int kDecodeWarps = kGroups * kGroupWarps;
 constexpr int kLoadWarps = 4;  // gather the tokens: warp i of them steps i, i + 4, ...
 constexpr int kThreads = (6 + kDecodeWarps + kLoadWarps) * 32;
-constexpr int kLoads = kTileTokens / 2 / 4;  // copies of a lane for a step, at most
 constexpr uint32_t kTmemCols = 512;  // two accumulators of 256 columns
-constexpr size_t kRingOff = (size_t)kStages * kStageBytes;
-constexpr size_t kBarOff = kRingOff + (size_t)kBoxes * kBoxBytes;
-constexpr size_t kSmemBytes = 1024 + kBarOff + 256;
+// By the most tokens of a tile: a stage is a slice of 64 of K of both operands, and a narrow tile leaves room for
+// more of them.  A stage's way around (tokens' loads, both SMs' arrivals, MMAs, their commit) takes about 2500
+// cycles however narrow it is, so that the number of stages sets the pace there.
+template <int TILE>
+struct Cfg {
+    static constexpr int kBBytes = TILE / 2 * kStep * 2;
+    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kStages = TILE == 64 ? 9 : TILE == 128 ? 7 : 5;
+    static constexpr size_t kRingOff = (size_t)kStages * kStageBytes;
+    static constexpr size_t kBarOff = kRingOff + (size_t)kBoxes * kBoxBytes;
+    static constexpr size_t kSmemBytes = 1024 + kBarOff + 256;
+    static constexpr int kLoads = TILE / 2 / 4;  // copies of a lane for a step, at most
+    static_assert(kSmemBytes <= 227 * 1024 && (2 * kStages + 4 + 2 * kBoxes) * 8 + 8 <= 256, "shared memory");
+};
 
 // Has the phase with `parity` completed?  (No waiting.)
 RFP2_DEV bool mbar_test(uint64_t *bar, uint32_t parity) {
@@ -291,15 +298,16 @@ RFP2_DEV void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 //                 register a token.
 // Gated: lanes 0-15 of a warp have gate rows, lanes 16-31 the up rows that go with them, and a shuffle brings
 // the two together.  Every wait is bounded; tensor memory is always freed.
-template <int ACT>
+template <int ACT, int TILE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap wmap, const GemmArgs a, int32_t *status) {
     constexpr bool kGated = ACT != RFP2_ACT_NONE;
+    constexpr int kStages = Cfg<TILE>::kStages, kStageBytes = Cfg<TILE>::kStageBytes, kLoads = Cfg<TILE>::kLoads;
     constexpr int kOut = kGated ? kRows / 2 : kRows;  // outputs of a CTA's rows
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *ring = smem + kRingOff;
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kBarOff);  // (even CTA) a stage of both CTAs is there
+    uint8_t *ring = smem + Cfg<TILE>::kRingOff;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg<TILE>::kBarOff);  // (even CTA) a stage of both CTAs is there
     uint64_t *empty = full + kStages;       // its MMAs are done
     uint64_t *accf = empty + kStages;       // [2] an accumulator is complete
     uint64_t *acce = accf + 2;              // [2] (even CTA) it has been read back
@@ -582,6 +590,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 using ProductFn = void (*)(CUtensorMap, GemmArgs, int32_t *);
 
+struct Product {
+    ProductFn fn;
+    size_t smem;
+};
+template <int TILE>
+Product product_of(int activation) {
+    return {activation == RFP2_ACT_NONE   ? product_kernel<RFP2_ACT_NONE, TILE>
+            : activation == RFP2_ACT_SILU ? product_kernel<RFP2_ACT_SILU, TILE>
+                                          : product_kernel<RFP2_ACT_GELU, TILE>,
+            Cfg<TILE>::kSmemBytes};
+}
+Product product_of(int activation, int tile) {
+    return tile == 64 ? product_of<64>(activation) : tile == 128 ? product_of<128>(activation) : product_of<256>(activation);
+}
+
+// Tokens of a tile at most: an expert that has more has its weights decoded again, so the mean (of P pairs over E
+// experts) fits in once or twice.  Against tiles of up to 256 for all: 16 tokens to 8 of 256 experts 39.5 -> 38.4
+// us, 2047 tokens 281 -> 277.
+int tile_of(int64_t P, int64_t E) { return P <= 32 * E ? 64 : P <= 64 * E ? 128 : 256; }
+
 // Sets the kernels up on a device; returns how many pairs it holds at a time (0: an error).
 int pairs_of(int dev) {
     static std::mutex mu;
@@ -589,16 +617,16 @@ int pairs_of(int dev) {
     std::lock_guard<std::mutex> lock(mu);
     if (dev < 64 && held[dev]) return held[dev];
     int pairs = 0;
-    const ProductFn kinds[] = {product_kernel<RFP2_ACT_NONE>, product_kernel<RFP2_ACT_SILU>, product_kernel<RFP2_ACT_GELU>};
     if (set_smem_limit(plan_kernel, 32 * (kMaxExperts + 1) * 4) != cudaSuccess) return 0;
-    for (const ProductFn k : kinds) {
-        if (set_smem_limit(k, (int)kSmemBytes) != cudaSuccess) return 0;
+    for (int i = 0; i < 9; ++i) {
+        const Product p = product_of(i % 3, 64 << i / 3);
+        if (set_smem_limit(p.fn, (int)p.smem) != cudaSuccess) return 0;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2);
         cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = kSmemBytes;
+        cfg.dynamicSmemBytes = p.smem;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void *>(k), &cfg) != cudaSuccess || n <= 0) return 0;
+        if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void *>(p.fn), &cfg) != cudaSuccess || n <= 0) return 0;
         pairs = pairs ? std::min(pairs, n) : n;
     }
     if (dev < 64) held[dev] = pairs;
@@ -659,15 +687,13 @@ extern "C" rfp2_status rfp2_moe_gemm(const uint8_t *W, int64_t E, int64_t M, int
     a.by_top_k = FastDiv((uint32_t)top_k);
     a.each = each;
     a.out = (int)out;
-    const int warps = (int)std::min<int64_t>(32, (P + 31) / 32);
+    const int tile = tile_of(P, E), warps = (int)std::min<int64_t>(32, (P + 31) / 32);
     cudaError_t e = launch(plan_kernel, dim3(1), dim3(kPlanThreads), (size_t)warps * (E + 1) * 4, s, true, ids, (int)P,
-                           (int)E, warps, a.plan, dev_status);
+                           (int)E, warps, tile, a.plan, dev_status);
     if (e != cudaSuccess) return RFP2_ECUDA;
     // at most a pair for every unit there can be
     const int64_t blocks = (out + (gated ? kRows : 2 * kRows) - 1) / (gated ? kRows : 2 * kRows);
     const dim3 grid((unsigned)(2 * std::min<int64_t>(pairs, most_tiles(P, E) * blocks)));
-    const ProductFn k = activation == RFP2_ACT_NONE   ? product_kernel<RFP2_ACT_NONE>
-                        : activation == RFP2_ACT_SILU ? product_kernel<RFP2_ACT_SILU>
-                                                      : product_kernel<RFP2_ACT_GELU>;
-    return from_cuda(launch(k, grid, dim3(kThreads), kSmemBytes, s, true, wmap, a, dev_status));
+    const Product k = product_of(activation, tile);
+    return from_cuda(launch(k.fn, grid, dim3(kThreads), k.smem, s, true, wmap, a, dev_status));
 }

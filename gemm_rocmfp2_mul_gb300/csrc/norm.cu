@@ -6,7 +6,7 @@
 // A row belongs to a CTA, or to a warp where it is short; it stays in registers between its sum and its
 // outputs.  Q8 codes are those of the formula, not of its fp32 roundings: code = round-half-away(127 u / U)
 // with u = |s weight| and U a block's largest, in which r drops out.  In fp32 the quotient is off by
-// 4e-7 of itself at most; where a half-integer is that near, u and U, exact in fp64 (48 bits), decide.
+// 4e-7 of itself at most; where a half-integer is that near, u and U as integers (48 bits) decide.
 #include <algorithm>
 #include <type_traits>
 
@@ -107,31 +107,51 @@ RFP2_DEV float over_row(float v, int warps, float *part) {
     return v;
 }
 
-// Is 254 u >= m U?  Exactly: u and U have 48 bits, the factors 8, and what a product loses is added back.
-RFP2_DEV bool reaches(double u, double m, double U) {
-    const double p = 254.0 * u, q = m * U;
-    return (p - q) + (fma(254.0, u, -p) - fma(m, U, -q)) >= 0.0;
+// |s w| exactly, as an integer in the same order: 48 bits of significand, normalised, below the exponent.
+RFP2_DEV uint64_t product_key(float s, float w) {
+    const auto part = [](float v, uint32_t &m) {
+        const uint32_t b = __float_as_uint(v), e = b >> 23 & 255u;
+        m = (b & 0x7FFFFFu) | (e ? 0x800000u : 0u);
+        return (int)max(e, 1u);
+    };
+    uint32_t ms, mw;
+    const int e = part(s, ms) + part(w, mw);
+    uint64_t m = (uint64_t)ms * mw;
+    if (m == 0) return 0;
+    const int up = __clzll((long long)m) - 16;
+    return (uint64_t)(e + 64 - up) << 48 | (m << up & 0xFFFFFFFFFFFFull);
 }
 
-// The codes of the values s w of a block that 32 / V neighbouring lanes share, where they are `near` a border;
-// right but for one step before, unless the block is `tiny`.
+// Is 254 u >= c U, for keys u <= U of products and 1 <= c <= 255?
+RFP2_DEV bool reaches(uint64_t u, int c, uint64_t U) {
+    const int down = (int)(U >> 48) - (int)(u >> 48);
+    if (u == 0 || down > 8) return false;  // 254 u < 2^56 <= 2^47 2^9
+    const auto significand = [](uint64_t k) { return k & 0xFFFFFFFFFFFFull; };
+    return 254u * significand(u) >= ((uint64_t)c * significand(U)) << down;
+}
+
+// The codes of the values s w of a block that 32 / V neighbouring lanes share, where they are `near` a border.
+// In integers: fp64, in which a product is exact too, has two lanes an SM here, and a decode step's few rows
+// waited 2 us for it.
 template <int V>
-__device__ __noinline__ void exact_codes(const float *s, const float *w, int8_t *code, bool near, bool tiny) {
-    double U = 0.0;
+__device__ __noinline__ void exact_codes(const float *s, const float *w, int8_t *code, bool near) {
+    uint64_t U = 0;
 #pragma unroll 1
-    for (int e = 0; e < V; ++e) U = fmax(U, fabs((double)s[e] * (double)w[e]));
+    for (int e = 0; e < V; ++e) U = max(U, product_key(s[e], w[e]));
 #pragma unroll
-    for (int off = 1; off < 32 / V; off <<= 1) U = fmax(U, __shfl_xor_sync(0xffffffffu, U, off));
-    if (!near || !(U > 0.0 && U < CUDART_INF)) return;
+    for (int off = 1; off < 32 / V; off <<= 1) U = max(U, __shfl_xor_sync(0xffffffffu, U, off));
+    if (!near || U == 0) return;
+    const auto size = [](uint64_t k) { return (float)(k & 0xFFFFFFFFFFFFull); };
 #pragma unroll 1
     for (int e = 0; e < V; ++e) {
-        const double v = (double)s[e] * (double)w[e], u = fabs(v);
-        double k = tiny ? floor(127.0 * (u / U) + 0.5) : (double)abs(code[e]);
-        if (reaches(u, 2.0 * k + 1.0, U))
-            k += 1.0;
-        else if (!reaches(u, 2.0 * k - 1.0, U))
-            k -= 1.0;
-        code[e] = (int8_t)(v < 0.0 ? -(int)k : (int)k);
+        const uint64_t u = product_key(s[e], w[e]);
+        const int down = min((int)(U >> 48) - (int)(u >> 48), 32);
+        int k = u ? (int)(127.0f * (size(u) / size(U)) * __uint_as_float((127u - down) << 23) + 0.5f) : 0;
+        if (k < 127 && reaches(u, 2 * k + 1, U))
+            ++k;
+        else if (k > 0 && !reaches(u, 2 * k - 1, U))
+            --k;
+        code[e] = (int8_t)((__float_as_uint(s[e]) ^ __float_as_uint(w[e])) >> 31 ? -k : k);
     }
 }
 
@@ -163,7 +183,7 @@ RFP2_DEV float block_codes(const float (&s)[V], const float (&w)[V], const float
         int8_t k[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) cs[e] = s[e], cw[e] = w[e], k[e] = (int8_t)code[e];
-        exact_codes<V>(cs, cw, k, near, tiny);
+        exact_codes<V>(cs, cw, k, near);
 #pragma unroll
         for (int e = 0; e < V; ++e) code[e] = (uint8_t)k[e];
     }

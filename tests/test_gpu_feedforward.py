@@ -86,6 +86,40 @@ def test_two_graphs_share_a_workspace(g, example):
         assert torch.equal(a, b)
 
 
+def test_offsets_past_32_bits(g):
+    """Arrays of more than 2^32 bytes, and of more than 2^31 values: their last rows, against the same rows alone."""
+    import torch
+    r = torch.Generator(device="cuda").manual_seed(4)
+    K, T = 32768, 66000
+    x = torch.zeros((T, K), dtype=torch.bfloat16, device="cuda")
+    x[-3:] = torch.randn((3, K), generator=r, device="cuda").bfloat16()
+    w = 1.0 + 0.1 * torch.randn(K, generator=r, device="cuda")
+    far, near = g.rfp2_rms_norm(x, w, residual=x, want="both"), g.rfp2_rms_norm(x[-3:], w, residual=x[-3:], want="both")
+    for a, b in zip(far, near):   # (few rows go by another variant: the last bit of a sum may differ)
+        assert a[-3:].float().isfinite().all() and not a[:-3].any()
+        assert float((a[-3:].float() - b.float()).abs().max()) <= 2.0 ** -7 * float(b.float().abs().max())
+    y = x.view(T // 8, 8, K)
+    weights = torch.ones((T // 8, 8), device="cuda")
+    assert torch.equal(g.rfp2_moe_combine(y, weights)[-1:], g.rfp2_moe_combine(y[-1:], weights[-1:]))
+    del far, near, y
+    X = x[:, :16384].reshape(-1, 16384)[: 2 * T // 2].repeat(2, 1)   # 132000 rows of 32 KB
+    ids = torch.zeros((X.shape[0], 1), dtype=torch.int32, device="cuda")
+    W = torch.randint(0, 256, (1, 32, 512, 10), generator=r, device="cuda", dtype=torch.uint8)
+    W[..., 8:] %= 24
+    out = g.rfp2_moe_gemm(W, 1, 32, 16384, ids, X)
+    alone = g.rfp2_moe_gemm(W, 1, 32, 16384, ids[-3:], X[-3:].contiguous())
+    assert torch.equal(out[-3:], alone) and bool(alone.any()) and not out[T: -3].any()
+    # the last expert's weights, 5 GB in
+    E, M = 4, 262144
+    W = torch.zeros((E, M, 512, 10), dtype=torch.uint8, device="cuda")
+    W[-1, -64:] = torch.randint(0, 256, (64, 512, 10), generator=r, device="cuda", dtype=torch.uint8)
+    W[-1, -64:, :, 8:] %= 24
+    X, ids = X[-3:].contiguous(), torch.full((3, 1), E - 1, dtype=torch.int32, device="cuda")
+    out = g.rfp2_moe_gemm(W, E, M, 16384, ids, X)
+    alone = g.rfp2_moe_gemm(W[-1, -64:].contiguous()[None], 1, 64, 16384, torch.zeros_like(ids), X)
+    assert torch.equal(out[..., -64:], alone) and not out[..., :-64].any()
+
+
 def test_tensors_of_another_device_are_refused(g):
     """As with the other operators: without memory, so that no call below can come to a launch."""
     import torch

@@ -181,7 +181,7 @@ def test_nothing_to_do_and_refusals(g):
     for call in (lambda: g.rfp2_rms_norm(x, w[:32]), lambda: g.rfp2_rms_norm(x, w, residual=x[:2]),
                  lambda: g.rfp2_rms_norm(x, w, residual=x.half()), lambda: g.rfp2_rms_norm(x, w, want="z"),
                  lambda: g.rfp2_rms_norm(x[:, ::2], w[:32]), lambda: g.rfp2_rms_norm(x, w, want="q8", q=torch.empty((4, 32), dtype=torch.int8, device="cuda")),
-                 lambda: g.rfp2_rms_norm(x[0], w)):
+                 lambda: g.rfp2_rms_norm(x[0], w), lambda: g.rfp2_rms_norm(x, w, total=x.clone())):
         with pytest.raises(ValueError):
             call()
     for call in (lambda: g.rfp2_rms_norm(x.double(), w), lambda: g.rfp2_rms_norm(x.cpu(), w)):

@@ -52,7 +52,8 @@ def test_choice(g, E, top_k, scoring, biased):
 @pytest.mark.parametrize("biased", [False, True])
 @pytest.mark.parametrize("group_top", [1, 2])
 @pytest.mark.parametrize("E,groups,keep,top_k", [(256, 8, 4, 8), (256, 8, 1, 8), (64, 8, 3, 6), (60, 4, 2, 4), (160, 5, 5, 3),
-                                                 (32, 32, 7, 7), (512, 16, 4, 12), (96, 3, 2, 8)])
+                                                 (32, 32, 7, 7), (512, 16, 4, 12), (96, 3, 2, 8), (256, 2, 1, 4), (256, 4, 3, 5), (512, 4, 2, 8),
+                                                 (512, 8, 5, 8), (1024, 8, 3, 5), (768, 8, 2, 4)])
 def test_groups(g, E, groups, keep, top_k, group_top, biased, scoring):
     bias = 0.1 * np.random.default_rng(2).standard_normal(E).astype(np.float32) if biased else None
     for dtype, masked in (("float32", 0.0), ("bfloat16", 0.6), ("float32", 0.97)):
