@@ -6,9 +6,9 @@
 //  2. the product on the tensor cores: units of a tile and 256 weight rows (128 gate rows and the 128 up rows
 //     that go with them).
 //
-// Measured (one GB300, GPU time a call): 8192 tokens to 2 of 8 experts of 14336 x 4096, gated: 1363 us, 1.41
-// PFLOP/s (0.73 of cuBLAS's burst rate, which has no weights to decode; 0.77 is what rfp2_gemm has); 2047 to 8
-// of 256 of 1536 x 2048, gated: 277 us; 16 to 8 of 256 of 768 x 2048: 38 us.  Wide tiles are bound by the
+// Measured (one GB300, GPU time a call): 8192 tokens to 2 of 8 experts of 14336 x 4096, gated: 1287 us, 1.50
+// PFLOP/s (0.78 of cuBLAS's burst rate, which has no weights to decode; 0.77 is what rfp2_gemm has); 2047 to 8
+// of 256 of 1536 x 2048, gated: 260 us; 16 to 8 of 256 of 768 x 2048: 38 us.  Wide tiles are bound by the
 // shared-memory port, narrow ones by a stage's way around and by the decoding.
 #include <algorithm>
 #include <mutex>
@@ -166,8 +166,8 @@ struct GemmArgs {
 };
 
 // Both activations are gate / (1 + exp(-v)): v = gate, or twice tanh's argument.  The fast exponential and quotient
-// are off by 2^-21 (2 + |v|) of the result, which is rounded to bf16; exact ones are twice an output's
-// instructions, and the epilogue of a narrow tile is as long as its products.
+// are off by 2^-21 (2 + |v|) of the result, which is rounded to bf16; with exact ones the epilogue held the
+// MMAs up (1363 -> 1287 us of the case above, 277 -> 260).
 RFP2_DEV float activated(int activation, float gate, float up) {
     const float v = activation == RFP2_ACT_SILU ? gate : 1.5957691216057308f * fmaf(0.044715f * gate * gate, gate, gate);
     return __fdividef(gate, 1.0f + __expf(-v)) * up;

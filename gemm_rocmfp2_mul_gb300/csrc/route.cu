@@ -11,9 +11,9 @@
 // order by values in fp64, one of them a lane.  What that cannot settle (a run of more than a warp's
 // lanes; groups too near to tell apart) is done by fp64 values of all experts.
 //
-// Bound by instructions, not by the logits' bytes: about 1700 a token with a bias, groups and eight picks.
-// Measured (one GB300, GPU time a call): 16384 x 256, sigmoid, bias, 4 of 8 groups, 8 experts: 44 us; without
-// groups and bias 19; 4 x 256 2.6 us.
+// Bound by instructions, not by the logits' bytes: about 1500 a token with a bias, groups and eight picks.
+// Measured (one GB300, GPU time a call): 16384 x 256, sigmoid, bias, 4 of 8 groups, 8 experts: 32 us; 4 x 256 2.7
+// us.
 #include <algorithm>
 
 #include "activation.cuh"
@@ -89,7 +89,7 @@ RFP2_DEV double unordered(uint64_t k) {
 // What experts are chosen by, in fp64, for rows with near ties that fp32 cannot settle: values[e] is the ordered
 // score, with the bias if there is one.
 template <typename T, bool SOFTMAX>
-RFP2_DEV void exact_values(const RouteArgs &a, const T *x, uint64_t *values, int lane) {
+__device__ __noinline__ void exact_values(const RouteArgs &a, const T *x, uint64_t *values, int lane) {
     double top = 0.0, total = 1.0;
     if (SOFTMAX) {
         float m = -CUDART_INF_F;
@@ -98,13 +98,12 @@ RFP2_DEV void exact_values(const RouteArgs &a, const T *x, uint64_t *values, int
         for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, off));
         top = m;
         total = 0.0;
-#pragma unroll 4
         for (int e = lane; e < a.E; e += 32)
             if (to_f32(x[e]) > -CUDART_INF_F) total += exp((double)to_f32(x[e]) - top);
         total = warp_sum(total);
     }
     __syncwarp();
-#pragma unroll 4
+#pragma unroll 2
     for (int e = lane; e < a.E; e += 32) {
         const double l = to_f32(x[e]);
         double v = SOFTMAX ? exp(l - top) / total : sigmoid(l);
@@ -184,9 +183,10 @@ __device__ __noinline__ int choose_exactly(const RouteArgs &a, const T *x, uint6
     return pick;
 }
 
-// V experts a lane.
+// V experts a lane.  (The arguments stay in constant memory although the functions above take their address: from
+// a copy on the stack the picks of a few tokens took half as long again.)
 template <typename T, int V, bool SOFTMAX>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ RouteArgs a) {
     extern __shared__ uint64_t values[];  // [kWarps][E], of rows that need them
     pdl_wait();
     pdl_launch_dependents();
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
             if constexpr (V >= 8) {
                 // The lanes' values fall into eight slots of whole groups or whole parts of them: all slots are
                 // reduced at once, half of them handed to the other half of the lanes at each step (16384 rows of
-                // 256 experts in 8 groups: 47.5 us with two redux a group, 32 like this).
+                // 256 experts in 8 groups: 47.5 us with two redux a group, 44 like this).
                 if (a.E == V * 32 && a.groups <= 8 && (a.groups & (a.groups - 1)) == 0) {
                     counted = true;
                     uint32_t b1[8], b2[8];
