@@ -6,10 +6,10 @@
 // A row belongs to a CTA, or to a warp where it is short; it stays in registers between its sum and its
 // outputs.  Q8 codes are those of the formula, not of its fp32 roundings: code = round-half-away(127 u / U)
 // with u = |s weight| and U a block's largest, in which r drops out.  In fp32 the quotient is off by
-// 4e-7 of itself at most; where a half-integer is that near, u and U as integers (48 bits) decide.
+// 5.4e-7 of itself at most (nine roundings); where a half-integer is that near, u and U as integers (48 bits) decide.
 //
 // Measured (one GB300, GPU time a call): 16384 x 5120 bf16 with a residual 97.5 us, 6.9 TB/s read and written
-// (the copy rate); 4999 x 1376 f16 to values and codes 17.7 us, bound by instructions; 4 x 4096 fp32 to
+// (the copy rate); 4999 x 1376 f16 to values and codes 16.9 us, bound by instructions; 4 x 4096 fp32 to
 // codes 3.5 us.  A persistent grid took 205 us of the first: its loop kept the addresses of a row's
 // values in registers that the values then lacked.
 #include <algorithm>
@@ -172,16 +172,17 @@ RFP2_DEV float block_codes(const float (&s)[V], const float (&w)[V], const float
     for (int e = 0; e < V; ++e) top = max(top, __float_as_uint(y[e]) & 0x7FFFFFFFu);
 #pragma unroll
     for (int off = 1; off < kLanes; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-    const float most = __uint_as_float(top), d = __fdiv_rn(most, 127.0f);
-    const bool finite = top < 0x7F800000u, any = finite && d != 0.0f, tiny = most < 0x1p-90f;
-    const float by = __fdiv_rn(127.0f, most);
-    bool near = any && tiny;
+    const float most = __uint_as_float(top), d = most * (1.0f / 127.0f);
+    const bool finite = top < 0x7F800000u, any = finite && d != 0.0f;
+    const float by = __fdividef(127.0f, most);  // (0 for the largest, infinity for the smallest: those are decided exactly)
+    bool near = any && (most < 0x1p-90f || most > 0x1p120f);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
         const float t = y[e] * by, m = t + kWhole;
         code[e] = __float_as_uint(m);
-        near |= any && fabsf(t - (m - kWhole)) >= fmaf(fabsf(t), -6e-7f, 0.5f);
+        near |= fabsf(t - (m - kWhole)) >= fmaf(fabsf(t), -6e-7f, 0.5f);
     }
+    near &= any;
     if (__any_sync(0xffffffffu, near)) {
         // (copies, so that the values themselves stay in registers)
         float cs[V], cw[V];

@@ -6,8 +6,8 @@
 // redux of order-preserving integers) and the lowest index that has it (another).
 //
 // What is chosen is what the formula in 64 bits chooses.  Without a bias values are compared by their
-// logits, exactly.  With one, fp32 values are off by `slack` at most (below), so picks further apart than
-// twice that are in their true order; a run of nearer ones is taken to its end, past top_k, and put in
+// logits, exactly.  With one, picks whose fp32 values are further apart than twice what such a value may be off by
+// (`slack` below) are in their true order; a run of nearer ones is taken to its end, past top_k, and put in
 // order by values in fp64, one of them a lane.  What that cannot settle (a run of more than a warp's
 // lanes; groups too near to tell apart) is done by fp64 values of all experts.
 //
