@@ -9,8 +9,8 @@
 // 5.4e-7 of itself at most (nine roundings); where a half-integer is that near, u and U as integers (48 bits) decide.
 //
 // Measured (one GB300, GPU time a call): 16384 x 5120 bf16 with a residual 97.5 us, 6.9 TB/s read and written
-// (the copy rate); 4999 x 1376 f16 to values and codes 16.9 us, bound by instructions; 4 x 4096 fp32 to
-// codes 3.5 us.  A persistent grid took 205 us of the first: its loop kept the addresses of a row's
+// (the copy rate); 4999 x 1376 f16 to values and codes 15.9 us, bound by instructions; 4 x 4096 fp32 to
+// codes 3.4 us.  A persistent grid took 205 us of the first: its loop kept the addresses of a row's
 // values in registers that the values then lacked.
 #include <algorithm>
 #include <type_traits>
