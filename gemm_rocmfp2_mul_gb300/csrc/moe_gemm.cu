@@ -358,6 +358,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int blocks = (a.out + 2 * kOut - 1) / (2 * kOut);
     const int units = a.plan.header[0] * blocks;
 
+    // Has a warp's wait ended well?  Each lane has a time limit of its own, and what follows is done by whole warps:
+    // at the limit the lanes leave together.
+    const auto goes_on = [&](bool there) {
+        if (__all_sync(0xffffffffu, there)) return true;
+        if (lane == 0) record_status(status, RFP2_ETIMEOUT);
+        *abort_flag = 1;
+        return false;
+    };
+
     if (warp == 0 || warp >= 7 + kDecodeWarps) {
         // ---- gathers: lane l copies chunk l % 8 of rows l / 8, l / 8 + 4, ...  Each warp waits for its own copies
         // before it hands the stage over; the other three have theirs on their way meanwhile.
@@ -382,13 +391,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < kLoads; ++i) row[i] = (int)a.by_top_k(row[i]);
             for (int kb = wl; kb < nk; kb += kLoadWarps) {
                 const int g = gbase + kb, s = g % kStages;
-                const bool free = !*abort_flag && (g < kStages || wait_for(&empty[s], ((g / kStages) - 1) & 1));
-                if (!__all_sync(0xffffffffu, free)) {
-                    if (lane == 0) record_status(status, RFP2_ETIMEOUT);
-                    *abort_flag = 1;
-                    ok = false;
-                    break;
-                }
+                ok = goes_on(!*abort_flag && (g < kStages || wait_for(&empty[s], ((g / kStages) - 1) & 1)));
+                if (!ok) break;
                 // (few instructions a copy, and none for the rows that a narrow tile lacks: the decoders keep the
                 // schedulers busy)
                 const uint8_t *x = reinterpret_cast<const uint8_t *>(a.X + kb * kStep + (lane & 7) * 8);
@@ -417,25 +421,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint64_t adesc0 = smem_desc_sw128(smem_addr(smem)), bdesc0 = smem_desc_sw128(smem_addr(smem) + kABytes);
         for (int u = pair; u < units && ok; u += npairs, ++it) {
             const int b = it & 1;
-            const bool free = !*abort_flag && (it < 2 || wait_for(&acce[b], ((it >> 1) - 1) & 1));
-            if (!__all_sync(0xffffffffu, free)) {
-                if (lane == 0) record_status(status, RFP2_ETIMEOUT);
-                *abort_flag = 1;
-                break;
-            }
+            if (!goes_on(!*abort_flag && (it < 2 || wait_for(&acce[b], ((it >> 1) - 1) & 1)))) break;
             tc_fence_after();
             const uint32_t idesc = idesc_bf16_f32(2 * kRows, width);
             const uint32_t d = tmem + (uint32_t)(b * kTileTokens);
             if (u + npairs < units) width = unit_at(a, u + npairs, blocks).width;
             for (int kb = 0; kb < nk; ++kb) {
                 if (!__all_sync(0xffffffffu, ready)) {
-                    const bool there = !*abort_flag && wait_for(&full[s], phase);
-                    if (!__all_sync(0xffffffffu, there)) {
-                        if (lane == 0) record_status(status, RFP2_ETIMEOUT);
-                        *abort_flag = 1;
-                        ok = false;
-                        break;
-                    }
+                    ok = goes_on(!*abort_flag && wait_for(&full[s], phase));
+                    if (!ok) break;
                 }
                 tc_fence_after();
                 const int s1 = s + 1 == kStages ? 0 : s + 1;
@@ -466,11 +460,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int m = (2 * un.block + (int)rank) * kOut + (kGated ? q * 16 + (lane & 15) : q * 32 + lane);
             float bias = 0.0f;
             if (a.bias && m < a.out) bias = a.bias[(int64_t)un.tile.x * a.M + m + (kGated && lane >= 16 ? a.out : 0)];
-            if (*abort_flag || !wait_for(&accf[b], (it >> 1) & 1)) {
-                record_status(status, RFP2_ETIMEOUT);
-                *abort_flag = 1;
-                break;
-            }
+            if (!goes_on(!*abort_flag && wait_for(&accf[b], (it >> 1) & 1))) break;
             tc_fence_after();
 #pragma unroll 1
             for (int c0 = 0; c0 < un.width; c0 += 32) {
@@ -559,12 +549,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int h = 0; h < 4; ++h) decode_half(code[h], twice_scale(scales[h]), o[h]);
                 }
                 if (gd >= kStages) there = there && wait_for(&empty[s], ((gd / kStages) - 1) & 1);
-                if (!__all_sync(0xffffffffu, there)) {
-                    if (lane == 0) record_status(status, RFP2_ETIMEOUT);
-                    *abort_flag = 1;
-                    ok = false;
-                    break;
-                }
+                ok = goes_on(there);
+                if (!ok) break;
                 uint8_t *to = smem + (size_t)s * kStageBytes + row * 128;
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
