@@ -242,18 +242,35 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         if (a.groups > 1) {
             float mine = -CUDART_INF_F;  // lane g: what group g counts
             float room = 0.0f;           // how far any of them may be off
+            // What a group of largest values m1 and m2 (0: none) counts, and how far that may be off.  A sum of two
+            // finite values may leave fp32's range: a group that has experts counts as the lowest value at least
+            // (-infinity is one without), and such sums are for fp64 to tell apart.
+            const auto counts = [&](uint32_t m1, uint32_t m2, float &off) {
+                off = 0.0f;
+                if (!m1) return -CUDART_INF_F;
+                float v = unordered(m1);
+                off = slack<SOFTMAX>(v);
+                if (by_sum && m2) {
+                    off += slack<SOFTMAX>(unordered(m2));
+                    v += unordered(m2);
+                    if (fabsf(v) == CUDART_INF_F) {
+                        v = copysignf(CUDART_MAX_NORMAL_F, v);
+                        off = CUDART_INF_F;
+                    }
+                }
+                return v;
+            };
             // group g's largest values, from each lane's two largest
             const auto count = [&](int g, uint32_t b1, uint32_t b2) {
                 const uint32_t m1 = __reduce_max_sync(kAll, b1);
-                float v = m1 ? unordered(m1) : -CUDART_INF_F;
+                uint32_t m2 = 0;
                 if (by_sum) {
                     const int owner = __ffs(__ballot_sync(kAll, b1 == m1)) - 1;
-                    const uint32_t m2 = __reduce_max_sync(kAll, lane == owner ? b2 : b1);
-                    room = fmaxf(room, slack<SOFTMAX>(v) + (m2 ? slack<SOFTMAX>(unordered(m2)) : 0.0f));
-                    if (m2) v += unordered(m2);
-                } else if (m1) {
-                    room = fmaxf(room, slack<SOFTMAX>(v));
+                    m2 = __reduce_max_sync(kAll, lane == owner ? b2 : b1);
                 }
+                float off;
+                const float v = counts(m1, m2, off);
+                room = fmaxf(room, off);
                 if (lane == g) mine = v;
             };
             bool counted = false;
@@ -295,12 +312,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
                     int shift = 2;
                     for (int n = 8; n > a.groups; n /= 2, ++shift)
                         merge(b1[0], b2[0], __shfl_xor_sync(kAll, b1[0], 1 << shift), __shfl_xor_sync(kAll, b2[0], 1 << shift));
-                    float v = b1[0] ? unordered(b1[0]) : -CUDART_INF_F;
-                    float off = b1[0] ? slack<SOFTMAX>(v) : 0.0f;
-                    if (by_sum && b2[0]) {
-                        off += slack<SOFTMAX>(unordered(b2[0]));
-                        v += unordered(b2[0]);
-                    }
+                    float off;
+                    float v = counts(b1[0], b2[0], off);
                     room = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(off)));
                     v = __shfl_sync(kAll, v, (lane << shift) & 31);
                     if (lane < a.groups) mine = v;
