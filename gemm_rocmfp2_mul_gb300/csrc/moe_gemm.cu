@@ -165,12 +165,18 @@ struct GemmArgs {
     FastDiv by_top_k;
 };
 
-// Both activations are gate / (1 + exp(-v)): v = gate, or twice tanh's argument.  The fast exponential and quotient
-// are off by 2^-21 (2 + |v|) of the result, which is rounded to bf16; with exact ones the epilogue held the
-// MMAs up (1363 -> 1287 us of the case above, 277 -> 260).
+// Both activations are gate / (1 + exp(-v)): v = gate, or twice tanh's argument.  With h = exp(-|v| / 2) they are
+// gate s / (1 + h^2) s, where s is 1 for v >= 0 and h below: the divisor stays within [1, 2], where a reciprocal
+// needs no care for its range, and act(gate) * up is formed before it would underflow (h is 0 from |v| = 174 on).
+// The approximate exponential and reciprocal are off by 2^-21 (2 + |v|) of the result at most, which is rounded to
+// bf16; with exact ones the epilogue held the MMAs up (1363 -> 1287 us of the case above, 277 -> 260).
 RFP2_DEV float activated(int activation, float gate, float up) {
     const float v = activation == RFP2_ACT_SILU ? gate : 1.5957691216057308f * fmaf(0.044715f * gate * gate, gate, gate);
-    return __fdividef(gate, 1.0f + __expf(-v)) * up;
+    float h, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h) : "f"(-0.72134752044448170f * fabsf(v)));  // log2(e) / 2
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(h, h, 1.0f)));
+    const float s = v < 0.0f ? h : 1.0f;
+    return gate * s * r * (up * s);
 }
 
 // The rows of pairs without an expert: zeros for -1, NaN for another id.

@@ -37,3 +37,43 @@ def test_biases_of_the_lowest_and_the_largest_value(g, E, groups, scoring):
             want, w = plain.route(x.double().cpu().numpy(), 8, scoring, bias, groups, keep, 2)
             np.testing.assert_array_equal(ids.cpu().numpy(), want)
             assert np.all(np.abs(weights.double().cpu().numpy() - w) <= w * 2.0 ** -20)
+
+
+def products(g, gate, up, kind):
+    """rfp2_moe_gemm of rows whose gate and up values are exactly these bf16 numbers: y [T]."""
+    import torch
+    W = np.zeros((1, 32, 8, 10), np.uint8)
+    W[..., :8] = 0xAA                       # level 1 everywhere
+    W[0, :16, 0, 8] = W[0, 16:, 0, 9] = 64  # gate rows see the first 16 columns, up rows the next, with scale 1
+    X = torch.zeros((len(gate), 256), dtype=torch.bfloat16, device="cuda")
+    X[:, 3], X[:, 20] = gate, up
+    ids = torch.zeros((len(gate), 1), dtype=torch.int32, device="cuda")
+    y = g.rfp2_moe_gemm(torch.from_numpy(W).cuda(), 1, 32, 256, ids, X, activation=kind)
+    assert bool(((y == y[..., :1]) | y.isnan()).all())
+    return y[:, 0, 0]
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_activations_of_very_negative_gates(g, kind):
+    """act(gate) far below 1, times an up value that brings it back: where 1 + exp(-v) is near the end of fp32's
+    range and past it.  v is off by five roundings of up to 2^-24 |v| and its exponential by (2 + 1.2 |v|) 2^-23:
+    2^-13 of the result at |v| <= 170, beside its own rounding."""
+    import torch
+    gate = torch.linspace(-160, 2, 649, device="cuda") if kind == "silu" else torch.linspace(-12.5, 1, 649, device="cuda")
+    gate = gate.bfloat16()
+    for up in (1.0, -2.0 ** 100):
+        y = products(g, gate, torch.full_like(gate, up), kind).double().cpu().numpy()
+        a = gate.double().cpu().numpy()
+        v = a if kind == "silu" else 2.0 * np.sqrt(2.0 / np.pi) * (a + 0.044715 * a ** 3)
+        ref = a / (1.0 + np.exp(-v)) * up
+        # (below 2^-126 a bf16 has steps of 2^-133)
+        assert np.all(np.abs(y - ref) <= np.abs(ref) * (2.0 ** -8 + 2.0 ** -13) + 2.0 ** -133)
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_activations_at_the_ends(g, kind):
+    """Gates of any size and NaN: 0 below, the gate above."""
+    import torch
+    gate = torch.tensor([-3e38, -1e20, -1e10, -300.0, 0.0, 300.0, 1e10, 1e20, 3e38, float("nan")], device="cuda").bfloat16()
+    y = products(g, gate, torch.ones_like(gate), kind)
+    assert not y[:5].any() and torch.equal(y[5:9], gate[5:9]) and bool(y[9].isnan())
