@@ -397,8 +397,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < kLoads; ++i) row[i] = (int)a.by_top_k(row[i]);
             for (int kb = wl; kb < nk; kb += kLoadWarps) {
                 const int g = gbase + kb, s = g % kStages;
-                ok = goes_on(!*abort_flag && (g < kStages || wait_for(&empty[s], ((g / kStages) - 1) & 1)));
-                if (!ok) break;
+                if (!goes_on(!*abort_flag && (g < kStages || wait_for(&empty[s], ((g / kStages) - 1) & 1)))) {
+                    ok = false;
+                    break;
+                }
                 // (few instructions a copy, and none for the rows that a narrow tile lacks: the decoders keep the
                 // schedulers busy)
                 const uint8_t *x = reinterpret_cast<const uint8_t *>(a.X + kb * kStep + (lane & 7) * 8);
@@ -434,8 +436,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (u + npairs < units) width = unit_at(a, u + npairs, blocks).width;
             for (int kb = 0; kb < nk; ++kb) {
                 if (!__all_sync(0xffffffffu, ready)) {
-                    ok = goes_on(!*abort_flag && wait_for(&full[s], phase));
-                    if (!ok) break;
+                    if (!goes_on(!*abort_flag && wait_for(&full[s], phase))) {
+                        ok = false;
+                        break;
+                    }
                 }
                 tc_fence_after();
                 const int s1 = s + 1 == kStages ? 0 : s + 1;
@@ -555,8 +559,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int h = 0; h < 4; ++h) decode_half(code[h], twice_scale(scales[h]), o[h]);
                 }
                 if (gd >= kStages) there = there && wait_for(&empty[s], ((gd / kStages) - 1) & 1);
-                ok = goes_on(there);
-                if (!ok) break;
+                if (!goes_on(there)) {
+                    ok = false;
+                    break;
+                }
                 uint8_t *to = smem + (size_t)s * kStageBytes + row * 128;
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
