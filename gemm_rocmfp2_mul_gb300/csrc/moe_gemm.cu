@@ -179,12 +179,28 @@ RFP2_DEV float activated(int activation, float gate, float up) {
     return gate * s * r * (up * s);
 }
 
-// The rows of pairs without an expert: zeros for -1, NaN for another id.
-RFP2_DEV void fill_rest(const GemmArgs &a, int64_t thread, int64_t threads) {
-    const int first = a.plan.header[1], rest = a.plan.header[2] - first;
-    for (int64_t i = thread; i < (int64_t)rest * a.out; i += threads) {
-        const int p = a.plan.pairs[first + i / a.out];
-        a.Y[(int64_t)p * a.out + i % a.out] = __float2bfloat16(a.ids[p] == -1 ? 0.0f : CUDART_NAN_F);
+// The rows of pairs without an expert: zeros for -1, NaN for another id.  A warp a row, in words of 16 bytes (a row
+// is a multiple of 16 values); warp `of` of `warps` takes every warps-th row, and 32 of them have their places and
+// ids on their way together.  By a warp that has no other work, beside the products: 57344 of 65536 rows of 7168 take
+// 0.2 ms, as a plain fill does.  (Single values, written by the epilogue ahead of its first tile, took 5.5 ms, in
+// which the MMAs waited; of arrays that fill the memory nearly the time limit of their waits.)
+RFP2_DEV void fill_rest(const GemmArgs &a, int of, int warps) {
+    const int lane = threadIdx.x & 31;
+    const int first = a.plan.header[1], rest = a.plan.header[2] - first, words = a.out / 8;
+    for (int i0 = of; i0 < rest; i0 += 32 * warps) {
+        const int i = i0 + lane * warps;
+        int p = 0;
+        uint32_t fill = 0;
+        if (i < rest) {
+            p = a.plan.pairs[first + i];
+            fill = a.ids[p] == -1 ? 0u : 0x7FFF7FFFu;
+        }
+        const int n = min(32, (rest - i0 + warps - 1) / warps);
+        for (int j = 0; j < n; ++j) {
+            const uint32_t f = __shfl_sync(0xffffffffu, fill, j);
+            uint4 *row = reinterpret_cast<uint4 *>(a.Y + (int64_t)__shfl_sync(0xffffffffu, p, j) * a.out);
+            for (int w = lane; w < words; w += 32) row[w] = make_uint4(f, f, f, f);
+        }
     }
 }
 
@@ -306,7 +322,8 @@ RFP2_DEV void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 //                 16 bytes a lane and copy, a step of K a warp at a time;
 //   warp 6        streams the packed rows of its 128 weight rows, 256 of K to a box, into a ring of boxes;
 //   warps 7-22    decode them exactly to bf16 into the A half of the stages, a row a thread;
-//   warp 1        (even CTA) issues M = 256 pair MMAs over both CTAs' stages;
+//   warp 1        (even CTA) issues M = 256 pair MMAs over both CTAs' stages; (odd CTA) writes the rows of pairs
+//                 without an expert;
 //   warps 2-5     read one of two accumulators back while the MMAs fill the other: a lane has a weight row, a
 //                 register a token.
 // Gated: lanes 0-15 of a warp have gate rows, lanes 16-31 the up rows that go with them, and a shuffle brings
@@ -458,9 +475,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (elect_one()) umma_commit_pair_both(&accf[b]);  // complete, or idle after an abort
             __syncwarp();
         }
+    } else if (warp == 1) {
+        fill_rest(a, pair, npairs);  // (the odd CTA has no MMAs to issue)
     } else if (warp >= 2 && warp < 6) {
         // ---- epilogue
-        fill_rest(a, (int64_t)blockIdx.x * 128 + threadIdx.x - 64, (int64_t)gridDim.x * 128);
         const int q = warp & 3;  // lanes 32 q ... of the accumulators
         const uint32_t acce0 = cluster_map(&acce[0], 0);
         int it = 0;

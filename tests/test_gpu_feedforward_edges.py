@@ -77,3 +77,57 @@ def test_activations_at_the_ends(g, kind):
     gate = torch.tensor([-3e38, -1e20, -1e10, -300.0, 0.0, 300.0, 1e10, 1e20, 3e38, float("nan")], device="cuda").bfloat16()
     y = products(g, gate, torch.ones_like(gate), kind)
     assert not y[:5].any() and torch.equal(y[5:9], gate[5:9]) and bool(y[9].isnan())
+
+
+@pytest.mark.parametrize("M,kind", [(16, "none"), (32, "silu"), (1040, "none"), (4128, "gelu")])
+def test_rows_without_an_expert(g, M, kind):
+    """Most rows lost, in stretches and here and there, of every length that a warp writes: zeros for -1, NaN for
+    another id, the others as without them."""
+    import torch
+    r = np.random.default_rng(4)
+    T, k, E = 900, 4, 6
+    W = r.integers(0, 256, (E, M, 8, 10), dtype=np.uint8)
+    W[..., 8:] %= 28
+    W, X = torch.from_numpy(W).cuda(), torch.randn((T, 256), device="cuda").bfloat16()
+    ids = r.integers(0, E, (T, k)).astype(np.int32)
+    want = g.rfp2_moe_gemm(W, E, M, 256, torch.from_numpy(ids).cuda(), X, activation=kind)
+    lost = r.random((T, k)) < 0.5
+    lost[200:700] = True
+    bad = lost & (r.random((T, k)) < 0.3)
+    ids[lost] = -1
+    ids[bad] = E + 3
+    Y = torch.full_like(want, 5.0)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    g.rfp2_moe_gemm(W, E, M, 256, torch.from_numpy(ids).cuda(), X, activation=kind, Y=Y, dev_status=status)
+    assert int(status) == 7
+    assert bool(Y[bad].isnan().all()) and not Y[lost & ~bad].any() and torch.equal(Y[~lost], want[~lost])
+
+
+def test_rows_without_an_expert_hold_nothing_up(g):
+    """57344 of 65536 rows without an expert, 822 MB of zeros: written at a fair share of the rate of a plain fill
+    (a tenth at least, beside the products of the others), where a value at a time took far longer than that
+    and kept the tensor cores waiting, whose waits have a limit."""
+    import torch
+    T, k, M, K, E = 8192, 8, 7168, 256, 8
+    W = torch.zeros((E, M, K // 32, 10), dtype=torch.uint8, device="cuda")
+    X = torch.randn((T, K), device="cuda").bfloat16()
+    ids = torch.full((T, k), -1, dtype=torch.int32, device="cuda")
+    ids[:, 0] = torch.arange(T, device="cuda") % E
+    Y, workspace = torch.empty((T, k, M), dtype=torch.bfloat16, device="cuda"), g.rfp2_moe_gemm_workspace(ids, E)
+
+    def best(call):
+        times = []
+        for _ in range(6):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            call()
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times[1:])
+
+    fill = best(Y.zero_)
+    some = best(lambda: g.rfp2_moe_gemm(W, E, M, K, ids[:, :1].contiguous(), X, workspace=workspace))
+    both = best(lambda: g.rfp2_moe_gemm(W, E, M, K, ids, X, Y=Y, workspace=workspace))
+    print(f"fill {fill:.3f} ms, products {some:.3f} ms, together {both:.3f} ms")
+    assert both - some < 10 * fill
