@@ -52,6 +52,12 @@ RFP2_DEV float near_sigmoid(float x) {
     const float e = __expf(-fabsf(x));
     return __fdividef(x >= 0.0f ? 1.0f : e, 1.0f + e);
 }
+// exp(x - y): what the difference loses to rounding (up to 2^-18 where it is 64) is put back to first order.
+RFP2_DEV float exp_of_difference(float x, float y) {
+    const float d = x - y, back = d - x, lost = (x - (d - back)) - (y + back);
+    const float e = expf(d);
+    return e > 0.0f ? fmaf(e, lost, e) : 0.0f;  // (0: the difference may be infinite)
+}
 RFP2_DEV double sigmoid(double x) { return 1.0 / (1.0 + exp(-x)); }
 
 RFP2_DEV float warp_sum(float v) {
@@ -427,11 +433,11 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
 #pragma unroll
             for (int off = 16; off >= 1; off >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, off));
             if (!SOFTMAX) most = fminf(most, 0.0f);
-            if (pick >= 0) w = SOFTMAX ? expf(l - most) : expf(fminf(l, 0.0f) - most) / (1.0f + expf(-fabsf(l)));
+            if (pick >= 0) w = SOFTMAX ? exp_of_difference(l, most) : exp_of_difference(fminf(l, 0.0f), most) / (1.0f + expf(-fabsf(l)));
             const float sum = warp_sum(w);
             w = sum > 0.0f ? w / sum : 0.0f;
         } else if (pick >= 0) {
-            w = SOFTMAX ? expf(l - top) / total : sigmoid(l);
+            w = SOFTMAX ? exp_of_difference(l, top) / total : sigmoid(l);
         }
         if (lane < a.top_k) {
             a.ids[t * a.top_k + lane] = pick;

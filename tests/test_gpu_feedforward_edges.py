@@ -131,3 +131,16 @@ def test_rows_without_an_expert_hold_nothing_up(g):
     both = best(lambda: g.rfp2_moe_gemm(W, E, M, K, ids, X, Y=Y, workspace=workspace))
     print(f"fill {fill:.3f} ms, products {some:.3f} ms, together {both:.3f} ms")
     assert both - some < 10 * fill
+
+
+@pytest.mark.parametrize("scoring,renormalise", [("softmax", True), ("softmax", False), ("sigmoid", True)])
+def test_weights_of_experts_far_apart(g, scoring, renormalise):
+    """Weights are within 2^-20 of themselves however far apart the logits are: what a difference of two loses
+    (2^-18 where it is 64) is not lost to its exponential."""
+    import torch
+    r = np.random.default_rng(2)
+    x = torch.from_numpy((-60.0 * r.random((200, 16)) ** 2 - (0.1 if scoring == "softmax" else 18.0)).astype(np.float32)).cuda()
+    ids, weights = g.rfp2_moe_route(x, 16, scoring=scoring, renormalise=renormalise)
+    want, w = plain.route(x.double().cpu().numpy(), 16, scoring, renormalise=renormalise)
+    np.testing.assert_array_equal(ids.cpu().numpy(), want)
+    assert np.all(np.abs(weights.double().cpu().numpy() - w) <= w * 2.0 ** -20)
