@@ -260,9 +260,10 @@ __global__ void __launch_bounds__(most_threads<V, N>(), 1) norm_kernel(const Nor
 #pragma unroll
         for (int e = 0; e < V; ++e) sum = fmaf(s[i][e], s[i][e], sum);
     sum = over_row<false>(sum, warps, part[0]);
-    float r = 1.0f / sqrtf(sum / (float)a.K + a.eps);
-    if (!(sum < 0x1p126f) || sum < 0x1p-90f) {
-        // squares out of range: of values below 1 in size, by a power of two
+    const float square = sum / (float)a.K + a.eps;
+    float r = 1.0f / sqrtf(square);
+    if (!(square < CUDART_INF_F) || sum < 0x1p-90f) {
+        // squares (or their mean and eps) out of range: of values below 1 in size, by a power of two
         float most = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i)

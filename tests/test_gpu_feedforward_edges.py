@@ -144,3 +144,17 @@ def test_weights_of_experts_far_apart(g, scoring, renormalise):
     want, w = plain.route(x.double().cpu().numpy(), 16, scoring, renormalise=renormalise)
     np.testing.assert_array_equal(ids.cpu().numpy(), want)
     assert np.all(np.abs(weights.double().cpu().numpy() - w) <= w * 2.0 ** -20)
+
+
+@pytest.mark.parametrize("K", [1, 64, 1001])
+def test_an_eps_near_the_largest_value(g, K):
+    """Also where it leaves fp32's range together with a mean that does not."""
+    import torch
+    x = torch.randn((4, K), generator=torch.Generator(device="cuda").manual_seed(3), device="cuda").double()
+    x[1:3] *= (torch.tensor([[2.0 ** 125.9], [2.0 ** 127.9]], device="cuda") / x[1:3].square().sum(-1, keepdim=True)).sqrt()
+    x[3] *= 2.0 ** 100
+    x = x.float()
+    for eps in (1e38, 3.3e38, float(np.finfo(np.float32).max)):
+        y = g.rfp2_rms_norm(x, torch.full((K,), 2.0 ** 40, device="cuda"), eps=eps).y.double().cpu().numpy()
+        ref = plain.norm(x.double().cpu().numpy(), np.full(K, 2.0 ** 40), np.float64(np.float32(eps)))
+        assert np.all(np.abs(y - ref) <= np.abs(ref) * 31 * plain.U)
