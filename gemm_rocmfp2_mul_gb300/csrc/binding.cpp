@@ -258,7 +258,8 @@ int attn_decode(PyObject *const *a) {
                             stream_of(device));
 }
 
-// An input of a call that has no gradient.
+// A tensor of a call that has no gradient: an input, or an output, of which autograd would go on to believe what it
+// was before.
 const at::Tensor &no_gradient(const at::Tensor &t, const char *name) {
     if (t.requires_grad() && at::GradMode::is_enabled())
         refuse(PyExc_RuntimeError, name, "requires a gradient, which the call does not give");
@@ -282,10 +283,11 @@ int rms_norm(PyObject *const *a) {
     };
     const at::Tensor *residual = like_x(a[3], "residual"), *total = like_x(a[4], "total");
     if (residual) no_gradient(*residual, "residual");
+    if (total) no_gradient(*total, "total");
     const at::Tensor *y = nullptr;
     int y_type = RFP2_F32;
     if (a[5] != Py_None) {
-        y = &rows(a[5], "y", 2, device);
+        y = &no_gradient(rows(a[5], "y", 2, device), "y");
         y_type = type_code(*y, "y");
         if (!same_shape(*y, x)) refuse(PyExc_ValueError, "y must have x's shape");
     }
@@ -293,7 +295,7 @@ int rms_norm(PyObject *const *a) {
     float *d = nullptr;
     if (a[6] != Py_None && a[7] != Py_None) {
         const at::Tensor &qt = array(a[6], "q", at::kChar, "torch.int8", device);
-        const at::Tensor &dt = array(a[7], "d", at::kFloat, "torch.float32", device);
+        const at::Tensor &dt = no_gradient(array(a[7], "d", at::kFloat, "torch.float32", device), "d");
         if (!same_shape(qt, x) || dt.dim() != 2 || dt.size(0) != T || dt.size(1) != K / 32)
             refuse(PyExc_ValueError, "q must be [T, K] and d [T, K/32]");
         q = qt.data_ptr<int8_t>();
@@ -323,7 +325,7 @@ int moe_route(PyObject *const *a) {
         bias = b.data_ptr<float>();
     }
     const at::Tensor &ids = array(a[8], "ids", at::kInt, "torch.int32", device);
-    const at::Tensor &weights = array(a[9], "weights", at::kFloat, "torch.float32", device);
+    const at::Tensor &weights = no_gradient(array(a[9], "weights", at::kFloat, "torch.float32", device), "weights");
     if (ids.dim() != 2 || ids.size(0) != T || !same_shape(ids, weights))
         refuse(PyExc_ValueError, "ids and weights must be [T, top_k]");
     wrote(ids);
@@ -348,7 +350,7 @@ int moe_combine(PyObject *const *a) {
         if (!per_slot(i)) refuse(PyExc_ValueError, "ids must be [T, top_k]");
         ids = i.data_ptr<int32_t>();
     }
-    const at::Tensor &out = rows(a[4], "out", 2, device);
+    const at::Tensor &out = no_gradient(rows(a[4], "out", 2, device), "out");
     const int out_type = type_code(out, "out");
     if (out.size(0) != T || out.size(1) != M) refuse(PyExc_ValueError, "out must be [T, M]");
     const at::Tensor *residual = nullptr;
@@ -385,7 +387,7 @@ int moe_gemm(PyObject *const *a) {
         bias = b.data_ptr<float>();
     }
     const int activation = (int)whole(a[7]);
-    const at::Tensor &Y = array(a[8], "Y", at::kBFloat16, "torch.bfloat16", device);
+    const at::Tensor &Y = no_gradient(array(a[8], "Y", at::kBFloat16, "torch.bfloat16", device), "Y");
     if (Y.dim() != 3 || Y.size(0) != T || Y.size(1) != top_k || Y.size(2) != (activation == RFP2_ACT_NONE ? M : M / 2))
         refuse(PyExc_ValueError, "Y must be [T, top_k, M], M/2 when gated");
     const at::Tensor &workspace = array(a[9], "workspace", at::kByte, "torch.uint8", device);

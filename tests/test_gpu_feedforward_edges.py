@@ -158,3 +158,22 @@ def test_an_eps_near_the_largest_value(g, K):
         y = g.rfp2_rms_norm(x, torch.full((K,), 2.0 ** 40, device="cuda"), eps=eps).y.double().cpu().numpy()
         ref = plain.norm(x.double().cpu().numpy(), np.full(K, 2.0 ** 40), np.float64(np.float32(eps)))
         assert np.all(np.abs(y - ref) <= np.abs(ref) * 31 * plain.U)
+
+
+def test_outputs_that_require_a_gradient_are_refused(g):
+    """What autograd knows of such a tensor would no longer be true of its values."""
+    import torch
+    x, w = torch.randn((4, 64), device="cuda"), torch.ones(64, device="cuda")
+    leaf = lambda *shape, dtype=torch.float32: torch.zeros(shape, dtype=dtype, device="cuda", requires_grad=True)
+    grown = (leaf(4, 64) * 2.0)
+    W, X = torch.zeros((2, 64, 8, 10), dtype=torch.uint8, device="cuda"), torch.zeros((4, 256), dtype=torch.bfloat16, device="cuda")
+    ids = torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    calls = [lambda: g.rfp2_rms_norm(x, w, y=leaf(4, 64)), lambda: g.rfp2_rms_norm(x, w, y=grown),
+             lambda: g.rfp2_rms_norm(x, w, residual=x, total=grown), lambda: g.rfp2_rms_norm(x, w, want="q8", d=leaf(4, 2)),
+             lambda: g.rfp2_moe_route(x, 2, weights=leaf(4, 2)), lambda: g.rfp2_moe_combine(x.view(4, 2, 32), x[:, :2].contiguous(), out=grown[:, :32]),
+             lambda: g.rfp2_moe_gemm(W, 2, 64, 256, ids, X, Y=leaf(4, 2, 64, dtype=torch.bfloat16))]
+    for call in calls:
+        with pytest.raises(RuntimeError, match="gradient"):
+            call()
+        with torch.no_grad():
+            call()
