@@ -649,14 +649,14 @@ def rfp2_rms_norm(x, weight, eps=1e-6, residual=None, want="y", dtype=None, y=No
     x or residual.  There is no gradient."""
     if want not in ("y", "q8", "both"):
         raise ValueError(f"want must be 'y', 'q8' or 'both', got {want!r}")
+    if (want == "q8" and y is not None) or (want == "y" and (q is not None or d is not None)):
+        raise ValueError(f"a buffer was passed for what want={want!r} leaves out")
+    if y is not None and dtype not in (None, y.dtype):
+        raise ValueError(f"y is {y.dtype}, dtype {dtype}")
     torch = _torch()
-    if want == "q8":
-        y = None
-    elif y is None:
+    if want != "q8" and y is None:
         y = _empty(x.shape, dtype or x.dtype, x)
-    if want == "y":
-        q = d = None
-    else:
+    if want != "y":
         q = _empty(x.shape, torch.int8, x) if q is None else q
         d = _empty((*x.shape[:-1], x.shape[-1] // 32), torch.float32, x) if d is None else d
     if residual is None:
@@ -721,7 +721,10 @@ def rfp2_moe_combine(y, weights, ids=None, residual=None, out=None, dtype=None):
     """The sum of a token's experts: [T, M] = sum_j weights[t, j] * y[t, j] + residual[t], of y [T, top_k, M] (any
     token and slot strides) and weights fp32 [T, top_k].  ids: slots with a negative id are not read.  The result has
     the residual's type, else `dtype`, else y's; out may be residual.  There is no gradient."""
-    if out is None:
+    if out is not None:
+        if dtype not in (None, out.dtype):
+            raise ValueError(f"out is {out.dtype}, dtype {dtype}")
+    else:
         if y.dim() != 3:
             raise ValueError(f"y must have 3 dimensions, got {y.dim()}")
         out = _empty((y.shape[0], y.shape[2]), residual.dtype if residual is not None else dtype or y.dtype, y)
