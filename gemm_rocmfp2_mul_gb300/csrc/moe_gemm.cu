@@ -155,13 +155,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const int32_t *__
 }
 
 struct GemmArgs {
-    const uint8_t *W;
     const __nv_bfloat16 *X;
     const float *bias;
     __nv_bfloat16 *Y;
     const int32_t *ids;
     Plan plan;
-    int E, M, K, each, out;
+    int M, K, each, out;
     FastDiv by_top_k;
 };
 
@@ -698,13 +697,11 @@ extern "C" rfp2_status rfp2_moe_gemm(const uint8_t *W, int64_t E, int64_t M, int
         return RFP2_ECUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     GemmArgs a;
-    a.W = W;
     a.X = reinterpret_cast<const __nv_bfloat16 *>(X);
     a.bias = bias;
     a.Y = reinterpret_cast<__nv_bfloat16 *>(Y);
     a.ids = ids;
     a.plan = carve_plan(workspace, P);
-    a.E = (int)E;
     a.M = (int)M;
     a.K = (int)K;
     a.by_top_k = FastDiv((uint32_t)top_k);

@@ -348,8 +348,7 @@ cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream) {
     const auto warps_for = [&](int n) { return (runs + 32 * n - 1) / (32 * n); };
     int n = !wide ? 8 : a.T <= 2 * sms ? 1 : a.q ? 2 : 4;
     if (wide && n == 1 && warps_for(1) > 32) n = 2;
-    if (wide && n == 2 && warps_for(2) > 32) n = 4;
-    if (wide && n == 4 && warps_for(4) > 16) n = 8;
+    if (wide && ((n == 2 && warps_for(2) > 32) || (n == 4 && warps_for(4) > 16))) n = 8;
     if (!wide && warps_for(8) > 16) n = 32;
     const int warps = warps_for(n);
     const int threads = warps == 1 ? 128 : warps * 32, rows = warps == 1 ? 4 : 1;
@@ -359,12 +358,11 @@ cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream) {
     const auto pick = [&](auto q8) {
         constexpr bool Q8 = decltype(q8)::value;
         if (wide)
-            k = n == 1   ? norm_kernel<T, W, 1, Q8>
-                : n == 2 ? norm_kernel<T, W, 2, Q8>
-                : n == 4 ? norm_kernel<T, W, 4, Q8>
-                         : norm_kernel<T, W, 8, Q8>;
+            k = n == 1 ? norm_kernel<T, W, 1, Q8> : n == 2 ? norm_kernel<T, W, 2, Q8> : norm_kernel<T, W, 8, Q8>;
         else
             k = n == 8 ? norm_kernel<T, 1, 8, Q8> : norm_kernel<T, 1, 32, Q8>;
+        if constexpr (!Q8)
+            if (n == 4) k = norm_kernel<T, W, 4, false>;
     };
     if (a.q)
         pick(std::true_type());

@@ -21,7 +21,7 @@
 namespace rfp2 {
 namespace {
 
-constexpr int kWarps = 4;  // tokens of a CTA at a time
+constexpr int kWarps = 4;  // tokens of a CTA
 constexpr unsigned kAll = 0xffffffffu;
 
 struct RouteArgs {
@@ -118,13 +118,6 @@ __device__ __noinline__ void exact_values(const RouteArgs &a, const T *x, uint64
     }
     __syncwarp();
 }
-// The value of expert e: without a bias, its logit's.
-template <typename T>
-RFP2_DEV uint64_t exact_value(const RouteArgs &a, const T *x, const uint64_t *values, int e) {
-    if (a.bias) return values[e];
-    const float l = to_f32(x[e]);
-    return l > -CUDART_INF_F ? (uint64_t)ordered(l) : 0ull;
-}
 
 // The groups that are kept, a bit each, by values in fp64.  (`values`: a place for E numbers, here and below.)
 template <typename T, bool SOFTMAX>
@@ -134,7 +127,7 @@ __device__ __noinline__ unsigned keep_exactly(const RouteArgs &a, const T *x, ui
     for (int g = 0; g < a.groups; ++g) {
         uint64_t b1 = 0, b2 = 0;
         for (int e = g * a.group_size + lane; e < (g + 1) * a.group_size; e += 32) {
-            const uint64_t v = a.group_top > 1 ? values[e] : exact_value(a, x, values, e);
+            const uint64_t v = values[e];
             b2 = max(b2, min(b1, v));
             b1 = max(b1, v);
         }
@@ -155,7 +148,8 @@ __device__ __noinline__ unsigned keep_exactly(const RouteArgs &a, const T *x, ui
     return __ballot_sync(kAll, lane < a.groups && rank < a.keep && mine);
 }
 
-// Lane j's pick j of the kept groups' experts (-1: none), by values in fp64.
+// Lane j's pick j of the kept groups' experts (-1: none), by values in fp64 (of a call with a bias: without one
+// picks are certain).
 template <typename T, bool SOFTMAX>
 __device__ __noinline__ int choose_exactly(const RouteArgs &a, const T *x, uint64_t *values, unsigned kept, int lane) {
     exact_values<T, SOFTMAX>(a, x, values, lane);
@@ -166,7 +160,7 @@ __device__ __noinline__ int choose_exactly(const RouteArgs &a, const T *x, uint6
         int at = a.E;
         for (int e = lane; e < a.E; e += 32) {
             if (a.groups > 1 && !(kept >> a.by_size(e) & 1)) continue;
-            const uint64_t v = exact_value(a, x, values, e);
+            const uint64_t v = values[e];
             if (v > best && before(last, last_e, v, e)) {
                 best = v;
                 at = e;
@@ -197,252 +191,252 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    for (int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); t < a.T; t += (int64_t)gridDim.x * kWarps) {
-        const T *row = static_cast<const T *>(a.logits) + t * a.stride;
-        float x[V];
-        bool bad = false;
+    const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (t >= a.T) return;
+    const T *row = static_cast<const T *>(a.logits) + t * a.stride;
+    float x[V];
+    bool bad = false;
 #pragma unroll
-        for (int j = 0; j < V; ++j) x[j] = j * 32 + lane < a.E ? to_f32(row[j * 32 + lane]) : -CUDART_INF_F;
-        float bias[V];
+    for (int j = 0; j < V; ++j) x[j] = j * 32 + lane < a.E ? to_f32(row[j * 32 + lane]) : -CUDART_INF_F;
+    float bias[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            bias[j] = a.bias && j * 32 + lane < a.E ? a.bias[j * 32 + lane] : 0.0f;
-            bad |= x[j] != x[j] || bias[j] != bias[j] || (SOFTMAX && x[j] == CUDART_INF_F);
+    for (int j = 0; j < V; ++j) {
+        bias[j] = a.bias && j * 32 + lane < a.E ? a.bias[j * 32 + lane] : 0.0f;
+        bad |= x[j] != x[j] || bias[j] != bias[j] || (SOFTMAX && x[j] == CUDART_INF_F);
+    }
+    if (__any_sync(kAll, bad)) {
+        if (lane < a.top_k) {
+            a.ids[t * a.top_k + lane] = -1;
+            a.weights[t * a.top_k + lane] = CUDART_NAN_F;
         }
-        if (__any_sync(kAll, bad)) {
-            if (lane < a.top_k) {
-                a.ids[t * a.top_k + lane] = -1;
-                a.weights[t * a.top_k + lane] = CUDART_NAN_F;
+        return;
+    }
+    float top = 0.0f, total = 1.0f;
+    if (SOFTMAX) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) m = max(m, ordered(x[j]));
+        top = unordered(__reduce_max_sync(kAll, m));
+        if (top == -CUDART_INF_F) top = 0.0f;  // all are masked
+        float e[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) e[j] = expf(x[j] - top);
+#pragma unroll
+        for (int w = V / 2; w >= 1; w /= 2)
+#pragma unroll
+            for (int j = 0; j < w; ++j) e[j] += e[j + w];
+        total = warp_sum(e[0]);
+    }
+    const bool by_sum = a.groups > 1 && a.group_top > 1;
+    const float part_of = 1.0f / total;
+    // keys: what experts are chosen by; `part`: what groups are
+    uint32_t key[V], part[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        float score = 0.0f;
+        if (a.bias || by_sum) score = SOFTMAX ? __expf(x[j] - top) * part_of : near_sigmoid(x[j]);
+        const float value = a.bias ? score + bias[j] : x[j];
+        key[j] = x[j] > -CUDART_INF_F && value > -CUDART_INF_F ? ordered(value) : 0u;
+        part[j] = key[j] == 0 ? 0u : by_sum && !a.bias ? ordered(score) : key[j];
+    }
+    unsigned kept = kAll;
+    if (a.groups > 1) {
+        float mine = -CUDART_INF_F;  // lane g: what group g counts
+        float room = 0.0f;           // how far any of them may be off
+        // What a group of largest values m1 and m2 (0: none) counts, and how far that may be off.  A sum of two
+        // finite values may leave fp32's range: a group that has experts counts as the lowest value at least
+        // (-infinity is one without), and such sums are for fp64 to tell apart.
+        const auto counts = [&](uint32_t m1, uint32_t m2, float &off) {
+            off = 0.0f;
+            if (!m1) return -CUDART_INF_F;
+            float v = unordered(m1);
+            off = slack<SOFTMAX>(v);
+            if (by_sum && m2) {
+                off += slack<SOFTMAX>(unordered(m2));
+                v += unordered(m2);
+                if (fabsf(v) == CUDART_INF_F) {
+                    v = copysignf(CUDART_MAX_NORMAL_F, v);
+                    off = CUDART_INF_F;
+                }
             }
-            continue;
-        }
-        float top = 0.0f, total = 1.0f;
-        if (SOFTMAX) {
-            uint32_t m = 0;
+            return v;
+        };
+        // group g's largest values, from each lane's two largest
+        const auto count = [&](int g, uint32_t b1, uint32_t b2) {
+            const uint32_t m1 = __reduce_max_sync(kAll, b1);
+            uint32_t m2 = 0;
+            if (by_sum) {
+                const int owner = __ffs(__ballot_sync(kAll, b1 == m1)) - 1;
+                m2 = __reduce_max_sync(kAll, lane == owner ? b2 : b1);
+            }
+            float off;
+            const float v = counts(m1, m2, off);
+            room = fmaxf(room, off);
+            if (lane == g) mine = v;
+        };
+        bool counted = false;
+        if constexpr (V >= 8) {
+            // The lanes' values fall into eight slots of whole groups or whole parts of them: all slots are
+            // reduced at once, half of them handed to the other half of the lanes at each step (16384 rows of
+            // 256 experts in 8 groups: 47.5 us with two redux a group, 44 like this).
+            if (a.E == V * 32 && a.groups <= 8 && (a.groups & (a.groups - 1)) == 0) {
+                counted = true;
+                uint32_t b1[8], b2[8];
 #pragma unroll
-            for (int j = 0; j < V; ++j) m = max(m, ordered(x[j]));
-            top = unordered(__reduce_max_sync(kAll, m));
-            if (top == -CUDART_INF_F) top = 0.0f;  // all are masked
-            float e[V];
+                for (int g = 0; g < 8; ++g) {
+                    b1[g] = b2[g] = 0;
 #pragma unroll
-            for (int j = 0; j < V; ++j) e[j] = expf(x[j] - top);
-#pragma unroll
-            for (int w = V / 2; w >= 1; w /= 2)
-#pragma unroll
-                for (int j = 0; j < w; ++j) e[j] += e[j + w];
-            total = warp_sum(e[0]);
-        }
-        const bool by_sum = a.groups > 1 && a.group_top > 1;
-        const float part_of = 1.0f / total;
-        // keys: what experts are chosen by; `part`: what groups are
-        uint32_t key[V], part[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float score = 0.0f;
-            if (a.bias || by_sum) score = SOFTMAX ? __expf(x[j] - top) * part_of : near_sigmoid(x[j]);
-            const float value = a.bias ? score + bias[j] : x[j];
-            key[j] = x[j] > -CUDART_INF_F && value > -CUDART_INF_F ? ordered(value) : 0u;
-            part[j] = key[j] == 0 ? 0u : by_sum && !a.bias ? ordered(score) : key[j];
-        }
-        unsigned kept = kAll;
-        if (a.groups > 1) {
-            float mine = -CUDART_INF_F;  // lane g: what group g counts
-            float room = 0.0f;           // how far any of them may be off
-            // What a group of largest values m1 and m2 (0: none) counts, and how far that may be off.  A sum of two
-            // finite values may leave fp32's range: a group that has experts counts as the lowest value at least
-            // (-infinity is one without), and such sums are for fp64 to tell apart.
-            const auto counts = [&](uint32_t m1, uint32_t m2, float &off) {
-                off = 0.0f;
-                if (!m1) return -CUDART_INF_F;
-                float v = unordered(m1);
-                off = slack<SOFTMAX>(v);
-                if (by_sum && m2) {
-                    off += slack<SOFTMAX>(unordered(m2));
-                    v += unordered(m2);
-                    if (fabsf(v) == CUDART_INF_F) {
-                        v = copysignf(CUDART_MAX_NORMAL_F, v);
-                        off = CUDART_INF_F;
+                    for (int j = g * (V / 8); j < (g + 1) * (V / 8); ++j) {
+                        b2[g] = max(b2[g], min(b1[g], part[j]));
+                        b1[g] = max(b1[g], part[j]);
                     }
                 }
-                return v;
-            };
-            // group g's largest values, from each lane's two largest
-            const auto count = [&](int g, uint32_t b1, uint32_t b2) {
-                const uint32_t m1 = __reduce_max_sync(kAll, b1);
-                uint32_t m2 = 0;
-                if (by_sum) {
-                    const int owner = __ffs(__ballot_sync(kAll, b1 == m1)) - 1;
-                    m2 = __reduce_max_sync(kAll, lane == owner ? b2 : b1);
+                const auto merge = [&](uint32_t &u1, uint32_t &u2, uint32_t o1, uint32_t o2) {
+                    u2 = max(min(u1, o1), max(u2, o2));
+                    u1 = max(u1, o1);
+                };
+#pragma unroll
+                for (int half = 4; half >= 1; half /= 2) {
+                    const bool upper = lane & (4 * half);
+#pragma unroll
+                    for (int g = 0; g < half; ++g) {
+                        const uint32_t o1 = __shfl_xor_sync(kAll, upper ? b1[g] : b1[g + half], 4 * half);
+                        const uint32_t o2 = __shfl_xor_sync(kAll, upper ? b2[g] : b2[g + half], 4 * half);
+                        b1[g] = upper ? b1[g + half] : b1[g];
+                        b2[g] = upper ? b2[g + half] : b2[g];
+                        merge(b1[g], b2[g], o1, o2);
+                    }
                 }
+                // lanes 4 s ... have slot s
+                merge(b1[0], b2[0], __shfl_xor_sync(kAll, b1[0], 2), __shfl_xor_sync(kAll, b2[0], 2));
+                merge(b1[0], b2[0], __shfl_xor_sync(kAll, b1[0], 1), __shfl_xor_sync(kAll, b2[0], 1));
+                int shift = 2;
+                for (int n = 8; n > a.groups; n /= 2, ++shift)
+                    merge(b1[0], b2[0], __shfl_xor_sync(kAll, b1[0], 1 << shift), __shfl_xor_sync(kAll, b2[0], 1 << shift));
                 float off;
-                const float v = counts(m1, m2, off);
-                room = fmaxf(room, off);
-                if (lane == g) mine = v;
-            };
-            bool counted = false;
-            if constexpr (V >= 8) {
-                // The lanes' values fall into eight slots of whole groups or whole parts of them: all slots are
-                // reduced at once, half of them handed to the other half of the lanes at each step (16384 rows of
-                // 256 experts in 8 groups: 47.5 us with two redux a group, 44 like this).
-                if (a.E == V * 32 && a.groups <= 8 && (a.groups & (a.groups - 1)) == 0) {
-                    counted = true;
-                    uint32_t b1[8], b2[8];
-#pragma unroll
-                    for (int g = 0; g < 8; ++g) {
-                        b1[g] = b2[g] = 0;
-#pragma unroll
-                        for (int j = g * (V / 8); j < (g + 1) * (V / 8); ++j) {
-                            b2[g] = max(b2[g], min(b1[g], part[j]));
-                            b1[g] = max(b1[g], part[j]);
-                        }
-                    }
-                    const auto merge = [&](uint32_t &u1, uint32_t &u2, uint32_t o1, uint32_t o2) {
-                        u2 = max(min(u1, o1), max(u2, o2));
-                        u1 = max(u1, o1);
-                    };
-#pragma unroll
-                    for (int half = 4; half >= 1; half /= 2) {
-                        const bool upper = lane & (4 * half);
-#pragma unroll
-                        for (int g = 0; g < half; ++g) {
-                            const uint32_t o1 = __shfl_xor_sync(kAll, upper ? b1[g] : b1[g + half], 4 * half);
-                            const uint32_t o2 = __shfl_xor_sync(kAll, upper ? b2[g] : b2[g + half], 4 * half);
-                            b1[g] = upper ? b1[g + half] : b1[g];
-                            b2[g] = upper ? b2[g + half] : b2[g];
-                            merge(b1[g], b2[g], o1, o2);
-                        }
-                    }
-                    // lanes 4 s ... have slot s
-                    merge(b1[0], b2[0], __shfl_xor_sync(kAll, b1[0], 2), __shfl_xor_sync(kAll, b2[0], 2));
-                    merge(b1[0], b2[0], __shfl_xor_sync(kAll, b1[0], 1), __shfl_xor_sync(kAll, b2[0], 1));
-                    int shift = 2;
-                    for (int n = 8; n > a.groups; n /= 2, ++shift)
-                        merge(b1[0], b2[0], __shfl_xor_sync(kAll, b1[0], 1 << shift), __shfl_xor_sync(kAll, b2[0], 1 << shift));
-                    float off;
-                    float v = counts(b1[0], b2[0], off);
-                    room = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(off)));
-                    v = __shfl_sync(kAll, v, (lane << shift) & 31);
-                    if (lane < a.groups) mine = v;
-                }
+                float v = counts(b1[0], b2[0], off);
+                room = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(off)));
+                v = __shfl_sync(kAll, v, (lane << shift) & 31);
+                if (lane < a.groups) mine = v;
             }
-            if (!counted) {
-                for (int g = 0; g < a.groups; ++g) {
-                    const int from = g * a.group_size, to = from + a.group_size;
-                    uint32_t b1 = 0, b2 = 0;
+        }
+        if (!counted) {
+            for (int g = 0; g < a.groups; ++g) {
+                const int from = g * a.group_size, to = from + a.group_size;
+                uint32_t b1 = 0, b2 = 0;
 #pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        const int e = j * 32 + lane;
-                        const uint32_t k = e >= from && e < to ? part[j] : 0u;
-                        b2 = max(b2, min(b1, k));
-                        b1 = max(b1, k);
-                    }
-                    count(g, b1, b2);
+                for (int j = 0; j < V; ++j) {
+                    const int e = j * 32 + lane;
+                    const uint32_t k = e >= from && e < to ? part[j] : 0u;
+                    b2 = max(b2, min(b1, k));
+                    b1 = max(b1, k);
                 }
+                count(g, b1, b2);
+            }
+        }
+        int rank = 0;
+        for (int g = 0; g < a.groups; ++g) {
+            const float o = __shfl_sync(kAll, mine, g);
+            rank += before(o, g, mine, lane);
+        }
+        kept = __ballot_sync(kAll, lane < a.groups && rank < a.keep && mine > -CUDART_INF_F);
+        if (a.keep < a.groups && (a.bias || by_sum)) {
+            // Are the last group that is kept and the first that is not far enough apart?
+            const unsigned in = __ballot_sync(kAll, lane < a.groups && rank == a.keep - 1);
+            const unsigned out = __ballot_sync(kAll, lane < a.groups && rank == a.keep);
+            const float u = __shfl_sync(kAll, mine, __ffs(in) - 1), w = __shfl_sync(kAll, mine, __ffs(out) - 1);
+            if (w > -CUDART_INF_F && !(u - w > 2.0f * room))
+                kept = keep_exactly<T, SOFTMAX>(a, row, values + (threadIdx.x >> 5) * a.E, lane);
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int e = j * 32 + lane;
+            if (e < a.E && !(kept >> a.by_size(e) & 1)) key[j] = 0;
+        }
+    }
+    int pick = -1;
+    bool unsure = false;
+    {
+        int n = 0;           // picks so far
+        bool near = false;   // are two neighbours too near to tell apart?
+        float last = 0.0f;
+        while (true) {
+            uint32_t best = 0, at = ~0u;
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (key[j] > best) {
+                    best = key[j];
+                    at = j * 32 + lane;
+                }
+            const uint32_t m = __reduce_max_sync(kAll, best);
+            if (m == 0) break;
+            if (a.bias) {
+                const float v = unordered(m);
+                const bool apart = last - v > slack<SOFTMAX>(last);
+                if (n >= a.top_k && apart) break;
+                near |= n > 0 && !apart;
+                last = v;
+            }
+            if (n == 32) {
+                unsure = true;  // the run goes on past the lanes
+                break;
+            }
+            const uint32_t e = __reduce_min_sync(kAll, best == m ? at : ~0u);
+            if (lane == n) pick = e;
+            ++n;
+            if (n >= a.top_k && !a.bias) break;
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if ((uint32_t)(j * 32 + lane) == e) key[j] = 0;
+        }
+        if (near && !unsure) {
+            double denominator = 1.0;
+            if (SOFTMAX) {
+                denominator = 0.0;
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (x[j] > -CUDART_INF_F) denominator += exp((double)x[j] - (double)top);
+                denominator = warp_sum(denominator);
+            }
+            uint64_t v = 0;
+            if (lane < n) {
+                const double l = to_f32(row[pick]);
+                v = ordered((SOFTMAX ? exp(l - (double)top) / denominator : sigmoid(l)) + (double)a.bias[pick]);
             }
             int rank = 0;
-            for (int g = 0; g < a.groups; ++g) {
-                const float o = __shfl_sync(kAll, mine, g);
-                rank += before(o, g, mine, lane);
+            for (int o = 0; o < n; ++o) {
+                const uint64_t w = __shfl_sync(kAll, v, o);
+                const int e = __shfl_sync(kAll, pick, o);
+                rank += before(w, e, v, pick);
             }
-            kept = __ballot_sync(kAll, lane < a.groups && rank < a.keep && mine > -CUDART_INF_F);
-            if (a.keep < a.groups && (a.bias || by_sum)) {
-                // Are the last group that is kept and the first that is not far enough apart?
-                const unsigned in = __ballot_sync(kAll, lane < a.groups && rank == a.keep - 1);
-                const unsigned out = __ballot_sync(kAll, lane < a.groups && rank == a.keep);
-                const float u = __shfl_sync(kAll, mine, __ffs(in) - 1), w = __shfl_sync(kAll, mine, __ffs(out) - 1);
-                if (w > -CUDART_INF_F && !(u - w > 2.0f * room))
-                    kept = keep_exactly<T, SOFTMAX>(a, row, values + (threadIdx.x >> 5) * a.E, lane);
+            int mine = -1;
+            for (int o = 0; o < n; ++o) {
+                const int r = __shfl_sync(kAll, rank, o), e = __shfl_sync(kAll, pick, o);
+                if (r == lane) mine = e;
             }
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int e = j * 32 + lane;
-                if (e < a.E && !(kept >> a.by_size(e) & 1)) key[j] = 0;
-            }
+            pick = mine;
         }
-        int pick = -1;
-        bool unsure = false;
-        {
-            int n = 0;           // picks so far
-            bool near = false;   // are two neighbours too near to tell apart?
-            float last = 0.0f;
-            while (true) {
-                uint32_t best = 0, at = ~0u;
+    }
+    if (unsure) pick = choose_exactly<T, SOFTMAX>(a, row, values + (threadIdx.x >> 5) * a.E, kept, lane);
+    if (lane >= a.top_k) pick = -1;
+    // Scores of the picks.  Their shares of one another are formed from the logits, so that they hold
+    // where the scores themselves underflow.
+    const float l = pick >= 0 ? to_f32(row[pick]) : -CUDART_INF_F;
+    float w = 0.0f;
+    if (a.renormalise) {
+        float most = l;
 #pragma unroll
-                for (int j = 0; j < V; ++j)
-                    if (key[j] > best) {
-                        best = key[j];
-                        at = j * 32 + lane;
-                    }
-                const uint32_t m = __reduce_max_sync(kAll, best);
-                if (m == 0) break;
-                if (a.bias) {
-                    const float v = unordered(m);
-                    const bool apart = last - v > slack<SOFTMAX>(last);
-                    if (n >= a.top_k && apart) break;
-                    near |= n > 0 && !apart;
-                    last = v;
-                }
-                if (n == 32) {
-                    unsure = true;  // the run goes on past the lanes
-                    break;
-                }
-                const uint32_t e = __reduce_min_sync(kAll, best == m ? at : ~0u);
-                if (lane == n) pick = e;
-                ++n;
-                if (n >= a.top_k && !a.bias) break;
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    if ((uint32_t)(j * 32 + lane) == e) key[j] = 0;
-            }
-            if (near && !unsure) {
-                double denominator = 1.0;
-                if (SOFTMAX) {
-                    denominator = 0.0;
-#pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        if (x[j] > -CUDART_INF_F) denominator += exp((double)x[j] - (double)top);
-                    denominator = warp_sum(denominator);
-                }
-                uint64_t v = 0;
-                if (lane < n) {
-                    const double l = to_f32(row[pick]);
-                    v = ordered((SOFTMAX ? exp(l - (double)top) / denominator : sigmoid(l)) + (double)a.bias[pick]);
-                }
-                int rank = 0;
-                for (int o = 0; o < n; ++o) {
-                    const uint64_t w = __shfl_sync(kAll, v, o);
-                    const int e = __shfl_sync(kAll, pick, o);
-                    rank += before(w, e, v, pick);
-                }
-                int mine = -1;
-                for (int o = 0; o < n; ++o) {
-                    const int r = __shfl_sync(kAll, rank, o), e = __shfl_sync(kAll, pick, o);
-                    if (r == lane) mine = e;
-                }
-                pick = mine;
-            }
-        }
-        if (unsure) pick = choose_exactly<T, SOFTMAX>(a, row, values + (threadIdx.x >> 5) * a.E, kept, lane);
-        if (lane >= a.top_k) pick = -1;
-        // Scores of the picks.  Their shares of one another are formed from the logits, so that they hold
-        // where the scores themselves underflow.
-        const float l = pick >= 0 ? to_f32(row[pick]) : -CUDART_INF_F;
-        float w = 0.0f;
-        if (a.renormalise) {
-            float most = l;
-#pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, off));
-            if (!SOFTMAX) most = fminf(most, 0.0f);
-            if (pick >= 0) w = SOFTMAX ? exp_of_difference(l, most) : exp_of_difference(fminf(l, 0.0f), most) / (1.0f + expf(-fabsf(l)));
-            const float sum = warp_sum(w);
-            w = sum > 0.0f ? w / sum : 0.0f;
-        } else if (pick >= 0) {
-            w = SOFTMAX ? exp_of_difference(l, top) / total : sigmoid(l);
-        }
-        if (lane < a.top_k) {
-            a.ids[t * a.top_k + lane] = pick;
-            a.weights[t * a.top_k + lane] = w * a.scale;
-        }
+        for (int off = 16; off >= 1; off >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, off));
+        if (!SOFTMAX) most = fminf(most, 0.0f);
+        if (pick >= 0) w = SOFTMAX ? exp_of_difference(l, most) : exp_of_difference(fminf(l, 0.0f), most) / (1.0f + expf(-fabsf(l)));
+        const float sum = warp_sum(w);
+        w = sum > 0.0f ? w / sum : 0.0f;
+    } else if (pick >= 0) {
+        w = SOFTMAX ? exp_of_difference(l, top) / total : sigmoid(l);
+    }
+    if (lane < a.top_k) {
+        a.ids[t * a.top_k + lane] = pick;
+        a.weights[t * a.top_k + lane] = w * a.scale;
     }
 }
 
