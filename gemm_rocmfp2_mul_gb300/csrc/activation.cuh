@@ -1,6 +1,6 @@
-// Activations in memory: fp32, bf16 or f16, read to fp32 and written back with
-// one rounding, four or eight neighbouring values at a time where 16-byte
-// words fit, and the rotary angles that rope.cu and kvcache.cu share.
+// Activations in memory: fp32, bf16 or f16, read to fp32 (or held as they are) and
+// written back with one rounding, four or eight neighbouring values at a time where
+// 16-byte words fit, and the rotary angles that rope.cu and kvcache.cu share.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -61,6 +61,23 @@ RFP2_DEV void store_values(T *p, const float (&v)[N]) {
         for (int e = 0; e < N; ++e) p[e] = from_f32<T>(v[e]);
     }
 }
+
+// V values as they are in memory, in words of 16 bytes where V > 1.
+template <typename T, int V>
+struct Held {
+    T v[V];
+    RFP2_DEV void load(const T *p) {
+        if constexpr (V == 1) {
+            v[0] = *p;
+        } else {
+#pragma unroll
+            for (int w = 0; w < V * (int)sizeof(T) / 16; ++w) {
+                const uint4 u = reinterpret_cast<const uint4 *>(p)[w];
+                memcpy(v + w * (16 / sizeof(T)), &u, 16);
+            }
+        }
+    }
+};
 
 // Rotary angles.  theta = position * f in turns is position * (f / 2 pi) mod
 // 1.  With f / 2 pi mod 1 as a 64-bit binary fraction, the product with an

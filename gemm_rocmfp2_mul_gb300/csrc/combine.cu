@@ -30,23 +30,6 @@ struct CombineArgs {
     FastDiv by_lanes;
 };
 
-// V values as they are in memory, in words of 16 bytes where V > 1.
-template <typename T, int V>
-struct Held {
-    T v[V];
-    RFP2_DEV void load(const T *p) {
-        if constexpr (V == 1) {
-            v[0] = *p;
-        } else {
-#pragma unroll
-            for (int w = 0; w < V * (int)sizeof(T) / 16; ++w) {
-                const uint4 u = reinterpret_cast<const uint4 *>(p)[w];
-                memcpy(v + w * (16 / sizeof(T)), &u, 16);
-            }
-        }
-    }
-};
-
 // Weights of up to N slots, and which of them are read.
 template <int N>
 struct Slots {

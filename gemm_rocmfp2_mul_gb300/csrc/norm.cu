@@ -75,21 +75,6 @@ RFP2_DEV void store_typed(void *p, int type, int64_t at, const float (&v)[V]) {
         store_run(static_cast<__half *>(p) + at, v);
 }
 
-// V values as they are in memory, in words of 16 bytes where V > 1.
-template <typename T, int V>
-struct Held {
-    T v[V];
-    RFP2_DEV void load(const T *p) {
-        if constexpr (V == 1) {
-            v[0] = *p;
-        } else {
-            static_assert(V * sizeof(T) == 16, "one word");
-            const uint4 u = *reinterpret_cast<const uint4 *>(p);
-            memcpy(v, &u, 16);
-        }
-    }
-};
-
 // Sum (or maximum) over the warps that share a row; `part` has 32 places, and successive calls take
 // turns between two of them.
 template <bool MAX>
