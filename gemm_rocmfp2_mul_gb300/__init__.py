@@ -269,7 +269,8 @@ def rfp2_moe_workspace_bytes(T: int, top_k: int, K: int) -> int:
 
 
 def rfp2_moe_gemv(W, E, M, K, ids, x, y=None, workspace=None, dev_status=None):
-    """MoE expert-indexed GEMV: y fp32 [T, top_k, M] = W[ids[t, j]] x_t."""
+    """MoE expert-indexed GEMV: y fp32 [T, top_k, M] = W[ids[t, j]] x_t.  An id outside [0, E), -1 among them, gives a
+    row of NaN and RFP2_EBADID.  For up to about three tokens an expert; rfp2_moe_gemm is faster above."""
     torch = _torch()
     _need(W, torch.uint8, "W")
     _need(ids, torch.int32, "ids")
@@ -645,7 +646,7 @@ class Norm(NamedTuple):
 def rfp2_rms_norm(x, weight, eps=1e-6, residual=None, want="y", dtype=None, y=None, q=None, d=None, total=None):
     """Root-mean-square norm of x [T, K] (any row stride), after adding `residual` where there is one:
     s / sqrt(mean(s^2) + eps) * weight.  want: "y" (values, of `dtype`, x's unless given), "q8" (the Q8
-    blocks that rfp2_gemv_q8 reads, K % 32 == 0) or "both".  Buffers that are passed are filled; total and y may be
+    blocks that rfp2_gemv_q8 reads, for up to 8 rows with K % 256 == 0; of any number of rows with K % 32 == 0) or "both".  Buffers that are passed are filled; total and y may be
     x or residual.  There is no gradient."""
     if want not in ("y", "q8", "both"):
         raise ValueError(f"want must be 'y', 'q8' or 'both', got {want!r}")
@@ -675,7 +676,8 @@ def rfp2_moe_route(logits, top_k, scoring="softmax", bias=None, groups=1, keep=1
     """The experts of each token, from the router's logits [T, E]: (ids int32 [T, top_k], largest first, and
     weights fp32 [T, top_k]).  scoring: "softmax" or "sigmoid"; bias fp32 [E] is added for the choice alone; with
     groups > 1 only the `keep` groups are chosen from whose group_top largest values sum to most.  A logit of
-    -infinity masks its expert; where none is left the id is -1 and the weight 0.  There is no gradient."""
+    -infinity masks its expert; where none is left the id is -1 and the weight 0 (rfp2_moe_gemm has a row of zeros for
+    it, rfp2_moe_gemv one of NaN, which rfp2_moe_combine with ids does not read).  There is no gradient."""
     if ids is None or weights is None:
         torch = _torch()
         if logits.dim() != 2:
@@ -706,7 +708,8 @@ def rfp2_moe_gemm(W, E, M, K, ids, X, bias=None, activation="none", Y=None, work
     """The routed experts' products on the tensor cores, for any number of tokens: bf16 [T, top_k, M] =
     W[ids[t, j]] x + bias[ids[t, j]] with X bf16 [T, K], or [T, top_k, K] (a row for every slot), ids int32
     [T, top_k] and bias fp32 [E, M].  activation "silu" or "gelu": [T, top_k, M/2] = act(gate) * up, W's first M/2 rows
-    being the gate's.  An id of -1 is no expert: its row becomes zeros.  There is no gradient."""
+    being the gate's.  An id of -1 is no expert: its row becomes zeros.  rfp2_moe_gemv is faster for fewer than about
+    three tokens an expert.  There is no gradient."""
     if Y is None:
         Y = _empty((*ids.shape, M if activation == "none" else M // 2), _torch().bfloat16, X)
     if workspace is None:

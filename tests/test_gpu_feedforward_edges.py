@@ -177,3 +177,34 @@ def test_outputs_that_require_a_gradient_are_refused(g):
             call()
         with torch.no_grad():
             call()
+
+
+def test_router_gemv_combination(g):
+    """The path of a few tokens: router, rfp2_moe_gemv, combination.  A slot whose id is -1 has a row of NaN from the
+    products, as that call answers any id outside, which the combination with ids does not read."""
+    import torch
+    r = np.random.default_rng(5)
+    T, E, M, K, k = 6, 12, 64, 256, 4
+    W = r.integers(0, 256, (E, M, K // 32, 10), dtype=np.uint8)
+    W[..., 8:] %= 28
+    logits = torch.from_numpy(r.standard_normal((T, E)).astype(np.float32)).cuda()
+    logits[2, 2:] = logits[4] = -float("inf")
+    x = torch.from_numpy(r.standard_normal((T, K)).astype(np.float32)).cuda()
+    rest = torch.from_numpy(r.standard_normal((T, M)).astype(np.float32)).cuda()
+    ids, weights = g.rfp2_moe_route(logits, k)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = g.rfp2_moe_gemv(torch.from_numpy(W).cuda(), E, M, K, ids, x, dev_status=status)
+    assert int(status) == 7 and bool((y.isnan().all(-1) == (ids < 0)).all()) and int((ids < 0).sum()) == 2 + k
+    out = g.rfp2_moe_combine(y, weights, ids=ids, residual=rest)
+    # activations in 8 bits: off by half a step of 1/127 of their block's largest at most
+    w, X = plain.weights_of(W), x.double().cpu().numpy()
+    half = np.abs(X).reshape(T, -1, 32).max(-1).repeat(32, -1) / 254
+    found, probs = ids.cpu().numpy(), weights.double().cpu().numpy()
+    for t in range(T):
+        ref, off = rest[t].double().cpu().numpy(), 2.0 ** -20
+        for j in range(k):
+            if found[t, j] >= 0:
+                a = w[found[t, j]]
+                ref, off = ref + probs[t, j] * (a @ X[t]), off + probs[t, j] * (np.abs(a) @ (half[t] + 2.0 ** -18 * np.abs(X[t])))
+        assert np.all(np.abs(out[t].double().cpu().numpy() - ref) <= off)
+    assert torch.equal(out[4], rest[4])
