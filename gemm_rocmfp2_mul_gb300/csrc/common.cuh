@@ -93,6 +93,21 @@ RFP2_DEV bool mbar_wait_sleepy(uint64_t *bar, uint32_t parity) {
     }
 }
 
+RFP2_DEV void record_status(int32_t *dev_status, int32_t code) {
+    if (dev_status) atomicCAS(reinterpret_cast<int *>(dev_status), 0, code);
+}
+
+// Has a whole warp's wait ended well?  Each lane has a time limit of its own, and
+// what follows is done by whole warps (tcgen05.ld, shuffles, __syncwarp): at
+// the limit its lanes leave together, with the status recorded and the CTA's
+// abort flag raised.
+RFP2_DEV bool warp_goes_on(bool there, volatile int *abort_flag, int32_t *status) {
+    if (__all_sync(0xffffffffu, there)) return true;
+    if ((threadIdx.x & 31) == 0) record_status(status, RFP2_ETIMEOUT);
+    *abort_flag = 1;
+    return false;
+}
+
 // ---- clusters ----------------------------------------------------------------
 RFP2_DEV uint32_t cluster_ctarank() {
     uint32_t r;
@@ -166,10 +181,6 @@ RFP2_DEV uint64_t policy_evict_first() {
 // allow the next grid in the stream to begin launching.
 RFP2_DEV void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 RFP2_DEV void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" :::); }
-
-RFP2_DEV void record_status(int32_t *dev_status, int32_t code) {
-    if (dev_status) atomicCAS(reinterpret_cast<int *>(dev_status), 0, code);
-}
 
 // Named barrier over `nthreads` threads (a multiple of 32).
 RFP2_DEV void named_bar_sync(uint32_t id, uint32_t nthreads) {

@@ -306,11 +306,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GemmCfg<kDecode>::kT
         int it = 0;
         for (int t = pair; t < nslots; t += npairs, ++it) {
             const int b = it & 1;
-            if (*abort_flag || !mbar_wait(&accf[b], (it >> 1) & 1)) {
-                record_status(status, RFP2_ETIMEOUT);
-                *abort_flag = 1;
-                break;
-            }
+            if (!warp_goes_on(!*abort_flag && mbar_wait(&accf[b], (it >> 1) & 1), abort_flag, status)) break;
             tc_fence_after();
             const Slot sl = slot_tile(t, t_full, split_lg, ntm);
             const int row0 = sl.tile_m * PM + (int)rank * BM + q * 32;
@@ -397,9 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GemmCfg<kDecode>::kT
                     const int gd = gbase + kb, s = gd % kStages, ps = ud % kPStages;
                     bool w_ok = !*abort_flag && mbar_wait(&pfull[ps], (ud / kPStages) & 1);
                     if (gd >= kStages) w_ok = w_ok && mbar_wait(&empty[s], ((gd / kStages) - 1) & 1);
-                    if (!__all_sync(0xffffffffu, w_ok)) {
-                        if (lane == 0) record_status(status, RFP2_ETIMEOUT);
-                        *abort_flag = 1;
+                    if (!warp_goes_on(w_ok, abort_flag, status)) {
                         ok = false;
                         break;
                     }

@@ -380,14 +380,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int blocks = (a.out + 2 * kOut - 1) / (2 * kOut);
     const int units = a.plan.header[0] * blocks;
 
-    // Has a warp's wait ended well?  Each lane has a time limit of its own, and what follows is done by whole warps:
-    // at the limit the lanes leave together.
-    const auto goes_on = [&](bool there) {
-        if (__all_sync(0xffffffffu, there)) return true;
-        if (lane == 0) record_status(status, RFP2_ETIMEOUT);
-        *abort_flag = 1;
-        return false;
-    };
+    const auto goes_on = [&](bool there) { return warp_goes_on(there, abort_flag, status); };
 
     if (warp == 0 || warp >= 7 + kDecodeWarps) {
         // ---- gathers: lane l copies chunk l % 8 of rows l / 8, l / 8 + 4, ...  Each warp waits for its own copies

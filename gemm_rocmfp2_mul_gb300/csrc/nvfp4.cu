@@ -343,16 +343,16 @@ __global__ void __launch_bounds__(kNvThreads, 1)
         bool ok = true;
         for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x, ++it) {
             const int b = it & 1;
-            if (it >= 2 && (*abort_flag || !mbar_wait(&acc_empty[b], ((it >> 1) - 1) & 1))) {
-                fail();
+            if (it >= 2 &&
+                !warp_goes_on(!*abort_flag && mbar_wait(&acc_empty[b], ((it >> 1) - 1) & 1), abort_flag, status)) {
                 ok = false;
                 break;
             }
             for (int kk = 0; kk < nk; ++kk, ++gs) {
                 const int s = gs % kNvStages;
                 const uint32_t ph = (gs / kNvStages) & 1;
-                if (*abort_flag || !mbar_wait(&full[s], ph) || !mbar_wait(&sf_full[s], ph)) {
-                    fail();
+                if (!warp_goes_on(!*abort_flag && mbar_wait(&full[s], ph) && mbar_wait(&sf_full[s], ph), abort_flag,
+                                  status)) {
                     ok = false;
                     break;
                 }
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kNvThreads, 1)
             __syncwarp();
         }
         // the tensor cores finish every issued MMA before the memory is freed
-        if (gs > 0 && !mbar_wait(&empty[(gs - 1) % kNvStages], ((gs - 1) / kNvStages) & 1)) fail();
+        if (gs > 0) warp_goes_on(mbar_wait(&empty[(gs - 1) % kNvStages], ((gs - 1) / kNvStages) & 1), abort_flag, status);
     } else if (warp < 6) {
         // ---- scale warps: this warp's lane quadrant of every scale slot.  A
         // stage's copies land only after the MMAs of the slot's previous
@@ -386,8 +386,7 @@ __global__ void __launch_bounds__(kNvThreads, 1)
         for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
             for (int kk = 0; kk < nk; ++kk, ++gs) {
                 const int s = gs % kNvStages;
-                if (*abort_flag || !mbar_wait(&full[s], (gs / kNvStages) & 1)) {
-                    fail();
+                if (!warp_goes_on(!*abort_flag && mbar_wait(&full[s], (gs / kNvStages) & 1), abort_flag, status)) {
                     ok = false;
                     break;
                 }
@@ -411,10 +410,7 @@ __global__ void __launch_bounds__(kNvThreads, 1)
         int it = 0;
         for (int t = blockIdx.x; t < ntiles; t += gridDim.x, ++it) {
             const int tm = t % ntm, tn = t / ntm, b = it & 1;
-            if (*abort_flag || !mbar_wait(&acc_full[b], (it >> 1) & 1)) {
-                fail();
-                break;
-            }
+            if (!warp_goes_on(!*abort_flag && mbar_wait(&acc_full[b], (it >> 1) & 1), abort_flag, status)) break;
             tc_fence_after();
             const int m = tm * kBM + 32 * qe + lane;
 #pragma unroll 1

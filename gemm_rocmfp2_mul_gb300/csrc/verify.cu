@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(VTHREADS, 1)
         }
         if (elect_one()) umma_commit(mdone);
         __syncwarp();
-        if (!mbar_wait(mdone, 0) && lane == 0) record_status(status, RFP2_ETIMEOUT);
+        warp_goes_on(mbar_wait(mdone, 0), abort_flag, status);
     } else if (warp >= 4) {
         // ---- decode: group g takes slice g of every packed stage (stage t =
         // 4p + g), then reads back its quarter of the tokens
@@ -434,11 +434,7 @@ __global__ void __launch_bounds__(VTHREADS, 1)
         bool ok = true;
         int drained = 0;  // rounds read back so far
         auto drain = [&](int r) {
-            if (*abort_flag || !mbar_wait(accf, r & 1)) {
-                record_status(status, RFP2_ETIMEOUT);
-                *abort_flag = 1;
-                return false;
-            }
+            if (!warp_goes_on(!*abort_flag && mbar_wait(accf, r & 1), abort_flag, status)) return false;
             tc_fence_after();
             constexpr int TC = TQ < 16 ? TQ : 16;  // columns per read
 #pragma unroll
@@ -468,11 +464,8 @@ __global__ void __launch_bounds__(VTHREADS, 1)
                 ++drained;
             }
             const int p = t / 4, ps = p % VPSTAGES, as = t % kASlots;
-            if (*abort_flag || !mbar_wait(&pfull[ps], (p / VPSTAGES) & 1)) {
-                record_status(status, RFP2_ETIMEOUT);
-                *abort_flag = 1;
-                break;
-            }
+            // (one vote, after the decode: what a slice that did not come decodes to is not stored)
+            bool there = !*abort_flag && mbar_wait(&pfull[ps], (p / VPSTAGES) & 1);
             // this slice's 20 bytes of the row: blocks 2g and 2g + 1 of the stage
             const uint32_t *src = reinterpret_cast<const uint32_t *>(prow + (size_t)ps * kPStageBytes);
             uint32_t v[5];
@@ -486,11 +479,8 @@ __global__ void __launch_bounds__(VTHREADS, 1)
             decode_block_f16(block_from_words<2>(v, 0), w);
             decode_block_f16(block_from_words<2>(v, 1), w + 16);
             const int u = t / VQ;
-            if (u >= AQ && (*abort_flag || !mbar_wait(&emptyq[(u - AQ) % QS], ((u - AQ) / QS) & 1))) {
-                record_status(status, RFP2_ETIMEOUT);
-                *abort_flag = 1;
-                break;
-            }
+            if (u >= AQ) there = there && !*abort_flag && mbar_wait(&emptyq[(u - AQ) % QS], ((u - AQ) / QS) & 1);
+            if (!warp_goes_on(there, abort_flag, status)) break;
             tc_fence_after();
             tmem_st_32cols(tmem + lane_base + (uint32_t)(kACol0 + as * 32), w);
             tmem_st_wait();
