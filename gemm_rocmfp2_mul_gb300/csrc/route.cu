@@ -12,8 +12,8 @@
 // lanes; groups too near to tell apart) is done by fp64 values of all experts.
 //
 // Bound by instructions, not by the logits' bytes: about 1500 a token with a bias, groups and eight picks.
-// Measured (one GB300, GPU time a call): 16384 x 256, sigmoid, bias, 4 of 8 groups, 8 experts: 32 us; 4 x 256 2.7
-// us.
+// Measured (one GB300, GPU time a call): 16384 x 256, sigmoid, bias, 4 of 8 groups, 8 experts: 33 us, four tokens of
+// it 3.7 us; 4 x 256 softmax 2.5 us; 4999 x 60 3.0 us.
 #include <algorithm>
 
 #include "activation.cuh"
@@ -71,11 +71,13 @@ RFP2_DEV double warp_sum(double v) {
     return v;
 }
 
-// Twice how far a value in fp32 may be off: a softmax score is at most 1 and off by 1e-6 of itself (expf, the
-// difference before it half a unit of at most its own size, ten levels of a sum, a quotient), a sigmoid by
-// 5e-7 (near_sigmoid), and its sum with the bias is rounded.
+// Twice how far a value in fp32 may be off.  A softmax score is off by 1.2e-6 at most, absolutely (of itself a small
+// one by far more): its exponential's (2 + 1.2 d) 2^-23 e^-d at distance d from the top is largest at d = 0, the
+// rounding of d adds at most 2^-25, the sum is off by ten levels of 2^-24 and by what its terms are, which share
+// what a score of 1 leaves, and reciprocal and product round once each.  A sigmoid is off by 5e-7 (near_sigmoid).
+// Their sum with the bias is rounded.
 template <bool SOFTMAX>
-RFP2_DEV float slack(float v) { return (SOFTMAX ? 2e-6f : 1e-6f) + 1.3e-7f * fabsf(v); }
+RFP2_DEV float slack(float v) { return (SOFTMAX ? 2.4e-6f : 1e-6f) + 1.3e-7f * fabsf(v); }
 
 // Does pair (v, i) come before (w, j)?
 template <typename F>
