@@ -208,3 +208,74 @@ def test_router_gemv_combination(g):
                 ref, off = ref + probs[t, j] * (a @ X[t]), off + probs[t, j] * (np.abs(a) @ (half[t] + 2.0 ** -18 * np.abs(X[t])))
         assert np.all(np.abs(out[t].double().cpu().numpy() - ref) <= off)
     assert torch.equal(out[4], rest[4])
+
+
+FIRST = """
+import sys
+import torch
+import gemm_rocmfp2_mul_gb300 as g
+x, w = torch.ones((4, 256), device="cuda"), torch.ones(256, device="cuda")
+W = torch.full((2, 64, 8, 10), 0xAA, dtype=torch.uint8, device="cuda")
+W[..., 8:] = 64
+stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+stream.wait_stream(torch.cuda.current_stream())
+with torch.cuda.stream(stream):
+    with torch.cuda.graph(graph, stream=stream):
+        n = g.rfp2_rms_norm(x, w, residual=x, dtype=torch.bfloat16)
+        ids, weights = g.rfp2_moe_route(x[:, :2], 2)
+        y = g.rfp2_moe_gemm(W, 2, 64, 256, ids, n.y)
+        out = g.rfp2_moe_combine(y, weights, ids=ids)
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+stream.synchronize()
+assert bool((out == 256).all()), out
+"""
+
+
+def test_first_calls_are_captured():
+    """A process whose first calls are captured: what a call sets up once is set up there."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_calls_of_several_threads(g):
+    """Host threads on streams of their own, the same weights, every operator."""
+    import threading
+    import torch
+    r = np.random.default_rng(6)
+    W = r.integers(0, 256, (8, 128, 8, 10), dtype=np.uint8)
+    W[..., 8:] %= 28
+    W, w = torch.from_numpy(W).cuda(), torch.ones(256, device="cuda")
+    inputs = [torch.randn((70 + 40 * i, 256), device="cuda") for i in range(4)]
+
+    def layer(x):
+        n = g.rfp2_rms_norm(x, w, residual=x, dtype=torch.bfloat16)
+        ids, weights = g.rfp2_moe_route(x[:, :8], 3, scoring="sigmoid")
+        y = g.rfp2_moe_gemm(W, 8, 128, 256, ids, n.y, activation="silu")
+        return g.rfp2_moe_combine(y, weights, ids=ids)
+
+    want = [layer(x) for x in inputs]
+    torch.cuda.synchronize()
+    got, failed = [None] * 4, []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    got[i] = layer(inputs[i])
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
