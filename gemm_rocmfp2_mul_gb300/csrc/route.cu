@@ -246,20 +246,14 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         float mine = -CUDART_INF_F;  // lane g: what group g counts
         float room = 0.0f;           // how far any of them may be off
         // What a group of largest values m1 and m2 (0: none) counts, and how far that may be off.  A sum of two
-        // finite values may leave fp32's range: a group that has experts counts as the lowest value at least
-        // (-infinity is one without), and such sums are for fp64 to tell apart.
+        // finite values may leave fp32's range: kept within it, a group that has experts is never taken for one
+        // without (-infinity), and sums past one end are equal here, for fp64 to tell apart.
         const auto counts = [&](uint32_t m1, uint32_t m2, float &off) {
-            off = 0.0f;
-            if (!m1) return -CUDART_INF_F;
-            float v = unordered(m1);
-            off = slack<SOFTMAX>(v);
+            float v = m1 ? unordered(m1) : -CUDART_INF_F;
+            off = m1 ? slack<SOFTMAX>(v) : 0.0f;
             if (by_sum && m2) {
                 off += slack<SOFTMAX>(unordered(m2));
-                v += unordered(m2);
-                if (fabsf(v) == CUDART_INF_F) {
-                    v = copysignf(CUDART_MAX_NORMAL_F, v);
-                    off = CUDART_INF_F;
-                }
+                v = fminf(fmaxf(v + unordered(m2), -CUDART_MAX_NORMAL_F), CUDART_MAX_NORMAL_F);
             }
             return v;
         };
