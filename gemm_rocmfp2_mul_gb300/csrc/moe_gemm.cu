@@ -6,10 +6,10 @@
 //  2. the product on the tensor cores: units of a tile and 256 weight rows (128 gate rows and the 128 up rows
 //     that go with them).
 //
-// Measured (one GB300, GPU time a call): 8192 tokens to 2 of 8 experts of 14336 x 4096, gated: 1287 us, 1.50
-// PFLOP/s (0.78 of cuBLAS's burst rate, which has no weights to decode; 0.77 is what rfp2_gemm has); 2047 to 8
-// of 256 of 1536 x 2048, gated: 260 us; 16 to 8 of 256 of 768 x 2048: 38 us.  Wide tiles are bound by the
-// shared-memory port, narrow ones by a stage's way around and by the decoding.
+// Measured (one GB300, GPU time a call): 8192 tokens to 2 of 8 experts of 14336 x 4096, gated: 1160-1305 us by how
+// long the chip has been busy, 1.47-1.66 PFLOP/s (0.76-0.86 of cuBLAS's burst rate, which has no weights to decode;
+// 0.77 is what rfp2_gemm has); 2047 to 8 of 256 of 1536 x 2048, gated: 254 us; 16 to 8 of 256 of 768 x 2048: 38 us.
+// Wide tiles are bound by the shared-memory port, narrow ones by a stage's way around.
 #include <algorithm>
 #include <mutex>
 
@@ -168,7 +168,7 @@ struct GemmArgs {
 // gate s / (1 + h^2) s, where s is 1 for v >= 0 and h below: the divisor stays within [1, 2], where a reciprocal
 // needs no care for its range, and act(gate) * up is formed before it would underflow (h is 0 from |v| = 174 on).
 // The approximate exponential and reciprocal are off by 2^-21 (2 + |v|) of the result at most, which is rounded to
-// bf16; with exact ones the epilogue held the MMAs up (1363 -> 1287 us of the case above, 277 -> 260).
+// bf16; with exact ones the epilogue held the MMAs up (1363 us of the first case above and 277 of the second).
 RFP2_DEV float activated(int activation, float gate, float up) {
     const float v = activation == RFP2_ACT_SILU ? gate : 1.5957691216057308f * fmaf(0.044715f * gate * gate, gate, gate);
     float h, r;

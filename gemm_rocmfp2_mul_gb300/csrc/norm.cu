@@ -11,7 +11,9 @@
 // Measured (one GB300, GPU time a call): 16384 x 5120 bf16 with a residual 97.5 us, 6.9 TB/s read and written
 // (the copy rate); 4999 x 1376 f16 to values and codes 15.9 us, bound by instructions; 4 x 4096 fp32 to
 // codes 3.4 us.  A persistent grid took 205 us of the first: its loop kept the addresses of a row's
-// values in registers that the values then lacked.
+// values in registers that the values then lacked.  Rows of odd length or alignment above 4096 values hold 32 fp32
+// values a thread of up to 1024 and spill (4999 x 5121 bf16 112 us, 0.9 TB/s), as fp32 rows with codes above 8192 do
+// (2000 x 16384 68 us).
 #include <algorithm>
 #include <type_traits>
 

@@ -527,7 +527,9 @@ rfp2_status rfp2_attn_decode(const void *q, int dtype, int64_t B, int64_t nq, in
  *   total and y may each be x or residual, with the same type and stride; any
  *   other overlap is not allowed.
  * Squares that leave fp32's range are taken of values scaled by a power of two,
- * so rows of any finite size have their norm.
+ * so rows of any finite size have their norm.  y has the digits that s * r has
+ * in fp32 (those below 2^-126 fewer), and codes are exact for |weight| up to
+ * 2^36.
  * Errors: EINVAL (null, negative size, bad dtype, no output, q without d, eps
  * not positive and finite, such an overlap), ESHAPE (K > 32768, K % 32 with q, T > 2^31 - 1, an
  * output's row stride below K, an input's below 0), EALIGN (a pointer not aligned to its type, q not to 16
